@@ -394,6 +394,76 @@ MP_API mp_status rht16(const void* x_bf16, int64_t rows, int64_t cols, uint16_t 
 MP_API mp_status mx_quantize(const void* x, mp_dtype x_dtype, int64_t rows, int64_t cols, mp_dtype elem_dtype,
                              void* codes, uint8_t* scales, void* dequant_bf16, void* stream);
 
+/* =========================================================================
+ * 5. Block operators with 8-bit outputs and 8-bit checkpoints
+ * ========================================================================= */
+
+/* The places of a transformer block where a row operation feeds an FP8 GEMM,
+ * fused with the cast, and their backward passes.  A checkpoint is the tensor
+ * in E4M3 with one FP32 scale per 1x128 tile of a row: the bytes and scales
+ * of fp8_quantize_blockwise(1, 128, MP_E4M3), written by the forward pass from
+ * the same read and taken by the backward pass in place of the tensor.  One
+ * difference from that call: a tile with 0 < amax < fp8_max / FLT_MAX (below
+ * 2^-112) becomes zeros.
+ * FP8 outputs (fp8_dtype MP_E4M3 or MP_E5M2) take scale_block 128 (FP32
+ * scales [rows][ceil(cols/128)], the rule of fp8_quantize_blockwise applied
+ * to the binary32 result) or 32 (UE8M0 bytes [rows][cols/32], the rule of
+ * mx_quantize; cols % 32 == 0).
+ * x_dtype, w_dtype, dw_dtype: MP_F32, MP_F16 or MP_BF16; every tensor called
+ * x, residual, h, dy, dh, dx, gate, up, dp, dgate, dup has type x_dtype.
+ * cols % 16 == 0 (else MP_ESHAPE); tensors 16-byte aligned, FP32 scales and
+ * rstd 4-byte, UE8M0 bytes not at all.  Sums are binary32 in an order fixed
+ * by the shape, so results repeat. */
+
+/* rmsnorm_residual_fp8 — h = x + residual rounded to x_dtype (h = x if
+ * residual is NULL); rstd = 1 / sqrt(mean(h^2) + eps) per row; y = the cast of
+ * (h * rstd) * weight.  h, rstd and the checkpoint of h (ckpt [rows, cols],
+ * ckpt_scales) may be NULL; a checkpoint needs both its pointers.  h may be x
+ * or residual.  weight [cols].  eps finite and >= 0; a row of zeros with eps 0
+ * has rstd = inf and gives NaN codes.  A row whose sum of squares exceeds
+ * binary32 has rstd = 0.  cols <= 32768, rows < 2^31 (else MP_ESHAPE).  rows
+ * or cols 0: nothing is written.  One kernel launch. */
+MP_API mp_status rmsnorm_residual_fp8(const void* x, const void* residual, mp_dtype x_dtype, int64_t rows,
+                                      int64_t cols, const void* weight, mp_dtype w_dtype, float eps, void* h,
+                                      void* y, mp_dtype fp8_dtype, int32_t scale_block, void* y_scales, float* rstd,
+                                      void* ckpt, float* ckpt_scales, void* stream);
+
+/* rmsnorm_residual_backward — from dy (the gradient of the normed, unquantised
+ * rows), dh (the gradient that reaches h along the stream; may be NULL), rstd,
+ * and exactly one of h and its checkpoint (ckpt with ckpt_scales): with v the
+ * stream's values, xh = v * rstd, g = dy * weight,
+ *     dx = rstd * (g - xh * mean(g * xh)) + dh   (of x and of residual alike)
+ *     dweight[c] = sum over rows of dy * xh      (dw_dtype [cols], overwritten)
+ * dx may be dy, dh or h.  d_workspace: rmsnorm_workspace_size(rows, cols)
+ * bytes, 16-byte aligned, any contents (else MP_EWORKSPACE).  Same limits as
+ * the forward call; rows 0 writes dweight = 0 and needs no workspace.  Two
+ * kernel launches. */
+MP_API size_t rmsnorm_workspace_size(int64_t rows, int64_t cols);
+MP_API mp_status rmsnorm_residual_backward(const void* dy, const void* dh, mp_dtype x_dtype, int64_t rows,
+                                           int64_t cols, const void* h, const void* ckpt, const float* ckpt_scales,
+                                           const void* weight, mp_dtype w_dtype, const float* rstd, void* dx,
+                                           void* dweight, mp_dtype dw_dtype, void* d_workspace,
+                                           size_t workspace_bytes, void* stream);
+
+/* swiglu_fp8 — y = the cast of (gate * s(gate)) * up, s the logistic function.
+ * gate and up [rows, cols] with rows `ld` elements apart (the two halves of
+ * one product have ld = 2 * cols): ld >= cols and rows 16-byte aligned where
+ * rows > 1 (else MP_ESHAPE).  ckpt (may be NULL, with ckpt_scales): gate's
+ * and then up's checkpoint, [2][rows][cols] codes and [2][rows][ceil(cols/128)]
+ * scales.  rows, cols < 2^31.  One kernel launch. */
+MP_API mp_status swiglu_fp8(const void* gate, const void* up, int64_t ld, mp_dtype x_dtype, int64_t rows,
+                            int64_t cols, void* y, mp_dtype fp8_dtype, int32_t scale_block, void* y_scales,
+                            void* ckpt, float* ckpt_scales, void* stream);
+
+/* swiglu_backward — from dp [rows, cols] (the gradient of the unquantised
+ * product) and exactly one of (gate, up) with row distance ld and their
+ * checkpoint: dup = dp * (gate * s), dgate = dp * up * (s + gate * s * (1 - s)),
+ * written with row distance d_ld (rules of ld).  dgate and dup may be gate and
+ * up.  One kernel launch. */
+MP_API mp_status swiglu_backward(const void* dp, mp_dtype x_dtype, int64_t rows, int64_t cols, const void* gate,
+                                 const void* up, int64_t ld, const void* ckpt, const float* ckpt_scales, void* dgate,
+                                 void* dup, int64_t d_ld, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

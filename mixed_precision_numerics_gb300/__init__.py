@@ -112,6 +112,11 @@ def _load() -> ctypes.CDLL:
         "nvfp4_noalloc_scratch_bytes": (S, []),
         "nvfp4_quantize_noalloc": (I32, [P, I64, I64, I32, I32, U64, I32, U16, P, P, P, P, P, P]),
         "mx_quantize": (I32, [P, I32, I64, I64, I32, P, P, P, P]),
+        "rmsnorm_residual_fp8": (I32, [P, P, I32, I64, I64, P, I32, F, P, P, I32, I32, P, P, P, P, P]),
+        "rmsnorm_workspace_size": (S, [I64, I64]),
+        "rmsnorm_residual_backward": (I32, [P, P, I32, I64, I64, P, P, P, P, I32, P, P, P, I32, P, S, P]),
+        "swiglu_fp8": (I32, [P, P, I64, I32, I64, I64, P, I32, I32, P, P, P, P]),
+        "swiglu_backward": (I32, [P, I32, I64, I64, P, P, I64, P, P, P, P, I64, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -464,7 +469,145 @@ def mx_quantize(x, codes, scales, elem_dtype: int = MP_E2M1, dequant=None, strea
                                           _ptr(scales), _ptr(dequant), _stream(stream)))
 
 
+# ---- block operators with 8-bit outputs and 8-bit checkpoints ------------------------------
+
+
+def _same(t, name: str, nbytes: int, x, dtype, align: int = 16) -> None:
+    """_dev, and the element type: a tensor of another 16-bit type has the right size."""
+    if t is None or isinstance(t, int):
+        return
+    _dev(t, name, nbytes, like=x, align=align)
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: {t.dtype}, the call needs {dtype}")
+
+
+def _row_pitch(t, name: str, x, rows: int, cols: int) -> int:
+    """Elements between the rows of a [rows, cols] matrix that may be a column range of a wider one."""
+    import torch
+
+    if not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor is required (the kernels read and write device memory)")
+    want = x.device if x is not t else torch.device("cuda", torch.cuda.current_device())
+    if t.device != want:
+        raise ValueError(f"{name}: on {t.device}, the call runs on {want}")
+    if tuple(t.shape) != (rows, cols) or t.dtype != x.dtype:
+        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, the call needs {(rows, cols)} {x.dtype}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return t.stride(0) if rows > 1 else cols
+
+
+def _fp8_out(y, y_scales, scale_block: int, rows: int, cols: int, x) -> None:
+    _dev(y, "y", rows * cols, like=x)
+    if scale_block == 32:
+        _dev(y_scales, "y_scales", rows * (cols // 32), like=x, align=1)
+    else:
+        _dev(y_scales, "y_scales", 4 * rows * -(-cols // 128), like=x, align=4)
+
+
+def rmsnorm_residual_fp8(x, weight, y, y_scales, *, residual=None, h=None, rstd=None, ckpt=None, ckpt_scales=None,
+                         eps: float = 1e-5, fp8_dtype: int = MP_E4M3, scale_block: int = 128, stream=None) -> None:
+    """h = x + residual; y = FP8 of h / rms(h) * weight.  x: [rows, cols]; weight: [cols]; y: rows*cols
+    bytes; y_scales: float32 [rows, ceil(cols/128)], or with scale_block 32 one UE8M0 byte per 32
+    elements.  h (as x), rstd (float32 [rows]) and ckpt (rows*cols bytes, with ckpt_scales float32
+    [rows, ceil(cols/128)]) are outputs the backward pass reads; each may be None."""
+    import torch
+
+    rows, cols = x.shape
+    n, nb = rows * cols, x.element_size() * rows * cols
+    _dev(x, "x", nb)
+    _same(residual, "residual", nb, x, x.dtype)
+    _same(h, "h", nb, x, x.dtype)
+    _dev(weight, "weight", cols * weight.element_size(), like=x)
+    _fp8_out(y, y_scales, scale_block, rows, cols, x)
+    _same(rstd, "rstd", 4 * rows, x, torch.float32, align=4)
+    _dev(ckpt, "ckpt", n, like=x)
+    _same(ckpt_scales, "ckpt_scales", 4 * rows * -(-cols // 128), x, torch.float32, align=4)
+    _check("rmsnorm_residual_fp8",
+           lib.rmsnorm_residual_fp8(_ptr(x), _ptr(residual), _dtype_code(x), rows, cols, _ptr(weight),
+                                    _dtype_code(weight), float(eps), _ptr(h), _ptr(y), fp8_dtype, scale_block,
+                                    _ptr(y_scales), _ptr(rstd), _ptr(ckpt), _ptr(ckpt_scales), _stream(stream)))
+
+
+def rmsnorm_workspace_size(rows: int, cols: int) -> int:
+    return int(lib.rmsnorm_workspace_size(rows, cols))
+
+
+def new_rmsnorm_workspace(rows: int, cols: int, device="cuda"):
+    """Scratch of rmsnorm_residual_backward for that many rows or fewer."""
+    import torch
+
+    return torch.empty(rmsnorm_workspace_size(rows, cols), dtype=torch.uint8, device=device)
+
+
+def rmsnorm_residual_backward(dy, weight, rstd, dx, dweight, workspace, *, h=None, ckpt=None, ckpt_scales=None,
+                              dh=None, stream=None) -> None:
+    """dx (as dy) and dweight ([cols], any of the three float types) from dy, rstd and the stream: either h
+    or its 8-bit checkpoint (ckpt, ckpt_scales).  dh: the gradient reaching the stream from above, or None."""
+    import torch
+
+    rows, cols = dy.shape
+    nb = dy.element_size() * rows * cols
+    _dev(dy, "dy", nb)
+    _same(dh, "dh", nb, dy, dy.dtype)
+    _same(h, "h", nb, dy, dy.dtype)
+    _dev(ckpt, "ckpt", rows * cols, like=dy)
+    _same(ckpt_scales, "ckpt_scales", 4 * rows * -(-cols // 128), dy, torch.float32, align=4)
+    _dev(weight, "weight", cols * weight.element_size(), like=dy)
+    _same(rstd, "rstd", 4 * rows, dy, torch.float32, align=4)
+    _same(dx, "dx", nb, dy, dy.dtype)
+    _dev(dweight, "dweight", cols * dweight.element_size(), like=dy)
+    _dev(workspace, "workspace", like=dy)
+    wp, wb = _ws(workspace)
+    _check("rmsnorm_residual_backward",
+           lib.rmsnorm_residual_backward(_ptr(dy), _ptr(dh), _dtype_code(dy), rows, cols, _ptr(h), _ptr(ckpt),
+                                         _ptr(ckpt_scales), _ptr(weight), _dtype_code(weight), _ptr(rstd), _ptr(dx),
+                                         _ptr(dweight), _dtype_code(dweight), wp, wb, _stream(stream)))
+
+
+def swiglu_fp8(gate, up, y, y_scales, *, ckpt=None, ckpt_scales=None, fp8_dtype: int = MP_E4M3,
+               scale_block: int = 128, stream=None) -> None:
+    """y = FP8 of silu(gate) * up.  gate, up: [rows, cols], each may be a column range of one wider
+    matrix; ckpt: 2*rows*cols bytes (gate's codes, then up's), ckpt_scales: float32 [2, rows, ceil(cols/128)]."""
+    import torch
+
+    rows, cols = gate.shape
+    ld = _row_pitch(gate, "gate", gate, rows, cols)
+    if _row_pitch(up, "up", gate, rows, cols) != ld:
+        raise ValueError("up: the rows of gate and up must be the same distance apart")
+    _fp8_out(y, y_scales, scale_block, rows, cols, gate)
+    _dev(ckpt, "ckpt", 2 * rows * cols, like=gate)
+    _same(ckpt_scales, "ckpt_scales", 8 * rows * -(-cols // 128), gate, torch.float32, align=4)
+    _check("swiglu_fp8",
+           lib.swiglu_fp8(_ptr(gate), _ptr(up), ld, _dtype_code(gate), rows, cols, _ptr(y), fp8_dtype, scale_block,
+                          _ptr(y_scales), _ptr(ckpt), _ptr(ckpt_scales), _stream(stream)))
+
+
+def swiglu_backward(dp, dgate, dup, *, gate=None, up=None, ckpt=None, ckpt_scales=None, stream=None) -> None:
+    """dgate, dup from dp and either gate and up or their 8-bit checkpoint of swiglu_fp8.  dgate and dup
+    ([rows, cols]) may be column ranges of one wider matrix, as gate and up may."""
+    import torch
+
+    rows, cols = dp.shape
+    _dev(dp, "dp", dp.element_size() * rows * cols)
+    ld = cols
+    if gate is not None and up is not None:
+        ld = _row_pitch(gate, "gate", dp, rows, cols)
+        if _row_pitch(up, "up", dp, rows, cols) != ld:
+            raise ValueError("up: the rows of gate and up must be the same distance apart")
+    d_ld = _row_pitch(dgate, "dgate", dp, rows, cols)
+    if _row_pitch(dup, "dup", dp, rows, cols) != d_ld:
+        raise ValueError("dup: the rows of dgate and dup must be the same distance apart")
+    _dev(ckpt, "ckpt", 2 * rows * cols, like=dp)
+    _same(ckpt_scales, "ckpt_scales", 8 * rows * -(-cols // 128), dp, torch.float32, align=4)
+    _check("swiglu_backward",
+           lib.swiglu_backward(_ptr(dp), _dtype_code(dp), rows, cols, _ptr(gate), _ptr(up), ld, _ptr(ckpt),
+                               _ptr(ckpt_scales), _ptr(dgate), _ptr(dup), d_ld, _stream(stream)))
+
+
 __all__ = [
+    "rmsnorm_residual_fp8", "rmsnorm_residual_backward", "rmsnorm_workspace_size", "new_rmsnorm_workspace",
+    "swiglu_fp8", "swiglu_backward",
     "AdamwHparams", "Fp8Meta", "MpError", "MpParam", "Param", "ScalerCfg", "ScalerState",
     "MP_F32", "MP_F16", "MP_BF16", "MP_E4M3", "MP_E5M2", "MP_E2M1", "MP_E2M3", "MP_E3M2", "mx_quantize",
     "mp_adamw_step", "mp_adamw_check", "mp_adamw_apply", "mp_adamw_workspace_size", "loss_scale_update",

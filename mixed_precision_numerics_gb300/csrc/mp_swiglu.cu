@@ -1,0 +1,218 @@
+// mp_swiglu.cu — the gated product of a feed-forward block with an FP8 output,
+// and its backward pass from gate and up or from their 8-bit checkpoint.
+//
+// Forward: p = (g * s(g)) * u with s the logistic function; y = p in FP8 with
+// one scale per 1x128 tile (FP32) or 1x32 block (UE8M0); optionally g and u in
+// E4M3 with 1x128 scales, the checkpoint.
+// Backward, with g and u as given or the checkpoint's values:
+//   du = dp * (g * s(g)),  dg = dp * u * (s(g) * (1 + g * (1 - s(g)))).
+//
+// One thread owns 16 elements end to end; every element is read and written
+// once.  gate and up (dgate and dup) may be column ranges of one wider matrix:
+// each pair has a row pitch.
+#include "mp_chain.cuh"
+#include "mp_internal.h"
+#include "mp_tile8.cuh"
+
+namespace mp {
+namespace {
+
+constexpr int kThreads = 256;
+
+// 1 / (1 + exp(-g)): within a few ulp of binary32; 0 where exp(-g) overflows
+// (g below -88, where the exact value is below 2^-126 too), NaN for NaN.
+__device__ __forceinline__ float logistic(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+
+// Thread q holds lane q % 8 of tile q / 8; tiles run along rows.
+struct Place {
+  int64_t row;
+  int u;      // unit within the row
+  bool in;    // within the tensor
+};
+__device__ __forceinline__ Place place_of(int64_t rows, int cols, int tiles) {
+  const int64_t q = (int64_t)blockIdx.x * kThreads + threadIdx.x, tile = q / kTileLanes;
+  Place p;
+  p.row = tile / tiles;
+  p.u = (int)(tile - p.row * tiles) * kTileLanes + (int)(q % kTileLanes);
+  p.in = p.row < rows && p.u * kUnit < cols;
+  return p;
+}
+
+struct SwigluFwd {
+  const void *gate, *up;
+  int64_t pitch;  // bytes between rows of gate, and of up
+  Fp8Out y, gate_ckpt, up_ckpt;
+  int64_t rows;
+  int32_t cols, tiles;
+};
+
+template <int XT>
+__global__ __launch_bounds__(kThreads) void k_swiglu_fwd(const __grid_constant__ SwigluFwd a) {
+  chain_wait();
+  chain_release();
+  const Place p = place_of(a.rows, a.cols, a.tiles);
+  Unit<XT> gr, ur;
+  gr.zero();
+  ur.zero();
+  if (p.in) {
+    gr.load(static_cast<const char*>(a.gate) + p.row * a.pitch, p.u);
+    ur.load(static_cast<const char*>(a.up) + p.row * a.pitch, p.u);
+  }
+  float g[kUnit], u[kUnit];
+  gr.floats(g);
+  ur.floats(u);
+  if (a.gate_ckpt.codes) {
+    cast_store(g, a.gate_ckpt, p.row, a.cols, p.u, p.in, [&](int i) { return gr.sign80(i); });
+    cast_store(u, a.up_ckpt, p.row, a.cols, p.u, p.in, [&](int i) { return ur.sign80(i); });
+  }
+#pragma unroll
+  for (int i = 0; i < kUnit; ++i) g[i] = __fmul_rn(__fmul_rn(g[i], logistic(g[i])), u[i]);
+  cast_store(g, a.y, p.row, a.cols, p.u, p.in);
+}
+
+struct SwigluBwd {
+  const void *dp, *gate, *up;
+  const uint8_t* codes;  // the 8-bit checkpoint [2][rows][cols], or NULL where gate and up are given
+  const float* scales;   // [2][rows][tiles]
+  void *dgate, *dup;
+  int64_t pitch, dpitch, rows;  // bytes between rows of gate and up, of dgate and dup
+  int32_t cols, tiles;
+};
+
+template <int XT, bool SAVED>
+__global__ __launch_bounds__(kThreads) void k_swiglu_bwd(const __grid_constant__ SwigluBwd a) {
+  chain_wait();
+  chain_release();
+  const Place p = place_of(a.rows, a.cols, a.tiles);
+  if (!p.in) return;
+  Unit<XT> dr;
+  float g[kUnit], u[kUnit];
+  if constexpr (SAVED) {
+    const int64_t at = p.row * a.cols + p.u * kUnit, st = p.row * a.tiles + p.u / kTileLanes;
+    const uint4 gc = ld_cs(a.codes + at), uc = ld_cs(a.codes + a.rows * a.cols + at);
+    const float gs = __ldcs(a.scales + st), us = __ldcs(a.scales + a.rows * a.tiles + st);
+    dr.load(static_cast<const char*>(a.dp) + p.row * a.cols * (XT == XF32 ? 4 : 2), p.u);
+    e4m3_floats(gc, gs, g);
+    e4m3_floats(uc, us, u);
+  } else {
+    Unit<XT> gr, ur;
+    gr.load(static_cast<const char*>(a.gate) + p.row * a.pitch, p.u);
+    ur.load(static_cast<const char*>(a.up) + p.row * a.pitch, p.u);
+    dr.load(static_cast<const char*>(a.dp) + p.row * a.cols * (XT == XF32 ? 4 : 2), p.u);
+    gr.floats(g);
+    ur.floats(u);
+  }
+  Unit<XT> dg, du;
+#pragma unroll
+  for (int k = 0; k < kUnit / 2; ++k) {
+    const float2 d = dr.pair(k);
+    float og[2], ou[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float x = g[2 * k + j], dd = j ? d.y : d.x, s = logistic(x), xs = x * s;
+      ou[j] = dd * xs;
+      og[j] = dd * u[2 * k + j] * (s + xs * (1.0f - s));
+    }
+    dg.set_pair(k, og[0], og[1]);
+    du.set_pair(k, ou[0], ou[1]);
+  }
+  dg.store(static_cast<char*>(a.dgate) + p.row * a.dpitch, p.u);
+  du.store(static_cast<char*>(a.dup) + p.row * a.dpitch, p.u);
+}
+
+int64_t ctas_of(int64_t rows, int32_t tiles) { return (rows * tiles * kTileLanes + kThreads - 1) / kThreads; }
+
+template <int XT>
+mp_status launch_fwd(const SwigluFwd& a, cudaStream_t st) {
+  launch_chained(k_swiglu_fwd<XT>, dim3((unsigned)ctas_of(a.rows, a.tiles)), dim3(kThreads), 0, st, a);
+  note_launches(1);
+  return launch_status();
+}
+template <int XT>
+mp_status launch_bwd(const SwigluBwd& a, cudaStream_t st) {
+  const dim3 g((unsigned)ctas_of(a.rows, a.tiles)), b(kThreads);
+  if (a.codes)
+    launch_chained(k_swiglu_bwd<XT, true>, g, b, 0, st, a);
+  else
+    launch_chained(k_swiglu_bwd<XT, false>, g, b, 0, st, a);
+  note_launches(1);
+  return launch_status();
+}
+
+bool float_type(mp_dtype t) { return t == MP_F32 || t == MP_F16 || t == MP_BF16; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Row pitch in bytes of a matrix of `cols` columns whose rows start `ld`
+// elements apart; -1 if rows would overlap or not start on 16 bytes.
+int64_t pitch_of(int64_t ld, int64_t cols, int64_t rows, mp_dtype t) {
+  const int64_t es = t == MP_F32 ? 4 : 2;
+  if (rows > 1 && (ld < cols || ld >= (1ll << 31) || (ld * es) % 16 != 0)) return -1;
+  return rows > 1 ? ld * es : 0;
+}
+bool shape_ok(int64_t rows, int64_t cols, int step) {
+  if (rows >= (1ll << 31) || cols >= (1ll << 31) || cols % step != 0) return false;
+  return rows * ((cols + kTile - 1) / kTile) < (1ll << 31) * (kThreads / kTileLanes);  // grid of one dimension
+}
+
+}  // namespace
+}  // namespace mp
+
+extern "C" MP_API mp_status swiglu_fp8(const void* gate, const void* up, int64_t ld, mp_dtype x_dtype, int64_t rows,
+                                       int64_t cols, void* y, mp_dtype fp8_dtype, int32_t scale_block, void* y_scales,
+                                       void* ckpt, float* ckpt_scales, void* stream) {
+  using namespace mp;
+  if (rows < 0 || cols < 0) return MP_EINVAL;
+  if (!float_type(x_dtype)) return MP_EINVAL;
+  if (fp8_dtype != MP_E4M3 && fp8_dtype != MP_E5M2) return MP_EINVAL;
+  if (scale_block != 128 && scale_block != 32) return MP_EINVAL;
+  if (!shape_ok(rows, cols, scale_block == 32 ? 32 : 16)) return MP_ESHAPE;
+  if (rows == 0 || cols == 0) return MP_OK;
+  if (!gate || !up || !y || !y_scales || (!ckpt != !ckpt_scales)) return MP_EINVAL;
+  const int64_t pitch = pitch_of(ld, cols, rows, x_dtype);
+  if (pitch < 0) return MP_ESHAPE;
+  if (!aligned16(gate) || !aligned16(up) || !aligned16(y) || !aligned16(ckpt) || !aligned4(ckpt_scales) ||
+      (scale_block == 128 && !aligned4(y_scales)))
+    return MP_EALIGN;
+  SwigluFwd a;
+  a.gate = gate, a.up = up, a.pitch = pitch, a.rows = rows, a.cols = (int32_t)cols;
+  a.tiles = (int32_t)((cols + kTile - 1) / kTile);
+  a.y = Fp8Out{static_cast<uint8_t*>(y), y_scales, scale_block == 32 ? (int32_t)(cols / 32) : a.tiles,
+               fp8_dtype == MP_E5M2, scale_block == 32};
+  uint8_t* cb = static_cast<uint8_t*>(ckpt);
+  a.gate_ckpt = Fp8Out{cb, ckpt_scales, a.tiles, false, false};
+  a.up_ckpt = Fp8Out{cb ? cb + rows * cols : nullptr, ckpt_scales ? ckpt_scales + rows * a.tiles : nullptr, a.tiles,
+                     false, false};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  switch (x_dtype) {
+    case MP_F32: return launch_fwd<XF32>(a, st);
+    case MP_F16: return launch_fwd<XF16>(a, st);
+    default: return launch_fwd<XBF16>(a, st);
+  }
+}
+
+extern "C" MP_API mp_status swiglu_backward(const void* dp, mp_dtype x_dtype, int64_t rows, int64_t cols,
+                                            const void* gate, const void* up, int64_t ld, const void* ckpt,
+                                            const float* ckpt_scales, void* dgate, void* dup, int64_t d_ld,
+                                            void* stream) {
+  using namespace mp;
+  if (rows < 0 || cols < 0) return MP_EINVAL;
+  if (!float_type(x_dtype)) return MP_EINVAL;
+  if (!shape_ok(rows, cols, 16)) return MP_ESHAPE;
+  if (rows == 0 || cols == 0) return MP_OK;
+  if (!dp || !dgate || !dup || (!ckpt != !ckpt_scales) || (!gate != !up) || (!gate == !ckpt)) return MP_EINVAL;
+  const int64_t pitch = gate ? pitch_of(ld, cols, rows, x_dtype) : 0, dpitch = pitch_of(d_ld, cols, rows, x_dtype);
+  if (pitch < 0 || dpitch < 0) return MP_ESHAPE;
+  if (!aligned16(dp) || !aligned16(gate) || !aligned16(up) || !aligned16(ckpt) || !aligned4(ckpt_scales) ||
+      !aligned16(dgate) || !aligned16(dup))
+    return MP_EALIGN;
+  SwigluBwd a;
+  a.dp = dp, a.gate = gate, a.up = up, a.codes = static_cast<const uint8_t*>(ckpt), a.scales = ckpt_scales;
+  a.dgate = dgate, a.dup = dup, a.pitch = pitch, a.dpitch = dpitch, a.rows = rows, a.cols = (int32_t)cols;
+  a.tiles = (int32_t)((cols + kTile - 1) / kTile);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  switch (x_dtype) {
+    case MP_F32: return launch_bwd<XF32>(a, st);
+    case MP_F16: return launch_bwd<XF16>(a, st);
+    default: return launch_bwd<XBF16>(a, st);
+  }
+}
