@@ -78,54 +78,50 @@ __global__ __launch_bounds__(L ? kCta : kMaxThreads) void k_norm_fwd(const __gri
   constexpr int R = L ? kCta / L : 1;
   const int t = L ? threadIdx.x % (L ? L : 1) : threadIdx.x, sub = L ? threadIdx.x / (L ? L : 1) : 0;
   const int stride = L ? L : blockDim.x, units = a.cols / kUnit;
-  const int64_t pitch = (int64_t)a.cols * (XT == XF32 ? 4 : 2);
   int parity = 0;
   for (int64_t row0 = (int64_t)blockIdx.x * R; row0 < a.rows; row0 += (int64_t)gridDim.x * R, parity ^= 1) {
     const int64_t row = row0 + sub;
+    Place p[U];
     Unit<XT> h[U];
-    float ss = 0.0f;
+    float2 ss = both(0.0f);
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      const int u = t + k * stride;
-      const bool in = u < units && row < a.rows;
+      p[k].row = (int32_t)row;
+      p[k].u = t + k * stride;
+      p[k].at = row * a.cols + p[k].u * kUnit;
+      p[k].in = row < a.rows && p[k].u < units;
+      p[k].tile_in = row < a.rows && (p[k].u & ~7) < units;
       h[k].zero();
-      if (in) {
-        h[k].load(static_cast<const char*>(a.x) + row * pitch, u);
+      if (p[k].in) {
+        h[k].load(a.x, p[k].at);
         if (a.residual) {
           Unit<XT> r;
-          r.load(static_cast<const char*>(a.residual) + row * pitch, u);
-#pragma unroll
-          for (int j = 0; j < kUnit / 2; ++j) {
-            const float2 p = h[k].pair(j), q = r.pair(j);
-            h[k].set_pair(j, __fadd_rn(p.x, q.x), __fadd_rn(p.y, q.y));
-          }
+          r.load(a.residual, p[k].at);
+          h[k].add(r);
         }
-        if (a.h) h[k].store(static_cast<char*>(a.h) + row * pitch, u);
+        if (a.h) h[k].store(a.h, p[k].at);
       }
-      float f[kUnit];
+      float2 f[kPairs];
       h[k].floats(f);
-      if (a.ckpt.codes) cast_store(f, a.ckpt, row, a.cols, u, in, [&](int i) { return h[k].sign80(i); });
+      if (a.ckpt.codes) cast_store(f, a.ckpt, p[k], [&](int i) { return h[k].sign80(i); });
 #pragma unroll
-      for (int i = 0; i < kUnit; ++i) ss = fmaf(f[i], f[i], ss);
+      for (int i = 0; i < kPairs; ++i) ss = fma2(f[i], f[i], ss);
     }
-    const float sum = row_sum<L>(ss, slots[parity]);
+    const float sum = row_sum<L>(ss.x + ss.y, slots[parity]);
     const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, (float)a.cols), a.eps)));
     if (t == 0 && row < a.rows && a.rstd) a.rstd[row] = rstd;
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      const int u = t + k * stride;
-      const bool in = u < units && row < a.rows;
-      float f[kUnit], w[kUnit];
-      h[k].floats(f);
-      if (in) {
-        load_weights(a.weight, a.wt, u, w);
+      float2 f[kPairs], w[kPairs];
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i) f[i] = __fmul_rn(__fmul_rn(f[i], rstd), w[i]);
-      } else {
+      for (int i = 0; i < kPairs; ++i) f[i] = w[i] = both(0.0f);
+      if (p[k].in) {
+        h[k].floats(f);
+        load_weights(a.weight, a.wt, p[k].u, w);
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i) f[i] = 0.0f;
+        for (int i = 0; i < kPairs; ++i) f[i] = mul2(mul2(f[i], both(rstd)), w[i]);
       }
-      cast_store(f, a.y, row, a.cols, u, in);
+      cast_store(f, a.y, p[k]);
     }
   }
 }
@@ -174,12 +170,11 @@ __global__ __launch_bounds__(L ? kCta : kMaxThreads) void k_norm_bwd(const __gri
   constexpr int R = L ? kCta / L : 1;
   const int t = L ? threadIdx.x % (L ? L : 1) : threadIdx.x, sub = L ? threadIdx.x / (L ? L : 1) : 0;
   const int stride = L ? L : blockDim.x, units = a.cols / kUnit;
-  const int64_t pitch = (int64_t)a.cols * (XT == XF32 ? 4 : 2);
-  float acc[U][kUnit];
+  float2 acc[U][kPairs];
 #pragma unroll
   for (int k = 0; k < U; ++k)
 #pragma unroll
-    for (int i = 0; i < kUnit; ++i) acc[k][i] = 0.0f;
+    for (int i = 0; i < kPairs; ++i) acc[k][i] = both(0.0f);
   int parity = 0;
   for (int64_t row0 = (int64_t)blockIdx.x * R; row0 < a.rows; row0 += (int64_t)gridDim.x * R, parity ^= 1) {
     const int64_t row = row0 + sub;
@@ -187,68 +182,62 @@ __global__ __launch_bounds__(L ? kCta : kMaxThreads) void k_norm_bwd(const __gri
     const float rstd = live ? a.rstd[row] : 0.0f;
     Unit<XT> dy[U], v[U];
     uint4 code[U];
-    float scale[U], dot = 0.0f;
+    float scale[U];
+    float2 dot = both(0.0f);
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const int u = t + k * stride;
+      const int64_t at = row * a.cols + u * kUnit;
       dy[k].zero();
       v[k].zero();
       code[k] = make_uint4(0u, 0u, 0u, 0u);
       scale[k] = 0.0f;
       if (live && u < units) {
-        dy[k].load(static_cast<const char*>(a.dy) + row * pitch, u);
+        dy[k].load(a.dy, at);
         if constexpr (SAVED) {
-          code[k] = ld_cs(a.codes + row * a.cols + u * kUnit);
+          code[k] = ld_cs(a.codes + at);
           scale[k] = a.scales[row * a.tiles + u / kTileLanes];
         } else {
-          v[k].load(static_cast<const char*>(a.h) + row * pitch, u);
+          v[k].load(a.h, at);
         }
       }
     }
+    float2 g[U][kPairs], xh[U][kPairs];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const int u = t + k * stride;
       if (live && u < units) {
-        float d[kUnit], x[kUnit], w[kUnit];
-        dy[k].floats(d);
-        if constexpr (SAVED)
-          e4m3_floats(code[k], scale[k], x);
-        else
-          v[k].floats(x);
+        float2 w[kPairs];
         load_weights(a.weight, a.wt, u, w);
+        if constexpr (SAVED) {
+          e4m3_floats(code[k], scale[k] * rstd, xh[k]);
+        } else {
+          v[k].floats(xh[k]);
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i) {
-          const float xh = x[i] * rstd;
-          acc[k][i] = fmaf(d[i], xh, acc[k][i]);
-          dot = fmaf(d[i] * w[i], xh, dot);
+          for (int i = 0; i < kPairs; ++i) xh[k][i] = mul2(xh[k][i], both(rstd));
+        }
+        dy[k].floats(g[k]);
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          acc[k][i] = fma2(g[k][i], xh[k][i], acc[k][i]);
+          g[k][i] = mul2(g[k][i], w[i]);
+          dot = fma2(g[k][i], xh[k][i], dot);
         }
       }
     }
-    const float c = __fdiv_rn(row_sum<L>(dot, slots[parity]), (float)a.cols);
+    const float c = __fdiv_rn(row_sum<L>(dot.x + dot.y, slots[parity]), (float)a.cols);
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const int u = t + k * stride;
       if (live && u < units) {
-        float d[kUnit], x[kUnit], w[kUnit];
-        dy[k].floats(d);
-        if constexpr (SAVED)
-          e4m3_floats(code[k], scale[k], x);
-        else
-          v[k].floats(x);
-        load_weights(a.weight, a.wt, u, w);
+        const int64_t at = row * a.cols + u * kUnit;
+        Unit<XT> e, o;
+        e.zero();
+        if (a.dh) e.load(a.dh, at);
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i) d[i] = rstd * (d[i] * w[i] - (x[i] * rstd) * c);
-        if (a.dh) {
-          Unit<XT> e;
-          e.load(static_cast<const char*>(a.dh) + row * pitch, u);
-          float f[kUnit];
-          e.floats(f);
-#pragma unroll
-          for (int i = 0; i < kUnit; ++i) d[i] += f[i];
-        }
-        Unit<XT> o;
-        o.set(d);
-        o.store(static_cast<char*>(a.dx) + row * pitch, u);
+        for (int i = 0; i < kPairs; ++i)
+          o.set_pair(i, fma2(fma2(xh[k][i], both(-c), g[k][i]), both(rstd), e.pair(i)));
+        o.store(a.dx, at);
       }
     }
   }
@@ -261,12 +250,15 @@ __global__ __launch_bounds__(L ? kCta : kMaxThreads) void k_norm_bwd(const __gri
         float4* p = reinterpret_cast<float4*>(part + u * kUnit);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          p[i] = make_float4(acc[k][4 * i], acc[k][4 * i + 1], acc[k][4 * i + 2], acc[k][4 * i + 3]);
+          p[i] = make_float4(acc[k][2 * i].x, acc[k][2 * i].y, acc[k][2 * i + 1].x, acc[k][2 * i + 1].y);
       }
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kUnit; ++i) fold[threadIdx.x * kUnit + i] = acc[0][i];  // [sub][t][i]
+    for (int i = 0; i < kPairs; ++i) {  // [sub][t][element]
+      fold[threadIdx.x * kUnit + 2 * i] = acc[0][i].x;
+      fold[threadIdx.x * kUnit + 2 * i + 1] = acc[0][i].y;
+    }
     __syncthreads();
     for (int col = threadIdx.x; col < a.cols; col += kCta) {
       float s = 0.0f;

@@ -19,31 +19,39 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// 1 / (1 + exp(-g)): within a few ulp of binary32; 0 where exp(-g) overflows
-// (g below -88, where the exact value is below 2^-126 too), NaN for NaN.
-__device__ __forceinline__ float logistic(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// 1 / (1 + exp(-g)) through the hardware's base-2 exponential and reciprocal:
+// within (|g| + 8) * 2^-24, relative; 0 where exp(-g) overflows (g below -88,
+// where the exact value is below 2^-126 too), NaN for NaN.
+__device__ __forceinline__ float2 logistic2(float2 g) {
+  const float2 t = mul2(g, both(-1.442695041f));
+  float2 e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  e = add2(e, both(1.0f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+  return r;
+}
 
 // Thread q holds lane q % 8 of tile q / 8; tiles run along rows.
-struct Place {
-  int64_t row;
-  int u;      // unit within the row
-  bool in;    // within the tensor
-};
-__device__ __forceinline__ Place place_of(int64_t rows, int cols, int tiles) {
-  const int64_t q = (int64_t)blockIdx.x * kThreads + threadIdx.x, tile = q / kTileLanes;
+__device__ __forceinline__ Place place_of(int64_t rows, int cols, const FastDiv& tiles) {
+  const uint32_t tile = blockIdx.x * (kThreads / kTileLanes) + threadIdx.x / kTileLanes;  // below 2^31
   Place p;
-  p.row = tile / tiles;
-  p.u = (int)(tile - p.row * tiles) * kTileLanes + (int)(q % kTileLanes);
-  p.in = p.row < rows && p.u * kUnit < cols;
+  p.row = (int32_t)div_by(tile, tiles);
+  p.u = (int32_t)((tile - p.row * tiles.d) * kTileLanes + threadIdx.x % kTileLanes);
+  p.tile_in = p.row < rows;
+  p.in = p.tile_in && p.u * kUnit < cols;
+  p.at = (int64_t)p.row * cols + p.u * kUnit;
   return p;
 }
 
 struct SwigluFwd {
   const void *gate, *up;
-  int64_t pitch;  // bytes between rows of gate, and of up
+  int64_t ld;  // elements between rows of gate, and of up
   Fp8Out y, gate_ckpt, up_ckpt;
   int64_t rows;
-  int32_t cols, tiles;
+  int32_t cols;
+  FastDiv tiles;
 };
 
 template <int XT>
@@ -55,19 +63,20 @@ __global__ __launch_bounds__(kThreads) void k_swiglu_fwd(const __grid_constant__
   gr.zero();
   ur.zero();
   if (p.in) {
-    gr.load(static_cast<const char*>(a.gate) + p.row * a.pitch, p.u);
-    ur.load(static_cast<const char*>(a.up) + p.row * a.pitch, p.u);
+    const int64_t at = p.row * a.ld + p.u * kUnit;
+    gr.load(a.gate, at);
+    ur.load(a.up, at);
   }
-  float g[kUnit], u[kUnit];
+  float2 g[kPairs], u[kPairs];
   gr.floats(g);
   ur.floats(u);
   if (a.gate_ckpt.codes) {
-    cast_store(g, a.gate_ckpt, p.row, a.cols, p.u, p.in, [&](int i) { return gr.sign80(i); });
-    cast_store(u, a.up_ckpt, p.row, a.cols, p.u, p.in, [&](int i) { return ur.sign80(i); });
+    cast_store(g, a.gate_ckpt, p, [&](int i) { return gr.sign80(i); });
+    cast_store(u, a.up_ckpt, p, [&](int i) { return ur.sign80(i); });
   }
 #pragma unroll
-  for (int i = 0; i < kUnit; ++i) g[i] = __fmul_rn(__fmul_rn(g[i], logistic(g[i])), u[i]);
-  cast_store(g, a.y, p.row, a.cols, p.u, p.in);
+  for (int k = 0; k < kPairs; ++k) g[k] = mul2(mul2(g[k], logistic2(g[k])), u[k]);
+  cast_store(g, a.y, p);
 }
 
 struct SwigluBwd {
@@ -75,8 +84,9 @@ struct SwigluBwd {
   const uint8_t* codes;  // the 8-bit checkpoint [2][rows][cols], or NULL where gate and up are given
   const float* scales;   // [2][rows][tiles]
   void *dgate, *dup;
-  int64_t pitch, dpitch, rows;  // bytes between rows of gate and up, of dgate and dup
-  int32_t cols, tiles;
+  int64_t ld, d_ld, rows;  // elements between rows of gate and up, of dgate and dup
+  int32_t cols;
+  FastDiv tiles;
 };
 
 template <int XT, bool SAVED>
@@ -86,45 +96,43 @@ __global__ __launch_bounds__(kThreads) void k_swiglu_bwd(const __grid_constant__
   const Place p = place_of(a.rows, a.cols, a.tiles);
   if (!p.in) return;
   Unit<XT> dr;
-  float g[kUnit], u[kUnit];
+  float2 g[kPairs], u[kPairs];
   if constexpr (SAVED) {
-    const int64_t at = p.row * a.cols + p.u * kUnit, st = p.row * a.tiles + p.u / kTileLanes;
-    const uint4 gc = ld_cs(a.codes + at), uc = ld_cs(a.codes + a.rows * a.cols + at);
-    const float gs = __ldcs(a.scales + st), us = __ldcs(a.scales + a.rows * a.tiles + st);
-    dr.load(static_cast<const char*>(a.dp) + p.row * a.cols * (XT == XF32 ? 4 : 2), p.u);
+    const int64_t st = (int64_t)p.row * a.tiles.d + p.u / kTileLanes;
+    const uint4 gc = ld_cs(a.codes + p.at), uc = ld_cs(a.codes + a.rows * a.cols + p.at);
+    const float gs = __ldcs(a.scales + st), us = __ldcs(a.scales + a.rows * a.tiles.d + st);
+    dr.load(a.dp, p.at);
     e4m3_floats(gc, gs, g);
     e4m3_floats(uc, us, u);
   } else {
     Unit<XT> gr, ur;
-    gr.load(static_cast<const char*>(a.gate) + p.row * a.pitch, p.u);
-    ur.load(static_cast<const char*>(a.up) + p.row * a.pitch, p.u);
-    dr.load(static_cast<const char*>(a.dp) + p.row * a.cols * (XT == XF32 ? 4 : 2), p.u);
+    const int64_t at = p.row * a.ld + p.u * kUnit;
+    gr.load(a.gate, at);
+    ur.load(a.up, at);
+    dr.load(a.dp, p.at);
     gr.floats(g);
     ur.floats(u);
   }
   Unit<XT> dg, du;
 #pragma unroll
-  for (int k = 0; k < kUnit / 2; ++k) {
-    const float2 d = dr.pair(k);
-    float og[2], ou[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float x = g[2 * k + j], dd = j ? d.y : d.x, s = logistic(x), xs = x * s;
-      ou[j] = dd * xs;
-      og[j] = dd * u[2 * k + j] * (s + xs * (1.0f - s));
-    }
-    dg.set_pair(k, og[0], og[1]);
-    du.set_pair(k, ou[0], ou[1]);
+  for (int k = 0; k < kPairs; ++k) {
+    const float2 d = dr.pair(k), s = logistic2(g[k]), xs = mul2(g[k], s);
+    du.set_pair(k, mul2(d, xs));
+    const float2 one_s = fma2(s, both(-1.0f), both(1.0f));
+    dg.set_pair(k, mul2(mul2(d, u[k]), fma2(xs, one_s, s)));
   }
-  dg.store(static_cast<char*>(a.dgate) + p.row * a.dpitch, p.u);
-  du.store(static_cast<char*>(a.dup) + p.row * a.dpitch, p.u);
+  const int64_t at = p.row * a.d_ld + p.u * kUnit;
+  dg.store(a.dgate, at);
+  du.store(a.dup, at);
 }
 
-int64_t ctas_of(int64_t rows, int32_t tiles) { return (rows * tiles * kTileLanes + kThreads - 1) / kThreads; }
+unsigned ctas_of(int64_t rows, const FastDiv& tiles) {
+  return (unsigned)((rows * tiles.d * kTileLanes + kThreads - 1) / kThreads);
+}
 
 template <int XT>
 mp_status launch_fwd(const SwigluFwd& a, cudaStream_t st) {
-  launch_chained(k_swiglu_fwd<XT>, dim3((unsigned)ctas_of(a.rows, a.tiles)), dim3(kThreads), 0, st, a);
+  launch_chained(k_swiglu_fwd<XT>, dim3(ctas_of(a.rows, a.tiles)), dim3(kThreads), 0, st, a);
   note_launches(1);
   return launch_status();
 }
@@ -142,16 +150,16 @@ mp_status launch_bwd(const SwigluBwd& a, cudaStream_t st) {
 bool float_type(mp_dtype t) { return t == MP_F32 || t == MP_F16 || t == MP_BF16; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// Row pitch in bytes of a matrix of `cols` columns whose rows start `ld`
-// elements apart; -1 if rows would overlap or not start on 16 bytes.
-int64_t pitch_of(int64_t ld, int64_t cols, int64_t rows, mp_dtype t) {
-  const int64_t es = t == MP_F32 ? 4 : 2;
-  if (rows > 1 && (ld < cols || ld >= (1ll << 31) || (ld * es) % 16 != 0)) return -1;
-  return rows > 1 ? ld * es : 0;
+// Whether a matrix of `cols` columns may have rows `ld` elements apart: they
+// must not overlap, and each has to start on 16 bytes.
+bool pitch_ok(int64_t ld, int64_t cols, int64_t rows, mp_dtype t) {
+  return rows <= 1 || (ld >= cols && ld < (1ll << 31) && ld % (t == MP_F32 ? 4 : 8) == 0);
 }
+// rows * tiles below 2^31 - 32, so that a tile's number is (2.7e11 elements:
+// more than the device's memory holds of any input)
 bool shape_ok(int64_t rows, int64_t cols, int step) {
   if (rows >= (1ll << 31) || cols >= (1ll << 31) || cols % step != 0) return false;
-  return rows * ((cols + kTile - 1) / kTile) < (1ll << 31) * (kThreads / kTileLanes);  // grid of one dimension
+  return rows * ((cols + kTile - 1) / kTile) < (1ll << 31) - kThreads / kTileLanes;
 }
 
 }  // namespace
@@ -168,20 +176,18 @@ extern "C" MP_API mp_status swiglu_fp8(const void* gate, const void* up, int64_t
   if (!shape_ok(rows, cols, scale_block == 32 ? 32 : 16)) return MP_ESHAPE;
   if (rows == 0 || cols == 0) return MP_OK;
   if (!gate || !up || !y || !y_scales || (!ckpt != !ckpt_scales)) return MP_EINVAL;
-  const int64_t pitch = pitch_of(ld, cols, rows, x_dtype);
-  if (pitch < 0) return MP_ESHAPE;
+  if (!pitch_ok(ld, cols, rows, x_dtype)) return MP_ESHAPE;
   if (!aligned16(gate) || !aligned16(up) || !aligned16(y) || !aligned16(ckpt) || !aligned4(ckpt_scales) ||
       (scale_block == 128 && !aligned4(y_scales)))
     return MP_EALIGN;
   SwigluFwd a;
-  a.gate = gate, a.up = up, a.pitch = pitch, a.rows = rows, a.cols = (int32_t)cols;
-  a.tiles = (int32_t)((cols + kTile - 1) / kTile);
-  a.y = Fp8Out{static_cast<uint8_t*>(y), y_scales, scale_block == 32 ? (int32_t)(cols / 32) : a.tiles,
+  const int32_t tiles = (int32_t)((cols + kTile - 1) / kTile);
+  a.gate = gate, a.up = up, a.ld = ld, a.rows = rows, a.cols = (int32_t)cols, a.tiles = fast_div(tiles);
+  a.y = Fp8Out{static_cast<uint8_t*>(y), y_scales, scale_block == 32 ? (int32_t)(cols / 32) : tiles,
                fp8_dtype == MP_E5M2, scale_block == 32};
   uint8_t* cb = static_cast<uint8_t*>(ckpt);
-  a.gate_ckpt = Fp8Out{cb, ckpt_scales, a.tiles, false, false};
-  a.up_ckpt = Fp8Out{cb ? cb + rows * cols : nullptr, ckpt_scales ? ckpt_scales + rows * a.tiles : nullptr, a.tiles,
-                     false, false};
+  a.gate_ckpt = Fp8Out{cb, ckpt_scales, tiles, false, false};
+  a.up_ckpt = Fp8Out{cb ? cb + rows * cols : nullptr, cb ? ckpt_scales + rows * tiles : nullptr, tiles, false, false};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (x_dtype) {
     case MP_F32: return launch_fwd<XF32>(a, st);
@@ -200,15 +206,14 @@ extern "C" MP_API mp_status swiglu_backward(const void* dp, mp_dtype x_dtype, in
   if (!shape_ok(rows, cols, 16)) return MP_ESHAPE;
   if (rows == 0 || cols == 0) return MP_OK;
   if (!dp || !dgate || !dup || (!ckpt != !ckpt_scales) || (!gate != !up) || (!gate == !ckpt)) return MP_EINVAL;
-  const int64_t pitch = gate ? pitch_of(ld, cols, rows, x_dtype) : 0, dpitch = pitch_of(d_ld, cols, rows, x_dtype);
-  if (pitch < 0 || dpitch < 0) return MP_ESHAPE;
+  if ((gate && !pitch_ok(ld, cols, rows, x_dtype)) || !pitch_ok(d_ld, cols, rows, x_dtype)) return MP_ESHAPE;
   if (!aligned16(dp) || !aligned16(gate) || !aligned16(up) || !aligned16(ckpt) || !aligned4(ckpt_scales) ||
       !aligned16(dgate) || !aligned16(dup))
     return MP_EALIGN;
   SwigluBwd a;
   a.dp = dp, a.gate = gate, a.up = up, a.codes = static_cast<const uint8_t*>(ckpt), a.scales = ckpt_scales;
-  a.dgate = dgate, a.dup = dup, a.pitch = pitch, a.dpitch = dpitch, a.rows = rows, a.cols = (int32_t)cols;
-  a.tiles = (int32_t)((cols + kTile - 1) / kTile);
+  a.dgate = dgate, a.dup = dup, a.ld = ld, a.d_ld = d_ld, a.rows = rows, a.cols = (int32_t)cols;
+  a.tiles = fast_div((uint32_t)((cols + kTile - 1) / kTile));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (x_dtype) {
     case MP_F32: return launch_bwd<XF32>(a, st);

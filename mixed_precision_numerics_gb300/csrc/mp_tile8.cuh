@@ -5,6 +5,12 @@
 // of 16-bit input in two 16-byte loads, and exactly one 16-byte store of FP8
 // codes.  A 1x128 tile is then eight lanes and a 1x32 block two, so a tile
 // maximum takes three shuffles (one for 1x32) and no shared memory.
+//
+// The forward kernels issue nearly as many instructions as the SMs can while
+// DRAM is busy, so the arithmetic is kept short: element pairs go through the
+// packed binary32 instructions (each half rounded as the scalar one would),
+// the stream's sum through the packed 16-bit addition, and a tile's two
+// divisions are one, shared between neighbouring lanes.
 #pragma once
 
 #include "mp_device.cuh"
@@ -14,10 +20,65 @@ namespace mp {
 enum { XF32 = 0, XF16 = 1, XBF16 = 2 };  // the values of mp_dtype
 
 constexpr int kUnit = 16;               // elements per unit
+constexpr int kPairs = kUnit / 2;
 constexpr int kTile = 128;              // elements per FP32 scale
 constexpr int kTileLanes = kTile / kUnit;
 
+// ---------------------------------------------------------------------------
+// Packed binary32 pairs.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint64_t pack64(float2 a) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack64(uint64_t a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack64(a)), "l"(pack64(b)));
+  return unpack64(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack64(a)), "l"(pack64(b)));
+  return unpack64(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pack64(a)), "l"(pack64(b)), "l"(pack64(c)));
+  return unpack64(r);
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
+// NaN-propagating max(|a|, |b|, |c|).
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// 32-bit division by a launch constant: n / d = umulhi(n, mul) >> shift for
+// n < 2^31 (round-up reciprocal, Granlund and Montgomery, PLDI'94).
+struct FastDiv {
+  uint32_t d, mul, shift;
+};
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f{d, 0u, 0u};
+  while ((1ull << f.shift) < d) ++f.shift;  // 2^shift >= d
+  f.mul = (uint32_t)(((1ull << (31 + f.shift)) + d - 1) / d);  // below 2^32, as 2^shift < 2d
+  return f;
+}
+__device__ __forceinline__ uint32_t div_by(uint32_t n, const FastDiv& f) {
+  return (uint32_t)(((uint64_t)n * f.mul) >> 31) >> f.shift;
+}
+
+// ---------------------------------------------------------------------------
 // One unit as loaded: 16 elements of type XT.
+// ---------------------------------------------------------------------------
 template <int XT>
 struct Unit {
   static constexpr int kBytes = kUnit * (XT == XF32 ? 4 : 2);
@@ -28,14 +89,14 @@ struct Unit {
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
   }
-  // unit `u` of the row that starts at `row`
-  __device__ __forceinline__ void load(const void* row, int64_t u) {
-    const unsigned char* p = static_cast<const unsigned char*>(row) + u * kBytes;
+  // the unit at element `at` of `base`
+  __device__ __forceinline__ void load(const void* base, int64_t at) {
+    const unsigned char* p = static_cast<const unsigned char*>(base) + at * (kBytes / kUnit);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) v[i] = ld_cs(p + 16 * i);
   }
-  __device__ __forceinline__ void store(void* row, int64_t u) const {
-    unsigned char* p = static_cast<unsigned char*>(row) + u * kBytes;
+  __device__ __forceinline__ void store(void* base, int64_t at) const {
+    unsigned char* p = static_cast<unsigned char*>(base) + at * (kBytes / kUnit);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) st_cs(p + 16 * i, v[i]);
   }
@@ -56,26 +117,43 @@ struct Unit {
     else
       return make_float2(bf16lo(word(k)), bf16hi(word(k)));
   }
-  __device__ __forceinline__ void floats(float (&f)[kUnit]) const {
+  __device__ __forceinline__ void floats(float2 (&f)[kPairs]) const {
 #pragma unroll
-    for (int k = 0; k < kUnit / 2; ++k) {
-      const float2 p = pair(k);
-      f[2 * k] = p.x;
-      f[2 * k + 1] = p.y;
-    }
+    for (int k = 0; k < kPairs; ++k) f[k] = pair(k);
   }
-  // rounds to XT, to nearest even
-  __device__ __forceinline__ void set_pair(int k, float a, float b) {
+  // Rounds a pair to XT, to nearest even.  The conversion gives 0x7FFF for
+  // every NaN, as pack_f16x2 / pack_bf16x2 do.
+  __device__ __forceinline__ void set_pair(int k, float2 a) {
     if constexpr (XT == XF32) {
-      set_word(2 * k, __float_as_uint(a));
-      set_word(2 * k + 1, __float_as_uint(b));
+      set_word(2 * k, __float_as_uint(a.x));
+      set_word(2 * k + 1, __float_as_uint(a.y));
     } else {
-      set_word(k, XT == XF16 ? pack_f16x2(a, b) : pack_bf16x2(a, b));
+      uint32_t r;
+      if constexpr (XT == XF16)
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(a.y), "f"(a.x));
+      else
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(a.y), "f"(a.x));
+      set_word(k, r);
     }
   }
-  __device__ __forceinline__ void set(const float (&f)[kUnit]) {
+  // Adds another unit, each sum rounded to XT.  For the 16-bit types one
+  // packed addition rounds once; rounding the binary32 sum gives the same
+  // value, as 24 bits are at least 2 * 11 + 2.
+  __device__ __forceinline__ void add(const Unit& o) {
+    if constexpr (XT == XF32) {
 #pragma unroll
-    for (int k = 0; k < kUnit / 2; ++k) set_pair(k, f[2 * k], f[2 * k + 1]);
+      for (int k = 0; k < kPairs; ++k) set_pair(k, add2(pair(k), o.pair(k)));
+    } else {
+#pragma unroll
+      for (int k = 0; k < kPairs; ++k) {
+        uint32_t r;
+        if constexpr (XT == XF16)
+          asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(word(k)), "r"(o.word(k)));
+        else
+          asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(word(k)), "r"(o.word(k)));
+        set_word(k, r);
+      }
+    }
   }
   // the sign bit of element i as stored (a conversion may drop a NaN's sign)
   __device__ __forceinline__ uint32_t sign80(int i) const {
@@ -86,49 +164,85 @@ struct Unit {
 
 // 16 weights of a vector of any of the three types (uniform branch).  The
 // vector is read again for every row: default caching keeps it in L1.
-__device__ __forceinline__ void load_weights(const void* w, int wt, int u, float (&f)[kUnit]) {
+__device__ __forceinline__ void load_weights(const void* w, int wt, int u, float2 (&f)[kPairs]) {
   if (wt == XF32) {
     const float4* p = static_cast<const float4*>(w) + u * 4;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float4 q = __ldg(p + i);
-      f[4 * i] = q.x, f[4 * i + 1] = q.y, f[4 * i + 2] = q.z, f[4 * i + 3] = q.w;
+      f[2 * i] = make_float2(q.x, q.y);
+      f[2 * i + 1] = make_float2(q.z, q.w);
     }
   } else {
     const uint4* p = static_cast<const uint4*>(w) + u * 2;
-    Unit<XBF16> r;
-    r.v[0] = __ldg(p);
-    r.v[1] = __ldg(p + 1);
+    const uint4 a = __ldg(p), b = __ldg(p + 1);
     if (wt == XBF16) {
+      Unit<XBF16> r;
+      r.v[0] = a, r.v[1] = b;
       r.floats(f);
     } else {
-      Unit<XF16> h;
-      h.v[0] = r.v[0];
-      h.v[1] = r.v[1];
-      h.floats(f);
+      Unit<XF16> r;
+      r.v[0] = a, r.v[1] = b;
+      r.floats(f);
     }
   }
 }
 
-// NaN-propagating max |v| of a unit, as ordered bits (NaN above infinity).
-__device__ __forceinline__ uint32_t unit_amax(const float (&v)[kUnit]) {
+// NaN-propagating max |v| of a unit as bits that order as integers (the
+// conversion-free NaN of the max instruction is above infinity).
+__device__ __forceinline__ uint32_t unit_amax(const float2 (&v)[kPairs]) {
   float a = 0.0f, b = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kUnit; i += 2) {
-    a = max_abs_nan(a, v[i]);
-    b = max_abs_nan(b, v[i + 1]);
+  for (int k = 0; k < kPairs; k += 2) {
+    a = max3_abs_nan(a, v[k].x, v[k].y);
+    b = max3_abs_nan(b, v[k + 1].x, v[k + 1].y);
   }
-  return amax_bits(max_abs_nan(a, b));
+  return __float_as_uint(max3_abs_nan(a, b, b));
+}
+// Maximum over the 8 lanes of a tile, or the 2 of a 1x32 block.
+__device__ __forceinline__ uint32_t pair_max(uint32_t m) { return max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1)); }
+__device__ __forceinline__ uint32_t tile_max(uint32_t m) {
+  m = pair_max(m);
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+  return max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
 }
 
+constexpr uint32_t kInfBits = 0x7F800000u;
+
+// Multiplier of a 1x128 tile (in every lane) and its stored scale (in odd
+// lanes), by fp8_quantize_blockwise's rule: scale = amax / top, multiplier
+// top / amax; both correctly rounded divisions at once, the even lane of each
+// neighbouring pair doing the one and the odd lane the other.  The multiplier
+// is 0 for a tile of zeros, with a non-finite element, or with an amax below
+// top / FLT_MAX (about 2^-112), where top / amax would be infinite: its
+// elements become zeros instead of the NaN that 0 * inf would give.
+__device__ __forceinline__ void tile_scale(uint32_t m, float top, float* mul, float* scale) {
+  const bool odd = threadIdx.x & 1;
+  const float amax = __uint_as_float(m);
+  const float q = __fdiv_rn(odd ? amax : top, odd ? top : amax);
+  const float p = __shfl_xor_sync(0xFFFFFFFFu, q, 1);
+  const float r = odd ? p : q;
+  *mul = (r < INFINITY && m < kInfBits) ? r : 0.0f;
+  *scale = m > kInfBits ? __uint_as_float(0x7FC00000u) : q;
+}
+// The same of a 1x32 block by mx_quantize's rule: e = max(floor(log2 amax) -
+// emax, -127), byte e + 127, multiplier 2^-e; byte 0xFF for a non-finite one.
+__device__ __forceinline__ void mx_scale(uint32_t m, uint32_t emax, float* mul, uint32_t* byte) {
+  const uint32_t E = m >> 23, b = E > emax ? E - emax : 0u;
+  *byte = m >= kInfBits ? 0xFFu : b;
+  *mul = __uint_as_float((254u - b) << 23);
+}
+
+// Saturating codes of a unit whose products with `mul` are not NaN.
 template <bool E5M2>
-__device__ __forceinline__ uint4 cast_unit(const float (&v)[kUnit], float mul) {
+__device__ __forceinline__ uint4 cast_unit(const float2 (&v)[kPairs], float mul) {
+  const float2 m = both(mul);
   uint32_t w[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float a = __fmul_rn(v[4 * k], mul), b = __fmul_rn(v[4 * k + 1], mul);
-    const float c = __fmul_rn(v[4 * k + 2], mul), d = __fmul_rn(v[4 * k + 3], mul);
-    w[k] = E5M2 ? cvt_e5m2x2(a, b) | (cvt_e5m2x2(c, d) << 16) : cvt_e4m3x2(a, b) | (cvt_e4m3x2(c, d) << 16);
+    const float2 a = mul2(v[2 * k], m), b = mul2(v[2 * k + 1], m);
+    w[k] = E5M2 ? cvt_e5m2x2(a.x, a.y) | (cvt_e5m2x2(b.x, b.y) << 16)
+                : cvt_e4m3x2(a.x, a.y) | (cvt_e4m3x2(b.x, b.y) << 16);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -136,11 +250,13 @@ __device__ __forceinline__ uint4 cast_unit(const float (&v)[kUnit], float mul) {
 // Codes of a unit in a tile that holds an infinity or a NaN: 0x7F with the
 // element's sign for each of those, a zero with its sign for a finite element.
 template <typename SignOf>
-__device__ __forceinline__ uint4 nonfinite_unit(const float (&v)[kUnit], SignOf sign80) {
+__device__ __forceinline__ uint4 nonfinite_unit(const float2 (&v)[kPairs], SignOf sign80) {
   uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-  for (int i = 0; i < kUnit; ++i)
-    w[i >> 2] |= ((fabsf(v[i]) < INFINITY ? 0u : 0x7Fu) | sign80(i)) << (8 * (i & 3));
+  for (int i = 0; i < kUnit; ++i) {
+    const float f = (i & 1) ? v[i >> 1].y : v[i >> 1].x;
+    w[i >> 2] |= ((fabsf(f) < INFINITY ? 0u : 0x7Fu) | sign80(i)) << (8 * (i & 3));
+  }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
@@ -152,67 +268,60 @@ struct Fp8Out {
   bool e5m2, mx;
 };
 
+// Place of a unit: element `at` = row * cols + u * 16 of a dense tensor.
+struct Place {
+  int64_t at;
+  int32_t row, u;
+  bool in;        // the unit lies in the tensor
+  bool tile_in;   // its tile's first unit does
+};
+
+// Stores a 1x128 tile's scale from lane 1 of its eight.
+__device__ __forceinline__ void store_tile_scale(const Fp8Out& o, const Place& p, float scale) {
+  if ((p.u & 7) == 1 && p.tile_in) static_cast<float*>(o.scales)[(int64_t)p.row * o.per_row + (p.u >> 3)] = scale;
+}
+
 // Casts a unit and stores its codes and its block's scale.  All 32 lanes of a
 // warp call this; the 8 lanes of a tile hold consecutive units of one row, and
-// a lane past the row's end holds zeros and stores nothing (in_row false).
-//
-// 1x128 tiles follow fp8_quantize_blockwise: scale = amax / fp8_max, elements
-// times r = fp8_max / amax, r = 0 for a tile of zeros or with a non-finite
-// element.  A tile with 0 < amax < fp8_max / FLT_MAX would need a multiplier
-// beyond binary32; it is cast with r = 0 too, so its elements (below 2^-112)
-// become zeros instead of the NaN that 0 * inf would give.
-// 1x32 blocks follow mx_quantize: e = max(floor(log2 amax) - emax, -127), scale
-// byte e + 127, elements times 2^-e; a non-finite block has byte 0xFF, codes 0.
+// a lane past the row's end holds zeros and stores no codes.
 template <typename SignOf>
-__device__ __forceinline__ void cast_store(const float (&v)[kUnit], const Fp8Out& o, int64_t row, int cols, int u,
-                                           bool in_row, SignOf sign80) {
+__device__ __forceinline__ void cast_store(const float2 (&v)[kPairs], const Fp8Out& o, const Place& p, SignOf sign80) {
   uint32_t m = unit_amax(v);
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-  float mul, scale = 0.0f;
-  uint32_t byte = 0u;
-  if (o.mx) {
-    const uint32_t E = m >> 23, emax = o.e5m2 ? 15u : 8u;
-    byte = m >= 0x7F800000u ? 0xFFu : (E > emax ? E - emax : 0u);
-    mul = m >= 0x7F800000u ? 0.0f : __uint_as_float((254u - byte) << 23);
-  } else {
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
-    const float amax = __uint_as_float(m), top = o.e5m2 ? 57344.0f : 448.0f;
-    scale = __fdiv_rn(amax, top);
-    mul = __fdiv_rn(top, amax);
-    if (!(mul < INFINITY) || m >= 0x7F800000u) mul = 0.0f;
-  }
+  float mul;
   uint4 c;
-  if (__builtin_expect(m >= 0x7F800000u, 0))
+  if (o.mx) {
+    uint32_t byte;
+    m = pair_max(m);
+    mx_scale(m, o.e5m2 ? 15u : 8u, &mul, &byte);
+    if ((p.u & 1) == 0 && p.in)
+      static_cast<uint8_t*>(o.scales)[(int64_t)p.row * o.per_row + (p.u >> 1)] = (uint8_t)byte;
+  } else {
+    float scale;
+    m = tile_max(m);
+    tile_scale(m, o.e5m2 ? 57344.0f : 448.0f, &mul, &scale);
+    store_tile_scale(o, p, scale);
+  }
+  if (__builtin_expect(m >= kInfBits, 0))
     c = o.mx ? make_uint4(0u, 0u, 0u, 0u) : nonfinite_unit(v, sign80);
   else
     c = o.e5m2 ? cast_unit<true>(v, mul) : cast_unit<false>(v, mul);
-  if (!in_row) return;
-  st_cs(o.codes + row * cols + u * kUnit, c);
-  if (o.mx) {
-    if ((u & 1) == 0) static_cast<uint8_t*>(o.scales)[row * o.per_row + (u >> 1)] = (uint8_t)byte;
-  } else {
-    if ((u & 7) == 0)
-      static_cast<float*>(o.scales)[row * o.per_row + (u >> 3)] = m > 0x7F800000u ? __uint_as_float(0x7FC00000u) : scale;
-  }
+  if (p.in) st_cs(o.codes + p.at, c);
 }
 
 // cast_store of computed values: a NaN's sign is the value's own.
-__device__ __forceinline__ void cast_store(const float (&v)[kUnit], const Fp8Out& o, int64_t row, int cols, int u,
-                                           bool in_row) {
-  cast_store(v, o, row, cols, u, in_row, [&](int i) { return (__float_as_uint(v[i]) >> 24) & 0x80u; });
+__device__ __forceinline__ void cast_store(const float2 (&v)[kPairs], const Fp8Out& o, const Place& p) {
+  cast_store(v, o, p, [&](int i) { return (__float_as_uint((i & 1) ? v[i >> 1].y : v[i >> 1].x) >> 24) & 0x80u; });
 }
 
-// Values of the 16 E4M3 codes of a unit times their tile's scale.
-__device__ __forceinline__ void e4m3_floats(uint4 c, float scale, float (&f)[kUnit]) {
+// Values of the 16 E4M3 codes of a unit times `scale`.
+__device__ __forceinline__ void e4m3_floats(uint4 c, float scale, float2 (&f)[kPairs]) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < kPairs; ++k) {
     const unsigned short two = (unsigned short)(w[k >> 1] >> (16 * (k & 1)));
     uint32_t h2;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(two));
-    f[2 * k] = __fmul_rn(f16lo(h2), scale);
-    f[2 * k + 1] = __fmul_rn(f16hi(h2), scale);
+    f[k] = mul2(make_float2(f16lo(h2), f16hi(h2)), both(scale));
   }
 }
 
