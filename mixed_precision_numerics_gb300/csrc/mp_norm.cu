@@ -13,6 +13,11 @@
 //
 // Both read and write every element once: the row lives in registers between
 // the two uses of it, before and after the row's sum.
+//
+// A CTA stays on its SM and takes row after row.  Each thread fetches its own
+// 16 elements of the next rows into shared memory with asynchronous copies
+// while it works on this one, so DRAM stays busy through the row's barrier and
+// no register waits for memory.
 #include <math.h>
 
 #include "mp_chain.cuh"
@@ -22,27 +27,34 @@
 namespace mp {
 namespace {
 
-constexpr int kCta = 256;          // threads of a CTA that takes several rows
-constexpr int kMaxThreads = 512;   // threads of a CTA that takes one row at a time
-constexpr int kMaxUnits = 4;       // units of a row per thread
-constexpr int kMaxCols = kMaxThreads * kMaxUnits * kUnit;
-constexpr int kMaxParts = 608;     // partial sums of dweight: four CTAs on each of 152 SMs
+constexpr int kCta = 256;           // threads of a CTA that takes several rows at a time
+constexpr int kMaxThreads = 1024;   // threads of a CTA that takes one row at a time
+constexpr int kMaxCols = kMaxThreads * kUnit;
+constexpr int kMaxParts = 608;      // partial sums of dweight: four CTAs on each of 152 SMs
 
-// How a row is laid over threads, by its length alone.  `lanes` > 0: that many
-// lanes of a warp hold the row and a CTA takes kCta / lanes rows; else a whole
-// CTA of `threads` holds it, `units` 16-element units a thread.
+// How a row is laid over threads, by its length alone: `lanes` of a warp (8,
+// 16 or 32) and kCta / lanes rows a CTA, or (lanes 0) a CTA of `threads`, one
+// 16-element unit a thread.
 struct RowShape {
-  int lanes, threads, units, rows_per_cta;
+  int lanes, threads, rows_per_cta;
 };
 RowShape row_shape(int64_t cols) {
   const int n = (int)(cols / kUnit);
-  if (n <= 32) {
-    const int l = n <= 8 ? 8 : n <= 16 ? 16 : 32;
-    return {l, kCta, 1, kCta / l};
-  }
-  const int u = n <= kMaxThreads ? 1 : n <= 2 * kMaxThreads ? 2 : 4;
-  const int t = ((n + u - 1) / u + 31) / 32 * 32;
-  return {0, t, u, 1};
+  if (n > 32) return {0, (n + 31) / 32 * 32, 1};
+  const int l = n <= 8 ? 8 : n <= 16 ? 16 : 32;
+  return {l, kCta, kCta / l};
+}
+// CTAs that take `groups` groups of rows in turn, `per_sm` resident on an SM.
+int resident_grid(int64_t groups, int per_sm) {
+  const int64_t most = (int64_t)sm_count() * (per_sm < 1 ? 1 : per_sm);
+  return (int)(groups < most ? groups : most);
+}
+
+// Raises a kernel's dynamic shared-memory limit where a launch needs more than
+// the default 48 KB.
+template <typename K>
+bool smem_ok(K kernel, int bytes, std::atomic<uint64_t>& done) {
+  return bytes <= 48 * 1024 || smem_opt_in(kernel, 224 * 1024, done);
 }
 
 // Sum over the threads that hold one row, in every one of them.
@@ -64,85 +76,116 @@ struct NormFwd {
   const void *x, *residual, *weight;
   void* h;
   float* rstd;
-  Fp8Out y, ckpt;
+  Fp8Out y;
+  uint8_t* ckpt;
+  float* ckpt_scales;
   int64_t rows;
   int32_t cols, wt;
-  float eps;
+  float eps, inv_cols;
 };
 
-template <int XT, int L, int U>
+// Bytes a thread's copies take in one stage, and the stages: two rows ahead for
+// the 16-bit types, one for FP32, whose rows are twice as long.
+template <int XT>
+struct FwdStage {
+  static constexpr int kPieces = 2 * Unit<XT>::kVecs;  // x and residual
+  static constexpr int kStages = XT == XF32 ? 1 : 2;
+};
+
+template <int XT, int L, bool SAVE>
 __global__ __launch_bounds__(L ? kCta : kMaxThreads) void k_norm_fwd(const __grid_constant__ NormFwd a) {
+  extern __shared__ __align__(16) unsigned char stages[];
   __shared__ float slots[2][32];
   chain_wait();
   chain_release();
-  constexpr int R = L ? kCta / L : 1;
-  const int t = L ? threadIdx.x % (L ? L : 1) : threadIdx.x, sub = L ? threadIdx.x / (L ? L : 1) : 0;
-  const int stride = L ? L : blockDim.x, units = a.cols / kUnit;
-  int parity = 0;
-  for (int64_t row0 = (int64_t)blockIdx.x * R; row0 < a.rows; row0 += (int64_t)gridDim.x * R, parity ^= 1) {
+  using St = FwdStage<XT>;
+  constexpr int R = L ? kCta / L : 1, S = St::kStages;
+  const int T = blockDim.x, units = a.cols / kUnit;
+  const int u = L ? threadIdx.x % (L ? L : 1) : threadIdx.x, sub = L ? threadIdx.x / (L ? L : 1) : 0;
+  const int uc = u < units ? u : units - 1;  // a lane past the row's end works on its last unit and stores nothing
+  const int64_t step = (int64_t)gridDim.x * R;
+  const uint32_t mine = smem_u32(stages) + threadIdx.x * 16;
+  auto fetch = [&](int stage, int64_t row) {
+    const int64_t at = (row < a.rows ? row : a.rows - 1) * a.cols + uc * kUnit;
+    const uint32_t slot = mine + stage * St::kPieces * T * 16;
+    copy_unit<XT>(slot, T, a.x, at);
+    if (a.residual) copy_unit<XT>(slot + Unit<XT>::kVecs * T * 16, T, a.residual, at);
+  };
+  int64_t row0 = (int64_t)blockIdx.x * R;
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    if (row0 + s * step < a.rows) fetch(s, row0 + s * step + sub);
+    copy_commit();
+  }
+  float2 w[kPairs];
+  load_weights(a.weight, a.wt, uc, w);
+  const int tiles = (a.cols + kTile - 1) / kTile;
+  for (int it = 0; row0 < a.rows; row0 += step, ++it) {
+    const int stage = S == 1 ? 0 : it & 1;
+    copy_wait<S - 1>();
+    const uint32_t slot = mine + stage * St::kPieces * T * 16;
+    Unit<XT> h[2];
+    h[0] = take_unit<XT>(slot, T);
+    if (a.residual) h[0].add(take_unit<XT>(slot + Unit<XT>::kVecs * T * 16, T));
+    if (row0 + S * step < a.rows) fetch(stage, row0 + S * step + sub);
+    copy_commit();
+    Place p;
     const int64_t row = row0 + sub;
-    Place p[U];
-    Unit<XT> h[U];
+    p.row = (int32_t)row;
+    p.u = u;
+    p.at = row * a.cols + u * kUnit;
+    p.in = row < a.rows && u < units;
+    p.tile_in = row < a.rows && (u & ~7) < units;
+    if (a.h && p.in) h[0].store(a.h, p.at);
     float2 ss = both(0.0f);
+    float amax = 0.0f;
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      p[k].row = (int32_t)row;
-      p[k].u = t + k * stride;
-      p[k].at = row * a.cols + p[k].u * kUnit;
-      p[k].in = row < a.rows && p[k].u < units;
-      p[k].tile_in = row < a.rows && (p[k].u & ~7) < units;
-      h[k].zero();
-      if (p[k].in) {
-        h[k].load(a.x, p[k].at);
-        if (a.residual) {
-          Unit<XT> r;
-          r.load(a.residual, p[k].at);
-          h[k].add(r);
-        }
-        if (a.h) h[k].store(a.h, p[k].at);
-      }
-      float2 f[kPairs];
-      h[k].floats(f);
-      if (a.ckpt.codes) cast_store(f, a.ckpt, p[k], [&](int i) { return h[k].sign80(i); });
-#pragma unroll
-      for (int i = 0; i < kPairs; ++i) ss = fma2(f[i], f[i], ss);
+    for (int i = 0; i < kPairs; ++i) {
+      const float2 f = h[0].pair(i);
+      ss = fma2(f, f, ss);
+      if constexpr (SAVE) amax = max3_abs_nan(amax, f.x, f.y);
     }
-    const float sum = row_sum<L>(ss.x + ss.y, slots[parity]);
-    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, (float)a.cols), a.eps)));
-    if (t == 0 && row < a.rows && a.rstd) a.rstd[row] = rstd;
+    const float sum = row_sum<L>(p.in ? ss.x + ss.y : 0.0f, slots[it & 1]);
+    const float rstd = rsqrtf(fmaf(sum, a.inv_cols, a.eps));
+    if (u == 0 && p.in && a.rstd) a.rstd[row] = rstd;
+    float2 y[kPairs];
+    h[0].forget();
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      float2 f[kPairs], w[kPairs];
-#pragma unroll
-      for (int i = 0; i < kPairs; ++i) f[i] = w[i] = both(0.0f);
-      if (p[k].in) {
-        h[k].floats(f);
-        load_weights(a.weight, a.wt, p[k].u, w);
-#pragma unroll
-        for (int i = 0; i < kPairs; ++i) f[i] = mul2(mul2(f[i], both(rstd)), w[i]);
-      }
-      cast_store(f, a.y, p[k]);
+    for (int i = 0; i < kPairs; ++i) y[i] = mul2(mul2(h[0].pair(i), both(rstd)), w[i]);
+    if constexpr (SAVE) {
+      const uint32_t mc[2] = {tile_max(p.in ? __float_as_uint(amax) : 0u), 0u};
+      uint8_t* const cc[2] = {a.ckpt, nullptr};
+      float* const cs[2] = {a.ckpt_scales, nullptr};
+      cast_store<2, XT>(y, a.y, p, mc, h, cc, cs, tiles);
+    } else {
+      cast_store<XT>(y, a.y, p);
     }
   }
 }
 
-template <int XT, int L, int U>
+template <int XT, int L, bool SAVE>
 mp_status launch_fwd(const NormFwd& a, const RowShape& s, cudaStream_t st) {
-  const int64_t ctas = (a.rows + s.rows_per_cta - 1) / s.rows_per_cta;
-  launch_chained(k_norm_fwd<XT, L, U>, dim3(full_grid(ctas)), dim3(s.threads), 0, st, a);
+  static std::atomic<uint64_t> opted{0};
+  const int64_t groups = (a.rows + s.rows_per_cta - 1) / s.rows_per_cta;
+  const int smem = FwdStage<XT>::kStages * FwdStage<XT>::kPieces * s.threads * 16;  // at most 128 KB
+  if (!smem_ok(k_norm_fwd<XT, L, SAVE>, smem, opted)) return MP_ECUDA;
+  launch_chained(k_norm_fwd<XT, L, SAVE>, dim3(resident_grid(groups, kMaxThreads / s.threads)), dim3(s.threads), smem,
+                 st, a);
   note_launches(1);
   return launch_status();
 }
 
-template <int XT>
+template <int XT, bool SAVE>
 mp_status launch_fwd_shape(const NormFwd& a, cudaStream_t st) {
   const RowShape s = row_shape(a.cols);
-  if (s.lanes == 8) return launch_fwd<XT, 8, 1>(a, s, st);
-  if (s.lanes == 16) return launch_fwd<XT, 16, 1>(a, s, st);
-  if (s.lanes == 32) return launch_fwd<XT, 32, 1>(a, s, st);
-  if (s.units == 1) return launch_fwd<XT, 0, 1>(a, s, st);
-  if (s.units == 2) return launch_fwd<XT, 0, 2>(a, s, st);
-  return launch_fwd<XT, 0, 4>(a, s, st);
+  if (s.lanes == 8) return launch_fwd<XT, 8, SAVE>(a, s, st);
+  if (s.lanes == 16) return launch_fwd<XT, 16, SAVE>(a, s, st);
+  if (s.lanes == 32) return launch_fwd<XT, 32, SAVE>(a, s, st);
+  return launch_fwd<XT, 0, SAVE>(a, s, st);
+}
+template <int XT>
+mp_status launch_fwd_type(const NormFwd& a, cudaStream_t st) {
+  return a.ckpt ? launch_fwd_shape<XT, true>(a, st) : launch_fwd_shape<XT, false>(a, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -156,108 +199,116 @@ struct NormBwd {
   float* parts;
   int64_t rows;
   int32_t cols, tiles, wt;
+  float inv_cols;
+};
+
+constexpr int kBwdThreads = 768;  // resident threads of the backward kernel on an SM, by its registers
+
+// Pieces of 16 bytes a thread fetches for one row (dy, the stream or its codes,
+// dh), followed by two words (the tile's scale, the row's rstd), and the stages.
+template <int XT, bool SAVED>
+struct BwdStage {
+  static constexpr int kV = Unit<XT>::kVecs;
+  static constexpr int kPieces = 2 * kV + (SAVED ? 1 : kV);
+  static constexpr int kBytes = kPieces * 16 + 8;
+  static constexpr int kStages = XT == XF32 ? 1 : 2;
 };
 
 // CTA c takes row groups c, c + gridDim.x, ...; each thread keeps the sums of
 // its own columns in registers over those rows (binary32, in row order) and
 // the CTA writes one row of `parts` at the end.
-template <int XT, bool SAVED, int L, int U>
-__global__ __launch_bounds__(L ? kCta : kMaxThreads) void k_norm_bwd(const __grid_constant__ NormBwd a) {
+template <int XT, bool SAVED, int L, bool WIDE>
+__global__ __launch_bounds__(L ? kCta : WIDE ? kMaxThreads : kMaxThreads / 2) void k_norm_bwd(
+    const __grid_constant__ NormBwd a) {
+  extern __shared__ __align__(16) unsigned char stages[];
   __shared__ float slots[2][32];
-  __shared__ float fold[L ? kCta * kUnit : 1];
   chain_wait();
   chain_release();
-  constexpr int R = L ? kCta / L : 1;
-  const int t = L ? threadIdx.x % (L ? L : 1) : threadIdx.x, sub = L ? threadIdx.x / (L ? L : 1) : 0;
-  const int stride = L ? L : blockDim.x, units = a.cols / kUnit;
-  float2 acc[U][kPairs];
+  using St = BwdStage<XT, SAVED>;
+  constexpr int R = L ? kCta / L : 1, S = St::kStages;
+  const int T = blockDim.x, units = a.cols / kUnit;
+  const int u = L ? threadIdx.x % (L ? L : 1) : threadIdx.x, sub = L ? threadIdx.x / (L ? L : 1) : 0;
+  const int uc = u < units ? u : units - 1;  // a lane past the row's end works on its last unit and stores nothing
+  const int64_t step = (int64_t)gridDim.x * R;
+  const uint32_t mine = smem_u32(stages) + threadIdx.x * 16;
+  const uint32_t words = smem_u32(stages) + St::kPieces * T * 16 + threadIdx.x * 4;
+  auto fetch = [&](int stage, int64_t row) {
+    const int64_t r = row < a.rows ? row : a.rows - 1, at = r * a.cols + uc * kUnit;
+    const uint32_t slot = mine + stage * St::kBytes * T, word = words + stage * St::kBytes * T;
+    copy_unit<XT>(slot, T, a.dy, at);
+    if (a.dh) copy_unit<XT>(slot + St::kV * T * 16, T, a.dh, at);
+    if constexpr (SAVED) {
+      copy16(slot + 2 * St::kV * T * 16, a.codes + at);
+      copy4(word, a.scales + r * a.tiles + uc / kTileLanes);
+    } else {
+      copy_unit<XT>(slot + 2 * St::kV * T * 16, T, a.h, at);
+    }
+    copy4(word + T * 4, a.rstd + r);
+  };
+  int64_t row0 = (int64_t)blockIdx.x * R;
 #pragma unroll
-  for (int k = 0; k < U; ++k)
+  for (int s = 0; s < S; ++s) {
+    if (row0 + s * step < a.rows) fetch(s, row0 + s * step + sub);
+    copy_commit();
+  }
+  float2 acc[kPairs];
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i) acc[k][i] = both(0.0f);
-  int parity = 0;
-  for (int64_t row0 = (int64_t)blockIdx.x * R; row0 < a.rows; row0 += (int64_t)gridDim.x * R, parity ^= 1) {
+  for (int i = 0; i < kPairs; ++i) acc[i] = both(0.0f);
+  for (int it = 0; row0 < a.rows; row0 += step, ++it) {
+    const int stage = S == 1 ? 0 : it & 1;
     const int64_t row = row0 + sub;
     const bool live = row < a.rows;
-    const float rstd = live ? a.rstd[row] : 0.0f;
-    Unit<XT> dy[U], v[U];
-    uint4 code[U];
-    float scale[U];
+    copy_wait<S - 1>();
+    const uint32_t slot = mine + stage * St::kBytes * T, word = words + stage * St::kBytes * T;
+    const float rstd = lds_f32(word + T * 4);
+    float2 xh[kPairs], g[kPairs];
+    if constexpr (SAVED) {
+      e4m3_floats(lds16(slot + 2 * St::kV * T * 16), lds_f32(word) * rstd, xh);
+    } else {
+      take_unit<XT>(slot + 2 * St::kV * T * 16, T).floats(xh);
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) xh[i] = mul2(xh[i], both(rstd));
+    }
+    take_unit<XT>(slot, T).floats(g);
     float2 dot = both(0.0f);
+    {
+      float2 w[kPairs];
+      load_weights(a.weight, a.wt, uc, w);
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int u = t + k * stride;
-      const int64_t at = row * a.cols + u * kUnit;
-      dy[k].zero();
-      v[k].zero();
-      code[k] = make_uint4(0u, 0u, 0u, 0u);
-      scale[k] = 0.0f;
-      if (live && u < units) {
-        dy[k].load(a.dy, at);
-        if constexpr (SAVED) {
-          code[k] = ld_cs(a.codes + at);
-          scale[k] = a.scales[row * a.tiles + u / kTileLanes];
-        } else {
-          v[k].load(a.h, at);
-        }
+      for (int i = 0; i < kPairs; ++i) {
+        if (L == 0 || live) acc[i] = fma2(g[i], xh[i], acc[i]);  // rows past the end repeat the last one
+        g[i] = mul2(g[i], w[i]);
+        dot = fma2(g[i], xh[i], dot);
       }
     }
-    float2 g[U][kPairs], xh[U][kPairs];
+    const float c = row_sum<L>(u < units ? dot.x + dot.y : 0.0f, slots[it & 1]) * a.inv_cols;
+    if (live && u < units) {
+      Unit<XT> o;
+      o.zero();
+      if (a.dh) o = take_unit<XT>(slot + St::kV * T * 16, T);
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int u = t + k * stride;
-      if (live && u < units) {
-        float2 w[kPairs];
-        load_weights(a.weight, a.wt, u, w);
-        if constexpr (SAVED) {
-          e4m3_floats(code[k], scale[k] * rstd, xh[k]);
-        } else {
-          v[k].floats(xh[k]);
-#pragma unroll
-          for (int i = 0; i < kPairs; ++i) xh[k][i] = mul2(xh[k][i], both(rstd));
-        }
-        dy[k].floats(g[k]);
-#pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-          acc[k][i] = fma2(g[k][i], xh[k][i], acc[k][i]);
-          g[k][i] = mul2(g[k][i], w[i]);
-          dot = fma2(g[k][i], xh[k][i], dot);
-        }
-      }
+      for (int i = 0; i < kPairs; ++i)
+        o.set_pair(i, fma2(fma2(xh[i], both(-c), g[i]), both(rstd), o.pair(i)));
+      o.store(a.dx, row * a.cols + u * kUnit);
     }
-    const float c = __fdiv_rn(row_sum<L>(dot.x + dot.y, slots[parity]), (float)a.cols);
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int u = t + k * stride;
-      if (live && u < units) {
-        const int64_t at = row * a.cols + u * kUnit;
-        Unit<XT> e, o;
-        e.zero();
-        if (a.dh) e.load(a.dh, at);
-#pragma unroll
-        for (int i = 0; i < kPairs; ++i)
-          o.set_pair(i, fma2(fma2(xh[k][i], both(-c), g[k][i]), both(rstd), e.pair(i)));
-        o.store(a.dx, at);
-      }
-    }
+    if (row0 + S * step < a.rows) fetch(stage, row0 + S * step + sub);
+    copy_commit();
   }
   float* part = a.parts + (int64_t)blockIdx.x * a.cols;
   if constexpr (L == 0) {
+    if (u < units) {
+      float4* q = reinterpret_cast<float4*>(part + u * kUnit);
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int u = t + k * stride;
-      if (u < units) {
-        float4* p = reinterpret_cast<float4*>(part + u * kUnit);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          p[i] = make_float4(acc[k][2 * i].x, acc[k][2 * i].y, acc[k][2 * i + 1].x, acc[k][2 * i + 1].y);
-      }
+      for (int i = 0; i < 4; ++i) q[i] = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
     }
   } else {
+    copy_wait<0>();
+    __syncthreads();  // the stages are free: every thread has taken its last row
+    float* fold = reinterpret_cast<float*>(stages);  // [sub][column], 16 KB
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i) {  // [sub][t][element]
-      fold[threadIdx.x * kUnit + 2 * i] = acc[0][i].x;
-      fold[threadIdx.x * kUnit + 2 * i + 1] = acc[0][i].y;
+    for (int i = 0; i < kPairs; ++i) {
+      fold[threadIdx.x * kUnit + 2 * i] = acc[i].x;
+      fold[threadIdx.x * kUnit + 2 * i + 1] = acc[i].y;
     }
     __syncthreads();
     for (int col = threadIdx.x; col < a.cols; col += kCta) {
@@ -268,28 +319,29 @@ __global__ __launch_bounds__(L ? kCta : kMaxThreads) void k_norm_bwd(const __gri
   }
 }
 
-// dweight[col] = sum over the partial rows: 32 columns a CTA, 16 warps that
-// each sum every 16th partial row, joined in a fixed order.
-constexpr int kFoldWarps = 16;
+// dweight[col] = sum over the partial rows: 32 columns a CTA, 32 warps that
+// each sum every 32nd partial row, joined in a fixed order.
+constexpr int kFoldWarps = 32;
 __global__ __launch_bounds__(32 * kFoldWarps) void k_norm_dweight(const float* parts, int32_t nparts, int32_t cols,
                                                                   void* dweight, int32_t dt) {
-  __shared__ float s[kFoldWarps][32];
+  __shared__ float s[kFoldWarps][33];
   chain_wait();
   chain_release();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
   float v = 0.0f;
-  if (col < cols)
+  if (col < cols) {
+#pragma unroll 4
     for (int p = warp; p < nparts; p += kFoldWarps) v += parts[(int64_t)p * cols + col];
+  }
   s[warp][lane] = v;
   __syncthreads();
-  if (warp != 0 || col >= cols) return;
-  v = 0.0f;
-#pragma unroll
-  for (int j = 0; j < kFoldWarps; ++j) v += s[j][lane];
+  v = warp_sum(s[lane][warp]);  // warp w joins the 32 sums of column w
+  const int out = blockIdx.x * 32 + warp;
+  if (lane != 0 || out >= cols) return;
   if (dt == XF32)
-    static_cast<float*>(dweight)[col] = v;
+    static_cast<float*>(dweight)[out] = v;
   else
-    static_cast<uint16_t*>(dweight)[col] = (uint16_t)(dt == XF16 ? pack_f16x2(v, 0.0f) : pack_bf16x2(v, 0.0f));
+    static_cast<uint16_t*>(dweight)[out] = (uint16_t)(dt == XF16 ? pack_f16x2(v, 0.0f) : pack_bf16x2(v, 0.0f));
 }
 
 int64_t parts_of(int64_t rows, int64_t cols) {
@@ -297,25 +349,31 @@ int64_t parts_of(int64_t rows, int64_t cols) {
   return groups < kMaxParts ? groups : kMaxParts;
 }
 
+template <int XT, bool SAVED, int L, bool WIDE>
+mp_status launch_bwd_rows(const NormBwd& a, const RowShape& s, int* parts, cudaStream_t st) {
+  static std::atomic<uint64_t> opted{0};
+  const int64_t groups = (a.rows + s.rows_per_cta - 1) / s.rows_per_cta;
+  using Stage = BwdStage<XT, SAVED>;
+  const int smem = Stage::kStages * Stage::kBytes * s.threads;  // at most 200 KB
+  if (!smem_ok(k_norm_bwd<XT, SAVED, L, WIDE>, smem, opted)) return MP_ECUDA;
+  const int grid = resident_grid(groups, kBwdThreads / s.threads);
+  *parts = grid < kMaxParts ? grid : kMaxParts;
+  launch_chained(k_norm_bwd<XT, SAVED, L, WIDE>, dim3(*parts), dim3(s.threads), smem, st, a);
+  note_launches(1);
+  return launch_status();
+}
+
 template <int XT, bool SAVED>
 mp_status launch_bwd(const NormBwd& a, void* dweight, int32_t dt, cudaStream_t st) {
   const RowShape s = row_shape(a.cols);
-  const int parts = (int)parts_of(a.rows, a.cols);
-  if (parts > 0) {
-    const dim3 g(parts), b(s.threads);
-    if (s.lanes == 8)
-      launch_chained(k_norm_bwd<XT, SAVED, 8, 1>, g, b, 0, st, a);
-    else if (s.lanes == 16)
-      launch_chained(k_norm_bwd<XT, SAVED, 16, 1>, g, b, 0, st, a);
-    else if (s.lanes == 32)
-      launch_chained(k_norm_bwd<XT, SAVED, 32, 1>, g, b, 0, st, a);
-    else if (s.units == 1)
-      launch_chained(k_norm_bwd<XT, SAVED, 0, 1>, g, b, 0, st, a);
-    else if (s.units == 2)
-      launch_chained(k_norm_bwd<XT, SAVED, 0, 2>, g, b, 0, st, a);
-    else
-      launch_chained(k_norm_bwd<XT, SAVED, 0, 4>, g, b, 0, st, a);
-    note_launches(1);
+  int parts = 0;
+  if (a.rows > 0) {
+    const mp_status r = s.lanes == 8    ? launch_bwd_rows<XT, SAVED, 8, false>(a, s, &parts, st)
+                        : s.lanes == 16 ? launch_bwd_rows<XT, SAVED, 16, false>(a, s, &parts, st)
+                        : s.lanes == 32 ? launch_bwd_rows<XT, SAVED, 32, false>(a, s, &parts, st)
+                        : s.threads <= kMaxThreads / 2 ? launch_bwd_rows<XT, SAVED, 0, false>(a, s, &parts, st)
+                                                       : launch_bwd_rows<XT, SAVED, 0, true>(a, s, &parts, st);
+    if (r != MP_OK) return r;
   }
   launch_chained(k_norm_dweight, dim3((a.cols + 31) / 32), dim3(32 * kFoldWarps), 0, st, (const float*)a.parts,
                  (int32_t)parts, a.cols, dweight, dt);
@@ -351,13 +409,13 @@ extern "C" MP_API mp_status rmsnorm_residual_fp8(const void* x, const void* resi
   a.x = x, a.residual = residual, a.weight = weight, a.h = h, a.rstd = rstd;
   a.y = Fp8Out{static_cast<uint8_t*>(y), y_scales, scale_block == 32 ? (int32_t)(cols / 32) : tiles,
                fp8_dtype == MP_E5M2, scale_block == 32};
-  a.ckpt = Fp8Out{static_cast<uint8_t*>(ckpt), ckpt_scales, tiles, false, false};
-  a.rows = rows, a.cols = (int32_t)cols, a.wt = w_dtype, a.eps = eps;
+  a.ckpt = static_cast<uint8_t*>(ckpt), a.ckpt_scales = ckpt_scales;
+  a.rows = rows, a.cols = (int32_t)cols, a.wt = w_dtype, a.eps = eps, a.inv_cols = 1.0f / (float)cols;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (x_dtype) {
-    case MP_F32: return launch_fwd_shape<XF32>(a, st);
-    case MP_F16: return launch_fwd_shape<XF16>(a, st);
-    default: return launch_fwd_shape<XBF16>(a, st);
+    case MP_F32: return launch_fwd_type<XF32>(a, st);
+    case MP_F16: return launch_fwd_type<XF16>(a, st);
+    default: return launch_fwd_type<XBF16>(a, st);
   }
 }
 
@@ -391,6 +449,7 @@ extern "C" MP_API mp_status rmsnorm_residual_backward(const void* dy, const void
   a.dy = dy, a.dh = dh, a.h = h, a.weight = weight, a.codes = static_cast<const uint8_t*>(ckpt);
   a.scales = ckpt_scales, a.rstd = rstd, a.dx = dx, a.parts = static_cast<float*>(d_workspace);
   a.rows = rows, a.cols = (int32_t)cols, a.tiles = (int32_t)((cols + kTile - 1) / kTile), a.wt = w_dtype;
+  a.inv_cols = 1.0f / (float)cols;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (x_dtype) {
     case MP_F32: return ckpt ? launch_bwd<XF32, true>(a, dweight, dw_dtype, st) : launch_bwd<XF32, false>(a, dweight, dw_dtype, st);

@@ -48,35 +48,47 @@ __device__ __forceinline__ Place place_of(int64_t rows, int cols, const FastDiv&
 struct SwigluFwd {
   const void *gate, *up;
   int64_t ld;  // elements between rows of gate, and of up
-  Fp8Out y, gate_ckpt, up_ckpt;
+  Fp8Out y;
+  uint8_t* ckpt;  // gate's, then up's; NULL for none
+  float* ckpt_scales;
   int64_t rows;
   int32_t cols;
   FastDiv tiles;
 };
 
-template <int XT>
+template <int XT, bool SAVE>
 __global__ __launch_bounds__(kThreads) void k_swiglu_fwd(const __grid_constant__ SwigluFwd a) {
   chain_wait();
   chain_release();
+  constexpr int N = SAVE ? 3 : 1;
   const Place p = place_of(a.rows, a.cols, a.tiles);
-  Unit<XT> gr, ur;
-  gr.zero();
-  ur.zero();
+  Unit<XT> raw[3];
+  raw[0].zero();
+  raw[1].zero();
   if (p.in) {
     const int64_t at = p.row * a.ld + p.u * kUnit;
-    gr.load(a.gate, at);
-    ur.load(a.up, at);
+    raw[0].load(a.gate, at);
+    raw[1].load(a.up, at);
   }
-  float2 g[kPairs], u[kPairs];
-  gr.floats(g);
-  ur.floats(u);
-  if (a.gate_ckpt.codes) {
-    cast_store(g, a.gate_ckpt, p, [&](int i) { return gr.sign80(i); });
-    cast_store(u, a.up_ckpt, p, [&](int i) { return ur.sign80(i); });
-  }
+  float2 y[kPairs];
+  float ag = 0.0f, au = 0.0f;
 #pragma unroll
-  for (int k = 0; k < kPairs; ++k) g[k] = mul2(mul2(g[k], logistic2(g[k])), u[k]);
-  cast_store(g, a.y, p);
+  for (int k = 0; k < kPairs; ++k) {
+    const float2 g = raw[0].pair(k), u = raw[1].pair(k);
+    if constexpr (SAVE) {
+      ag = max3_abs_nan(ag, g.x, g.y);
+      au = max3_abs_nan(au, u.x, u.y);
+    }
+    y[k] = mul2(mul2(g, logistic2(g)), u);
+  }
+  if constexpr (SAVE) {
+    const uint32_t mc[N] = {tile_max(__float_as_uint(ag)), tile_max(__float_as_uint(au)), 0u};
+    uint8_t* const cc[N] = {a.ckpt, a.ckpt + a.rows * a.cols, nullptr};
+    float* const cs[N] = {a.ckpt_scales, a.ckpt_scales + a.rows * a.tiles.d, nullptr};
+    cast_store<N, XT>(y, a.y, p, mc, raw, cc, cs, a.tiles.d);
+  } else {
+    cast_store<XT>(y, a.y, p);
+  }
 }
 
 struct SwigluBwd {
@@ -132,7 +144,11 @@ unsigned ctas_of(int64_t rows, const FastDiv& tiles) {
 
 template <int XT>
 mp_status launch_fwd(const SwigluFwd& a, cudaStream_t st) {
-  launch_chained(k_swiglu_fwd<XT>, dim3(ctas_of(a.rows, a.tiles)), dim3(kThreads), 0, st, a);
+  const dim3 g(ctas_of(a.rows, a.tiles)), b(kThreads);
+  if (a.ckpt)
+    launch_chained(k_swiglu_fwd<XT, true>, g, b, 0, st, a);
+  else
+    launch_chained(k_swiglu_fwd<XT, false>, g, b, 0, st, a);
   note_launches(1);
   return launch_status();
 }
@@ -185,9 +201,7 @@ extern "C" MP_API mp_status swiglu_fp8(const void* gate, const void* up, int64_t
   a.gate = gate, a.up = up, a.ld = ld, a.rows = rows, a.cols = (int32_t)cols, a.tiles = fast_div(tiles);
   a.y = Fp8Out{static_cast<uint8_t*>(y), y_scales, scale_block == 32 ? (int32_t)(cols / 32) : tiles,
                fp8_dtype == MP_E5M2, scale_block == 32};
-  uint8_t* cb = static_cast<uint8_t*>(ckpt);
-  a.gate_ckpt = Fp8Out{cb, ckpt_scales, tiles, false, false};
-  a.up_ckpt = Fp8Out{cb ? cb + rows * cols : nullptr, cb ? ckpt_scales + rows * tiles : nullptr, tiles, false, false};
+  a.ckpt = static_cast<uint8_t*>(ckpt), a.ckpt_scales = ckpt_scales;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (x_dtype) {
     case MP_F32: return launch_fwd<XF32>(a, st);

@@ -155,6 +155,12 @@ struct Unit {
       }
     }
   }
+  // Makes the compiler unpack the words again from here on, instead of keeping
+  // an earlier use's 16 floats in registers.
+  __device__ __forceinline__ void forget() {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) asm volatile("" : "+r"(v[i].x), "+r"(v[i].y), "+r"(v[i].z), "+r"(v[i].w));
+  }
   // the sign bit of element i as stored (a conversion may drop a NaN's sign)
   __device__ __forceinline__ uint32_t sign80(int i) const {
     if constexpr (XT == XF32) return (word(i) >> 24) & 0x80u;
@@ -163,19 +169,22 @@ struct Unit {
 };
 
 // 16 weights of a vector of any of the three types (uniform branch).  The
-// vector is read again for every row: default caching keeps it in L1.
+// loads are volatile: they stay where they are written, once a row, served by
+// L1, rather than being hoisted into 16 registers of every thread.
+__device__ __forceinline__ uint4 ld_again(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
 __device__ __forceinline__ void load_weights(const void* w, int wt, int u, float2 (&f)[kPairs]) {
+  const uint4* p = static_cast<const uint4*>(w);
   if (wt == XF32) {
-    const float4* p = static_cast<const float4*>(w) + u * 4;
+    Unit<XF32> r;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 q = __ldg(p + i);
-      f[2 * i] = make_float2(q.x, q.y);
-      f[2 * i + 1] = make_float2(q.z, q.w);
-    }
+    for (int i = 0; i < 4; ++i) r.v[i] = ld_again(p + u * 4 + i);
+    r.floats(f);
   } else {
-    const uint4* p = static_cast<const uint4*>(w) + u * 2;
-    const uint4 a = __ldg(p), b = __ldg(p + 1);
+    const uint4 a = ld_again(p + u * 2), b = ld_again(p + u * 2 + 1);
     if (wt == XBF16) {
       Unit<XBF16> r;
       r.v[0] = a, r.v[1] = b;
@@ -209,21 +218,31 @@ __device__ __forceinline__ uint32_t tile_max(uint32_t m) {
 
 constexpr uint32_t kInfBits = 0x7F800000u;
 
-// Multiplier of a 1x128 tile (in every lane) and its stored scale (in odd
-// lanes), by fp8_quantize_blockwise's rule: scale = amax / top, multiplier
-// top / amax; both correctly rounded divisions at once, the even lane of each
-// neighbouring pair doing the one and the odd lane the other.  The multiplier
-// is 0 for a tile of zeros, with a non-finite element, or with an amax below
-// top / FLT_MAX (about 2^-112), where top / amax would be infinite: its
-// elements become zeros instead of the NaN that 0 * inf would give.
-__device__ __forceinline__ void tile_scale(uint32_t m, float top, float* mul, float* scale) {
-  const bool odd = threadIdx.x & 1;
-  const float amax = __uint_as_float(m);
-  const float q = __fdiv_rn(odd ? amax : top, odd ? top : amax);
-  const float p = __shfl_xor_sync(0xFFFFFFFFu, q, 1);
-  const float r = odd ? p : q;
-  *mul = (r < INFINITY && m < kInfBits) ? r : 0.0f;
-  *scale = m > kInfBits ? __uint_as_float(0x7FC00000u) : q;
+// Multipliers and stored scales of N 1x128 tiles at once (the same eight lanes
+// hold all N), by fp8_quantize_blockwise's rule: scale = amax / top, multiplier
+// top / amax.  Both are correctly rounded divisions; lane 2k of the tile's
+// eight does tile k's multiplier and lane 2k + 1 its scale, so one division
+// serves them all.  mul[k] is valid in every lane, *scale in lane 2k + 1.  The
+// multiplier is 0 for a tile of zeros, with a non-finite element, or with an
+// amax below top / FLT_MAX (about 2^-112), where top / amax would be infinite:
+// its elements become zeros instead of the NaN that 0 * inf would give.
+template <int N>
+__device__ __forceinline__ void tile_scales(const uint32_t (&m)[N], const float (&top)[N], float (&mul)[N],
+                                            float* scale) {
+  const int lane = threadIdx.x & 7;
+  uint32_t mm = m[0];
+  float tt = top[0];
+#pragma unroll
+  for (int k = 1; k < N; ++k) {
+    mm = lane >= 2 * k ? m[k] : mm;
+    tt = lane >= 2 * k ? top[k] : tt;
+  }
+  const float amax = __uint_as_float(mm);
+  const float q = __fdiv_rn((lane & 1) ? amax : tt, (lane & 1) ? tt : amax);
+  const float r = (q < INFINITY && mm < kInfBits) ? q : 0.0f;
+#pragma unroll
+  for (int k = 0; k < N; ++k) mul[k] = __shfl_sync(0xFFFFFFFFu, r, (threadIdx.x & 24) + 2 * k);
+  *scale = mm > kInfBits ? __uint_as_float(0x7FC00000u) : q;
 }
 // The same of a 1x32 block by mx_quantize's rule: e = max(floor(log2 amax) -
 // emax, -127), byte e + 127, multiplier 2^-e; byte 0xFF for a non-finite one.
@@ -276,41 +295,113 @@ struct Place {
   bool tile_in;   // its tile's first unit does
 };
 
-// Stores a 1x128 tile's scale from lane 1 of its eight.
-__device__ __forceinline__ void store_tile_scale(const Fp8Out& o, const Place& p, float scale) {
-  if ((p.u & 7) == 1 && p.tile_in) static_cast<float*>(o.scales)[(int64_t)p.row * o.per_row + (p.u >> 3)] = scale;
+// Codes of 16 values of a tile or block whose maximum is m, stored if in range.
+template <typename SignOf>
+__device__ __forceinline__ void store_codes(const float2 (&v)[kPairs], uint8_t* codes, const Place& p, uint32_t m,
+                                            float mul, bool e5m2, bool mx, SignOf sign80) {
+  uint4 c;
+  if (__builtin_expect(m >= kInfBits, 0))
+    c = mx ? make_uint4(0u, 0u, 0u, 0u) : nonfinite_unit(v, sign80);
+  else
+    c = e5m2 ? cast_unit<true>(v, mul) : cast_unit<false>(v, mul);
+  if (p.in) st_cs(codes + p.at, c);
+}
+// The sign of a computed value is the value's own, a NaN's too.
+__device__ __forceinline__ uint32_t float_sign80(const float2 (&v)[kPairs], int i) {
+  return (__float_as_uint((i & 1) ? v[i >> 1].y : v[i >> 1].x) >> 24) & 0x80u;
 }
 
-// Casts a unit and stores its codes and its block's scale.  All 32 lanes of a
-// warp call this; the 8 lanes of a tile hold consecutive units of one row, and
-// a lane past the row's end holds zeros and stores no codes.
-template <typename SignOf>
-__device__ __forceinline__ void cast_store(const float2 (&v)[kPairs], const Fp8Out& o, const Place& p, SignOf sign80) {
-  uint32_t m = unit_amax(v);
-  float mul;
-  uint4 c;
+// Casts a unit's values y and stores codes and scale, and with N > 1 the N - 1
+// checkpoints of tensors whose tiles have maxima mc (raw holds their elements
+// as stored; codes in cc, scales in cs, `tiles` a row).  All 32 lanes of a
+// warp call this; the 8 lanes of a tile hold consecutive units of one row.  A
+// lane past the row's end may hold anything: `in` keeps it out of the maxima
+// (the caller's mc too) and of the stores.
+template <int N, int XT>
+__device__ __forceinline__ void cast_store(const float2 (&y)[kPairs], const Fp8Out& o, const Place& p,
+                                           const uint32_t (&mc)[N], Unit<XT> (&raw)[N], uint8_t* const (&cc)[N],
+                                           float* const (&cs)[N], int tiles) {
+  const int lane = threadIdx.x & 7;
+  uint32_t my = pair_max(p.in ? unit_amax(y) : 0u), m[N];
+  float top[N], mul[N], scale, mul_y;
+#pragma unroll
+  for (int k = 0; k < N - 1; ++k) m[k] = mc[k], top[k] = 448.0f;
+  top[N - 1] = o.e5m2 ? 57344.0f : 448.0f;
   if (o.mx) {
     uint32_t byte;
-    m = pair_max(m);
-    mx_scale(m, o.e5m2 ? 15u : 8u, &mul, &byte);
-    if ((p.u & 1) == 0 && p.in)
+    mx_scale(my, o.e5m2 ? 15u : 8u, &mul_y, &byte);
+    if ((lane & 1) == 0 && p.in)
       static_cast<uint8_t*>(o.scales)[(int64_t)p.row * o.per_row + (p.u >> 1)] = (uint8_t)byte;
+    m[N - 1] = 0u;
+    if constexpr (N > 1) tile_scales(m, top, mul, &scale);
   } else {
-    float scale;
-    m = tile_max(m);
-    tile_scale(m, o.e5m2 ? 57344.0f : 448.0f, &mul, &scale);
-    store_tile_scale(o, p, scale);
+    my = max(my, __shfl_xor_sync(0xFFFFFFFFu, my, 2));
+    my = m[N - 1] = max(my, __shfl_xor_sync(0xFFFFFFFFu, my, 4));
+    tile_scales(m, top, mul, &scale);
+    mul_y = mul[N - 1];
+    if (lane == 2 * N - 1 && p.tile_in) static_cast<float*>(o.scales)[(int64_t)p.row * o.per_row + (p.u >> 3)] = scale;
   }
-  if (__builtin_expect(m >= kInfBits, 0))
-    c = o.mx ? make_uint4(0u, 0u, 0u, 0u) : nonfinite_unit(v, sign80);
-  else
-    c = o.e5m2 ? cast_unit<true>(v, mul) : cast_unit<false>(v, mul);
-  if (p.in) st_cs(o.codes + p.at, c);
+  store_codes(y, o.codes, p, my, mul_y, o.e5m2, o.mx, [&](int i) { return float_sign80(y, i); });
+#pragma unroll
+  for (int k = 0; k < N - 1; ++k) {
+    if (lane == 2 * k + 1 && p.tile_in) cs[k][(int64_t)p.row * tiles + (p.u >> 3)] = scale;
+    float2 v[kPairs];
+    raw[k].forget();
+    raw[k].floats(v);
+    store_codes(v, cc[k], p, m[k], mul[k], false, false, [&](int i) { return raw[k].sign80(i); });
+  }
 }
 
-// cast_store of computed values: a NaN's sign is the value's own.
-__device__ __forceinline__ void cast_store(const float2 (&v)[kPairs], const Fp8Out& o, const Place& p) {
-  cast_store(v, o, p, [&](int i) { return (__float_as_uint((i & 1) ? v[i >> 1].y : v[i >> 1].x) >> 24) & 0x80u; });
+// Without checkpoints.
+template <int XT>
+__device__ __forceinline__ void cast_store(const float2 (&y)[kPairs], const Fp8Out& o, const Place& p) {
+  const uint32_t mc[1] = {0u};
+  Unit<XT> raw[1];
+  uint8_t* const cc[1] = {nullptr};
+  float* const cs[1] = {nullptr};
+  cast_store<1, XT>(y, o, p, mc, raw, cc, cs, 0);
+}
+
+// ---------------------------------------------------------------------------
+// Per-thread asynchronous copies into shared memory: a thread fetches its own
+// units some rows ahead and is the only one to read them, so no barrier is
+// needed, only its own wait.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {  // all but the newest N groups have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
+  return r;
+}
+__device__ __forceinline__ float lds_f32(uint32_t a) {
+  float r;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(r) : "r"(a) : "memory");
+  return r;
+}
+// A unit's 16-byte pieces lie `threads` slots of 16 bytes apart, so that a
+// warp's accesses are consecutive.
+template <int XT>
+__device__ __forceinline__ void copy_unit(uint32_t slot, int threads, const void* base, int64_t at) {
+  const unsigned char* p = static_cast<const unsigned char*>(base) + at * (Unit<XT>::kBytes / kUnit);
+#pragma unroll
+  for (int i = 0; i < Unit<XT>::kVecs; ++i) copy16(slot + i * threads * 16, p + 16 * i);
+}
+template <int XT>
+__device__ __forceinline__ Unit<XT> take_unit(uint32_t slot, int threads) {
+  Unit<XT> r;
+#pragma unroll
+  for (int i = 0; i < Unit<XT>::kVecs; ++i) r.v[i] = lds16(slot + i * threads * 16);
+  return r;
 }
 
 // Values of the 16 E4M3 codes of a unit times `scale`.
