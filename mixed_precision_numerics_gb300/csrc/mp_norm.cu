@@ -80,97 +80,68 @@ struct NormFwd {
   uint8_t* ckpt;
   float* ckpt_scales;
   int64_t rows;
-  int32_t cols, wt;
+  int32_t cols, tiles, wt;
   float eps, inv_cols;
-};
-
-// Bytes a thread's copies take in one stage, and the stages: two rows ahead for
-// the 16-bit types, one for FP32, whose rows are twice as long.
-template <int XT>
-struct FwdStage {
-  static constexpr int kPieces = 2 * Unit<XT>::kVecs;  // x and residual
-  static constexpr int kStages = XT == XF32 ? 1 : 2;
 };
 
 template <int XT, int L, bool SAVE>
 __global__ __launch_bounds__(L ? kCta : kMaxThreads) void k_norm_fwd(const __grid_constant__ NormFwd a) {
-  extern __shared__ __align__(16) unsigned char stages[];
-  __shared__ float slots[2][32];
+  __shared__ float slots[32];
   chain_wait();
   chain_release();
-  using St = FwdStage<XT>;
-  constexpr int R = L ? kCta / L : 1, S = St::kStages;
-  const int T = blockDim.x, units = a.cols / kUnit;
+  constexpr int R = L ? kCta / L : 1;
+  const int units = a.cols / kUnit;
   const int u = L ? threadIdx.x % (L ? L : 1) : threadIdx.x, sub = L ? threadIdx.x / (L ? L : 1) : 0;
-  const int uc = u < units ? u : units - 1;  // a lane past the row's end works on its last unit and stores nothing
-  const int64_t step = (int64_t)gridDim.x * R;
-  const uint32_t mine = smem_u32(stages) + threadIdx.x * 16;
-  auto fetch = [&](int stage, int64_t row) {
-    const int64_t at = (row < a.rows ? row : a.rows - 1) * a.cols + uc * kUnit;
-    const uint32_t slot = mine + stage * St::kPieces * T * 16;
-    copy_unit<XT>(slot, T, a.x, at);
-    if (a.residual) copy_unit<XT>(slot + Unit<XT>::kVecs * T * 16, T, a.residual, at);
-  };
-  int64_t row0 = (int64_t)blockIdx.x * R;
-#pragma unroll
-  for (int s = 0; s < S; ++s) {
-    if (row0 + s * step < a.rows) fetch(s, row0 + s * step + sub);
-    copy_commit();
+  Place p;
+  const int64_t row = (int64_t)blockIdx.x * R + sub;
+  p.row = (int32_t)row;
+  p.u = u;
+  p.at = row * a.cols + u * kUnit;
+  p.in = row < a.rows && u < units;
+  p.tile_in = row < a.rows && (u & ~7) < units;
+  Unit<XT> h[2];
+  Weights w;
+  h[0].zero();
+  if (p.in) {
+    h[0].load(a.x, p.at);
+    if (a.residual) {
+      Unit<XT> r;
+      r.load(a.residual, p.at);
+      h[0].add(r);
+    }
+    w.load(a.weight, a.wt, u);
+    if (a.h) h[0].store(a.h, p.at);
   }
-  float2 w[kPairs];
-  load_weights(a.weight, a.wt, uc, w);
-  const int tiles = (a.cols + kTile - 1) / kTile;
-  for (int it = 0; row0 < a.rows; row0 += step, ++it) {
-    const int stage = S == 1 ? 0 : it & 1;
-    copy_wait<S - 1>();
-    const uint32_t slot = mine + stage * St::kPieces * T * 16;
-    Unit<XT> h[2];
-    h[0] = take_unit<XT>(slot, T);
-    if (a.residual) h[0].add(take_unit<XT>(slot + Unit<XT>::kVecs * T * 16, T));
-    if (row0 + S * step < a.rows) fetch(stage, row0 + S * step + sub);
-    copy_commit();
-    Place p;
-    const int64_t row = row0 + sub;
-    p.row = (int32_t)row;
-    p.u = u;
-    p.at = row * a.cols + u * kUnit;
-    p.in = row < a.rows && u < units;
-    p.tile_in = row < a.rows && (u & ~7) < units;
-    if (a.h && p.in) h[0].store(a.h, p.at);
-    float2 ss = both(0.0f);
-    float amax = 0.0f;
+  float2 ss = both(0.0f);
+  float amax = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      const float2 f = h[0].pair(i);
-      ss = fma2(f, f, ss);
-      if constexpr (SAVE) amax = max3_abs_nan(amax, f.x, f.y);
-    }
-    const float sum = row_sum<L>(p.in ? ss.x + ss.y : 0.0f, slots[it & 1]);
-    const float rstd = rsqrtf(fmaf(sum, a.inv_cols, a.eps));
-    if (u == 0 && p.in && a.rstd) a.rstd[row] = rstd;
-    float2 y[kPairs];
-    h[0].forget();
+  for (int i = 0; i < kPairs; ++i) {
+    const float2 f = h[0].pair(i);
+    ss = fma2(f, f, ss);
+    if constexpr (SAVE) amax = max3_abs_nan(amax, f.x, f.y);
+  }
+  const float sum = row_sum<L>(ss.x + ss.y, slots);
+  const float rstd = rsqrtf(fmaf(sum, a.inv_cols, a.eps));
+  if (u == 0 && p.in && a.rstd) a.rstd[row] = rstd;
+  float2 y[kPairs];
+  w.floats(a.wt, y);
+  h[0].forget();
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i) y[i] = mul2(mul2(h[0].pair(i), both(rstd)), w[i]);
-    if constexpr (SAVE) {
-      const uint32_t mc[2] = {tile_max(p.in ? __float_as_uint(amax) : 0u), 0u};
-      uint8_t* const cc[2] = {a.ckpt, nullptr};
-      float* const cs[2] = {a.ckpt_scales, nullptr};
-      cast_store<2, XT>(y, a.y, p, mc, h, cc, cs, tiles);
-    } else {
-      cast_store<XT>(y, a.y, p);
-    }
+  for (int i = 0; i < kPairs; ++i) y[i] = mul2(mul2(h[0].pair(i), both(rstd)), y[i]);
+  if constexpr (SAVE) {
+    const uint32_t mc[2] = {tile_max(__float_as_uint(amax)), 0u};
+    uint8_t* const cc[2] = {a.ckpt, nullptr};
+    float* const cs[2] = {a.ckpt_scales, nullptr};
+    cast_store<2, XT>(y, a.y, p, mc, h, cc, cs, a.tiles);
+  } else {
+    cast_store<XT>(y, a.y, p);
   }
 }
 
 template <int XT, int L, bool SAVE>
 mp_status launch_fwd(const NormFwd& a, const RowShape& s, cudaStream_t st) {
-  static std::atomic<uint64_t> opted{0};
-  const int64_t groups = (a.rows + s.rows_per_cta - 1) / s.rows_per_cta;
-  const int smem = FwdStage<XT>::kStages * FwdStage<XT>::kPieces * s.threads * 16;  // at most 128 KB
-  if (!smem_ok(k_norm_fwd<XT, L, SAVE>, smem, opted)) return MP_ECUDA;
-  launch_chained(k_norm_fwd<XT, L, SAVE>, dim3(resident_grid(groups, kMaxThreads / s.threads)), dim3(s.threads), smem,
-                 st, a);
+  const int64_t groups = (a.rows + s.rows_per_cta - 1) / s.rows_per_cta;  // below 2^31
+  launch_chained(k_norm_fwd<XT, L, SAVE>, dim3((unsigned)groups), dim3(s.threads), 0, st, a);
   note_launches(1);
   return launch_status();
 }
@@ -273,7 +244,9 @@ __global__ __launch_bounds__(L ? kCta : WIDE ? kMaxThreads : kMaxThreads / 2) vo
     float2 dot = both(0.0f);
     {
       float2 w[kPairs];
-      load_weights(a.weight, a.wt, uc, w);
+      Weights ww;
+      ww.load(a.weight, a.wt, uc);
+      ww.floats(a.wt, w);
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
         if (L == 0 || live) acc[i] = fma2(g[i], xh[i], acc[i]);  // rows past the end repeat the last one
@@ -410,7 +383,7 @@ extern "C" MP_API mp_status rmsnorm_residual_fp8(const void* x, const void* resi
   a.y = Fp8Out{static_cast<uint8_t*>(y), y_scales, scale_block == 32 ? (int32_t)(cols / 32) : tiles,
                fp8_dtype == MP_E5M2, scale_block == 32};
   a.ckpt = static_cast<uint8_t*>(ckpt), a.ckpt_scales = ckpt_scales;
-  a.rows = rows, a.cols = (int32_t)cols, a.wt = w_dtype, a.eps = eps, a.inv_cols = 1.0f / (float)cols;
+  a.rows = rows, a.cols = (int32_t)cols, a.tiles = tiles, a.wt = w_dtype, a.eps = eps, a.inv_cols = 1.0f / (float)cols;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (x_dtype) {
     case MP_F32: return launch_fwd_type<XF32>(a, st);

@@ -168,34 +168,36 @@ struct Unit {
   }
 };
 
-// 16 weights of a vector of any of the three types (uniform branch).  The
-// loads are volatile: they stay where they are written, once a row, served by
-// L1, rather than being hoisted into 16 registers of every thread.
-__device__ __forceinline__ uint4 ld_again(const void* p) {
-  uint4 r;
-  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
-  return r;
-}
-__device__ __forceinline__ void load_weights(const void* w, int wt, int u, float2 (&f)[kPairs]) {
-  const uint4* p = static_cast<const uint4*>(w);
-  if (wt == XF32) {
-    Unit<XF32> r;
+// 16 weights of a vector of any of the three types (a uniform branch), as
+// loaded.  The vector is read again for every row: default caching keeps it in L1.
+struct Weights {
+  uint4 v[4];
+  __device__ __forceinline__ void load(const void* w, int wt, int u) {
+    const uint4* p = static_cast<const uint4*>(w);
+    if (wt == XF32) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r.v[i] = ld_again(p + u * 4 + i);
-    r.floats(f);
-  } else {
-    const uint4 a = ld_again(p + u * 2), b = ld_again(p + u * 2 + 1);
-    if (wt == XBF16) {
+      for (int i = 0; i < 4; ++i) v[i] = __ldg(p + u * 4 + i);
+    } else {
+      v[0] = __ldg(p + u * 2), v[1] = __ldg(p + u * 2 + 1);
+    }
+  }
+  __device__ __forceinline__ void floats(int wt, float2 (&f)[kPairs]) const {
+    if (wt == XF32) {
+      Unit<XF32> r;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r.v[i] = v[i];
+      r.floats(f);
+    } else if (wt == XBF16) {
       Unit<XBF16> r;
-      r.v[0] = a, r.v[1] = b;
+      r.v[0] = v[0], r.v[1] = v[1];
       r.floats(f);
     } else {
       Unit<XF16> r;
-      r.v[0] = a, r.v[1] = b;
+      r.v[0] = v[0], r.v[1] = v[1];
       r.floats(f);
     }
   }
-}
+};
 
 // NaN-propagating max |v| of a unit as bits that order as integers (the
 // conversion-free NaN of the max instruction is above infinity).
