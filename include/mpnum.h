@@ -71,7 +71,7 @@ MP_API int32_t mp_version(void);
 /* Number of kernels this library has launched in this process (diagnostic). */
 MP_API uint64_t mp_launch_count(void);
 /* Number of bounded waits on a tile copy that gave up inside this library's
- * FP8 kernels since it was loaded (0 in normal operation).  A kernel whose
+ * FP8 casts and norm backward kernel since it was loaded (0 in normal operation).  A kernel whose
  * copy engine stopped answering waits about two seconds per wait, counts the
  * failure here and returns; the outputs of that call are then incomplete.
  * Reads device memory synchronously: call it after synchronising the streams

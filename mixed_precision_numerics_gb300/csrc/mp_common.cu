@@ -77,7 +77,8 @@ MP_API int32_t mp_version(void) { return 10000; }
 
 MP_API mp_status mp_wait_failures(uint32_t* out) {
   if (!out) return MP_EINVAL;
-  *out = mp::fp8_wait_failures();
+  const uint32_t a = mp::fp8_wait_failures(), b = mp::norm_wait_failures();
+  *out = a > UINT32_MAX - b ? UINT32_MAX : a + b;
   return MP_OK;
 }
 

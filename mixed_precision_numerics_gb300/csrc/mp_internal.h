@@ -35,7 +35,8 @@ bool encode_tile_map_2d(CUtensorMap* map, const void* base, int esize, int64_t r
                         int box_cols);
 
 // Bounded waits that gave up in this library's kernels since it was loaded.
-uint32_t fp8_wait_failures();
+uint32_t fp8_wait_failures();   // mp_fp8.cu
+uint32_t norm_wait_failures();  // mp_norm.cu
 
 // Raises `kernel`'s dynamic shared-memory limit to `bytes` on the current
 // device the first time it launches there: the attribute belongs to the

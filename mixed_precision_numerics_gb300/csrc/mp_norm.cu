@@ -170,102 +170,143 @@ struct NormBwd {
   float* parts;
   int64_t rows;
   int32_t cols, tiles, wt;
+  int32_t stages;  // of the ring
   float inv_cols;
 };
 
-constexpr int kBwdThreads = 768;  // resident threads of the backward kernel on an SM, by its registers
+constexpr int kMaxStages = 4;
+constexpr int kRingBytes = 216 * 1024;  // shared memory of an SM for the rings of the CTAs on it
 
-// Pieces of 16 bytes a thread fetches for one row (dy, the stream or its codes,
-// dh), followed by two words (the tile's scale, the row's rstd), and the stages.
+__device__ unsigned int g_norm_wait_failures;  // bounded waits that gave up (read by mp_wait_failures)
+
+// One stage of the ring: dy, then dh (if any), then the stream or its codes,
+// of one group of rows, each as it lies in memory.
 template <int XT, bool SAVED>
-struct BwdStage {
-  static constexpr int kV = Unit<XT>::kVecs;
-  static constexpr int kPieces = 2 * kV + (SAVED ? 1 : kV);
-  static constexpr int kBytes = kPieces * 16 + 8;
-  static constexpr int kStages = XT == XF32 ? 1 : 2;
-};
+__host__ __device__ constexpr int stage_bytes(int elements, bool dh) {
+  constexpr int es = XT == XF32 ? 4 : 2;
+  return elements * (es + (dh ? es : 0) + (SAVED ? 1 : es));
+}
 
-// CTA c takes row groups c, c + gridDim.x, ...; each thread keeps the sums of
-// its own columns in registers over those rows (binary32, in row order) and
-// the CTA writes one row of `parts` at the end.
-template <int XT, bool SAVED, int L, bool WIDE>
-__global__ __launch_bounds__(L ? kCta : WIDE ? kMaxThreads : kMaxThreads / 2) void k_norm_bwd(
-    const __grid_constant__ NormBwd a) {
-  extern __shared__ __align__(16) unsigned char stages[];
+// CTA c takes row groups c, c + gridDim.x, ...  One thread keeps the ring of
+// `stages` groups filled with bulk copies (a group's rows are consecutive in
+// memory, so a group is two or three copies).  The barrier of a group's sum
+// also tells that every thread has done with the group before, whose stage is
+// then filled again.  Each thread keeps the sums of its own columns in
+// registers over its rows (binary32, in row order) and the CTA writes one row
+// of `parts` at the end.  A thread whose wait gave up works on what it finds
+// and stores nothing more, but keeps meeting the barriers.
+template <int XT, bool SAVED, int L, int MAXT>
+__global__ __launch_bounds__(MAXT) void k_norm_bwd(const __grid_constant__ NormBwd a) {
+  extern __shared__ __align__(128) unsigned char ring[];
   __shared__ float slots[2][32];
-  chain_wait();
-  chain_release();
-  using St = BwdStage<XT, SAVED>;
-  constexpr int R = L ? kCta / L : 1, S = St::kStages;
-  const int T = blockDim.x, units = a.cols / kUnit;
+  __shared__ uint64_t full[kMaxStages];
+  constexpr int R = L ? kCta / L : 1, es = XT == XF32 ? 4 : 2;
+  const int units = a.cols / kUnit, S = a.stages;
   const int u = L ? threadIdx.x % (L ? L : 1) : threadIdx.x, sub = L ? threadIdx.x / (L ? L : 1) : 0;
   const int uc = u < units ? u : units - 1;  // a lane past the row's end works on its last unit and stores nothing
   const int64_t step = (int64_t)gridDim.x * R;
-  const uint32_t mine = smem_u32(stages) + threadIdx.x * 16;
-  const uint32_t words = smem_u32(stages) + St::kPieces * T * 16 + threadIdx.x * 4;
-  auto fetch = [&](int stage, int64_t row) {
-    const int64_t r = row < a.rows ? row : a.rows - 1, at = r * a.cols + uc * kUnit;
-    const uint32_t slot = mine + stage * St::kBytes * T, word = words + stage * St::kBytes * T;
-    copy_unit<XT>(slot, T, a.dy, at);
-    if (a.dh) copy_unit<XT>(slot + St::kV * T * 16, T, a.dh, at);
-    if constexpr (SAVED) {
-      copy16(slot + 2 * St::kV * T * 16, a.codes + at);
-      copy4(word, a.scales + r * a.tiles + uc / kTileLanes);
-    } else {
-      copy_unit<XT>(slot + 2 * St::kV * T * 16, T, a.h, at);
-    }
-    copy4(word + T * 4, a.rstd + r);
+  const int group = R * a.cols;  // elements
+  const int bytes = stage_bytes<XT, SAVED>(group, a.dh != nullptr);
+  const int at_v = group * es * (a.dh ? 2 : 1);  // where the stream lies in a stage
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  chain_wait();
+  chain_release();
+  const uint64_t policy = policy_evict_first();
+  auto fetch = [&](int s, int64_t row0) {  // one thread
+    const int64_t left = a.rows - row0, at = row0 * a.cols;
+    const uint32_t n = (uint32_t)(left < R ? left : R) * a.cols;
+    unsigned char* st = ring + s * bytes;
+    mbar_arrive_expect_tx(&full[s], n * es * (a.dh ? 2 : 1) + n * (SAVED ? 1 : es));
+    bulk_g2s(st, static_cast<const char*>(a.dy) + at * es, n * es, &full[s], policy);
+    if (a.dh) bulk_g2s(st + group * es, static_cast<const char*>(a.dh) + at * es, n * es, &full[s], policy);
+    if constexpr (SAVED)
+      bulk_g2s(st + at_v, a.codes + at, n, &full[s], policy);
+    else
+      bulk_g2s(st + at_v, static_cast<const char*>(a.h) + at * es, n * es, &full[s], policy);
   };
   int64_t row0 = (int64_t)blockIdx.x * R;
-#pragma unroll
-  for (int s = 0; s < S; ++s) {
-    if (row0 + s * step < a.rows) fetch(s, row0 + s * step + sub);
-    copy_commit();
-  }
+  int issued = 0;  // fills so far, in thread 0; fill j is of stage j % S
+  if (threadIdx.x == 0)
+    for (; issued < S && row0 + issued * step < a.rows; ++issued) fetch(issued, row0 + issued * step);
   float2 acc[kPairs];
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) acc[i] = both(0.0f);
+  bool ok = true;
+  // The row's two scalars are read one group ahead.
+  auto scalars = [&](int64_t row, float* rstd, float* scale) {
+    const int64_t r = row < a.rows ? row : a.rows - 1;
+    *rstd = a.rstd[r];
+    *scale = SAVED ? a.scales[r * a.tiles + uc / kTileLanes] : 0.0f;
+  };
+  float rstd, scale, next_rstd, next_scale;
+  scalars(row0 + sub, &next_rstd, &next_scale);
+  int s = 0;
+  uint32_t phase = 0;
   for (int it = 0; row0 < a.rows; row0 += step, ++it) {
-    const int stage = S == 1 ? 0 : it & 1;
     const int64_t row = row0 + sub;
     const bool live = row < a.rows;
-    copy_wait<S - 1>();
-    const uint32_t slot = mine + stage * St::kBytes * T, word = words + stage * St::kBytes * T;
-    const float rstd = lds_f32(word + T * 4);
-    float2 xh[kPairs], g[kPairs];
+    rstd = next_rstd, scale = next_scale;
+    scalars(row + step, &next_rstd, &next_scale);
+    if (ok && !mbar_wait_bounded(&full[s], phase)) {
+      ok = false;
+      atomicAdd(&g_norm_wait_failures, 1u);
+    }
+    // a row past the end works on the group's first, whose copy is there
+    const unsigned char* st = ring + s * bytes;
+    const int e = (live ? sub : 0) * a.cols + uc * kUnit;
+    float2 xh[kPairs], g[kPairs], dot = both(0.0f);
     if constexpr (SAVED) {
-      e4m3_floats(lds16(slot + 2 * St::kV * T * 16), lds_f32(word) * rstd, xh);
+      e4m3_floats(*reinterpret_cast<const uint4*>(st + at_v + e), scale * rstd, xh);
     } else {
-      take_unit<XT>(slot + 2 * St::kV * T * 16, T).floats(xh);
+      Unit<XT> v;
+      v.take(st + at_v, e);
+      v.floats(xh);
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) xh[i] = mul2(xh[i], both(rstd));
     }
-    take_unit<XT>(slot, T).floats(g);
-    float2 dot = both(0.0f);
     {
-      float2 w[kPairs];
+      Unit<XT> dy;
+      dy.take(st, e);
       Weights ww;
       ww.load(a.weight, a.wt, uc);
+      float2 w[kPairs];
       ww.floats(a.wt, w);
+      dy.floats(g);
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
-        if (L == 0 || live) acc[i] = fma2(g[i], xh[i], acc[i]);  // rows past the end repeat the last one
+        if (L == 0 || live) acc[i] = fma2(g[i], xh[i], acc[i]);
         g[i] = mul2(g[i], w[i]);
         dot = fma2(g[i], xh[i], dot);
       }
     }
     const float c = row_sum<L>(u < units ? dot.x + dot.y : 0.0f, slots[it & 1]) * a.inv_cols;
-    if (live && u < units) {
-      Unit<XT> o;
-      o.zero();
-      if (a.dh) o = take_unit<XT>(slot + St::kV * T * 16, T);
-#pragma unroll
-      for (int i = 0; i < kPairs; ++i)
-        o.set_pair(i, fma2(fma2(xh[i], both(-c), g[i]), both(rstd), o.pair(i)));
-      o.store(a.dx, row * a.cols + u * kUnit);
+    if constexpr (L != 0) __syncthreads();
+    if (threadIdx.x == 0 && ok && S > 1 && it > 0 && row0 + (S - 1) * step < a.rows) {
+      fetch(s == 0 ? S - 1 : s - 1, row0 + (S - 1) * step);
+      ++issued;
     }
-    if (row0 + S * step < a.rows) fetch(stage, row0 + S * step + sub);
-    copy_commit();
+    Unit<XT> o;
+    o.zero();
+    if (a.dh) o.take(st + group * es, e);
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i)
+      o.set_pair(i, fma2(fma2(xh[i], both(-c), g[i]), both(rstd), o.pair(i)));
+    if (ok && live && u < units) o.store(a.dx, row * a.cols + u * kUnit);
+    if (S == 1) {
+      __syncthreads();
+      if (threadIdx.x == 0 && ok && row0 + step < a.rows) {
+        fetch(0, row0 + step);
+        ++issued;
+      }
+    }
+    if (++s == S) s = 0, phase ^= 1;
+  }
+  if (!ok && threadIdx.x == 0) {  // copies may still be on their way: wait for them, within the limit
+    for (int j = issued < S ? 0 : issued - S; j < issued; ++j) (void)mbar_wait_bounded(&full[j % S], (j / S) & 1);
   }
   float* part = a.parts + (int64_t)blockIdx.x * a.cols;
   if constexpr (L == 0) {
@@ -275,9 +316,8 @@ __global__ __launch_bounds__(L ? kCta : WIDE ? kMaxThreads : kMaxThreads / 2) vo
       for (int i = 0; i < 4; ++i) q[i] = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
     }
   } else {
-    copy_wait<0>();
-    __syncthreads();  // the stages are free: every thread has taken its last row
-    float* fold = reinterpret_cast<float*>(stages);  // [sub][column], 16 KB
+    __syncthreads();  // the stages are free: every thread has done with its last row
+    float* fold = reinterpret_cast<float*>(ring);  // [sub][column], 16 KB
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
       fold[threadIdx.x * kUnit + 2 * i] = acc[i].x;
@@ -322,16 +362,23 @@ int64_t parts_of(int64_t rows, int64_t cols) {
   return groups < kMaxParts ? groups : kMaxParts;
 }
 
-template <int XT, bool SAVED, int L, bool WIDE>
-mp_status launch_bwd_rows(const NormBwd& a, const RowShape& s, int* parts, cudaStream_t st) {
+template <int XT, bool SAVED, int L, int MAXT>
+mp_status launch_bwd_rows(NormBwd a, const RowShape& s, int* parts, cudaStream_t st) {
   static std::atomic<uint64_t> opted{0};
   const int64_t groups = (a.rows + s.rows_per_cta - 1) / s.rows_per_cta;
-  using Stage = BwdStage<XT, SAVED>;
-  const int smem = Stage::kStages * Stage::kBytes * s.threads;  // at most 200 KB
-  if (!smem_ok(k_norm_bwd<XT, SAVED, L, WIDE>, smem, opted)) return MP_ECUDA;
-  const int grid = resident_grid(groups, kBwdThreads / s.threads);
+  const int bytes = stage_bytes<XT, SAVED>(s.rows_per_cta * a.cols, a.dh != nullptr);  // at most 192 KB
+  // as many CTAs on an SM as the registers allow (MAXT threads), and as many
+  // stages, up to kMaxStages, as the shared memory of so many then holds
+  int per_sm = MAXT / s.threads;
+  while (per_sm > 1 && 2 * bytes > kRingBytes / per_sm) --per_sm;
+  a.stages = kRingBytes / per_sm / bytes;
+  if (a.stages > kMaxStages) a.stages = kMaxStages;
+  int smem = a.stages * bytes;
+  if (L && smem < kCta * kUnit * 4) smem = kCta * kUnit * 4;  // the fold of the column sums
+  if (!smem_ok(k_norm_bwd<XT, SAVED, L, MAXT>, smem, opted)) return MP_ECUDA;
+  const int grid = resident_grid(groups, per_sm);
   *parts = grid < kMaxParts ? grid : kMaxParts;
-  launch_chained(k_norm_bwd<XT, SAVED, L, WIDE>, dim3(*parts), dim3(s.threads), smem, st, a);
+  launch_chained(k_norm_bwd<XT, SAVED, L, MAXT>, dim3(*parts), dim3(s.threads), smem, st, a);
   note_launches(1);
   return launch_status();
 }
@@ -341,11 +388,11 @@ mp_status launch_bwd(const NormBwd& a, void* dweight, int32_t dt, cudaStream_t s
   const RowShape s = row_shape(a.cols);
   int parts = 0;
   if (a.rows > 0) {
-    const mp_status r = s.lanes == 8    ? launch_bwd_rows<XT, SAVED, 8, false>(a, s, &parts, st)
-                        : s.lanes == 16 ? launch_bwd_rows<XT, SAVED, 16, false>(a, s, &parts, st)
-                        : s.lanes == 32 ? launch_bwd_rows<XT, SAVED, 32, false>(a, s, &parts, st)
-                        : s.threads <= kMaxThreads / 2 ? launch_bwd_rows<XT, SAVED, 0, false>(a, s, &parts, st)
-                                                       : launch_bwd_rows<XT, SAVED, 0, true>(a, s, &parts, st);
+    const mp_status r = s.lanes == 8       ? launch_bwd_rows<XT, SAVED, 8, 768>(a, s, &parts, st)
+                        : s.lanes == 16    ? launch_bwd_rows<XT, SAVED, 16, 768>(a, s, &parts, st)
+                        : s.lanes == 32    ? launch_bwd_rows<XT, SAVED, 32, 768>(a, s, &parts, st)
+                        : s.threads <= 768 ? launch_bwd_rows<XT, SAVED, 0, 768>(a, s, &parts, st)
+                                           : launch_bwd_rows<XT, SAVED, 0, 1024>(a, s, &parts, st);
     if (r != MP_OK) return r;
   }
   launch_chained(k_norm_dweight, dim3((a.cols + 31) / 32), dim3(32 * kFoldWarps), 0, st, (const float*)a.parts,
@@ -358,6 +405,13 @@ bool float_type(mp_dtype t) { return t == MP_F32 || t == MP_F16 || t == MP_BF16;
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 }  // namespace
+
+uint32_t norm_wait_failures() {
+  uint32_t v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_norm_wait_failures, sizeof(v)) != cudaSuccess) return 0xFFFFFFFFu;
+  return v;
+}
+
 }  // namespace mp
 
 extern "C" MP_API mp_status rmsnorm_residual_fp8(const void* x, const void* residual, mp_dtype x_dtype, int64_t rows,

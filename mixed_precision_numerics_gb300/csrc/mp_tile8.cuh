@@ -100,6 +100,11 @@ struct Unit {
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) st_cs(p + 16 * i, v[i]);
   }
+  // the same from shared memory
+  __device__ __forceinline__ void take(const unsigned char* base, int at) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) v[i] = ld_plain(base + at * (kBytes / kUnit) + 16 * i);
+  }
   __device__ __forceinline__ uint32_t word(int k) const {  // k a constant after unrolling
     const uint4 q = v[k >> 2];
     return (k & 3) == 0 ? q.x : (k & 3) == 1 ? q.y : (k & 3) == 2 ? q.z : q.w;
@@ -362,48 +367,6 @@ __device__ __forceinline__ void cast_store(const float2 (&y)[kPairs], const Fp8O
   uint8_t* const cc[1] = {nullptr};
   float* const cs[1] = {nullptr};
   cast_store<1, XT>(y, o, p, mc, raw, cc, cs, 0);
-}
-
-// ---------------------------------------------------------------------------
-// Per-thread asynchronous copies into shared memory: a thread fetches its own
-// units some rows ahead and is the only one to read them, so no barrier is
-// needed, only its own wait.
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {  // all but the newest N groups have landed
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-  uint4 r;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
-  return r;
-}
-__device__ __forceinline__ float lds_f32(uint32_t a) {
-  float r;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(r) : "r"(a) : "memory");
-  return r;
-}
-// A unit's 16-byte pieces lie `threads` slots of 16 bytes apart, so that a
-// warp's accesses are consecutive.
-template <int XT>
-__device__ __forceinline__ void copy_unit(uint32_t slot, int threads, const void* base, int64_t at) {
-  const unsigned char* p = static_cast<const unsigned char*>(base) + at * (Unit<XT>::kBytes / kUnit);
-#pragma unroll
-  for (int i = 0; i < Unit<XT>::kVecs; ++i) copy16(slot + i * threads * 16, p + 16 * i);
-}
-template <int XT>
-__device__ __forceinline__ Unit<XT> take_unit(uint32_t slot, int threads) {
-  Unit<XT> r;
-#pragma unroll
-  for (int i = 0; i < Unit<XT>::kVecs; ++i) r.v[i] = lds16(slot + i * threads * 16);
-  return r;
 }
 
 // Values of the 16 E4M3 codes of a unit times `scale`.
