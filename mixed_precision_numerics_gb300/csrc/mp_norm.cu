@@ -50,11 +50,11 @@ int resident_grid(int64_t groups, int per_sm) {
   return (int)(groups < most ? groups : most);
 }
 
-// Raises a kernel's dynamic shared-memory limit where a launch needs more than
-// the default 48 KB.
+// Raises a kernel's dynamic shared-memory limit where a launch may need more
+// than the default: 48 KB, the kernel's static arrays included.
 template <typename K>
 bool smem_ok(K kernel, int bytes, std::atomic<uint64_t>& done) {
-  return bytes <= 48 * 1024 || smem_opt_in(kernel, 224 * 1024, done);
+  return bytes <= 32 * 1024 || smem_opt_in(kernel, 224 * 1024, done);
 }
 
 // Sum over the threads that hold one row, in every one of them.
@@ -170,17 +170,20 @@ struct NormBwd {
   float* parts;
   int64_t rows;
   int32_t cols, tiles, wt;
-  int32_t stages;  // of the ring
+  int32_t stages;   // of the ring
+  bool stage_dh;    // whether dh comes through it
   float inv_cols;
 };
 
 constexpr int kMaxStages = 4;
+constexpr int kBwdThreads = 1024;  // resident on an SM, at 64 registers
 constexpr int kRingBytes = 216 * 1024;  // shared memory of an SM for the rings of the CTAs on it
 
 __device__ unsigned int g_norm_wait_failures;  // bounded waits that gave up (read by mp_wait_failures)
 
-// One stage of the ring: dy, then dh (if any), then the stream or its codes,
-// of one group of rows, each as it lies in memory.
+// One stage of the ring: dy, then dh (if any, and if a stage with it fits: FP32
+// rows of over 13824 without a checkpoint read it directly), then the stream
+// or its codes, of one group of rows, each as it lies in memory.
 template <int XT, bool SAVED>
 __host__ __device__ constexpr int stage_bytes(int elements, bool dh) {
   constexpr int es = XT == XF32 ? 4 : 2;
@@ -195,7 +198,7 @@ __host__ __device__ constexpr int stage_bytes(int elements, bool dh) {
 // registers over its rows (binary32, in row order) and the CTA writes one row
 // of `parts` at the end.  A thread whose wait gave up works on what it finds
 // and stores nothing more, but keeps meeting the barriers.
-template <int XT, bool SAVED, int L, int MAXT>
+template <int XT, bool SAVED, bool W32, int L, int MAXT>
 __global__ __launch_bounds__(MAXT) void k_norm_bwd(const __grid_constant__ NormBwd a) {
   extern __shared__ __align__(128) unsigned char ring[];
   __shared__ float slots[2][32];
@@ -206,8 +209,9 @@ __global__ __launch_bounds__(MAXT) void k_norm_bwd(const __grid_constant__ NormB
   const int uc = u < units ? u : units - 1;  // a lane past the row's end works on its last unit and stores nothing
   const int64_t step = (int64_t)gridDim.x * R;
   const int group = R * a.cols;  // elements
-  const int bytes = stage_bytes<XT, SAVED>(group, a.dh != nullptr);
-  const int at_v = group * es * (a.dh ? 2 : 1);  // where the stream lies in a stage
+  const bool ring_dh = a.dh && a.stage_dh;
+  const int bytes = stage_bytes<XT, SAVED>(group, ring_dh);
+  const int at_v = group * es * (ring_dh ? 2 : 1);  // where the stream lies in a stage
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
     fence_mbar_init();
@@ -220,9 +224,9 @@ __global__ __launch_bounds__(MAXT) void k_norm_bwd(const __grid_constant__ NormB
     const int64_t left = a.rows - row0, at = row0 * a.cols;
     const uint32_t n = (uint32_t)(left < R ? left : R) * a.cols;
     unsigned char* st = ring + s * bytes;
-    mbar_arrive_expect_tx(&full[s], n * es * (a.dh ? 2 : 1) + n * (SAVED ? 1 : es));
+    mbar_arrive_expect_tx(&full[s], n * es * (ring_dh ? 2 : 1) + n * (SAVED ? 1 : es));
     bulk_g2s(st, static_cast<const char*>(a.dy) + at * es, n * es, &full[s], policy);
-    if (a.dh) bulk_g2s(st + group * es, static_cast<const char*>(a.dh) + at * es, n * es, &full[s], policy);
+    if (ring_dh) bulk_g2s(st + group * es, static_cast<const char*>(a.dh) + at * es, n * es, &full[s], policy);
     if constexpr (SAVED)
       bulk_g2s(st + at_v, a.codes + at, n, &full[s], policy);
     else
@@ -232,6 +236,24 @@ __global__ __launch_bounds__(MAXT) void k_norm_bwd(const __grid_constant__ NormB
   int issued = 0;  // fills so far, in thread 0; fill j is of stage j % S
   if (threadIdx.x == 0)
     for (; issued < S && row0 + issued * step < a.rows; ++issued) fetch(issued, row0 + issued * step);
+  // The weights in shared memory, as they are where they have the rows' 16-bit
+  // type, else in binary32.
+  unsigned char* wslots = ring + S * bytes;
+  if (u < units && sub == 0) {
+    Weights w;
+    w.load(a.weight, a.wt, u);
+    if constexpr (W32) {
+      Unit<XF32> f;
+      float2 ff[kPairs];
+      w.floats(a.wt, ff);
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) f.set_pair(i, ff[i]);
+      for (int i = 0; i < 4; ++i) reinterpret_cast<uint4*>(wslots)[u * 4 + i] = f.v[i];
+    } else {
+      for (int i = 0; i < 2; ++i) reinterpret_cast<uint4*>(wslots)[u * 2 + i] = w.v[i];
+    }
+  }
+  __syncthreads();
   float2 acc[kPairs];
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) acc[i] = both(0.0f);
@@ -258,29 +280,32 @@ __global__ __launch_bounds__(MAXT) void k_norm_bwd(const __grid_constant__ NormB
     // a row past the end works on the group's first, whose copy is there
     const unsigned char* st = ring + s * bytes;
     const int e = (live ? sub : 0) * a.cols + uc * kUnit;
-    float2 xh[kPairs], g[kPairs], dot = both(0.0f);
-    if constexpr (SAVED) {
-      e4m3_floats(*reinterpret_cast<const uint4*>(st + at_v + e), scale * rstd, xh);
-    } else {
-      Unit<XT> v;
-      v.take(st + at_v, e);
-      v.floats(xh);
+    // Half a unit at a time, and the stream's values once more after the sum:
+    // only the column sums and dy * w stay in registers across the barrier.
+    float2 g[kPairs], dot = both(0.0f);
+    uint4 code;
+    Unit<XT> dy, v, w;
+    const float vs = SAVED ? scale * rstd : rstd;
+    if constexpr (SAVED) code = lds16(st + at_v + e);
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) xh[i] = mul2(xh[i], both(rstd));
-    }
-    {
-      Unit<XT> dy;
-      dy.take(st, e);
-      Weights ww;
-      ww.load(a.weight, a.wt, uc);
-      float2 w[kPairs];
-      ww.floats(a.wt, w);
-      dy.floats(g);
+    for (int half = 0; half < 2; ++half) {
+      dy.take_half(st, e, half);
+      if constexpr (!SAVED) v.take_half(st + at_v, e, half);
+      Unit<XF32> w32;
+      if constexpr (W32)
+        w32.take_half(wslots, uc * kUnit, half);
+      else
+        w.take_half(wslots, uc * kUnit, half);
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
-        if (L == 0 || live) acc[i] = fma2(g[i], xh[i], acc[i]);
-        g[i] = mul2(g[i], w[i]);
-        dot = fma2(g[i], xh[i], dot);
+      for (int i = half * (kPairs / 2); i < (half + 1) * (kPairs / 2); ++i) {
+        float2 x;
+        if constexpr (SAVED)
+          x = e4m3_pair(code, i, vs);
+        else
+          x = mul2(v.pair(i), both(vs));
+        if (L == 0 || live) acc[i] = fma2(dy.pair(i), x, acc[i]);
+        g[i] = mul2(dy.pair(i), W32 ? w32.pair(i) : w.pair(i));
+        dot = fma2(g[i], x, dot);
       }
     }
     const float c = row_sum<L>(u < units ? dot.x + dot.y : 0.0f, slots[it & 1]) * a.inv_cols;
@@ -289,13 +314,28 @@ __global__ __launch_bounds__(MAXT) void k_norm_bwd(const __grid_constant__ NormB
       fetch(s == 0 ? S - 1 : s - 1, row0 + (S - 1) * step);
       ++issued;
     }
+    const bool out = ok && live && u < units;
     Unit<XT> o;
     o.zero();
-    if (a.dh) o.take(st + group * es, e);
+    if constexpr (SAVED) code = lds16(st + at_v + e);
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i)
-      o.set_pair(i, fma2(fma2(xh[i], both(-c), g[i]), both(rstd), o.pair(i)));
-    if (ok && live && u < units) o.store(a.dx, row * a.cols + u * kUnit);
+    for (int half = 0; half < 2; ++half) {
+      if (ring_dh)
+        o.take_half(st + group * es, e, half);
+      else if (a.dh && out)
+        o.load_half(a.dh, row * a.cols + u * kUnit, half);
+      if constexpr (!SAVED) v.take_half(st + at_v, e, half);
+#pragma unroll
+      for (int i = half * (kPairs / 2); i < (half + 1) * (kPairs / 2); ++i) {
+        float2 x;
+        if constexpr (SAVED)
+          x = e4m3_pair(code, i, vs);
+        else
+          x = mul2(v.pair(i), both(vs));
+        o.set_pair(i, fma2(fma2(x, both(-c), g[i]), both(rstd), o.pair(i)));
+      }
+      if (out) o.store_half(a.dx, row * a.cols + u * kUnit, half);
+    }
     if (S == 1) {
       __syncthreads();
       if (threadIdx.x == 0 && ok && row0 + step < a.rows) {
@@ -343,8 +383,9 @@ __global__ __launch_bounds__(32 * kFoldWarps) void k_norm_dweight(const float* p
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
   float v = 0.0f;
   if (col < cols) {
-#pragma unroll 4
-    for (int p = warp; p < nparts; p += kFoldWarps) v += parts[(int64_t)p * cols + col];
+#pragma unroll
+    for (int p = 0; p < kMaxParts / kFoldWarps; ++p)  // all of them in flight at once
+      if (warp + p * kFoldWarps < nparts) v += parts[(int64_t)(warp + p * kFoldWarps) * cols + col];
   }
   s[warp][lane] = v;
   __syncthreads();
@@ -362,37 +403,47 @@ int64_t parts_of(int64_t rows, int64_t cols) {
   return groups < kMaxParts ? groups : kMaxParts;
 }
 
-template <int XT, bool SAVED, int L, int MAXT>
+template <int XT, bool SAVED, bool W32, int L, int MAXT>
 mp_status launch_bwd_rows(NormBwd a, const RowShape& s, int* parts, cudaStream_t st) {
   static std::atomic<uint64_t> opted{0};
   const int64_t groups = (a.rows + s.rows_per_cta - 1) / s.rows_per_cta;
-  const int bytes = stage_bytes<XT, SAVED>(s.rows_per_cta * a.cols, a.dh != nullptr);  // at most 192 KB
-  // as many CTAs on an SM as the registers allow (MAXT threads), and as many
-  // stages, up to kMaxStages, as the shared memory of so many then holds
+  const int weights = a.cols * (W32 ? 4 : 2), elements = s.rows_per_cta * a.cols;
+  a.stage_dh = a.dh && stage_bytes<XT, SAVED>(elements, true) + weights <= kRingBytes;
+  const int bytes = stage_bytes<XT, SAVED>(elements, a.stage_dh);  // with the weights at most 213 KB
+  // as many CTAs on an SM as the registers allow, if each has two stages, and
+  // as many stages, up to kMaxStages, as shared memory then holds
   int per_sm = MAXT / s.threads;
-  while (per_sm > 1 && 2 * bytes > kRingBytes / per_sm) --per_sm;
-  a.stages = kRingBytes / per_sm / bytes;
+  while (per_sm > 1 && 2 * bytes + weights > kRingBytes / per_sm) --per_sm;
+  a.stages = (kRingBytes / per_sm - weights) / bytes;
   if (a.stages > kMaxStages) a.stages = kMaxStages;
-  int smem = a.stages * bytes;
+  int smem = a.stages * bytes + weights;
   if (L && smem < kCta * kUnit * 4) smem = kCta * kUnit * 4;  // the fold of the column sums
-  if (!smem_ok(k_norm_bwd<XT, SAVED, L, MAXT>, smem, opted)) return MP_ECUDA;
+  if (!smem_ok(k_norm_bwd<XT, SAVED, W32, L, MAXT>, smem, opted)) return MP_ECUDA;
   const int grid = resident_grid(groups, per_sm);
   *parts = grid < kMaxParts ? grid : kMaxParts;
-  launch_chained(k_norm_bwd<XT, SAVED, L, MAXT>, dim3(*parts), dim3(s.threads), smem, st, a);
+  launch_chained(k_norm_bwd<XT, SAVED, W32, L, MAXT>, dim3(*parts), dim3(s.threads), smem, st, a);
   note_launches(1);
   return launch_status();
 }
 
+template <int XT, bool SAVED, bool W32>
+mp_status launch_bwd_shape(const NormBwd& a, int* parts, cudaStream_t st) {
+  const RowShape s = row_shape(a.cols);
+  if (s.lanes == 8) return launch_bwd_rows<XT, SAVED, W32, 8, kBwdThreads>(a, s, parts, st);
+  if (s.lanes == 16) return launch_bwd_rows<XT, SAVED, W32, 16, kBwdThreads>(a, s, parts, st);
+  if (s.lanes == 32) return launch_bwd_rows<XT, SAVED, W32, 32, kBwdThreads>(a, s, parts, st);
+  return launch_bwd_rows<XT, SAVED, W32, 0, kBwdThreads>(a, s, parts, st);
+}
+
 template <int XT, bool SAVED>
 mp_status launch_bwd(const NormBwd& a, void* dweight, int32_t dt, cudaStream_t st) {
-  const RowShape s = row_shape(a.cols);
   int parts = 0;
   if (a.rows > 0) {
-    const mp_status r = s.lanes == 8       ? launch_bwd_rows<XT, SAVED, 8, 768>(a, s, &parts, st)
-                        : s.lanes == 16    ? launch_bwd_rows<XT, SAVED, 16, 768>(a, s, &parts, st)
-                        : s.lanes == 32    ? launch_bwd_rows<XT, SAVED, 32, 768>(a, s, &parts, st)
-                        : s.threads <= 768 ? launch_bwd_rows<XT, SAVED, 0, 768>(a, s, &parts, st)
-                                           : launch_bwd_rows<XT, SAVED, 0, 1024>(a, s, &parts, st);
+    mp_status r;
+    if constexpr (XT == XF32)
+      r = launch_bwd_shape<XT, SAVED, true>(a, &parts, st);
+    else
+      r = a.wt == XT ? launch_bwd_shape<XT, SAVED, false>(a, &parts, st) : launch_bwd_shape<XT, SAVED, true>(a, &parts, st);
     if (r != MP_OK) return r;
   }
   launch_chained(k_norm_dweight, dim3((a.cols + 31) / 32), dim3(32 * kFoldWarps), 0, st, (const float*)a.parts,

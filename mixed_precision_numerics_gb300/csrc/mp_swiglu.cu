@@ -114,8 +114,11 @@ __global__ __launch_bounds__(kThreads) void k_swiglu_bwd(const __grid_constant__
     const uint4 gc = ld_cs(a.codes + p.at), uc = ld_cs(a.codes + a.rows * a.cols + p.at);
     const float gs = __ldcs(a.scales + st), us = __ldcs(a.scales + a.rows * a.tiles.d + st);
     dr.load(a.dp, p.at);
-    e4m3_floats(gc, gs, g);
-    e4m3_floats(uc, us, u);
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) {
+      g[k] = e4m3_pair(gc, k, gs);
+      u[k] = e4m3_pair(uc, k, us);
+    }
   } else {
     Unit<XT> gr, ur;
     const int64_t at = p.row * a.ld + p.u * kUnit;

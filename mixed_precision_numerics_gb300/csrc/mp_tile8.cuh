@@ -76,6 +76,16 @@ __device__ __forceinline__ uint32_t div_by(uint32_t n, const FastDiv& f) {
   return (uint32_t)(((uint64_t)n * f.mul) >> 31) >> f.shift;
 }
 
+// 16 bytes of shared memory, read where this is written and not kept.
+__device__ __forceinline__ uint4 lds16(const void* p) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "r"(smem_u32(p))
+               : "memory");
+  return r;
+}
+
 // ---------------------------------------------------------------------------
 // One unit as loaded: 16 elements of type XT.
 // ---------------------------------------------------------------------------
@@ -100,10 +110,20 @@ struct Unit {
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) st_cs(p + 16 * i, v[i]);
   }
-  // the same from shared memory
-  __device__ __forceinline__ void take(const unsigned char* base, int at) {
+  // half (0 or 1) of the unit at element `at` of shared memory: 8 elements
+  __device__ __forceinline__ void take_half(const unsigned char* base, int at, int half) {
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) v[i] = ld_plain(base + at * (kBytes / kUnit) + 16 * i);
+    for (int i = half * (kVecs / 2); i < (half + 1) * (kVecs / 2); ++i) v[i] = lds16(base + at * (kBytes / kUnit) + 16 * i);
+  }
+  __device__ __forceinline__ void load_half(const void* base, int64_t at, int half) {
+    const unsigned char* p = static_cast<const unsigned char*>(base) + at * (kBytes / kUnit);
+#pragma unroll
+    for (int i = half * (kVecs / 2); i < (half + 1) * (kVecs / 2); ++i) v[i] = ld_cs(p + 16 * i);
+  }
+  __device__ __forceinline__ void store_half(void* base, int64_t at, int half) const {
+    unsigned char* p = static_cast<unsigned char*>(base) + at * (kBytes / kUnit);
+#pragma unroll
+    for (int i = half * (kVecs / 2); i < (half + 1) * (kVecs / 2); ++i) st_cs(p + 16 * i, v[i]);
   }
   __device__ __forceinline__ uint32_t word(int k) const {  // k a constant after unrolling
     const uint4 q = v[k >> 2];
@@ -174,7 +194,7 @@ struct Unit {
 };
 
 // 16 weights of a vector of any of the three types (a uniform branch), as
-// loaded.  The vector is read again for every row: default caching keeps it in L1.
+// stored.  The vector is read again for every row: default caching keeps it in L1.
 struct Weights {
   uint4 v[4];
   __device__ __forceinline__ void load(const void* w, int wt, int u) {
@@ -369,16 +389,12 @@ __device__ __forceinline__ void cast_store(const float2 (&y)[kPairs], const Fp8O
   cast_store<1, XT>(y, o, p, mc, raw, cc, cs, 0);
 }
 
-// Values of the 16 E4M3 codes of a unit times `scale`.
-__device__ __forceinline__ void e4m3_floats(uint4 c, float scale, float2 (&f)[kPairs]) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-  for (int k = 0; k < kPairs; ++k) {
-    const unsigned short two = (unsigned short)(w[k >> 1] >> (16 * (k & 1)));
-    uint32_t h2;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(two));
-    f[k] = mul2(make_float2(f16lo(h2), f16hi(h2)), both(scale));
-  }
+// Values of E4M3 codes 2k and 2k + 1 of a unit times `scale`.
+__device__ __forceinline__ float2 e4m3_pair(const uint4& c, int k, float scale) {
+  const uint32_t w = (k >> 1) == 0 ? c.x : (k >> 1) == 1 ? c.y : (k >> 1) == 2 ? c.z : c.w;
+  uint32_t h2;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((unsigned short)(w >> (16 * (k & 1)))));
+  return mul2(make_float2(f16lo(h2), f16hi(h2)), both(scale));
 }
 
 // Sum of one value per thread over the CTA's warps, in a fixed order, in every
