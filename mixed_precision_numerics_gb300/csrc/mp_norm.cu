@@ -57,16 +57,23 @@ bool smem_ok(K kernel, int bytes, std::atomic<uint64_t>& done) {
   return bytes <= 32 * 1024 || smem_opt_in(kernel, 224 * 1024, done);
 }
 
-// Sum over the threads that hold one row, in every one of them.
+// Sum over the L lanes that hold one row, in every one of them.
 template <int L>
-__device__ __forceinline__ float row_sum(float v, float* slot) {
-  if constexpr (L == 0) {
-    return block_sum(v, slot);
-  } else {
+__device__ __forceinline__ float lane_sum(float v) {
 #pragma unroll
-    for (int d = L / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-    return v;
-  }
+  for (int d = L / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+  return v;
+}
+// Sum over the `threads` of a team (whole warps; t the thread's place in it),
+// in a fixed order, in every one of them.  `slot` (a float for each warp) must
+// not be written again before every thread has passed the next barrier:
+// callers alternate between two.
+__device__ __forceinline__ float team_sum(float v, float* slot, int barrier, int t, int threads) {
+  v = lane_sum<32>(v);
+  const int lane = t & 31;
+  if (lane == 0) slot[t >> 5] = v;
+  named_barrier(barrier, threads);
+  return lane_sum<32>(lane < (threads >> 5) ? slot[lane] : 0.0f);
 }
 
 // ---------------------------------------------------------------------------
@@ -120,7 +127,8 @@ __global__ __launch_bounds__(L ? kCta : kMaxThreads) void k_norm_fwd(const __gri
     ss = fma2(f, f, ss);
     if constexpr (SAVE) amax = max3_abs_nan(amax, f.x, f.y);
   }
-  const float sum = row_sum<L>(ss.x + ss.y, slots);
+  const float part = ss.x + ss.y;
+  const float sum = L ? lane_sum<L ? L : 1>(part) : team_sum(part, slots, 1, threadIdx.x, blockDim.x);
   const float rstd = rsqrtf(fmaf(sum, a.inv_cols, a.eps));
   if (u == 0 && p.in && a.rstd) a.rstd[row] = rstd;
   float2 y[kPairs];
@@ -170,13 +178,14 @@ struct NormBwd {
   float* parts;
   int64_t rows;
   int32_t cols, tiles, wt;
-  int32_t stages;   // of the ring
+  int32_t team;     // threads of a team
+  int32_t stages;   // of its ring
   bool stage_dh;    // whether dh comes through it
   float inv_cols;
 };
 
 constexpr int kMaxStages = 4;
-constexpr int kBwdThreads = 1024;  // resident on an SM, at 64 registers
+constexpr int kMaxTeams = 8;     // a named barrier each
 constexpr int kRingBytes = 216 * 1024;  // shared memory of an SM for the rings of the CTAs on it
 
 __device__ unsigned int g_norm_wait_failures;  // bounded waits that gave up (read by mp_wait_failures)
@@ -190,39 +199,49 @@ __host__ __device__ constexpr int stage_bytes(int elements, bool dh) {
   return elements * (es + (dh ? es : 0) + (SAVED ? 1 : es));
 }
 
-// CTA c takes row groups c, c + gridDim.x, ...  One thread keeps the ring of
-// `stages` groups filled with bulk copies (a group's rows are consecutive in
-// memory, so a group is two or three copies).  The barrier of a group's sum
-// also tells that every thread has done with the group before, whose stage is
-// then filled again.  Each thread keeps the sums of its own columns in
-// registers over its rows (binary32, in row order) and the CTA writes one row
-// of `parts` at the end.  A thread whose wait gave up works on what it finds
-// and stores nothing more, but keeps meeting the barriers.
-template <int XT, bool SAVED, bool W32, int L, int MAXT>
-__global__ __launch_bounds__(MAXT) void k_norm_bwd(const __grid_constant__ NormBwd a) {
-  extern __shared__ __align__(128) unsigned char ring[];
-  __shared__ float slots[2][32];
-  __shared__ uint64_t full[kMaxStages];
+// A CTA holds `teams` of threads (as many as the SM's registers take, where a
+// row needs a whole team; one, where rows lie in a warp's lanes).  A team takes
+// every (gridDim.x * teams)-th group of rows.  Its first thread keeps the
+// team's ring of `stages` groups filled with bulk copies (a group's rows are
+// consecutive in memory, so a group is two or three copies).  The barrier of a
+// group's sum also tells that every thread of the team has done with the group
+// before, whose stage is then filled again.  Each thread keeps the sums of its
+// own columns in registers over its rows (binary32, in row order); at the end
+// the CTA joins its teams' sums and writes one row of `parts`.  A thread whose
+// wait gave up works on what it finds and stores nothing more, but keeps
+// meeting the barriers.
+template <int XT, bool SAVED, bool W32, int L>
+__global__ __launch_bounds__(L ? kCta : kMaxThreads) void k_norm_bwd(const __grid_constant__ NormBwd a) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ float slots[2 * 32];
+  __shared__ uint64_t bars[kMaxTeams * kMaxStages];
   constexpr int R = L ? kCta / L : 1, es = XT == XF32 ? 4 : 2;
   const int units = a.cols / kUnit, S = a.stages;
-  const int u = L ? threadIdx.x % (L ? L : 1) : threadIdx.x, sub = L ? threadIdx.x / (L ? L : 1) : 0;
+  const int T = L ? kCta : a.team;
+  const int team = L ? 0 : __shfl_sync(0xFFFFFFFFu, threadIdx.x / T, 0);  // the same in a warp, and known to be
+  const int t = L ? threadIdx.x : threadIdx.x - team * T;
+  const int u = L ? threadIdx.x % (L ? L : 1) : t, sub = L ? threadIdx.x / (L ? L : 1) : 0;
   const int uc = u < units ? u : units - 1;  // a lane past the row's end works on its last unit and stores nothing
-  const int64_t step = (int64_t)gridDim.x * R;
   const int group = R * a.cols;  // elements
   const bool ring_dh = a.dh && a.stage_dh;
   const int bytes = stage_bytes<XT, SAVED>(group, ring_dh);
   const int at_v = group * es * (ring_dh ? 2 : 1);  // where the stream lies in a stage
-  if (threadIdx.x == 0) {
+  unsigned char* const ring = smem + a.cols * (W32 ? 4 : 2) + team * S * bytes;
+  uint64_t* const full = bars + team * kMaxStages;
+  float* const slot = slots + team * (T >> 5);
+  if (t == 0) {
     for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
     fence_mbar_init();
   }
   __syncthreads();
   chain_wait();
   chain_release();
-  const uint64_t policy = policy_evict_first();
-  auto fetch = [&](int s, int64_t row0) {  // one thread
-    const int64_t left = a.rows - row0, at = row0 * a.cols;
-    const uint32_t n = (uint32_t)(left < R ? left : R) * a.cols;
+  const int32_t step = gridDim.x * (L ? R : blockDim.x / T);  // rows
+  int32_t row0 = (team * gridDim.x + blockIdx.x) * R;
+  auto fetch = [&](int s, int32_t row0) {  // one thread of the team
+    const uint64_t policy = policy_evict_first();
+    const int64_t at = (int64_t)row0 * a.cols;
+    const uint32_t n = (uint32_t)min((int32_t)a.rows - row0, R) * a.cols;
     unsigned char* st = ring + s * bytes;
     mbar_arrive_expect_tx(&full[s], n * es * (ring_dh ? 2 : 1) + n * (SAVED ? 1 : es));
     bulk_g2s(st, static_cast<const char*>(a.dy) + at * es, n * es, &full[s], policy);
@@ -232,25 +251,25 @@ __global__ __launch_bounds__(MAXT) void k_norm_bwd(const __grid_constant__ NormB
     else
       bulk_g2s(st + at_v, static_cast<const char*>(a.h) + at * es, n * es, &full[s], policy);
   };
-  int64_t row0 = (int64_t)blockIdx.x * R;
-  int issued = 0;  // fills so far, in thread 0; fill j is of stage j % S
-  if (threadIdx.x == 0)
-    for (; issued < S && row0 + issued * step < a.rows; ++issued) fetch(issued, row0 + issued * step);
+  int issued = 0;  // fills so far, in the fetching thread; fill j is of stage j % S
+  const int64_t rows = a.rows;
+  if (t == 0)
+    for (; issued < S && row0 + (int64_t)issued * step < rows; ++issued) fetch(issued, row0 + issued * step);
   // The weights in shared memory, as they are where they have the rows' 16-bit
   // type, else in binary32.
-  unsigned char* wslots = ring + S * bytes;
-  if (u < units && sub == 0) {
+  if (threadIdx.x < units) {
     Weights w;
-    w.load(a.weight, a.wt, u);
+    w.load(a.weight, a.wt, threadIdx.x);
+    uint4* ws = reinterpret_cast<uint4*>(smem) + threadIdx.x * (W32 ? 4 : 2);
     if constexpr (W32) {
       Unit<XF32> f;
       float2 ff[kPairs];
       w.floats(a.wt, ff);
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) f.set_pair(i, ff[i]);
-      for (int i = 0; i < 4; ++i) reinterpret_cast<uint4*>(wslots)[u * 4 + i] = f.v[i];
+      for (int i = 0; i < 4; ++i) ws[i] = f.v[i];
     } else {
-      for (int i = 0; i < 2; ++i) reinterpret_cast<uint4*>(wslots)[u * 2 + i] = w.v[i];
+      ws[0] = w.v[0], ws[1] = w.v[1];
     }
   }
   __syncthreads();
@@ -260,19 +279,18 @@ __global__ __launch_bounds__(MAXT) void k_norm_bwd(const __grid_constant__ NormB
   bool ok = true;
   // The row's two scalars are read one group ahead.
   auto scalars = [&](int64_t row, float* rstd, float* scale) {
-    const int64_t r = row < a.rows ? row : a.rows - 1;
-    *rstd = a.rstd[r];
-    *scale = SAVED ? a.scales[r * a.tiles + uc / kTileLanes] : 0.0f;
+    row = min(row, rows - 1);
+    *rstd = a.rstd[row];
+    *scale = SAVED ? a.scales[row * a.tiles + uc / kTileLanes] : 0.0f;
   };
   float rstd, scale, next_rstd, next_scale;
   scalars(row0 + sub, &next_rstd, &next_scale);
   int s = 0;
   uint32_t phase = 0;
-  for (int it = 0; row0 < a.rows; row0 += step, ++it) {
-    const int64_t row = row0 + sub;
-    const bool live = row < a.rows;
+  for (int it = 0; row0 < rows; ++it) {
+    const bool live = L == 0 || row0 + sub < rows;
     rstd = next_rstd, scale = next_scale;
-    scalars(row + step, &next_rstd, &next_scale);
+    scalars((int64_t)row0 + step + sub, &next_rstd, &next_scale);
     if (ok && !mbar_wait_bounded(&full[s], phase)) {
       ok = false;
       atomicAdd(&g_norm_wait_failures, 1u);
@@ -280,8 +298,8 @@ __global__ __launch_bounds__(MAXT) void k_norm_bwd(const __grid_constant__ NormB
     // a row past the end works on the group's first, whose copy is there
     const unsigned char* st = ring + s * bytes;
     const int e = (live ? sub : 0) * a.cols + uc * kUnit;
-    // Half a unit at a time, and the stream's values once more after the sum:
-    // only the column sums and dy * w stay in registers across the barrier.
+    // Half a unit at a time: across the barrier stay the column sums, dy * w,
+    // and a checkpoint's codes.
     float2 g[kPairs], dot = both(0.0f);
     uint4 code;
     Unit<XT> dy, v, w;
@@ -293,82 +311,75 @@ __global__ __launch_bounds__(MAXT) void k_norm_bwd(const __grid_constant__ NormB
       if constexpr (!SAVED) v.take_half(st + at_v, e, half);
       Unit<XF32> w32;
       if constexpr (W32)
-        w32.take_half(wslots, uc * kUnit, half);
+        w32.take_half(smem, uc * kUnit, half);
       else
-        w.take_half(wslots, uc * kUnit, half);
+        w.take_half(smem, uc * kUnit, half);
 #pragma unroll
       for (int i = half * (kPairs / 2); i < (half + 1) * (kPairs / 2); ++i) {
-        float2 x;
-        if constexpr (SAVED)
-          x = e4m3_pair(code, i, vs);
-        else
-          x = mul2(v.pair(i), both(vs));
-        if (L == 0 || live) acc[i] = fma2(dy.pair(i), x, acc[i]);
+        const float2 x = mul2(SAVED ? e4m3_floats(code, i) : v.pair(i), both(vs));
+        if (live) acc[i] = fma2(dy.pair(i), x, acc[i]);
         g[i] = mul2(dy.pair(i), W32 ? w32.pair(i) : w.pair(i));
         dot = fma2(g[i], x, dot);
       }
     }
-    const float c = row_sum<L>(u < units ? dot.x + dot.y : 0.0f, slots[it & 1]) * a.inv_cols;
-    if constexpr (L != 0) __syncthreads();
-    if (threadIdx.x == 0 && ok && S > 1 && it > 0 && row0 + (S - 1) * step < a.rows) {
+    float c = u < units ? dot.x + dot.y : 0.0f;
+    if constexpr (L != 0) {
+      c = lane_sum<L>(c);
+      __syncthreads();
+    } else {
+      c = team_sum(c, slot + (it & 1) * 32, team + 1, t, T);
+    }
+    if (t == 0 && ok && S > 1 && it > 0 && row0 + (int64_t)(S - 1) * step < rows) {
       fetch(s == 0 ? S - 1 : s - 1, row0 + (S - 1) * step);
       ++issued;
     }
+    const float k = -c * a.inv_cols * rstd * vs;
     const bool out = ok && live && u < units;
+    const int64_t at = (int64_t)(row0 + sub) * a.cols + u * kUnit;
     Unit<XT> o;
     o.zero();
-    if constexpr (SAVED) code = lds16(st + at_v + e);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       if (ring_dh)
         o.take_half(st + group * es, e, half);
       else if (a.dh && out)
-        o.load_half(a.dh, row * a.cols + u * kUnit, half);
+        o.load_half(a.dh, at, half);
       if constexpr (!SAVED) v.take_half(st + at_v, e, half);
 #pragma unroll
       for (int i = half * (kPairs / 2); i < (half + 1) * (kPairs / 2); ++i) {
-        float2 x;
-        if constexpr (SAVED)
-          x = e4m3_pair(code, i, vs);
-        else
-          x = mul2(v.pair(i), both(vs));
-        o.set_pair(i, fma2(fma2(x, both(-c), g[i]), both(rstd), o.pair(i)));
+        const float2 x = SAVED ? e4m3_floats(code, i) : v.pair(i);
+        o.set_pair(i, fma2(g[i], both(rstd), fma2(x, both(k), o.pair(i))));
       }
-      if (out) o.store_half(a.dx, row * a.cols + u * kUnit, half);
+      if (out) o.store_half(a.dx, at, half);
     }
-    if (S == 1) {
+    if (S == 1) {  // one team
       __syncthreads();
-      if (threadIdx.x == 0 && ok && row0 + step < a.rows) {
+      if (t == 0 && ok && row0 + (int64_t)step < rows) {
         fetch(0, row0 + step);
         ++issued;
       }
     }
     if (++s == S) s = 0, phase ^= 1;
+    if (row0 + (int64_t)step >= rows) break;  // before the sum could pass 32 bits
+    row0 += step;
   }
-  if (!ok && threadIdx.x == 0) {  // copies may still be on their way: wait for them, within the limit
+  if (!ok && t == 0) {  // copies may still be on their way: wait for them, within the limit
     for (int j = issued < S ? 0 : issued - S; j < issued; ++j) (void)mbar_wait_bounded(&full[j % S], (j / S) & 1);
   }
-  float* part = a.parts + (int64_t)blockIdx.x * a.cols;
-  if constexpr (L == 0) {
-    if (u < units) {
-      float4* q = reinterpret_cast<float4*>(part + u * kUnit);
+  __syncthreads();  // the rings are free: every team has done with its last row
+  float* fold = reinterpret_cast<float*>(smem);  // [team or sub-row][columns]
+  const int width = L ? L * kUnit : a.cols, deep = L ? R : blockDim.x / T;
+  if (L || u < units) {
+    float* f = fold + (L ? sub : team) * width + u * kUnit;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) q[i] = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
-    }
-  } else {
-    __syncthreads();  // the stages are free: every thread has done with its last row
-    float* fold = reinterpret_cast<float*>(ring);  // [sub][column], 16 KB
-#pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      fold[threadIdx.x * kUnit + 2 * i] = acc[i].x;
-      fold[threadIdx.x * kUnit + 2 * i + 1] = acc[i].y;
-    }
-    __syncthreads();
-    for (int col = threadIdx.x; col < a.cols; col += kCta) {
-      float s = 0.0f;
-      for (int j = 0; j < R; ++j) s += fold[j * (L * kUnit) + col];
-      part[col] = s;
-    }
+    for (int i = 0; i < kPairs; i += 2)
+      *reinterpret_cast<float4*>(f + 2 * i) = make_float4(acc[i].x, acc[i].y, acc[i + 1].x, acc[i + 1].y);
+  }
+  __syncthreads();
+  for (int col = threadIdx.x; col < a.cols; col += blockDim.x) {
+    float v = 0.0f;
+    for (int j = 0; j < deep; ++j) v += fold[j * width + col];
+    a.parts[(int64_t)blockIdx.x * a.cols + col] = v;
   }
 }
 
@@ -389,7 +400,7 @@ __global__ __launch_bounds__(32 * kFoldWarps) void k_norm_dweight(const float* p
   }
   s[warp][lane] = v;
   __syncthreads();
-  v = warp_sum(s[lane][warp]);  // warp w joins the 32 sums of column w
+  v = lane_sum<32>(s[lane][warp]);  // warp w joins the 32 sums of column w
   const int out = blockIdx.x * 32 + warp;
   if (lane != 0 || out >= cols) return;
   if (dt == XF32)
@@ -403,25 +414,31 @@ int64_t parts_of(int64_t rows, int64_t cols) {
   return groups < kMaxParts ? groups : kMaxParts;
 }
 
-template <int XT, bool SAVED, bool W32, int L, int MAXT>
+template <int XT, bool SAVED, bool W32, int L>
 mp_status launch_bwd_rows(NormBwd a, const RowShape& s, int* parts, cudaStream_t st) {
   static std::atomic<uint64_t> opted{0};
   const int64_t groups = (a.rows + s.rows_per_cta - 1) / s.rows_per_cta;
   const int weights = a.cols * (W32 ? 4 : 2), elements = s.rows_per_cta * a.cols;
   a.stage_dh = a.dh && stage_bytes<XT, SAVED>(elements, true) + weights <= kRingBytes;
   const int bytes = stage_bytes<XT, SAVED>(elements, a.stage_dh);  // with the weights at most 213 KB
-  // as many CTAs on an SM as the registers allow, if each has two stages, and
-  // as many stages, up to kMaxStages, as shared memory then holds
-  int per_sm = MAXT / s.threads;
-  while (per_sm > 1 && 2 * bytes + weights > kRingBytes / per_sm) --per_sm;
-  a.stages = (kRingBytes / per_sm - weights) / bytes;
+  // Rows of whole teams: as many teams as the registers allow, if each has two
+  // stages, and no more than spread the rows over all SMs.  Rows in lanes: as
+  // many CTAs.  Then as many stages, up to kMaxStages, as shared memory holds.
+  int per_sm = kMaxThreads / s.threads;
+  if (per_sm > kMaxTeams) per_sm = kMaxTeams;
+  while (per_sm > 1 && (2 * bytes + (L ? weights : 0)) * per_sm + weights > kRingBytes) --per_sm;
+  const int64_t spread = (groups + sm_count() - 1) / sm_count();
+  const int teams = L ? 1 : (int)(per_sm < spread ? per_sm : spread);
+  a.team = s.threads;
+  a.stages = ((L ? kRingBytes / per_sm : kRingBytes) - weights) / (bytes * teams);
   if (a.stages > kMaxStages) a.stages = kMaxStages;
-  int smem = a.stages * bytes + weights;
-  if (L && smem < kCta * kUnit * 4) smem = kCta * kUnit * 4;  // the fold of the column sums
-  if (!smem_ok(k_norm_bwd<XT, SAVED, W32, L, MAXT>, smem, opted)) return MP_ECUDA;
-  const int grid = resident_grid(groups, per_sm);
+  int smem = weights + teams * a.stages * bytes;
+  const int fold = (L ? kCta * kUnit : teams * a.cols) * 4;  // the join of the column sums
+  if (smem < fold) smem = fold;
+  if (!smem_ok(k_norm_bwd<XT, SAVED, W32, L>, smem, opted)) return MP_ECUDA;
+  const int grid = resident_grid((groups + teams - 1) / teams, L ? per_sm : 1);
   *parts = grid < kMaxParts ? grid : kMaxParts;
-  launch_chained(k_norm_bwd<XT, SAVED, W32, L, MAXT>, dim3(*parts), dim3(s.threads), smem, st, a);
+  launch_chained(k_norm_bwd<XT, SAVED, W32, L>, dim3(*parts), dim3(teams * s.threads), smem, st, a);
   note_launches(1);
   return launch_status();
 }
@@ -429,10 +446,10 @@ mp_status launch_bwd_rows(NormBwd a, const RowShape& s, int* parts, cudaStream_t
 template <int XT, bool SAVED, bool W32>
 mp_status launch_bwd_shape(const NormBwd& a, int* parts, cudaStream_t st) {
   const RowShape s = row_shape(a.cols);
-  if (s.lanes == 8) return launch_bwd_rows<XT, SAVED, W32, 8, kBwdThreads>(a, s, parts, st);
-  if (s.lanes == 16) return launch_bwd_rows<XT, SAVED, W32, 16, kBwdThreads>(a, s, parts, st);
-  if (s.lanes == 32) return launch_bwd_rows<XT, SAVED, W32, 32, kBwdThreads>(a, s, parts, st);
-  return launch_bwd_rows<XT, SAVED, W32, 0, kBwdThreads>(a, s, parts, st);
+  if (s.lanes == 8) return launch_bwd_rows<XT, SAVED, W32, 8>(a, s, parts, st);
+  if (s.lanes == 16) return launch_bwd_rows<XT, SAVED, W32, 16>(a, s, parts, st);
+  if (s.lanes == 32) return launch_bwd_rows<XT, SAVED, W32, 32>(a, s, parts, st);
+  return launch_bwd_rows<XT, SAVED, W32, 0>(a, s, parts, st);
 }
 
 template <int XT, bool SAVED>

@@ -116,8 +116,8 @@ __global__ __launch_bounds__(kThreads) void k_swiglu_bwd(const __grid_constant__
     dr.load(a.dp, p.at);
 #pragma unroll
     for (int k = 0; k < kPairs; ++k) {
-      g[k] = e4m3_pair(gc, k, gs);
-      u[k] = e4m3_pair(uc, k, us);
+      g[k] = mul2(e4m3_floats(gc, k), both(gs));
+      u[k] = mul2(e4m3_floats(uc, k), both(us));
     }
   } else {
     Unit<XT> gr, ur;

@@ -389,28 +389,12 @@ __device__ __forceinline__ void cast_store(const float2 (&y)[kPairs], const Fp8O
   cast_store<1, XT>(y, o, p, mc, raw, cc, cs, 0);
 }
 
-// Values of E4M3 codes 2k and 2k + 1 of a unit times `scale`.
-__device__ __forceinline__ float2 e4m3_pair(const uint4& c, int k, float scale) {
+// Values of E4M3 codes 2k and 2k + 1 of a unit, exact (through binary16).
+__device__ __forceinline__ float2 e4m3_floats(const uint4& c, int k) {
   const uint32_t w = (k >> 1) == 0 ? c.x : (k >> 1) == 1 ? c.y : (k >> 1) == 2 ? c.z : c.w;
-  uint32_t h2;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((unsigned short)(w >> (16 * (k & 1)))));
-  return mul2(make_float2(f16lo(h2), f16hi(h2)), both(scale));
-}
-
-// Sum of one value per thread over the CTA's warps, in a fixed order, in every
-// thread.  `slot` (32 floats) must not be rewritten before every thread has
-// passed the next barrier: callers alternate between two.
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-  return v;
-}
-__device__ __forceinline__ float block_sum(float v, float* slot) {
-  v = warp_sum(v);
-  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) slot[threadIdx.x >> 5] = v;
-  __syncthreads();
-  return warp_sum(lane < warps ? slot[lane] : 0.0f);
+  uint32_t h;
+  asm volatile("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)(w >> (16 * (k & 1)))));
+  return make_float2(f16lo(h), f16hi(h));
 }
 
 }  // namespace mp
