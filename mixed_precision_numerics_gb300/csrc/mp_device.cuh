@@ -218,8 +218,24 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
     if (mbar_try_wait(bar, parity)) return true;
   return false;
 }
+// Gives a copy that may be on its way to `bar` an eighth of that limit to land:
+// one of the two parities is of a completed phase, the other of the one that a
+// copy in flight would complete.
+__device__ __forceinline__ void mbar_drain(uint64_t* bar) {
+  for (uint32_t parity = 0; parity < 2; ++parity)
+    for (uint32_t i = 0; i < kWaitLimit / 8 && !mbar_try_wait(bar, parity); ++i) {
+    }
+}
 // Global -> shared bulk copy completing `bytes` of transaction on `bar`.
 // dst, src 16-byte aligned, bytes a multiple of 16.
+__device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar,
+                                         uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
 __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar,
                                          uint64_t policy) {
   asm volatile(

@@ -190,31 +190,34 @@ constexpr int kRingBytes = 216 * 1024;  // shared memory of an SM for the rings 
 
 __device__ unsigned int g_norm_wait_failures;  // bounded waits that gave up (read by mp_wait_failures)
 
-// One stage of the ring: dy, then dh (if any, and if a stage with it fits: FP32
-// rows of over 13824 without a checkpoint read it directly), then the stream
-// or its codes, of one group of rows, each as it lies in memory.
+// A group of rows comes through two rings of shared memory, by when its bytes
+// are done with: `early` (dy, and a checkpoint's codes) before the row's sum,
+// `late` (the stream itself, read before and after the sum, and dh) after it.
+// Bytes of one stage of each, of a group of so many elements.
 template <int XT, bool SAVED>
-__host__ __device__ constexpr int stage_bytes(int elements, bool dh) {
-  constexpr int es = XT == XF32 ? 4 : 2;
-  return elements * (es + (dh ? es : 0) + (SAVED ? 1 : es));
+__host__ __device__ constexpr int early_bytes(int elements) { return elements * ((XT == XF32 ? 4 : 2) + (SAVED ? 1 : 0)); }
+template <int XT, bool SAVED>
+__host__ __device__ constexpr int late_bytes(int elements, bool dh) {
+  return elements * (XT == XF32 ? 4 : 2) * ((SAVED ? 0 : 1) + (dh ? 1 : 0));
 }
 
 // A CTA holds `teams` of threads (as many as the SM's registers take, where a
 // row needs a whole team; one, where rows lie in a warp's lanes).  A team takes
 // every (gridDim.x * teams)-th group of rows.  Its first thread keeps the
-// team's ring of `stages` groups filled with bulk copies (a group's rows are
-// consecutive in memory, so a group is two or three copies).  The barrier of a
-// group's sum also tells that every thread of the team has done with the group
-// before, whose stage is then filled again.  Each thread keeps the sums of its
-// own columns in registers over its rows (binary32, in row order); at the end
-// the CTA joins its teams' sums and writes one row of `parts`.  A thread whose
-// wait gave up works on what it finds and stores nothing more, but keeps
-// meeting the barriers.
+// team's rings filled with bulk copies (a group's rows are consecutive in
+// memory, so a tensor's part of a group is one copy).  The barrier of a group's
+// sum tells that the whole team has done with the group's early stage and with
+// the late stage of the group before: both are filled again there, the early
+// one `stages` groups ahead.  Each thread keeps the sums of its own columns in
+// registers over its rows (binary32, in row order); at the end the CTA joins
+// its teams' sums and writes one row of `parts`.  A thread whose wait gave up
+// works on what it finds and stores nothing more, but keeps meeting the
+// barriers.
 template <int XT, bool SAVED, bool W32, int L>
 __global__ __launch_bounds__(L ? kCta : kMaxThreads) void k_norm_bwd(const __grid_constant__ NormBwd a) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float slots[2 * 32];
-  __shared__ uint64_t bars[kMaxTeams * kMaxStages];
+  __shared__ uint64_t bars[kMaxTeams * 2 * kMaxStages];
   constexpr int R = L ? kCta / L : 1, es = XT == XF32 ? 4 : 2;
   const int units = a.cols / kUnit, S = a.stages;
   const int T = L ? kCta : a.team;
@@ -224,37 +227,52 @@ __global__ __launch_bounds__(L ? kCta : kMaxThreads) void k_norm_bwd(const __gri
   const int uc = u < units ? u : units - 1;  // a lane past the row's end works on its last unit and stores nothing
   const int group = R * a.cols;  // elements
   const bool ring_dh = a.dh && a.stage_dh;
-  const int bytes = stage_bytes<XT, SAVED>(group, ring_dh);
-  const int at_v = group * es * (ring_dh ? 2 : 1);  // where the stream lies in a stage
-  unsigned char* const ring = smem + a.cols * (W32 ? 4 : 2) + team * S * bytes;
-  uint64_t* const full = bars + team * kMaxStages;
+  const uint32_t early = early_bytes<XT, SAVED>(group), late = late_bytes<XT, SAVED>(group, ring_dh);
+  const uint32_t weights = smem_u32(smem);
+  const uint32_t early0 = weights + a.cols * (W32 ? 4 : 2) + team * S * (early + late), late0 = early0 + S * early;
+  uint64_t* const full = bars + team * 2 * kMaxStages;  // [early or late][stage]
   float* const slot = slots + team * (T >> 5);
   if (t == 0) {
-    for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&full[kMaxStages + s], 1);
+    }
     fence_mbar_init();
   }
   __syncthreads();
   chain_wait();
   chain_release();
-  const int32_t step = gridDim.x * (L ? R : blockDim.x / T);  // rows
+  const int32_t rows = (int32_t)a.rows, step = gridDim.x * (L ? R : blockDim.x / T);
   int32_t row0 = (team * gridDim.x + blockIdx.x) * R;
-  auto fetch = [&](int s, int32_t row0) {  // one thread of the team
+  // One thread of the team: group of rows `from` (64 bits: it may lie past the
+  // end, and then nothing is done) into stage s.
+  auto fetch_early = [&](int s, int64_t from) {
+    if (from >= rows) return;
     const uint64_t policy = policy_evict_first();
-    const int64_t at = (int64_t)row0 * a.cols;
-    const uint32_t n = (uint32_t)min((int32_t)a.rows - row0, R) * a.cols;
-    unsigned char* st = ring + s * bytes;
-    mbar_arrive_expect_tx(&full[s], n * es * (ring_dh ? 2 : 1) + n * (SAVED ? 1 : es));
-    bulk_g2s(st, static_cast<const char*>(a.dy) + at * es, n * es, &full[s], policy);
-    if (ring_dh) bulk_g2s(st + group * es, static_cast<const char*>(a.dh) + at * es, n * es, &full[s], policy);
-    if constexpr (SAVED)
-      bulk_g2s(st + at_v, a.codes + at, n, &full[s], policy);
-    else
-      bulk_g2s(st + at_v, static_cast<const char*>(a.h) + at * es, n * es, &full[s], policy);
+    const uint32_t n = (uint32_t)min(rows - (int32_t)from, R) * a.cols, to = early0 + s * early;
+    mbar_arrive_expect_tx(&full[s], n * es + (SAVED ? n : 0));
+    bulk_g2s(to, static_cast<const char*>(a.dy) + from * a.cols * es, n * es, &full[s], policy);
+    if constexpr (SAVED) bulk_g2s(to + group * es, a.codes + from * a.cols, n, &full[s], policy);
   };
-  int issued = 0;  // fills so far, in the fetching thread; fill j is of stage j % S
-  const int64_t rows = a.rows;
-  if (t == 0)
-    for (; issued < S && row0 + (int64_t)issued * step < rows; ++issued) fetch(issued, row0 + issued * step);
+  auto fetch_late = [&](int s, int64_t from) {
+    if (from >= rows || late == 0) return;
+    const uint64_t policy = policy_evict_first();
+    const uint32_t n = (uint32_t)min(rows - (int32_t)from, R) * a.cols;
+    uint32_t to = late0 + s * late;
+    uint64_t* bar = &full[kMaxStages + s];
+    mbar_arrive_expect_tx(bar, n * es * ((SAVED ? 0 : 1) + (ring_dh ? 1 : 0)));
+    if constexpr (!SAVED) {
+      bulk_g2s(to, static_cast<const char*>(a.h) + from * a.cols * es, n * es, bar, policy);
+      to += group * es;
+    }
+    if (ring_dh) bulk_g2s(to, static_cast<const char*>(a.dh) + from * a.cols * es, n * es, bar, policy);
+  };
+  if (t == 0) {
+    for (int s = 0; s < S; ++s) {
+      fetch_early(s, row0 + (int64_t)s * step);
+      fetch_late(s, row0 + (int64_t)s * step);
+    }
+  }
   // The weights in shared memory, as they are where they have the rows' 16-bit
   // type, else in binary32.
   if (threadIdx.x < units) {
@@ -278,42 +296,40 @@ __global__ __launch_bounds__(L ? kCta : kMaxThreads) void k_norm_bwd(const __gri
   for (int i = 0; i < kPairs; ++i) acc[i] = both(0.0f);
   bool ok = true;
   // The row's two scalars are read one group ahead.
-  auto scalars = [&](int64_t row, float* rstd, float* scale) {
-    row = min(row, rows - 1);
-    *rstd = a.rstd[row];
-    *scale = SAVED ? a.scales[row * a.tiles + uc / kTileLanes] : 0.0f;
+  float next_rstd = 0.0f, next_scale = 0.0f;
+  auto scalars = [&](int64_t row) {
+    if (row >= rows) return;
+    next_rstd = a.rstd[row];
+    if constexpr (SAVED) next_scale = a.scales[row * a.tiles + uc / kTileLanes];
   };
-  float rstd, scale, next_rstd, next_scale;
-  scalars(row0 + sub, &next_rstd, &next_scale);
+  scalars(row0 + sub);
   int s = 0;
-  uint32_t phase = 0;
+  uint32_t phase = 0, ea = early0, la = late0;  // the stages of this group
   for (int it = 0; row0 < rows; ++it) {
     const bool live = L == 0 || row0 + sub < rows;
-    rstd = next_rstd, scale = next_scale;
-    scalars((int64_t)row0 + step + sub, &next_rstd, &next_scale);
-    if (ok && !mbar_wait_bounded(&full[s], phase)) {
+    const float rstd = next_rstd, vs = SAVED ? next_scale * rstd : rstd;
+    scalars((int64_t)row0 + step + sub);
+    if (ok && !(mbar_wait_bounded(&full[s], phase) && (SAVED || mbar_wait_bounded(&full[kMaxStages + s], phase)))) {
       ok = false;
       atomicAdd(&g_norm_wait_failures, 1u);
     }
     // a row past the end works on the group's first, whose copy is there
-    const unsigned char* st = ring + s * bytes;
-    const int e = (live ? sub : 0) * a.cols + uc * kUnit;
+    const uint32_t e = (L && live ? sub * a.cols : 0) + uc * kUnit;
     // Half a unit at a time: across the barrier stay the column sums, dy * w,
     // and a checkpoint's codes.
     float2 g[kPairs], dot = both(0.0f);
     uint4 code;
     Unit<XT> dy, v, w;
-    const float vs = SAVED ? scale * rstd : rstd;
-    if constexpr (SAVED) code = lds16(st + at_v + e);
+    if constexpr (SAVED) code = lds16(ea + group * es + e);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      dy.take_half(st, e, half);
-      if constexpr (!SAVED) v.take_half(st + at_v, e, half);
+      dy.take_half(ea + e * es, half);
+      if constexpr (!SAVED) v.take_half(la + e * es, half);
       Unit<XF32> w32;
       if constexpr (W32)
-        w32.take_half(smem, uc * kUnit, half);
+        w32.take_half(weights + uc * (kUnit * 4), half);
       else
-        w.take_half(smem, uc * kUnit, half);
+        w.take_half(weights + uc * (kUnit * 2), half);
 #pragma unroll
       for (int i = half * (kPairs / 2); i < (half + 1) * (kPairs / 2); ++i) {
         const float2 x = mul2(SAVED ? e4m3_floats(code, i) : v.pair(i), both(vs));
@@ -329,42 +345,45 @@ __global__ __launch_bounds__(L ? kCta : kMaxThreads) void k_norm_bwd(const __gri
     } else {
       c = team_sum(c, slot + (it & 1) * 32, team + 1, t, T);
     }
-    if (t == 0 && ok && S > 1 && it > 0 && row0 + (int64_t)(S - 1) * step < rows) {
-      fetch(s == 0 ? S - 1 : s - 1, row0 + (S - 1) * step);
-      ++issued;
+    if (t == 0 && ok) {
+      fetch_early(s, row0 + (int64_t)S * step);
+      if (S > 1 && it > 0) fetch_late(s == 0 ? S - 1 : s - 1, row0 + (int64_t)(S - 1) * step);
+    }
+    if (ok && SAVED && ring_dh && !mbar_wait_bounded(&full[kMaxStages + s], phase)) {
+      ok = false;
+      atomicAdd(&g_norm_wait_failures, 1u);
     }
     const float k = -c * a.inv_cols * rstd * vs;
     const bool out = ok && live && u < units;
-    const int64_t at = (int64_t)(row0 + sub) * a.cols + u * kUnit;
+    const int64_t at = ((int64_t)(row0 + sub) * a.cols + u * kUnit) * es;
     Unit<XT> o;
     o.zero();
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       if (ring_dh)
-        o.take_half(st + group * es, e, half);
+        o.take_half(la + (SAVED ? 0 : group * es) + e * es, half);
       else if (a.dh && out)
-        o.load_half(a.dh, at, half);
-      if constexpr (!SAVED) v.take_half(st + at_v, e, half);
+        o.load_half(static_cast<const char*>(a.dh) + at, half);
+      if constexpr (!SAVED) v.take_half(la + e * es, half);
 #pragma unroll
       for (int i = half * (kPairs / 2); i < (half + 1) * (kPairs / 2); ++i) {
         const float2 x = SAVED ? e4m3_floats(code, i) : v.pair(i);
         o.set_pair(i, fma2(g[i], both(rstd), fma2(x, both(k), o.pair(i))));
       }
-      if (out) o.store_half(a.dx, at, half);
+      if (out) o.store_half(static_cast<char*>(a.dx) + at, half);
     }
     if (S == 1) {  // one team
       __syncthreads();
-      if (t == 0 && ok && row0 + (int64_t)step < rows) {
-        fetch(0, row0 + step);
-        ++issued;
-      }
+      if (t == 0 && ok) fetch_late(0, row0 + (int64_t)step);
     }
-    if (++s == S) s = 0, phase ^= 1;
-    if (row0 + (int64_t)step >= rows) break;  // before the sum could pass 32 bits
+    if ((int64_t)row0 + step >= rows) break;  // before the sum could pass 32 bits
     row0 += step;
+    ea += early, la += late;
+    if (++s == S) s = 0, phase ^= 1, ea = early0, la = late0;
   }
-  if (!ok && t == 0) {  // copies may still be on their way: wait for them, within the limit
-    for (int j = issued < S ? 0 : issued - S; j < issued; ++j) (void)mbar_wait_bounded(&full[j % S], (j / S) & 1);
+  if (!ok && t == 0) {  // copies may still be on their way: give each stage's as long again
+    for (int j = 0; j < 2 * kMaxStages; ++j)
+      if (j % kMaxStages < S) mbar_drain(&full[j]);
   }
   __syncthreads();  // the rings are free: every team has done with its last row
   float* fold = reinterpret_cast<float*>(smem);  // [team or sub-row][columns]
@@ -418,9 +437,10 @@ template <int XT, bool SAVED, bool W32, int L>
 mp_status launch_bwd_rows(NormBwd a, const RowShape& s, int* parts, cudaStream_t st) {
   static std::atomic<uint64_t> opted{0};
   const int64_t groups = (a.rows + s.rows_per_cta - 1) / s.rows_per_cta;
-  const int weights = a.cols * (W32 ? 4 : 2), elements = s.rows_per_cta * a.cols;
-  a.stage_dh = a.dh && stage_bytes<XT, SAVED>(elements, true) + weights <= kRingBytes;
-  const int bytes = stage_bytes<XT, SAVED>(elements, a.stage_dh);  // with the weights at most 213 KB
+  const int weights = a.cols * (W32 ? 4 : 2), elements = s.rows_per_cta * a.cols, early = early_bytes<XT, SAVED>(elements);
+  // FP32 rows of over 13824 without a checkpoint do not fit with dh, which is then read directly.
+  a.stage_dh = a.dh && early + late_bytes<XT, SAVED>(elements, true) + weights <= kRingBytes;
+  const int bytes = early + late_bytes<XT, SAVED>(elements, a.stage_dh);  // with the weights at most 213 KB
   // Rows of whole teams: as many teams as the registers allow, if each has two
   // stages, and no more than spread the rows over all SMs.  Rows in lanes: as
   // many CTAs.  Then as many stages, up to kMaxStages, as shared memory holds.

@@ -77,11 +77,11 @@ __device__ __forceinline__ uint32_t div_by(uint32_t n, const FastDiv& f) {
 }
 
 // 16 bytes of shared memory, read where this is written and not kept.
-__device__ __forceinline__ uint4 lds16(const void* p) {
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
   uint4 r;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "r"(smem_u32(p))
+               : "r"(addr)
                : "memory");
   return r;
 }
@@ -110,18 +110,16 @@ struct Unit {
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) st_cs(p + 16 * i, v[i]);
   }
-  // half (0 or 1) of the unit at element `at` of shared memory: 8 elements
-  __device__ __forceinline__ void take_half(const unsigned char* base, int at, int half) {
+  // half (0 or 1: 8 elements) of the unit at an address of shared or global memory
+  __device__ __forceinline__ void take_half(uint32_t addr, int half) {
 #pragma unroll
-    for (int i = half * (kVecs / 2); i < (half + 1) * (kVecs / 2); ++i) v[i] = lds16(base + at * (kBytes / kUnit) + 16 * i);
+    for (int i = half * (kVecs / 2); i < (half + 1) * (kVecs / 2); ++i) v[i] = lds16(addr + 16 * i);
   }
-  __device__ __forceinline__ void load_half(const void* base, int64_t at, int half) {
-    const unsigned char* p = static_cast<const unsigned char*>(base) + at * (kBytes / kUnit);
+  __device__ __forceinline__ void load_half(const char* p, int half) {
 #pragma unroll
     for (int i = half * (kVecs / 2); i < (half + 1) * (kVecs / 2); ++i) v[i] = ld_cs(p + 16 * i);
   }
-  __device__ __forceinline__ void store_half(void* base, int64_t at, int half) const {
-    unsigned char* p = static_cast<unsigned char*>(base) + at * (kBytes / kUnit);
+  __device__ __forceinline__ void store_half(char* p, int half) const {
 #pragma unroll
     for (int i = half * (kVecs / 2); i < (half + 1) * (kVecs / 2); ++i) st_cs(p + 16 * i, v[i]);
   }
