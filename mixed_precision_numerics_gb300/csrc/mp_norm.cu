@@ -213,8 +213,8 @@ __host__ __device__ constexpr int late_bytes(int elements, bool dh) {
 // its teams' sums and writes one row of `parts`.  A thread whose wait gave up
 // works on what it finds and stores nothing more, but keeps meeting the
 // barriers.
-template <int XT, bool SAVED, bool W32, int L>
-__global__ __launch_bounds__(L ? kCta : kMaxThreads) void k_norm_bwd(const __grid_constant__ NormBwd a) {
+template <int XT, bool SAVED, bool W32, int L, int U>
+__global__ __launch_bounds__(L ? kCta : kMaxThreads / U) void k_norm_bwd(const __grid_constant__ NormBwd a) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float slots[2 * 32];
   __shared__ uint64_t bars[kMaxTeams * 2 * kMaxStages];
@@ -224,7 +224,11 @@ __global__ __launch_bounds__(L ? kCta : kMaxThreads) void k_norm_bwd(const __gri
   const int team = L ? 0 : __shfl_sync(0xFFFFFFFFu, threadIdx.x / T, 0);  // the same in a warp, and known to be
   const int t = L ? threadIdx.x : threadIdx.x - team * T;
   const int u = L ? threadIdx.x % (L ? L : 1) : t, sub = L ? threadIdx.x / (L ? L : 1) : 0;
-  const int uc = u < units ? u : units - 1;  // a lane past the row's end works on its last unit and stores nothing
+  // Unit k of a thread is u + k * T; one past the row's end works on the row's
+  // last unit and stores nothing.
+  int uc[U];
+#pragma unroll
+  for (int k = 0; k < U; ++k) uc[k] = min(u + k * T, units - 1);
   const int group = R * a.cols;  // elements
   const bool ring_dh = a.dh && a.stage_dh;
   const uint32_t early = early_bytes<XT, SAVED>(group), late = late_bytes<XT, SAVED>(group, ring_dh);
@@ -275,10 +279,10 @@ __global__ __launch_bounds__(L ? kCta : kMaxThreads) void k_norm_bwd(const __gri
   }
   // The weights in shared memory, as they are where they have the rows' 16-bit
   // type, else in binary32.
-  if (threadIdx.x < units) {
+  for (int k = threadIdx.x; k < units; k += blockDim.x) {
     Weights w;
-    w.load(a.weight, a.wt, threadIdx.x);
-    uint4* ws = reinterpret_cast<uint4*>(smem) + threadIdx.x * (W32 ? 4 : 2);
+    w.load(a.weight, a.wt, k);
+    uint4* ws = reinterpret_cast<uint4*>(smem) + k * (W32 ? 4 : 2);
     if constexpr (W32) {
       Unit<XF32> f;
       float2 ff[kPairs];
@@ -291,54 +295,69 @@ __global__ __launch_bounds__(L ? kCta : kMaxThreads) void k_norm_bwd(const __gri
     }
   }
   __syncthreads();
-  float2 acc[kPairs];
+  float2 acc[U][kPairs];
 #pragma unroll
-  for (int i = 0; i < kPairs; ++i) acc[i] = both(0.0f);
+  for (int k = 0; k < U; ++k)
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) acc[k][i] = both(0.0f);
   bool ok = true;
-  // The row's two scalars are read one group ahead.
-  float next_rstd = 0.0f, next_scale = 0.0f;
+  // The row's scalars are read one group ahead.
+  float next_rstd = 0.0f, next_scale[U];
   auto scalars = [&](int64_t row) {
     if (row >= rows) return;
     next_rstd = a.rstd[row];
-    if constexpr (SAVED) next_scale = a.scales[row * a.tiles + uc / kTileLanes];
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if constexpr (SAVED) next_scale[k] = a.scales[row * a.tiles + uc[k] / kTileLanes];
   };
   scalars(row0 + sub);
   int s = 0;
   uint32_t phase = 0, ea = early0, la = late0;  // the stages of this group
   for (int it = 0; row0 < rows; ++it) {
     const bool live = L == 0 || row0 + sub < rows;
-    const float rstd = next_rstd, vs = SAVED ? next_scale * rstd : rstd;
+    const float rstd = next_rstd;
+    float vs[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) vs[k] = SAVED ? next_scale[k] * rstd : rstd;
     scalars((int64_t)row0 + step + sub);
     if (ok && !(mbar_wait_bounded(&full[s], phase) && (SAVED || mbar_wait_bounded(&full[kMaxStages + s], phase)))) {
       ok = false;
       atomicAdd(&g_norm_wait_failures, 1u);
     }
     // a row past the end works on the group's first, whose copy is there
-    const uint32_t e = (L && live ? sub * a.cols : 0) + uc * kUnit;
+    uint32_t e[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) e[k] = (L && live ? sub * a.cols : 0) + uc[k] * kUnit;
     // Half a unit at a time: across the barrier stay the column sums, dy * w,
     // and a checkpoint's codes.
-    float2 g[kPairs], dot = both(0.0f);
-    uint4 code;
-    Unit<XT> dy, v, w;
-    if constexpr (SAVED) code = lds16(ea + group * es + e);
+    float2 g[U][kPairs];
+    float dot = 0.0f;
+    uint4 code[U];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      dy.take_half(ea + e * es, half);
-      if constexpr (!SAVED) v.take_half(la + e * es, half);
-      Unit<XF32> w32;
-      if constexpr (W32)
-        w32.take_half(weights + uc * (kUnit * 4), half);
-      else
-        w.take_half(weights + uc * (kUnit * 2), half);
+    for (int k = 0; k < U; ++k) {
+      float2 d = both(0.0f);
+      Unit<XT> dy, v, w;
+      if constexpr (SAVED) code[k] = lds16(ea + group * es + e[k]);
 #pragma unroll
-      for (int i = half * (kPairs / 2); i < (half + 1) * (kPairs / 2); ++i) {
-        const float2 x = mul2(SAVED ? e4m3_floats(code, i) : v.pair(i), both(vs));
-        if (live) acc[i] = fma2(dy.pair(i), x, acc[i]);
-        g[i] = mul2(dy.pair(i), W32 ? w32.pair(i) : w.pair(i));
-        dot = fma2(g[i], x, dot);
+      for (int half = 0; half < 2; ++half) {
+        dy.take_half(ea + e[k] * es, half);
+        if constexpr (!SAVED) v.take_half(la + e[k] * es, half);
+        Unit<XF32> w32;
+        if constexpr (W32)
+          w32.take_half(weights + uc[k] * (kUnit * 4), half);
+        else
+          w.take_half(weights + uc[k] * (kUnit * 2), half);
+#pragma unroll
+        for (int i = half * (kPairs / 2); i < (half + 1) * (kPairs / 2); ++i) {
+          const float2 x = mul2(SAVED ? e4m3_floats(code[k], i) : v.pair(i), both(vs[k]));
+          if (live) acc[k][i] = fma2(dy.pair(i), x, acc[k][i]);
+          g[k][i] = mul2(dy.pair(i), W32 ? w32.pair(i) : w.pair(i));
+          d = fma2(g[k][i], x, d);
+        }
       }
+      if (u + k * T < units) dot += d.x + d.y;
     }
-    float c = u < units ? dot.x + dot.y : 0.0f;
+    float c = dot;
     if constexpr (L != 0) {
       c = lane_sum<L>(c);
       __syncthreads();
@@ -353,24 +372,27 @@ __global__ __launch_bounds__(L ? kCta : kMaxThreads) void k_norm_bwd(const __gri
       ok = false;
       atomicAdd(&g_norm_wait_failures, 1u);
     }
-    const float k = -c * a.inv_cols * rstd * vs;
-    const bool out = ok && live && u < units;
-    const int64_t at = ((int64_t)(row0 + sub) * a.cols + u * kUnit) * es;
-    Unit<XT> o;
-    o.zero();
+    c *= -a.inv_cols * rstd;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if (ring_dh)
-        o.take_half(la + (SAVED ? 0 : group * es) + e * es, half);
-      else if (a.dh && out)
-        o.load_half(static_cast<const char*>(a.dh) + at, half);
-      if constexpr (!SAVED) v.take_half(la + e * es, half);
+    for (int k = 0; k < U; ++k) {
+      const bool out = ok && live && u + k * T < units;
+      const int64_t at = ((int64_t)(row0 + sub) * a.cols + (u + k * T) * kUnit) * es;
+      Unit<XT> o, v;
+      o.zero();
 #pragma unroll
-      for (int i = half * (kPairs / 2); i < (half + 1) * (kPairs / 2); ++i) {
-        const float2 x = SAVED ? e4m3_floats(code, i) : v.pair(i);
-        o.set_pair(i, fma2(g[i], both(rstd), fma2(x, both(k), o.pair(i))));
+      for (int half = 0; half < 2; ++half) {
+        if (ring_dh)
+          o.take_half(la + (SAVED ? 0 : group * es) + e[k] * es, half);
+        else if (a.dh && out)
+          o.load_half(static_cast<const char*>(a.dh) + at, half);
+        if constexpr (!SAVED) v.take_half(la + e[k] * es, half);
+#pragma unroll
+        for (int i = half * (kPairs / 2); i < (half + 1) * (kPairs / 2); ++i) {
+          const float2 x = SAVED ? e4m3_floats(code[k], i) : v.pair(i);
+          o.set_pair(i, fma2(g[k][i], both(rstd), fma2(x, both(c * vs[k]), o.pair(i))));
+        }
+        if (out) o.store_half(static_cast<char*>(a.dx) + at, half);
       }
-      if (out) o.store_half(static_cast<char*>(a.dx) + at, half);
     }
     if (S == 1) {  // one team
       __syncthreads();
@@ -388,11 +410,13 @@ __global__ __launch_bounds__(L ? kCta : kMaxThreads) void k_norm_bwd(const __gri
   __syncthreads();  // the rings are free: every team has done with its last row
   float* fold = reinterpret_cast<float*>(smem);  // [team or sub-row][columns]
   const int width = L ? L * kUnit : a.cols, deep = L ? R : blockDim.x / T;
-  if (L || u < units) {
-    float* f = fold + (L ? sub : team) * width + u * kUnit;
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    if (L == 0 && u + k * T >= units) break;
+    float* f = fold + (L ? sub : team) * width + (u + k * T) * kUnit;
 #pragma unroll
     for (int i = 0; i < kPairs; i += 2)
-      *reinterpret_cast<float4*>(f + 2 * i) = make_float4(acc[i].x, acc[i].y, acc[i + 1].x, acc[i + 1].y);
+      *reinterpret_cast<float4*>(f + 2 * i) = make_float4(acc[k][i].x, acc[k][i].y, acc[k][i + 1].x, acc[k][i + 1].y);
   }
   __syncthreads();
   for (int col = threadIdx.x; col < a.cols; col += blockDim.x) {
@@ -433,7 +457,7 @@ int64_t parts_of(int64_t rows, int64_t cols) {
   return groups < kMaxParts ? groups : kMaxParts;
 }
 
-template <int XT, bool SAVED, bool W32, int L>
+template <int XT, bool SAVED, bool W32, int L, int U>
 mp_status launch_bwd_rows(NormBwd a, const RowShape& s, int* parts, cudaStream_t st) {
   static std::atomic<uint64_t> opted{0};
   const int64_t groups = (a.rows + s.rows_per_cta - 1) / s.rows_per_cta;
@@ -444,21 +468,22 @@ mp_status launch_bwd_rows(NormBwd a, const RowShape& s, int* parts, cudaStream_t
   // Rows of whole teams: as many teams as the registers allow, if each has two
   // stages, and no more than spread the rows over all SMs.  Rows in lanes: as
   // many CTAs.  Then as many stages, up to kMaxStages, as shared memory holds.
-  int per_sm = kMaxThreads / s.threads;
+  const int team = L ? kCta : (s.threads / U + 31) / 32 * 32;
+  int per_sm = kMaxThreads / U / team;
   if (per_sm > kMaxTeams) per_sm = kMaxTeams;
   while (per_sm > 1 && (2 * bytes + (L ? weights : 0)) * per_sm + weights > kRingBytes) --per_sm;
   const int64_t spread = (groups + sm_count() - 1) / sm_count();
   const int teams = L ? 1 : (int)(per_sm < spread ? per_sm : spread);
-  a.team = s.threads;
+  a.team = team;
   a.stages = ((L ? kRingBytes / per_sm : kRingBytes) - weights) / (bytes * teams);
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   int smem = weights + teams * a.stages * bytes;
   const int fold = (L ? kCta * kUnit : teams * a.cols) * 4;  // the join of the column sums
   if (smem < fold) smem = fold;
-  if (!smem_ok(k_norm_bwd<XT, SAVED, W32, L>, smem, opted)) return MP_ECUDA;
+  if (!smem_ok(k_norm_bwd<XT, SAVED, W32, L, U>, smem, opted)) return MP_ECUDA;
   const int grid = resident_grid((groups + teams - 1) / teams, L ? per_sm : 1);
   *parts = grid < kMaxParts ? grid : kMaxParts;
-  launch_chained(k_norm_bwd<XT, SAVED, W32, L>, dim3(*parts), dim3(teams * s.threads), smem, st, a);
+  launch_chained(k_norm_bwd<XT, SAVED, W32, L, U>, dim3(*parts), dim3(teams * team), smem, st, a);
   note_launches(1);
   return launch_status();
 }
@@ -466,10 +491,10 @@ mp_status launch_bwd_rows(NormBwd a, const RowShape& s, int* parts, cudaStream_t
 template <int XT, bool SAVED, bool W32>
 mp_status launch_bwd_shape(const NormBwd& a, int* parts, cudaStream_t st) {
   const RowShape s = row_shape(a.cols);
-  if (s.lanes == 8) return launch_bwd_rows<XT, SAVED, W32, 8>(a, s, parts, st);
-  if (s.lanes == 16) return launch_bwd_rows<XT, SAVED, W32, 16>(a, s, parts, st);
-  if (s.lanes == 32) return launch_bwd_rows<XT, SAVED, W32, 32>(a, s, parts, st);
-  return launch_bwd_rows<XT, SAVED, W32, 0>(a, s, parts, st);
+  if (s.lanes == 8) return launch_bwd_rows<XT, SAVED, W32, 8, 1>(a, s, parts, st);
+  if (s.lanes == 16) return launch_bwd_rows<XT, SAVED, W32, 16, 1>(a, s, parts, st);
+  if (s.lanes == 32) return launch_bwd_rows<XT, SAVED, W32, 32, 1>(a, s, parts, st);
+  return launch_bwd_rows<XT, SAVED, W32, 0, 2>(a, s, parts, st);
 }
 
 template <int XT, bool SAVED>
