@@ -214,7 +214,7 @@ __host__ __device__ constexpr int late_bytes(int elements, bool dh) {
 // works on what it finds and stores nothing more, but keeps meeting the
 // barriers.
 template <int XT, bool SAVED, bool W32, int L, int U>
-__global__ __launch_bounds__(L ? kCta : kMaxThreads / U) void k_norm_bwd(const __grid_constant__ NormBwd a) {
+__global__ __maxnreg__(U == 2 ? 112 : 64) void k_norm_bwd(const __grid_constant__ NormBwd a) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float slots[2 * 32];
   __shared__ uint64_t bars[kMaxTeams * 2 * kMaxStages];
@@ -426,30 +426,40 @@ __global__ __launch_bounds__(L ? kCta : kMaxThreads / U) void k_norm_bwd(const _
   }
 }
 
-// dweight[col] = sum over the partial rows: 32 columns a CTA, 32 warps that
-// each sum every 32nd partial row, joined in a fixed order.
-constexpr int kFoldWarps = 32;
-__global__ __launch_bounds__(32 * kFoldWarps) void k_norm_dweight(const float* parts, int32_t nparts, int32_t cols,
-                                                                  void* dweight, int32_t dt) {
-  __shared__ float s[kFoldWarps][33];
+// dweight[col] = sum over the partial rows: 32 columns a CTA, 8 warps that each
+// sum every 8th partial row, joined in a fixed order.  At 32 registers a CTA
+// fits beside one of the kernel before it, and is there when that one ends.
+constexpr int kFoldWarps = 8, kFoldLoads = 20;
+__global__ __launch_bounds__(32 * kFoldWarps, 8) void k_norm_dweight(const float* parts, int32_t nparts, int32_t cols,
+                                                                     void* dweight, int32_t dt) {
+  __shared__ float s[kFoldWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
   chain_wait();
   chain_release();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
   float v = 0.0f;
   if (col < cols) {
+    const float* at = parts + (int64_t)warp * cols + col;
+    for (int p = warp; p < nparts; p += kFoldWarps * kFoldLoads) {
+      float x[kFoldLoads];  // all in flight at once
 #pragma unroll
-    for (int p = 0; p < kMaxParts / kFoldWarps; ++p)  // all of them in flight at once
-      if (warp + p * kFoldWarps < nparts) v += parts[(int64_t)(warp + p * kFoldWarps) * cols + col];
+      for (int j = 0; j < kFoldLoads; ++j) {
+        x[j] = p + j * kFoldWarps < nparts ? *at : 0.0f;
+        at += (int64_t)kFoldWarps * cols;
+      }
+#pragma unroll
+      for (int j = 0; j < kFoldLoads; ++j) v += x[j];
+    }
   }
   s[warp][lane] = v;
   __syncthreads();
-  v = lane_sum<32>(s[lane][warp]);  // warp w joins the 32 sums of column w
-  const int out = blockIdx.x * 32 + warp;
-  if (lane != 0 || out >= cols) return;
+  if (warp != 0 || col >= cols) return;
+  v = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kFoldWarps; ++j) v += s[j][lane];
   if (dt == XF32)
-    static_cast<float*>(dweight)[out] = v;
+    static_cast<float*>(dweight)[col] = v;
   else
-    static_cast<uint16_t*>(dweight)[out] = (uint16_t)(dt == XF16 ? pack_f16x2(v, 0.0f) : pack_bf16x2(v, 0.0f));
+    static_cast<uint16_t*>(dweight)[col] = (uint16_t)(dt == XF16 ? pack_f16x2(v, 0.0f) : pack_bf16x2(v, 0.0f));
 }
 
 int64_t parts_of(int64_t rows, int64_t cols) {
