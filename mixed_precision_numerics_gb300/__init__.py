@@ -175,16 +175,23 @@ def _stream(stream) -> int | None:
     import torch
 
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without a Stream object around it, whose making costs more than a small kernel
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
-def _dtype_code(t) -> int:
-    import torch
+_CODES: dict = {}
 
-    return {torch.float32: MP_F32, torch.float16: MP_F16, torch.bfloat16: MP_BF16}[t.dtype]
+
+def _dtype_code(t) -> int:
+    if not _CODES:
+        import torch
+
+        _CODES.update({torch.float32: MP_F32, torch.float16: MP_F16, torch.bfloat16: MP_BF16})
+    return _CODES[t.dtype]
 
 
 def mp_status_str(status: int) -> str:
@@ -472,37 +479,56 @@ def mx_quantize(x, codes, scales, elem_dtype: int = MP_E2M1, dequant=None, strea
 # ---- block operators with 8-bit outputs and 8-bit checkpoints ------------------------------
 
 
-def _same(t, name: str, nbytes: int, x, dtype, align: int = 16) -> None:
-    """_dev, and the element type: a tensor of another 16-bit type has the right size."""
+def _in(t, name: str, nbytes: int, like, dev: int, dtype=None, align: int = 16) -> int | None:
+    """The pointer of an argument that passes _dev's checks on device number
+    `dev` and, where `dtype` is given, has that element type (a tensor of
+    another 16-bit type has the right size).  A call has up to ten arguments and
+    a one-token kernel takes two microseconds: what passes is seen in few steps,
+    and _dev says what does not."""
     if t is None or isinstance(t, int):
-        return
-    _dev(t, name, nbytes, like=x, align=align)
-    if t.dtype != dtype:
+        return t
+    p = t.data_ptr()
+    if t.get_device() != dev or not t.is_contiguous() or (t.nbytes < nbytes and p % align == 0):
+        _dev(t, name, nbytes, like=None if t is like else like, align=align)
+    if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name}: {t.dtype}, the call needs {dtype}")
+    return p
 
 
-def _row_pitch(t, name: str, x, rows: int, cols: int) -> int:
-    """Elements between the rows of a [rows, cols] matrix that may be a column range of a wider one."""
+def _matrix(t, name: str, rows: int, cols: int, like, dev: int) -> tuple[int, int]:
+    """Pointer and row distance (in elements) of a [rows, cols] matrix of like's
+    type that may be a column range of a wider one."""
+    if t.get_device() != dev or t.shape != like.shape or t.dtype != like.dtype:
+        if not t.is_cuda:
+            raise ValueError(f"{name}: a CUDA tensor is required (the kernels read and write device memory)")
+        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, the call needs {(rows, cols)} {like.dtype} "
+                         f"on cuda:{dev}")
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return t.data_ptr(), ld if rows > 1 else cols
+
+
+def _pair(a, b, names: tuple[str, str], rows: int, cols: int, like, dev: int) -> tuple[int, int, int]:
+    pa, ld = _matrix(a, names[0], rows, cols, like, dev)
+    pb, ld_b = _matrix(b, names[1], rows, cols, like, dev)
+    if ld != ld_b:
+        raise ValueError(f"{names[1]}: its rows lie {ld_b} elements apart, those of {names[0]} {ld}")
+    return pa, pb, ld
+
+
+def _current_device(t) -> int:
+    """The current device's number; -2, which no tensor is on, for a host tensor
+    (so that its check fails without a GPU being needed)."""
     import torch
 
-    if not t.is_cuda:
-        raise ValueError(f"{name}: a CUDA tensor is required (the kernels read and write device memory)")
-    want = x.device if x is not t else torch.device("cuda", torch.cuda.current_device())
-    if t.device != want:
-        raise ValueError(f"{name}: on {t.device}, the call runs on {want}")
-    if tuple(t.shape) != (rows, cols) or t.dtype != x.dtype:
-        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, the call needs {(rows, cols)} {x.dtype}")
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return t.stride(0) if rows > 1 else cols
+    return torch.cuda.current_device() if t.is_cuda else -2
 
 
-def _fp8_out(y, y_scales, scale_block: int, rows: int, cols: int, x) -> None:
-    _dev(y, "y", rows * cols, like=x)
-    if scale_block == 32:
-        _dev(y_scales, "y_scales", rows * (cols // 32), like=x, align=1)
-    else:
-        _dev(y_scales, "y_scales", 4 * rows * -(-cols // 128), like=x, align=4)
+def _float32():
+    import torch
+
+    return torch.float32
 
 
 def rmsnorm_residual_fp8(x, weight, y, y_scales, *, residual=None, h=None, rstd=None, ckpt=None, ckpt_scales=None,
@@ -511,22 +537,19 @@ def rmsnorm_residual_fp8(x, weight, y, y_scales, *, residual=None, h=None, rstd=
     bytes; y_scales: float32 [rows, ceil(cols/128)], or with scale_block 32 one UE8M0 byte per 32
     elements.  h (as x), rstd (float32 [rows]) and ckpt (rows*cols bytes, with ckpt_scales float32
     [rows, ceil(cols/128)]) are outputs the backward pass reads; each may be None."""
-    import torch
-
     rows, cols = x.shape
-    n, nb = rows * cols, x.element_size() * rows * cols
-    _dev(x, "x", nb)
-    _same(residual, "residual", nb, x, x.dtype)
-    _same(h, "h", nb, x, x.dtype)
-    _dev(weight, "weight", cols * weight.element_size(), like=x)
-    _fp8_out(y, y_scales, scale_block, rows, cols, x)
-    _same(rstd, "rstd", 4 * rows, x, torch.float32, align=4)
-    _dev(ckpt, "ckpt", n, like=x)
-    _same(ckpt_scales, "ckpt_scales", 4 * rows * -(-cols // 128), x, torch.float32, align=4)
+    dt, dev, n = x.dtype, _current_device(x), rows * cols
+    nb, tile_bytes = n * x.element_size(), 4 * rows * -(-cols // 128)
+    scale_bytes, scale_align = (n // 32, 1) if scale_block == 32 else (tile_bytes, 4)
     _check("rmsnorm_residual_fp8",
-           lib.rmsnorm_residual_fp8(_ptr(x), _ptr(residual), _dtype_code(x), rows, cols, _ptr(weight),
-                                    _dtype_code(weight), float(eps), _ptr(h), _ptr(y), fp8_dtype, scale_block,
-                                    _ptr(y_scales), _ptr(rstd), _ptr(ckpt), _ptr(ckpt_scales), _stream(stream)))
+           lib.rmsnorm_residual_fp8(_in(x, "x", nb, x, dev), _in(residual, "residual", nb, x, dev, dt), _dtype_code(x),
+                                    rows, cols, _in(weight, "weight", cols * weight.element_size(), x, dev),
+                                    _dtype_code(weight), eps, _in(h, "h", nb, x, dev, dt), _in(y, "y", n, x, dev),
+                                    fp8_dtype, scale_block,
+                                    _in(y_scales, "y_scales", scale_bytes, x, dev, None, scale_align),
+                                    _in(rstd, "rstd", 4 * rows, x, dev, _float32(), 4), _in(ckpt, "ckpt", n, x, dev),
+                                    _in(ckpt_scales, "ckpt_scales", tile_bytes, x, dev, _float32(), 4),
+                                    _stream(stream)))
 
 
 def rmsnorm_workspace_size(rows: int, cols: int) -> int:
@@ -544,65 +567,54 @@ def rmsnorm_residual_backward(dy, weight, rstd, dx, dweight, workspace, *, h=Non
                               dh=None, stream=None) -> None:
     """dx (as dy) and dweight ([cols], any of the three float types) from dy, rstd and the stream: either h
     or its 8-bit checkpoint (ckpt, ckpt_scales).  dh: the gradient reaching the stream from above, or None."""
-    import torch
-
     rows, cols = dy.shape
-    nb = dy.element_size() * rows * cols
-    _dev(dy, "dy", nb)
-    _same(dh, "dh", nb, dy, dy.dtype)
-    _same(h, "h", nb, dy, dy.dtype)
-    _dev(ckpt, "ckpt", rows * cols, like=dy)
-    _same(ckpt_scales, "ckpt_scales", 4 * rows * -(-cols // 128), dy, torch.float32, align=4)
-    _dev(weight, "weight", cols * weight.element_size(), like=dy)
-    _same(rstd, "rstd", 4 * rows, dy, torch.float32, align=4)
-    _same(dx, "dx", nb, dy, dy.dtype)
-    _dev(dweight, "dweight", cols * dweight.element_size(), like=dy)
-    _dev(workspace, "workspace", like=dy)
-    wp, wb = _ws(workspace)
+    dt, dev, n = dy.dtype, _current_device(dy), rows * cols
+    nb = n * dy.element_size()
     _check("rmsnorm_residual_backward",
-           lib.rmsnorm_residual_backward(_ptr(dy), _ptr(dh), _dtype_code(dy), rows, cols, _ptr(h), _ptr(ckpt),
-                                         _ptr(ckpt_scales), _ptr(weight), _dtype_code(weight), _ptr(rstd), _ptr(dx),
-                                         _ptr(dweight), _dtype_code(dweight), wp, wb, _stream(stream)))
+           lib.rmsnorm_residual_backward(_in(dy, "dy", nb, dy, dev), _in(dh, "dh", nb, dy, dev, dt), _dtype_code(dy),
+                                         rows, cols, _in(h, "h", nb, dy, dev, dt), _in(ckpt, "ckpt", n, dy, dev),
+                                         _in(ckpt_scales, "ckpt_scales", 4 * rows * -(-cols // 128), dy, dev,
+                                             _float32(), 4),
+                                         _in(weight, "weight", cols * weight.element_size(), dy, dev),
+                                         _dtype_code(weight), _in(rstd, "rstd", 4 * rows, dy, dev, _float32(), 4),
+                                         _in(dx, "dx", nb, dy, dev, dt),
+                                         _in(dweight, "dweight", cols * dweight.element_size(), dy, dev),
+                                         _dtype_code(dweight), _in(workspace, "workspace", 0, dy, dev),
+                                         0 if workspace is None else workspace.nbytes, _stream(stream)))
 
 
 def swiglu_fp8(gate, up, y, y_scales, *, ckpt=None, ckpt_scales=None, fp8_dtype: int = MP_E4M3,
                scale_block: int = 128, stream=None) -> None:
     """y = FP8 of silu(gate) * up.  gate, up: [rows, cols], each may be a column range of one wider
     matrix; ckpt: 2*rows*cols bytes (gate's codes, then up's), ckpt_scales: float32 [2, rows, ceil(cols/128)]."""
-    import torch
-
     rows, cols = gate.shape
-    ld = _row_pitch(gate, "gate", gate, rows, cols)
-    if _row_pitch(up, "up", gate, rows, cols) != ld:
-        raise ValueError("up: the rows of gate and up must be the same distance apart")
-    _fp8_out(y, y_scales, scale_block, rows, cols, gate)
-    _dev(ckpt, "ckpt", 2 * rows * cols, like=gate)
-    _same(ckpt_scales, "ckpt_scales", 8 * rows * -(-cols // 128), gate, torch.float32, align=4)
+    dev, n = _current_device(gate), rows * cols
+    tile_bytes = 4 * rows * -(-cols // 128)
+    scale_bytes, scale_align = (n // 32, 1) if scale_block == 32 else (tile_bytes, 4)
+    pg, pu, ld = _pair(gate, up, ("gate", "up"), rows, cols, gate, dev)
     _check("swiglu_fp8",
-           lib.swiglu_fp8(_ptr(gate), _ptr(up), ld, _dtype_code(gate), rows, cols, _ptr(y), fp8_dtype, scale_block,
-                          _ptr(y_scales), _ptr(ckpt), _ptr(ckpt_scales), _stream(stream)))
+           lib.swiglu_fp8(pg, pu, ld, _dtype_code(gate), rows, cols, _in(y, "y", n, gate, dev), fp8_dtype, scale_block,
+                          _in(y_scales, "y_scales", scale_bytes, gate, dev, None, scale_align),
+                          _in(ckpt, "ckpt", 2 * n, gate, dev),
+                          _in(ckpt_scales, "ckpt_scales", 2 * tile_bytes, gate, dev, _float32(), 4), _stream(stream)))
 
 
 def swiglu_backward(dp, dgate, dup, *, gate=None, up=None, ckpt=None, ckpt_scales=None, stream=None) -> None:
     """dgate, dup from dp and either gate and up or their 8-bit checkpoint of swiglu_fp8.  dgate and dup
     ([rows, cols]) may be column ranges of one wider matrix, as gate and up may."""
-    import torch
-
     rows, cols = dp.shape
-    _dev(dp, "dp", dp.element_size() * rows * cols)
-    ld = cols
+    dev, n = _current_device(dp), rows * cols
+    pg, pu, ld = None, None, cols
     if gate is not None and up is not None:
-        ld = _row_pitch(gate, "gate", dp, rows, cols)
-        if _row_pitch(up, "up", dp, rows, cols) != ld:
-            raise ValueError("up: the rows of gate and up must be the same distance apart")
-    d_ld = _row_pitch(dgate, "dgate", dp, rows, cols)
-    if _row_pitch(dup, "dup", dp, rows, cols) != d_ld:
-        raise ValueError("dup: the rows of dgate and dup must be the same distance apart")
-    _dev(ckpt, "ckpt", 2 * rows * cols, like=dp)
-    _same(ckpt_scales, "ckpt_scales", 8 * rows * -(-cols // 128), dp, torch.float32, align=4)
+        pg, pu, ld = _pair(gate, up, ("gate", "up"), rows, cols, dp, dev)
+    elif gate is not None or up is not None:
+        raise ValueError("gate and up: both or neither")
+    pdg, pdu, d_ld = _pair(dgate, dup, ("dgate", "dup"), rows, cols, dp, dev)
     _check("swiglu_backward",
-           lib.swiglu_backward(_ptr(dp), _dtype_code(dp), rows, cols, _ptr(gate), _ptr(up), ld, _ptr(ckpt),
-                               _ptr(ckpt_scales), _ptr(dgate), _ptr(dup), d_ld, _stream(stream)))
+           lib.swiglu_backward(_in(dp, "dp", n * dp.element_size(), dp, dev), _dtype_code(dp), rows, cols, pg, pu, ld,
+                               _in(ckpt, "ckpt", 2 * n, dp, dev),
+                               _in(ckpt_scales, "ckpt_scales", 8 * rows * -(-cols // 128), dp, dev, _float32(), 4),
+                               pdg, pdu, d_ld, _stream(stream)))
 
 
 __all__ = [
