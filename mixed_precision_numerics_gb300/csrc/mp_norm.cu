@@ -106,19 +106,17 @@ __global__ __launch_bounds__(L ? kCta : kMaxThreads) void k_norm_fwd(const __gri
   p.at = row * a.cols + u * kUnit;
   p.in = row < a.rows && u < units;
   p.tile_in = row < a.rows && (u & ~7) < units;
-  Unit<XT> h[2];
+  Unit<XT> h[2], r;
   Weights w;
   h[0].zero();
+  r.zero();
   if (p.in) {
     h[0].load(a.x, p.at);
-    if (a.residual) {
-      Unit<XT> r;
-      r.load(a.residual, p.at);
-      h[0].add(r);
-    }
+    if (a.residual) r.load(a.residual, p.at);
     w.load(a.weight, a.wt, u);
-    if (a.h) h[0].store(a.h, p.at);
   }
+  if (a.residual) h[0].add(r);
+  if (p.in && a.h) h[0].store(a.h, p.at);
   float2 ss = both(0.0f);
   float amax = 0.0f;
 #pragma unroll

@@ -243,30 +243,27 @@ __device__ __forceinline__ uint32_t tile_max(uint32_t m) {
 
 constexpr uint32_t kInfBits = 0x7F800000u;
 
-// Multipliers and stored scales of N 1x128 tiles at once (the same eight lanes
-// hold all N), by fp8_quantize_blockwise's rule: scale = amax / top, multiplier
-// top / amax.  Both are correctly rounded divisions; lane 2k of the tile's
-// eight does tile k's multiplier and lane 2k + 1 its scale, so one division
-// serves them all.  mul[k] is valid in every lane, *scale in lane 2k + 1.  The
-// multiplier is 0 for a tile of zeros, with a non-finite element, or with an
-// amax below top / FLT_MAX (about 2^-112), where top / amax would be infinite:
-// its elements become zeros instead of the NaN that 0 * inf would give.
-template <int N>
-__device__ __forceinline__ void tile_scales(const uint32_t (&m)[N], const float (&top)[N], float (&mul)[N],
-                                            float* scale) {
+// Multipliers and stored scales of the first M of N 1x128 tiles at once (the
+// same eight lanes hold them all), by fp8_quantize_blockwise's rule: scale =
+// amax / top, multiplier top / amax, with `top` for tile N - 1 (the output) and
+// 448 for the others (checkpoints).  Both are correctly rounded divisions; lane
+// 2k of the tile's eight does tile k's multiplier and lane 2k + 1 its scale, so
+// one division serves them all.  mul[k] is valid in every lane, *scale in lane
+// 2k + 1.  The multiplier is 0 for a tile of zeros, with a non-finite element,
+// or with an amax below top / FLT_MAX (about 2^-112), where top / amax would be
+// infinite: its elements become zeros instead of the NaN that 0 * inf would give.
+template <int N, int M>
+__device__ __forceinline__ void tile_scales(const uint32_t (&m)[N], float top, float (&mul)[N], float* scale) {
   const int lane = threadIdx.x & 7;
   uint32_t mm = m[0];
-  float tt = top[0];
 #pragma unroll
-  for (int k = 1; k < N; ++k) {
-    mm = lane >= 2 * k ? m[k] : mm;
-    tt = lane >= 2 * k ? top[k] : tt;
-  }
+  for (int k = 1; k < M; ++k) mm = lane >= 2 * k ? m[k] : mm;
+  const float tt = M == N && lane >= 2 * (N - 1) ? top : 448.0f;
   const float amax = __uint_as_float(mm);
   const float q = __fdiv_rn((lane & 1) ? amax : tt, (lane & 1) ? tt : amax);
   const float r = (q < INFINITY && mm < kInfBits) ? q : 0.0f;
 #pragma unroll
-  for (int k = 0; k < N; ++k) mul[k] = __shfl_sync(0xFFFFFFFFu, r, (threadIdx.x & 24) + 2 * k);
+  for (int k = 0; k < M; ++k) mul[k] = __shfl_sync(0xFFFFFFFFu, r, (threadIdx.x & 24) + 2 * k);
   *scale = mm > kInfBits ? __uint_as_float(0x7FC00000u) : q;
 }
 // The same of a 1x32 block by mx_quantize's rule: e = max(floor(log2 amax) -
@@ -347,22 +344,22 @@ __device__ __forceinline__ void cast_store(const float2 (&y)[kPairs], const Fp8O
                                            const uint32_t (&mc)[N], Unit<XT> (&raw)[N], uint8_t* const (&cc)[N],
                                            float* const (&cs)[N], int tiles) {
   const int lane = threadIdx.x & 7;
-  uint32_t my = pair_max(p.in ? unit_amax(y) : 0u), m[N];
-  float top[N], mul[N], scale, mul_y;
-#pragma unroll
-  for (int k = 0; k < N - 1; ++k) m[k] = mc[k], top[k] = 448.0f;
-  top[N - 1] = o.e5m2 ? 57344.0f : 448.0f;
+  uint32_t my = pair_max(p.in ? unit_amax(y) : 0u);
+  float mul[N], scale, mul_y;
   if (o.mx) {
     uint32_t byte;
     mx_scale(my, o.e5m2 ? 15u : 8u, &mul_y, &byte);
     if ((lane & 1) == 0 && p.in)
       static_cast<uint8_t*>(o.scales)[(int64_t)p.row * o.per_row + (p.u >> 1)] = (uint8_t)byte;
-    m[N - 1] = 0u;
-    if constexpr (N > 1) tile_scales(m, top, mul, &scale);
+    if constexpr (N > 1) tile_scales<N, N - 1>(mc, 448.0f, mul, &scale);
   } else {
     my = max(my, __shfl_xor_sync(0xFFFFFFFFu, my, 2));
-    my = m[N - 1] = max(my, __shfl_xor_sync(0xFFFFFFFFu, my, 4));
-    tile_scales(m, top, mul, &scale);
+    my = max(my, __shfl_xor_sync(0xFFFFFFFFu, my, 4));
+    uint32_t m[N];
+#pragma unroll
+    for (int k = 0; k < N - 1; ++k) m[k] = mc[k];
+    m[N - 1] = my;
+    tile_scales<N, N>(m, o.e5m2 ? 57344.0f : 448.0f, mul, &scale);
     mul_y = mul[N - 1];
     if (lane == 2 * N - 1 && p.tile_in) static_cast<float*>(o.scales)[(int64_t)p.row * o.per_row + (p.u >> 3)] = scale;
   }
@@ -373,7 +370,7 @@ __device__ __forceinline__ void cast_store(const float2 (&y)[kPairs], const Fp8O
     float2 v[kPairs];
     raw[k].forget();
     raw[k].floats(v);
-    store_codes(v, cc[k], p, m[k], mul[k], false, false, [&](int i) { return raw[k].sign80(i); });
+    store_codes(v, cc[k], p, mc[k], mul[k], false, false, [&](int i) { return raw[k].sign80(i); });
   }
 }
 
