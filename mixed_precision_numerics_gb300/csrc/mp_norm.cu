@@ -30,6 +30,7 @@ namespace {
 constexpr int kCta = 256;           // threads of a CTA that takes several rows at a time
 constexpr int kMaxThreads = 1024;   // threads of a CTA that takes one row at a time
 constexpr int kMaxCols = kMaxThreads * kUnit;
+constexpr int kRegisters = 65536;   // of an SM
 constexpr int kMaxParts = 608;      // partial sums of dweight: four CTAs on each of 152 SMs
 
 // How a row is laid over threads, by its length alone: `lanes` of a warp (8,
@@ -44,6 +45,8 @@ RowShape row_shape(int64_t cols) {
   const int l = n <= 8 ? 8 : n <= 16 ? 16 : 32;
   return {l, kCta, kCta / l};
 }
+// Threads that hold such a row with `u` units each.
+int team_of(const RowShape& s, int u) { return (s.threads / u + 31) / 32 * 32; }
 // CTAs that take `groups` groups of rows in turn, `per_sm` resident on an SM.
 int resident_grid(int64_t groups, int per_sm) {
   const int64_t most = (int64_t)sm_count() * (per_sm < 1 ? 1 : per_sm);
@@ -91,74 +94,100 @@ struct NormFwd {
   float eps, inv_cols;
 };
 
-template <int XT, int L, bool SAVE>
-__global__ __launch_bounds__(L ? kCta : kMaxThreads) void k_norm_fwd(const __grid_constant__ NormFwd a) {
+// A row lies in L lanes of a warp or (L = 0) in the CTA, U units a thread: unit
+// k of thread t is t + k * threads.
+template <int XT, int L, int U, bool SAVE>
+__global__ __launch_bounds__(L ? kCta : kMaxThreads / U) void k_norm_fwd(const __grid_constant__ NormFwd a) {
   __shared__ float slots[32];
   chain_wait();
   chain_release();
   constexpr int R = L ? kCta / L : 1;
-  const int units = a.cols / kUnit;
+  const int units = a.cols / kUnit, T = blockDim.x;
   const int u = L ? threadIdx.x % (L ? L : 1) : threadIdx.x, sub = L ? threadIdx.x / (L ? L : 1) : 0;
-  Place p;
   const int64_t row = (int64_t)blockIdx.x * R + sub;
-  p.row = (int32_t)row;
-  p.u = u;
-  p.at = row * a.cols + u * kUnit;
-  p.in = row < a.rows && u < units;
-  p.tile_in = row < a.rows && (u & ~7) < units;
-  Unit<XT> h[2], r;
-  Weights w;
-  h[0].zero();
-  r.zero();
-  if (p.in) {
-    h[0].load(a.x, p.at);
-    if (a.residual) r.load(a.residual, p.at);
-    w.load(a.weight, a.wt, u);
-  }
-  if (a.residual) h[0].add(r);
-  if (p.in && a.h) h[0].store(a.h, p.at);
-  float2 ss = both(0.0f);
-  float amax = 0.0f;
+  Place p[U];
+  Unit<XT> h[U][2], r[U];
+  Weights w[U];
 #pragma unroll
-  for (int i = 0; i < kPairs; ++i) {
-    const float2 f = h[0].pair(i);
-    ss = fma2(f, f, ss);
-    if constexpr (SAVE) amax = max3_abs_nan(amax, f.x, f.y);
+  for (int k = 0; k < U; ++k) {
+    p[k].row = (int32_t)row;
+    p[k].u = u + k * T;
+    p[k].at = row * a.cols + p[k].u * kUnit;
+    p[k].in = row < a.rows && p[k].u < units;
+    p[k].tile_in = row < a.rows && (p[k].u & ~7) < units;
+    h[k][0].zero();
+    r[k].zero();
+    if (p[k].in) {
+      h[k][0].load(a.x, p[k].at);
+      if (a.residual) r[k].load(a.residual, p[k].at);
+      w[k].load(a.weight, a.wt, p[k].u);
+    }
+  }
+  float2 ss = both(0.0f);
+  float amax[U];
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    if (a.residual) h[k][0].add(r[k]);
+    if (p[k].in && a.h) h[k][0].store(a.h, p[k].at);
+    amax[k] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      const float2 f = h[k][0].pair(i);
+      ss = fma2(f, f, ss);
+      if constexpr (SAVE) amax[k] = max3_abs_nan(amax[k], f.x, f.y);
+    }
   }
   const float part = ss.x + ss.y;
-  const float sum = L ? lane_sum<L ? L : 1>(part) : team_sum(part, slots, 1, threadIdx.x, blockDim.x);
+  const float sum = L ? lane_sum<L ? L : 1>(part) : team_sum(part, slots, 1, threadIdx.x, T);
   const float rstd = rsqrtf(fmaf(sum, a.inv_cols, a.eps));
-  if (u == 0 && p.in && a.rstd) a.rstd[row] = rstd;
-  float2 y[kPairs];
-  w.floats(a.wt, y);
-  h[0].forget();
+  if (u == 0 && row < a.rows && a.rstd) a.rstd[row] = rstd;
 #pragma unroll
-  for (int i = 0; i < kPairs; ++i) y[i] = mul2(mul2(h[0].pair(i), both(rstd)), y[i]);
-  if constexpr (SAVE) {
-    const uint32_t mc[2] = {tile_max(__float_as_uint(amax)), 0u};
-    uint8_t* const cc[2] = {a.ckpt, nullptr};
-    float* const cs[2] = {a.ckpt_scales, nullptr};
-    cast_store<2, XT>(y, a.y, p, mc, h, cc, cs, a.tiles);
-  } else {
-    cast_store<XT>(y, a.y, p);
+  for (int k = 0; k < U; ++k) {
+    float2 y[kPairs];
+    w[k].floats(a.wt, y);
+    h[k][0].forget();
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) y[i] = mul2(mul2(h[k][0].pair(i), both(rstd)), y[i]);
+    if constexpr (SAVE) {
+      const uint32_t mc[2] = {tile_max(__float_as_uint(amax[k])), 0u};
+      uint8_t* const cc[2] = {a.ckpt, nullptr};
+      float* const cs[2] = {a.ckpt_scales, nullptr};
+      cast_store<2, XT>(y, a.y, p[k], mc, h[k], cc, cs, a.tiles);
+    } else {
+      cast_store<XT>(y, a.y, p[k]);
+    }
   }
 }
 
-template <int XT, int L, bool SAVE>
+template <int XT, int L, int U, bool SAVE>
 mp_status launch_fwd(const NormFwd& a, const RowShape& s, cudaStream_t st) {
   const int64_t groups = (a.rows + s.rows_per_cta - 1) / s.rows_per_cta;  // below 2^31
-  launch_chained(k_norm_fwd<XT, L, SAVE>, dim3((unsigned)groups), dim3(s.threads), 0, st, a);
+  launch_chained(k_norm_fwd<XT, L, U, SAVE>, dim3((unsigned)groups), dim3(L ? kCta : team_of(s, U)), 0, st, a);
   note_launches(1);
   return launch_status();
+}
+
+// Whether a row's CTA takes two units a thread: where more units are then on
+// an SM at a time, at 96 registers a thread (one unit: 64).  16-bit types; for
+// FP32 the two units' registers leave fewer.  [16384 x 5120] BF16 104.6 us
+// with two, 107.6 with one; [10240 x 8192], where as many are resident, 116.6
+// with two, 110.3 with one; FP32 [8192 x 4096] 80.7 and 73.2.
+template <int XT>
+bool two_units(const RowShape& s) {
+  if (XT == XF32) return false;
+  const int one = kRegisters / 64 / s.threads * s.threads, t = team_of(s, 2);
+  return kRegisters / 96 / t * t * 2 > one;
 }
 
 template <int XT, bool SAVE>
 mp_status launch_fwd_shape(const NormFwd& a, cudaStream_t st) {
   const RowShape s = row_shape(a.cols);
-  if (s.lanes == 8) return launch_fwd<XT, 8, SAVE>(a, s, st);
-  if (s.lanes == 16) return launch_fwd<XT, 16, SAVE>(a, s, st);
-  if (s.lanes == 32) return launch_fwd<XT, 32, SAVE>(a, s, st);
-  return launch_fwd<XT, 0, SAVE>(a, s, st);
+  if (s.lanes == 8) return launch_fwd<XT, 8, 1, SAVE>(a, s, st);
+  if (s.lanes == 16) return launch_fwd<XT, 16, 1, SAVE>(a, s, st);
+  if (s.lanes == 32) return launch_fwd<XT, 32, 1, SAVE>(a, s, st);
+  if constexpr (XT != XF32)
+    if (two_units<XT>(s)) return launch_fwd<XT, 0, 2, SAVE>(a, s, st);
+  return launch_fwd<XT, 0, 1, SAVE>(a, s, st);
 }
 template <int XT>
 mp_status launch_fwd_type(const NormFwd& a, cudaStream_t st) {
@@ -476,7 +505,7 @@ mp_status launch_bwd_rows(NormBwd a, const RowShape& s, int* parts, cudaStream_t
   // Rows of whole teams: as many teams as the registers allow, if each has two
   // stages, and no more than spread the rows over all SMs.  Rows in lanes: as
   // many CTAs.  Then as many stages, up to kMaxStages, as shared memory holds.
-  const int team = L ? kCta : (s.threads / U + 31) / 32 * 32;
+  const int team = L ? kCta : team_of(s, U);
   int per_sm = kMaxThreads / U / team;
   if (per_sm > kMaxTeams) per_sm = kMaxTeams;
   while (per_sm > 1 && (2 * bytes + (L ? weights : 0)) * per_sm + weights > kRingBytes) --per_sm;
