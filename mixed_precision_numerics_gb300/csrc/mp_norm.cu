@@ -212,21 +212,26 @@ struct NormBwd {
 };
 
 constexpr int kMaxStages = 4;
-constexpr int kMaxTeams = 8;     // a named barrier each
-constexpr int kRingBytes = 216 * 1024;  // shared memory of an SM for the rings of the CTAs on it
+constexpr int kMaxTeams = 15;    // a named barrier each
+constexpr int kSmemBytes = 224 * 1024;  // shared memory of a CTA that has an SM to itself, its dynamic part
+constexpr int kSmemShared = 216 * 1024; // of all CTAs that share one
 
 __device__ unsigned int g_norm_wait_failures;  // bounded waits that gave up (read by mp_wait_failures)
 
 // A group of rows comes through two rings of shared memory, by when its bytes
-// are done with: `early` (dy, and a checkpoint's codes) before the row's sum,
-// `late` (the stream itself, read before and after the sum, and dh) after it.
-// Bytes of one stage of each, of a group of so many elements.
-template <int XT, bool SAVED>
-__host__ __device__ constexpr int early_bytes(int elements) { return elements * ((XT == XF32 ? 4 : 2) + (SAVED ? 1 : 0)); }
+// are done with: `early` (dy) before the row's sum, `late` (the stream or its
+// codes, read before and after the sum, then dh) after it.  Bytes of one stage
+// of each, of a group of so many elements.
+template <int XT>
+__host__ __device__ constexpr int early_bytes(int elements) { return elements * (XT == XF32 ? 4 : 2); }
 template <int XT, bool SAVED>
 __host__ __device__ constexpr int late_bytes(int elements, bool dh) {
-  return elements * (XT == XF32 ? 4 : 2) * ((SAVED ? 0 : 1) + (dh ? 1 : 0));
+  return elements * ((SAVED ? 1 : XT == XF32 ? 4 : 2) + (dh ? (XT == XF32 ? 4 : 2) : 0));
 }
+
+// Bytes of the weights in binary32, the units a multiple of four so that each
+// 16-byte piece of them starts on a multiple of 64 bytes.
+__host__ __device__ constexpr int weight_bytes(int units) { return (units + 3) / 4 * 4 * kUnit * 4; }
 
 // A CTA holds `teams` of threads (as many as the SM's registers take, where a
 // row needs a whole team; one, where rows lie in a warp's lanes).  A team takes
@@ -240,12 +245,12 @@ __host__ __device__ constexpr int late_bytes(int elements, bool dh) {
 // its teams' sums and writes one row of `parts`.  A thread whose wait gave up
 // works on what it finds and stores nothing more, but keeps meeting the
 // barriers.
-template <int XT, bool SAVED, bool W32, int L, int U>
-__global__ __maxnreg__(U == 2 ? 112 : 64) void k_norm_bwd(const __grid_constant__ NormBwd a) {
+template <int XT, bool SAVED, int L, int U>
+__global__ __maxnreg__(U == 2 ? 128 : 64) void k_norm_bwd(const __grid_constant__ NormBwd a) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float slots[2 * 32];
-  __shared__ uint64_t bars[kMaxTeams * 2 * kMaxStages];
-  constexpr int R = L ? kCta / L : 1, es = XT == XF32 ? 4 : 2;
+  __shared__ uint64_t bars[kMaxTeams * 3 * kMaxStages];
+  constexpr int R = L ? kCta / L : 1, es = XT == XF32 ? 4 : 2, ves = SAVED ? 1 : es;
   const int units = a.cols / kUnit, S = a.stages;
   const int T = L ? kCta : a.team;
   const int team = L ? 0 : __shfl_sync(0xFFFFFFFFu, threadIdx.x / T, 0);  // the same in a warp, and known to be
@@ -253,20 +258,22 @@ __global__ __maxnreg__(U == 2 ? 112 : 64) void k_norm_bwd(const __grid_constant_
   const int u = L ? threadIdx.x % (L ? L : 1) : t, sub = L ? threadIdx.x / (L ? L : 1) : 0;
   // Unit k of a thread is u + k * T; one past the row's end works on the row's
   // last unit and stores nothing.
-  int uc[U];
+  uint32_t eu[U];  // its first element
 #pragma unroll
-  for (int k = 0; k < U; ++k) uc[k] = min(u + k * T, units - 1);
+  for (int k = 0; k < U; ++k) eu[k] = min(u + k * T, units - 1) * kUnit;
   const int group = R * a.cols;  // elements
   const bool ring_dh = a.dh && a.stage_dh;
-  const uint32_t early = early_bytes<XT, SAVED>(group), late = late_bytes<XT, SAVED>(group, ring_dh);
+  const uint32_t early = early_bytes<XT>(group), late = late_bytes<XT, SAVED>(group, ring_dh);
   const uint32_t weights = smem_u32(smem);
-  const uint32_t early0 = weights + a.cols * (W32 ? 4 : 2) + team * S * (early + late), late0 = early0 + S * early;
-  uint64_t* const full = bars + team * 2 * kMaxStages;  // [early or late][stage]
+  const uint32_t early0 = weights + weight_bytes(units) + team * S * (early + late), late0 = early0 + S * early;
+  uint64_t* const full = bars + team * 3 * kMaxStages;  // [early or late][stage]
+  uint64_t* const done = full + 2 * kMaxStages;         // [stage]: each warp has done with the late one
   float* const slot = slots + team * (T >> 5);
   if (t == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&full[kMaxStages + s], 1);
+      mbar_init(&done[s], T >> 5);
     }
     fence_mbar_init();
   }
@@ -281,22 +288,17 @@ __global__ __maxnreg__(U == 2 ? 112 : 64) void k_norm_bwd(const __grid_constant_
     if (from >= rows) return;
     const uint64_t policy = policy_evict_first();
     const uint32_t n = (uint32_t)min(rows - (int32_t)from, R) * a.cols, to = early0 + s * early;
-    mbar_arrive_expect_tx(&full[s], n * es + (SAVED ? n : 0));
+    mbar_arrive_expect_tx(&full[s], n * es);
     bulk_g2s(to, static_cast<const char*>(a.dy) + from * a.cols * es, n * es, &full[s], policy);
-    if constexpr (SAVED) bulk_g2s(to + group * es, a.codes + from * a.cols, n, &full[s], policy);
   };
   auto fetch_late = [&](int s, int64_t from) {
-    if (from >= rows || late == 0) return;
+    if (from >= rows) return;
     const uint64_t policy = policy_evict_first();
-    const uint32_t n = (uint32_t)min(rows - (int32_t)from, R) * a.cols;
-    uint32_t to = late0 + s * late;
+    const uint32_t n = (uint32_t)min(rows - (int32_t)from, R) * a.cols, to = late0 + s * late;
     uint64_t* bar = &full[kMaxStages + s];
-    mbar_arrive_expect_tx(bar, n * es * ((SAVED ? 0 : 1) + (ring_dh ? 1 : 0)));
-    if constexpr (!SAVED) {
-      bulk_g2s(to, static_cast<const char*>(a.h) + from * a.cols * es, n * es, bar, policy);
-      to += group * es;
-    }
-    if (ring_dh) bulk_g2s(to, static_cast<const char*>(a.dh) + from * a.cols * es, n * es, bar, policy);
+    mbar_arrive_expect_tx(bar, n * ves + (ring_dh ? n * es : 0));
+    bulk_g2s(to, (SAVED ? reinterpret_cast<const char*>(a.codes) : static_cast<const char*>(a.h)) + from * a.cols * ves, n * ves, bar, policy);
+    if (ring_dh) bulk_g2s(to + group * ves, static_cast<const char*>(a.dh) + from * a.cols * es, n * es, bar, policy);
   };
   if (t == 0) {
     for (int s = 0; s < S; ++s) {
@@ -304,22 +306,16 @@ __global__ __maxnreg__(U == 2 ? 112 : 64) void k_norm_bwd(const __grid_constant_
       fetch_late(s, row0 + (int64_t)s * step);
     }
   }
-  // The weights in shared memory, as they are where they have the rows' 16-bit
-  // type, else in binary32.
+  // The weights in shared memory, in binary32: 16-byte piece p of unit k at p * pieces + 16 * k.
+  const uint32_t pieces = weight_bytes(units) / 4;
   for (int k = threadIdx.x; k < units; k += blockDim.x) {
     Weights w;
+    float2 f[kPairs];
     w.load(a.weight, a.wt, k);
-    uint4* ws = reinterpret_cast<uint4*>(smem) + k * (W32 ? 4 : 2);
-    if constexpr (W32) {
-      Unit<XF32> f;
-      float2 ff[kPairs];
-      w.floats(a.wt, ff);
+    w.floats(a.wt, f);
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) f.set_pair(i, ff[i]);
-      for (int i = 0; i < 4; ++i) ws[i] = f.v[i];
-    } else {
-      ws[0] = w.v[0], ws[1] = w.v[1];
-    }
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<float4*>(smem + q * pieces + 16 * k) = make_float4(f[2 * q].x, f[2 * q].y, f[2 * q + 1].x, f[2 * q + 1].y);
   }
   __syncthreads();
   float2 acc[U][kPairs];
@@ -335,9 +331,13 @@ __global__ __maxnreg__(U == 2 ? 112 : 64) void k_norm_bwd(const __grid_constant_
     next_rstd = a.rstd[row];
 #pragma unroll
     for (int k = 0; k < U; ++k)
-      if constexpr (SAVED) next_scale[k] = a.scales[row * a.tiles + uc[k] / kTileLanes];
+      if constexpr (SAVED) next_scale[k] = a.scales[row * a.tiles + eu[k] / kTile];
   };
   scalars(row0 + sub);
+  // The elements of a unit's half that this lane works on first, and second:
+  // lanes 4 to 7 of eight begin with the other half, so that the 16-byte reads
+  // of eight lanes, 32 bytes apart, cover all banks.
+  const uint32_t first = threadIdx.x & 4 ? 8 : 0, second = 8 - first;
   int s = 0;
   uint32_t phase = 0, ea = early0, la = late0;  // the stages of this group
   for (int it = 0; row0 < rows; ++it) {
@@ -347,38 +347,41 @@ __global__ __maxnreg__(U == 2 ? 112 : 64) void k_norm_bwd(const __grid_constant_
 #pragma unroll
     for (int k = 0; k < U; ++k) vs[k] = SAVED ? next_scale[k] * rstd : rstd;
     scalars((int64_t)row0 + step + sub);
-    if (ok && !(mbar_wait_bounded(&full[s], phase) && (SAVED || mbar_wait_bounded(&full[kMaxStages + s], phase)))) {
-      ok = false;
-      atomicAdd(&g_norm_wait_failures, 1u);
+    if (ok) ok = mbar_wait_bounded(&full[s], phase) && mbar_wait_bounded(&full[kMaxStages + s], phase);
+    if (t == 0 && ok && S > 1 && it > 0) {  // the late stage of the group before
+      const int before = s == 0 ? S - 1 : s - 1;
+      ok = mbar_wait_bounded(&done[before], s == 0 ? phase ^ 1 : phase);
+      if (ok) fetch_late(before, row0 + (int64_t)(S - 1) * step);
     }
     // a row past the end works on the group's first, whose copy is there
-    uint32_t e[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) e[k] = (L && live ? sub * a.cols : 0) + uc[k] * kUnit;
-    // Half a unit at a time: across the barrier stay the column sums, dy * w,
-    // and a checkpoint's codes.
+    const uint32_t es0 = L && live ? sub * a.cols : 0;
+    // Half a unit at a time, and the stream's values twice: across the barrier
+    // stay the column sums and dy * w.
     float2 g[U][kPairs];
     float dot = 0.0f;
-    uint4 code[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       float2 d = both(0.0f);
-      Unit<XT> dy, v, w;
-      if constexpr (SAVED) code[k] = lds16(ea + group * es + e[k]);
+      Unit<XT> dy, v;
+      Unit<XF32> w;
+      uint2 code;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        dy.take_half(ea + e[k] * es, half);
-        if constexpr (!SAVED) v.take_half(la + e[k] * es, half);
-        Unit<XF32> w32;
-        if constexpr (W32)
-          w32.take_half(weights + uc[k] * (kUnit * 4), half);
+        const uint32_t at = es0 + eu[k] + (half ? second : first);
+        dy.take_half(ea + at * es, half);
+        if constexpr (SAVED)
+          code = lds8(la + at);
         else
-          w.take_half(weights + uc[k] * (kUnit * 2), half);
+          v.take_half(la + at * es, half);
+        const uint32_t wp = weights + (half ? second : first) / 4 * pieces + eu[k];
+        w.v[2 * half] = lds16(wp);
+        w.v[2 * half + 1] = lds16(wp + pieces);
 #pragma unroll
-        for (int i = half * (kPairs / 2); i < (half + 1) * (kPairs / 2); ++i) {
-          const float2 x = mul2(SAVED ? e4m3_floats(code[k], i) : v.pair(i), both(vs[k]));
+        for (int j = 0; j < kPairs / 2; ++j) {
+          const int i = half * (kPairs / 2) + j;
+          const float2 x = mul2(SAVED ? e4m3_floats(j < 2 ? code.x : code.y, j) : v.pair(i), both(vs[k]));
           if (live) acc[k][i] = fma2(dy.pair(i), x, acc[k][i]);
-          g[k][i] = mul2(dy.pair(i), W32 ? w32.pair(i) : w.pair(i));
+          g[k][i] = mul2(dy.pair(i), w.pair(i));
           d = fma2(g[k][i], x, d);
         }
       }
@@ -391,46 +394,49 @@ __global__ __maxnreg__(U == 2 ? 112 : 64) void k_norm_bwd(const __grid_constant_
     } else {
       c = team_sum(c, slot + (it & 1) * 32, team + 1, t, T);
     }
-    if (t == 0 && ok) {
-      fetch_early(s, row0 + (int64_t)S * step);
-      if (S > 1 && it > 0) fetch_late(s == 0 ? S - 1 : s - 1, row0 + (int64_t)(S - 1) * step);
-    }
-    if (ok && SAVED && ring_dh && !mbar_wait_bounded(&full[kMaxStages + s], phase)) {
-      ok = false;
-      atomicAdd(&g_norm_wait_failures, 1u);
-    }
+    if (t == 0 && ok) fetch_early(s, row0 + (int64_t)S * step);
     c *= -a.inv_cols * rstd;
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const bool out = ok && live && u + k * T < units;
-      const int64_t at = ((int64_t)(row0 + sub) * a.cols + (u + k * T) * kUnit) * es;
+      const int64_t to = (int64_t)(row0 + sub) * a.cols + (u + k * T) * kUnit;
       Unit<XT> o, v;
+      uint2 code;
       o.zero();
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
+        const uint32_t h = half ? second : first, at = es0 + eu[k] + h;
         if (ring_dh)
-          o.take_half(la + (SAVED ? 0 : group * es) + e[k] * es, half);
+          o.take_half(la + group * ves + at * es, half);
         else if (a.dh && out)
-          o.load_half(static_cast<const char*>(a.dh) + at, half);
-        if constexpr (!SAVED) v.take_half(la + e[k] * es, half);
+          o.load_half(static_cast<const char*>(a.dh) + (to + h) * es, half);
+        if constexpr (SAVED)
+          code = lds8(la + at);
+        else
+          v.take_half(la + at * es, half);
 #pragma unroll
-        for (int i = half * (kPairs / 2); i < (half + 1) * (kPairs / 2); ++i) {
-          const float2 x = SAVED ? e4m3_floats(code[k], i) : v.pair(i);
+        for (int j = 0; j < kPairs / 2; ++j) {
+          const int i = half * (kPairs / 2) + j;
+          const float2 x = SAVED ? e4m3_floats(j < 2 ? code.x : code.y, j) : v.pair(i);
           o.set_pair(i, fma2(g[k][i], both(rstd), fma2(x, both(c * vs[k]), o.pair(i))));
         }
-        if (out) o.store_half(static_cast<char*>(a.dx) + at, half);
+        if (out) o.store_half(static_cast<char*>(a.dx) + (to + h) * es, half);
       }
     }
-    if (S == 1) {  // one team
-      __syncthreads();
-      if (t == 0 && ok) fetch_late(0, row0 + (int64_t)step);
+    __syncwarp();
+    if ((t & 31) == 0) mbar_arrive(&done[s]);
+    if (t == 0 && ok && S == 1) {
+      ok = mbar_wait_bounded(&done[0], phase);
+      if (ok) fetch_late(0, row0 + (int64_t)step);
     }
     if ((int64_t)row0 + step >= rows) break;  // before the sum could pass 32 bits
     row0 += step;
     ea += early, la += late;
     if (++s == S) s = 0, phase ^= 1, ea = early0, la = late0;
   }
-  if (!ok && t == 0) {  // copies may still be on their way: give each stage's as long again
+  if (!ok) atomicAdd(&g_norm_wait_failures, 1u);
+  if (!ok && t == 0) {
+    // Copies may still be on their way.
     for (int j = 0; j < 2 * kMaxStages; ++j)
       if (j % kMaxStages < S) mbar_drain(&full[j]);
   }
@@ -443,7 +449,7 @@ __global__ __maxnreg__(U == 2 ? 112 : 64) void k_norm_bwd(const __grid_constant_
     float* f = fold + (L ? sub : team) * width + (u + k * T) * kUnit;
 #pragma unroll
     for (int i = 0; i < kPairs; i += 2)
-      *reinterpret_cast<float4*>(f + 2 * i) = make_float4(acc[k][i].x, acc[k][i].y, acc[k][i + 1].x, acc[k][i + 1].y);
+      *reinterpret_cast<float4*>(f + (i < kPairs / 2 ? first : second) + 2 * i % 8) = make_float4(acc[k][i].x, acc[k][i].y, acc[k][i + 1].x, acc[k][i + 1].y);
   }
   __syncthreads();
   for (int col = threadIdx.x; col < a.cols; col += blockDim.x) {
@@ -454,8 +460,7 @@ __global__ __maxnreg__(U == 2 ? 112 : 64) void k_norm_bwd(const __grid_constant_
 }
 
 // dweight[col] = sum over the partial rows: 32 columns a CTA, 8 warps that each
-// sum every 8th partial row, joined in a fixed order.  At 32 registers a CTA
-// fits beside one of the kernel before it, and is there when that one ends.
+// sum every 8th partial row, joined in a fixed order.
 constexpr int kFoldWarps = 8, kFoldLoads = 20;
 __global__ __launch_bounds__(32 * kFoldWarps, 8) void k_norm_dweight(const float* parts, int32_t nparts, int32_t cols,
                                                                      void* dweight, int32_t dt) {
@@ -494,55 +499,47 @@ int64_t parts_of(int64_t rows, int64_t cols) {
   return groups < kMaxParts ? groups : kMaxParts;
 }
 
-template <int XT, bool SAVED, bool W32, int L, int U>
+template <int XT, bool SAVED, int L, int U>
 mp_status launch_bwd_rows(NormBwd a, const RowShape& s, int* parts, cudaStream_t st) {
   static std::atomic<uint64_t> opted{0};
   const int64_t groups = (a.rows + s.rows_per_cta - 1) / s.rows_per_cta;
-  const int weights = a.cols * (W32 ? 4 : 2), elements = s.rows_per_cta * a.cols, early = early_bytes<XT, SAVED>(elements);
-  // FP32 rows of over 13824 without a checkpoint do not fit with dh, which is then read directly.
-  a.stage_dh = a.dh && early + late_bytes<XT, SAVED>(elements, true) + weights <= kRingBytes;
-  const int bytes = early + late_bytes<XT, SAVED>(elements, a.stage_dh);  // with the weights at most 213 KB
-  // Rows of whole teams: as many teams as the registers allow, if each has two
-  // stages, and no more than spread the rows over all SMs.  Rows in lanes: as
-  // many CTAs.  Then as many stages, up to kMaxStages, as shared memory holds.
+  const int weights = weight_bytes(a.cols / kUnit), elements = s.rows_per_cta * a.cols, early = early_bytes<XT>(elements);
+  // FP32 rows of over 14336 without a checkpoint do not fit with dh, which is then read directly.
+  a.stage_dh = a.dh && early + late_bytes<XT, SAVED>(elements, true) + weights <= kSmemBytes;
+  const int bytes = early + late_bytes<XT, SAVED>(elements, a.stage_dh);  // with the weights at most 224 KB
+  // Rows in lanes: as many CTAs on an SM as registers allow.  Rows of whole
+  // teams: one CTA of as many teams, but of no more than spread the rows over
+  // all SMs.  Either so many that each has two stages; then as many stages, up
+  // to kMaxStages, as there is room.
   const int team = L ? kCta : team_of(s, U);
   int per_sm = kMaxThreads / U / team;
-  if (per_sm > kMaxTeams) per_sm = kMaxTeams;
-  while (per_sm > 1 && (2 * bytes + (L ? weights : 0)) * per_sm + weights > kRingBytes) --per_sm;
+  if (L == 0 && per_sm > kMaxTeams) per_sm = kMaxTeams;
+  while (per_sm > 1 && (L ? (2 * bytes + weights) * per_sm > kSmemShared : 2 * bytes * per_sm + weights > kSmemBytes)) --per_sm;
   const int64_t spread = (groups + sm_count() - 1) / sm_count();
   const int teams = L ? 1 : (int)(per_sm < spread ? per_sm : spread);
   a.team = team;
-  a.stages = ((L ? kRingBytes / per_sm : kRingBytes) - weights) / (bytes * teams);
+  a.stages = ((L ? kSmemShared / per_sm : kSmemBytes) - weights) / (bytes * teams);
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   int smem = weights + teams * a.stages * bytes;
   const int fold = (L ? kCta * kUnit : teams * a.cols) * 4;  // the join of the column sums
   if (smem < fold) smem = fold;
-  if (!smem_ok(k_norm_bwd<XT, SAVED, W32, L, U>, smem, opted)) return MP_ECUDA;
+  if (!smem_ok(k_norm_bwd<XT, SAVED, L, U>, smem, opted)) return MP_ECUDA;
   const int grid = resident_grid((groups + teams - 1) / teams, L ? per_sm : 1);
   *parts = grid < kMaxParts ? grid : kMaxParts;
-  launch_chained(k_norm_bwd<XT, SAVED, W32, L, U>, dim3(*parts), dim3(teams * team), smem, st, a);
+  launch_chained(k_norm_bwd<XT, SAVED, L, U>, dim3(*parts), dim3(teams * team), smem, st, a);
   note_launches(1);
   return launch_status();
-}
-
-template <int XT, bool SAVED, bool W32>
-mp_status launch_bwd_shape(const NormBwd& a, int* parts, cudaStream_t st) {
-  const RowShape s = row_shape(a.cols);
-  if (s.lanes == 8) return launch_bwd_rows<XT, SAVED, W32, 8, 1>(a, s, parts, st);
-  if (s.lanes == 16) return launch_bwd_rows<XT, SAVED, W32, 16, 1>(a, s, parts, st);
-  if (s.lanes == 32) return launch_bwd_rows<XT, SAVED, W32, 32, 1>(a, s, parts, st);
-  return launch_bwd_rows<XT, SAVED, W32, 0, 2>(a, s, parts, st);
 }
 
 template <int XT, bool SAVED>
 mp_status launch_bwd(const NormBwd& a, void* dweight, int32_t dt, cudaStream_t st) {
   int parts = 0;
   if (a.rows > 0) {
-    mp_status r;
-    if constexpr (XT == XF32)
-      r = launch_bwd_shape<XT, SAVED, true>(a, &parts, st);
-    else
-      r = a.wt == XT ? launch_bwd_shape<XT, SAVED, false>(a, &parts, st) : launch_bwd_shape<XT, SAVED, true>(a, &parts, st);
+    const RowShape s = row_shape(a.cols);
+    const mp_status r = s.lanes == 8    ? launch_bwd_rows<XT, SAVED, 8, 1>(a, s, &parts, st)
+                        : s.lanes == 16 ? launch_bwd_rows<XT, SAVED, 16, 1>(a, s, &parts, st)
+                        : s.lanes == 32 ? launch_bwd_rows<XT, SAVED, 32, 1>(a, s, &parts, st)
+                                        : launch_bwd_rows<XT, SAVED, 0, 2>(a, s, &parts, st);
     if (r != MP_OK) return r;
   }
   launch_chained(k_norm_dweight, dim3((a.cols + 31) / 32), dim3(32 * kFoldWarps), 0, st, (const float*)a.parts,

@@ -114,10 +114,11 @@ __global__ __launch_bounds__(kThreads) void k_swiglu_bwd(const __grid_constant__
     const uint4 gc = ld_cs(a.codes + p.at), uc = ld_cs(a.codes + a.rows * a.cols + p.at);
     const float gs = __ldcs(a.scales + st), us = __ldcs(a.scales + a.rows * a.tiles.d + st);
     dr.load(a.dp, p.at);
+    const uint32_t gw[4] = {gc.x, gc.y, gc.z, gc.w}, uw[4] = {uc.x, uc.y, uc.z, uc.w};
 #pragma unroll
     for (int k = 0; k < kPairs; ++k) {
-      g[k] = mul2(e4m3_floats(gc, k), both(gs));
-      u[k] = mul2(e4m3_floats(uc, k), both(us));
+      g[k] = mul2(e4m3_floats(gw[k >> 1], k), both(gs));
+      u[k] = mul2(e4m3_floats(uw[k >> 1], k), both(us));
     }
   } else {
     Unit<XT> gr, ur;

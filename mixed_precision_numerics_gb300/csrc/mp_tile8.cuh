@@ -86,6 +86,12 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
   return r;
 }
 
+__device__ __forceinline__ uint2 lds8(uint32_t addr) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr) : "memory");
+  return r;
+}
+
 // ---------------------------------------------------------------------------
 // One unit as loaded: 16 elements of type XT.
 // ---------------------------------------------------------------------------
@@ -110,18 +116,19 @@ struct Unit {
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) st_cs(p + 16 * i, v[i]);
   }
-  // half (0 or 1: 8 elements) of the unit at an address of shared or global memory
+  // A unit in halves of 8 elements: half `half` of this from an address of
+  // shared or global memory.
   __device__ __forceinline__ void take_half(uint32_t addr, int half) {
 #pragma unroll
-    for (int i = half * (kVecs / 2); i < (half + 1) * (kVecs / 2); ++i) v[i] = lds16(addr + 16 * i);
+    for (int i = 0; i < kVecs / 2; ++i) v[half * (kVecs / 2) + i] = lds16(addr + 16 * i);
   }
   __device__ __forceinline__ void load_half(const char* p, int half) {
 #pragma unroll
-    for (int i = half * (kVecs / 2); i < (half + 1) * (kVecs / 2); ++i) v[i] = ld_cs(p + 16 * i);
+    for (int i = 0; i < kVecs / 2; ++i) v[half * (kVecs / 2) + i] = ld_cs(p + 16 * i);
   }
   __device__ __forceinline__ void store_half(char* p, int half) const {
 #pragma unroll
-    for (int i = half * (kVecs / 2); i < (half + 1) * (kVecs / 2); ++i) st_cs(p + 16 * i, v[i]);
+    for (int i = 0; i < kVecs / 2; ++i) st_cs(p + 16 * i, v[half * (kVecs / 2) + i]);
   }
   __device__ __forceinline__ uint32_t word(int k) const {  // k a constant after unrolling
     const uint4 q = v[k >> 2];
@@ -384,9 +391,9 @@ __device__ __forceinline__ void cast_store(const float2 (&y)[kPairs], const Fp8O
   cast_store<1, XT>(y, o, p, mc, raw, cc, cs, 0);
 }
 
-// Values of E4M3 codes 2k and 2k + 1 of a unit, exact (through binary16).
-__device__ __forceinline__ float2 e4m3_floats(const uint4& c, int k) {
-  const uint32_t w = (k >> 1) == 0 ? c.x : (k >> 1) == 1 ? c.y : (k >> 1) == 2 ? c.z : c.w;
+// Values of the two E4M3 codes in the low (k even) or high half of a word,
+// exact (through binary16).
+__device__ __forceinline__ float2 e4m3_floats(uint32_t w, int k) {
   uint32_t h;
   asm volatile("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)(w >> (16 * (k & 1)))));
   return make_float2(f16lo(h), f16hi(h));
