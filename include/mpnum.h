@@ -421,7 +421,7 @@ MP_API mp_status mx_quantize(const void* x, mp_dtype x_dtype, int64_t rows, int6
  * ckpt_scales) may be NULL; a checkpoint needs both its pointers.  h may be x
  * or residual.  weight [cols].  eps finite and >= 0; a row of zeros with eps 0
  * has rstd = inf and gives NaN codes.  A row whose sum of squares exceeds
- * binary32 has rstd = 0.  cols <= 16384, rows < 2^31 (else MP_ESHAPE).  rows
+ * binary32 has rstd = 0.  cols <= 16384, rows <= 2^31 - 32 (else MP_ESHAPE).  rows
  * or cols 0: nothing is written.  One kernel launch. */
 MP_API mp_status rmsnorm_residual_fp8(const void* x, const void* residual, mp_dtype x_dtype, int64_t rows,
                                       int64_t cols, const void* weight, mp_dtype w_dtype, float eps, void* h,

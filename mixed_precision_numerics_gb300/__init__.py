@@ -171,13 +171,27 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
-def _stream(stream) -> int | None:
+_CUDA: tuple = ()
+
+
+def _cuda() -> tuple:
+    """The functions that give the current device's number and a device's current
+    stream handle, and torch.float32.  The handle comes without a Stream object
+    around it, whose making takes longer than a small kernel."""
+    global _CUDA
     import torch
 
+    _CUDA = (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+             getattr(torch._C, "_cuda_getCurrentRawStream", lambda d: torch.cuda.current_stream(d).cuda_stream),
+             torch.float32)
+    return _CUDA
+
+
+def _stream(stream) -> int | None:
     if stream is None:
-        # the current stream's handle without a Stream object around it, whose making costs more than a small kernel
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
+        import torch
+
+        return (_CUDA or _cuda())[1](torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -517,18 +531,15 @@ def _pair(a, b, names: tuple[str, str], rows: int, cols: int, like, dev: int) ->
     return pa, pb, ld
 
 
-def _current_device(t) -> int:
-    """The current device's number; -2, which no tensor is on, for a host tensor
-    (so that its check fails without a GPU being needed)."""
-    import torch
-
-    return torch.cuda.current_device() if t.is_cuda else -2
-
-
-def _float32():
-    import torch
-
-    return torch.float32
+def _where(t, stream) -> tuple:
+    """(current device number, stream handle, torch.float32) of a call on `t`; for
+    a host tensor a device that no tensor is on, so that its check fails without
+    a GPU being needed."""
+    device, current, f32 = _CUDA or _cuda()
+    if not t.is_cuda:
+        return -2, None, f32
+    dev = device()
+    return dev, current(dev) if stream is None else _stream(stream), f32
 
 
 def rmsnorm_residual_fp8(x, weight, y, y_scales, *, residual=None, h=None, rstd=None, ckpt=None, ckpt_scales=None,
@@ -538,7 +549,7 @@ def rmsnorm_residual_fp8(x, weight, y, y_scales, *, residual=None, h=None, rstd=
     elements.  h (as x), rstd (float32 [rows]) and ckpt (rows*cols bytes, with ckpt_scales float32
     [rows, ceil(cols/128)]) are outputs the backward pass reads; each may be None."""
     rows, cols = x.shape
-    dt, dev, n = x.dtype, _current_device(x), rows * cols
+    (dev, at, f32), dt, n = _where(x, stream), x.dtype, rows * cols
     nb, tile_bytes = n * x.element_size(), 4 * rows * -(-cols // 128)
     scale_bytes, scale_align = (n // 32, 1) if scale_block == 32 else (tile_bytes, 4)
     _check("rmsnorm_residual_fp8",
@@ -547,9 +558,8 @@ def rmsnorm_residual_fp8(x, weight, y, y_scales, *, residual=None, h=None, rstd=
                                     _dtype_code(weight), eps, _in(h, "h", nb, x, dev, dt), _in(y, "y", n, x, dev),
                                     fp8_dtype, scale_block,
                                     _in(y_scales, "y_scales", scale_bytes, x, dev, None, scale_align),
-                                    _in(rstd, "rstd", 4 * rows, x, dev, _float32(), 4), _in(ckpt, "ckpt", n, x, dev),
-                                    _in(ckpt_scales, "ckpt_scales", tile_bytes, x, dev, _float32(), 4),
-                                    _stream(stream)))
+                                    _in(rstd, "rstd", 4 * rows, x, dev, f32, 4), _in(ckpt, "ckpt", n, x, dev),
+                                    _in(ckpt_scales, "ckpt_scales", tile_bytes, x, dev, f32, 4), at))
 
 
 def rmsnorm_workspace_size(rows: int, cols: int) -> int:
@@ -568,19 +578,19 @@ def rmsnorm_residual_backward(dy, weight, rstd, dx, dweight, workspace, *, h=Non
     """dx (as dy) and dweight ([cols], any of the three float types) from dy, rstd and the stream: either h
     or its 8-bit checkpoint (ckpt, ckpt_scales).  dh: the gradient reaching the stream from above, or None."""
     rows, cols = dy.shape
-    dt, dev, n = dy.dtype, _current_device(dy), rows * cols
+    (dev, at, f32), dt, n = _where(dy, stream), dy.dtype, rows * cols
     nb = n * dy.element_size()
     _check("rmsnorm_residual_backward",
            lib.rmsnorm_residual_backward(_in(dy, "dy", nb, dy, dev), _in(dh, "dh", nb, dy, dev, dt), _dtype_code(dy),
                                          rows, cols, _in(h, "h", nb, dy, dev, dt), _in(ckpt, "ckpt", n, dy, dev),
                                          _in(ckpt_scales, "ckpt_scales", 4 * rows * -(-cols // 128), dy, dev,
-                                             _float32(), 4),
+                                             f32, 4),
                                          _in(weight, "weight", cols * weight.element_size(), dy, dev),
-                                         _dtype_code(weight), _in(rstd, "rstd", 4 * rows, dy, dev, _float32(), 4),
+                                         _dtype_code(weight), _in(rstd, "rstd", 4 * rows, dy, dev, f32, 4),
                                          _in(dx, "dx", nb, dy, dev, dt),
                                          _in(dweight, "dweight", cols * dweight.element_size(), dy, dev),
                                          _dtype_code(dweight), _in(workspace, "workspace", 0, dy, dev),
-                                         0 if workspace is None else workspace.nbytes, _stream(stream)))
+                                         0 if workspace is None else workspace.nbytes, at))
 
 
 def swiglu_fp8(gate, up, y, y_scales, *, ckpt=None, ckpt_scales=None, fp8_dtype: int = MP_E4M3,
@@ -588,7 +598,7 @@ def swiglu_fp8(gate, up, y, y_scales, *, ckpt=None, ckpt_scales=None, fp8_dtype:
     """y = FP8 of silu(gate) * up.  gate, up: [rows, cols], each may be a column range of one wider
     matrix; ckpt: 2*rows*cols bytes (gate's codes, then up's), ckpt_scales: float32 [2, rows, ceil(cols/128)]."""
     rows, cols = gate.shape
-    dev, n = _current_device(gate), rows * cols
+    (dev, at, f32), n = _where(gate, stream), rows * cols
     tile_bytes = 4 * rows * -(-cols // 128)
     scale_bytes, scale_align = (n // 32, 1) if scale_block == 32 else (tile_bytes, 4)
     pg, pu, ld = _pair(gate, up, ("gate", "up"), rows, cols, gate, dev)
@@ -596,14 +606,14 @@ def swiglu_fp8(gate, up, y, y_scales, *, ckpt=None, ckpt_scales=None, fp8_dtype:
            lib.swiglu_fp8(pg, pu, ld, _dtype_code(gate), rows, cols, _in(y, "y", n, gate, dev), fp8_dtype, scale_block,
                           _in(y_scales, "y_scales", scale_bytes, gate, dev, None, scale_align),
                           _in(ckpt, "ckpt", 2 * n, gate, dev),
-                          _in(ckpt_scales, "ckpt_scales", 2 * tile_bytes, gate, dev, _float32(), 4), _stream(stream)))
+                          _in(ckpt_scales, "ckpt_scales", 2 * tile_bytes, gate, dev, f32, 4), at))
 
 
 def swiglu_backward(dp, dgate, dup, *, gate=None, up=None, ckpt=None, ckpt_scales=None, stream=None) -> None:
     """dgate, dup from dp and either gate and up or their 8-bit checkpoint of swiglu_fp8.  dgate and dup
     ([rows, cols]) may be column ranges of one wider matrix, as gate and up may."""
     rows, cols = dp.shape
-    dev, n = _current_device(dp), rows * cols
+    (dev, at, f32), n = _where(dp, stream), rows * cols
     pg, pu, ld = None, None, cols
     if gate is not None and up is not None:
         pg, pu, ld = _pair(gate, up, ("gate", "up"), rows, cols, dp, dev)
@@ -613,8 +623,8 @@ def swiglu_backward(dp, dgate, dup, *, gate=None, up=None, ckpt=None, ckpt_scale
     _check("swiglu_backward",
            lib.swiglu_backward(_in(dp, "dp", n * dp.element_size(), dp, dev), _dtype_code(dp), rows, cols, pg, pu, ld,
                                _in(ckpt, "ckpt", 2 * n, dp, dev),
-                               _in(ckpt_scales, "ckpt_scales", 8 * rows * -(-cols // 128), dp, dev, _float32(), 4),
-                               pdg, pdu, d_ld, _stream(stream)))
+                               _in(ckpt_scales, "ckpt_scales", 8 * rows * -(-cols // 128), dp, dev, f32, 4),
+                               pdg, pdu, d_ld, at))
 
 
 __all__ = [

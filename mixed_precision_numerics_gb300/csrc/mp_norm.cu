@@ -30,6 +30,7 @@ namespace {
 constexpr int kCta = 256;           // threads of a CTA that takes several rows at a time
 constexpr int kMaxThreads = 1024;   // threads of a CTA that takes one row at a time
 constexpr int kMaxCols = kMaxThreads * kUnit;
+constexpr int64_t kMaxRows = (1ll << 31) - 32;  // a row's number and that of its group's last are 32-bit
 constexpr int kRegisters = 65536;   // of an SM
 constexpr int kMaxParts = 608;      // partial sums of dweight: four CTAs on each of 152 SMs
 
@@ -572,7 +573,7 @@ extern "C" MP_API mp_status rmsnorm_residual_fp8(const void* x, const void* resi
   if (fp8_dtype != MP_E4M3 && fp8_dtype != MP_E5M2) return MP_EINVAL;
   if (scale_block != 128 && scale_block != 32) return MP_EINVAL;
   if (!(eps >= 0.0f && eps < INFINITY)) return MP_EINVAL;
-  if (rows >= (1ll << 31) || cols > kMaxCols || cols % (scale_block == 32 ? 32 : 16) != 0) return MP_ESHAPE;
+  if (rows > kMaxRows || cols > kMaxCols || cols % (scale_block == 32 ? 32 : 16) != 0) return MP_ESHAPE;
   if (rows == 0 || cols == 0) return MP_OK;
   if (!x || !weight || !y || !y_scales || (!ckpt != !ckpt_scales)) return MP_EINVAL;
   if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(h) || !aligned16(y) ||
@@ -607,7 +608,7 @@ extern "C" MP_API mp_status rmsnorm_residual_backward(const void* dy, const void
   using namespace mp;
   if (rows < 0 || cols < 0) return MP_EINVAL;
   if (!float_type(x_dtype) || !float_type(w_dtype) || !float_type(dw_dtype)) return MP_EINVAL;
-  if (rows >= (1ll << 31) || cols > kMaxCols || cols % 16 != 0) return MP_ESHAPE;
+  if (rows > kMaxRows || cols > kMaxCols || cols % 16 != 0) return MP_ESHAPE;
   if (cols == 0) return MP_OK;
   if (!dweight) return MP_EINVAL;
   if (!aligned16(dweight)) return MP_EALIGN;

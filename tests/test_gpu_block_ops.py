@@ -558,6 +558,61 @@ def test_calls_on_another_stream_and_in_a_graph():
         assert_bits(a, b, "replayed output")
 
 
+def test_offsets_beyond_32_bits():
+    """A tensor of more than 2^32 elements: its last rows are what a call on them alone gives."""
+    rows, cols, tail = 2**18 + 37, 16384, 40
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[-tail:] = normal(95, tail, cols, dtype=torch.bfloat16)
+    last, w = x[-tail:].clone(), normal(96, cols)
+    y = torch.empty(rows, cols, dtype=torch.uint8, device="cuda")
+    ys, cs = (torch.empty(rows, 128, device="cuda") for _ in range(2))
+    ckpt, rstd = torch.empty_like(y), torch.empty(rows, device="cuda")
+    M.rmsnorm_residual_fp8(x, w, y, ys, rstd=rstd, ckpt=ckpt, ckpt_scales=cs)
+    o = norm(last, w)
+    for got, key in ((y, "y"), (ys, "y_scales"), (rstd, "rstd"), (ckpt, "ckpt"), (cs, "ckpt_scales")):
+        assert_bits(got[-tail:], o[key], key)
+    assert not (y[:-tail] & 0x7F).any()  # zeros, signed as their weights
+    del y, ys
+    dx, dw = torch.empty_like(x), torch.empty(cols, device="cuda")
+    M.rmsnorm_residual_backward(x, w, rstd, dx, dw, M.new_rmsnorm_workspace(rows, cols), ckpt=ckpt, ckpt_scales=cs)
+    want, want_w = norm_backward(last, w, o["rstd"], ckpt=o["ckpt"], scales=o["ckpt_scales"])
+    assert_bits(dx[-tail:], want, "dx")
+    # other rows add zeros, in other chains of additions
+    mag = (last.double() * dequantise(o["ckpt"], o["ckpt_scales"]) * o["rstd"].double()[:, None]).abs().sum(0)
+    assert bool(((dw.double() - want_w.double()).abs() <= 2 * (tail + 64) * EPS * mag).all())
+    del ckpt, cs, rstd
+    half = cols // 2
+    g, u = x[:, :half], x[:, half:]
+    y, ys = torch.empty(rows, half, dtype=torch.uint8, device="cuda"), torch.empty(rows, 64, device="cuda")
+    ckpt, cs = torch.empty(2, rows, half, dtype=torch.uint8, device="cuda"), torch.empty(2, rows, 64, device="cuda")
+    M.swiglu_fp8(g, u, y, ys, ckpt=ckpt, ckpt_scales=cs)
+    o = swiglu(last[:, :half], last[:, half:])
+    assert_bits(y[-tail:], o["y"], "codes")
+    assert_bits(ckpt[:, -tail:], o["ckpt"], "checkpoint codes")
+    assert_bits(cs[:, -tail:], o["ckpt_scales"], "checkpoint scales")
+    dp = torch.zeros(rows, half, dtype=torch.bfloat16, device="cuda")
+    dp[-tail:] = last[:, half:]
+    M.swiglu_backward(dp, dx[:, :half], dx[:, half:], ckpt=ckpt, ckpt_scales=cs)
+    dg, du = swiglu_backward(dp[-tail:].clone(), ckpt=o["ckpt"], ckpt_scales=o["ckpt_scales"])
+    assert_bits(dx[-tail:, :half], dg, "dgate")
+    assert_bits(dx[-tail:, half:], du, "dup")
+    assert not dx[:-tail].any()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_every_nan_written_in_16_bits_is_the_canonical_one(dtype):
+    dt = TYPES[dtype]
+    x, r = normal(97, 2, 128, dtype=dt), normal(98, 2, 128, dtype=dt)
+    x[0, 3], x[1, 5], r[1, 5] = -float("nan"), float("inf"), float("-inf")
+    w = torch.ones(128, device="cuda")
+    o = norm(x, w, residual=r)
+    assert int(bits(o["h"])[0, 3]) == 0x7FFF and int(bits(o["h"])[1, 5]) == 0x7FFF
+    dx, _ = norm_backward(x, w, o["rstd"], h=o["h"])
+    assert bool((bits(dx) == 0x7FFF).all())
+    dg, du = swiglu_backward(x, gate=o["h"], up=r)
+    assert int(bits(dg)[0, 3]) == 0x7FFF and int(bits(du)[1, 5]) == 0x7FFF
+
+
 def test_refusals_launch_nothing():
     x, w = normal(90, 4, 256, dtype=torch.bfloat16), normal(91, 256)
     y, ys, rstd = torch.empty(4, 256, dtype=torch.uint8, device="cuda"), torch.empty(4, 2, device="cuda"), torch.empty(4, device="cuda")
