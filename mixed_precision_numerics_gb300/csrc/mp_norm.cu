@@ -54,6 +54,19 @@ int resident_grid(int64_t groups, int per_sm) {
   return (int)(groups < most ? groups : most);
 }
 
+// Asks for the largest share of an SM's memory as shared memory, once a device.
+template <typename K>
+bool carveout_opt_in(K kernel, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0;
+  if (bit && (done.load(std::memory_order_acquire) & bit)) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+    return false;
+  if (bit) done.fetch_or(bit, std::memory_order_release);
+  return true;
+}
+
 // Raises a kernel's dynamic shared-memory limit where a launch may need more
 // than the default: 48 KB, the kernel's static arrays included.
 template <typename K>
@@ -168,16 +181,15 @@ mp_status launch_fwd(const NormFwd& a, const RowShape& s, cudaStream_t st) {
   return launch_status();
 }
 
-// Whether a row's CTA takes two units a thread: where more units are then on
-// an SM at a time, at 96 registers a thread (one unit: 64).  16-bit types; for
+// Whether a row's CTA takes two units a thread: where more rows are then on an
+// SM at a time, at 96 registers a thread (one unit: 64).  16-bit types; for
 // FP32 the two units' registers leave fewer.  [16384 x 5120] BF16 104.6 us
 // with two, 107.6 with one; [10240 x 8192], where as many are resident, 116.6
 // with two, 110.3 with one; FP32 [8192 x 4096] 80.7 and 73.2.
 template <int XT>
 bool two_units(const RowShape& s) {
   if (XT == XF32) return false;
-  const int one = kRegisters / 64 / s.threads * s.threads, t = team_of(s, 2);
-  return kRegisters / 96 / t * t * 2 > one;
+  return kRegisters / 96 / team_of(s, 2) > kRegisters / 64 / s.threads;
 }
 
 template <int XT, bool SAVE>
@@ -307,24 +319,6 @@ __global__ __maxnreg__(U == 2 ? 128 : 64) void k_norm_bwd(const __grid_constant_
       fetch_late(s, row0 + (int64_t)s * step);
     }
   }
-  // The weights in shared memory, in binary32: 16-byte piece p of unit k at p * pieces + 16 * k.
-  const uint32_t pieces = weight_bytes(units) / 4;
-  for (int k = threadIdx.x; k < units; k += blockDim.x) {
-    Weights w;
-    float2 f[kPairs];
-    w.load(a.weight, a.wt, k);
-    w.floats(a.wt, f);
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      *reinterpret_cast<float4*>(smem + q * pieces + 16 * k) = make_float4(f[2 * q].x, f[2 * q].y, f[2 * q + 1].x, f[2 * q + 1].y);
-  }
-  __syncthreads();
-  float2 acc[U][kPairs];
-#pragma unroll
-  for (int k = 0; k < U; ++k)
-#pragma unroll
-    for (int i = 0; i < kPairs; ++i) acc[k][i] = both(0.0f);
-  bool ok = true;
   // The row's scalars are read one group ahead.
   float next_rstd = 0.0f, next_scale[U];
   auto scalars = [&](int64_t row) {
@@ -335,6 +329,35 @@ __global__ __maxnreg__(U == 2 ? 128 : 64) void k_norm_bwd(const __grid_constant_
       if constexpr (SAVED) next_scale[k] = a.scales[row * a.tiles + eu[k] / kTile];
   };
   scalars(row0 + sub);
+  // The weights in shared memory, in binary32: 16-byte piece p of unit k at p * pieces + 16 * k.
+  const uint32_t pieces = weight_bytes(units) / 4;
+  {
+    Weights w[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int k = threadIdx.x + j * blockDim.x;
+      if (k < units) w[j].load(a.weight, a.wt, k);
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int k = threadIdx.x + j * blockDim.x;
+      float2 f[kPairs];
+      w[j].floats(a.wt, f);
+      if (k < units) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<float4*>(smem + q * pieces + 16 * k) =
+              make_float4(f[2 * q].x, f[2 * q].y, f[2 * q + 1].x, f[2 * q + 1].y);
+      }
+    }
+  }
+  __syncthreads();
+  float2 acc[U][kPairs];
+#pragma unroll
+  for (int k = 0; k < U; ++k)
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) acc[k][i] = both(0.0f);
+  bool ok = true;
   // The elements of a unit's half that this lane works on first, and second:
   // lanes 4 to 7 of eight begin with the other half, so that the 16-byte reads
   // of eight lanes, 32 bytes apart, cover all banks.
@@ -453,10 +476,13 @@ __global__ __maxnreg__(U == 2 ? 128 : 64) void k_norm_bwd(const __grid_constant_
       *reinterpret_cast<float4*>(f + (i < kPairs / 2 ? first : second) + 2 * i % 8) = make_float4(acc[k][i].x, acc[k][i].y, acc[k][i + 1].x, acc[k][i + 1].y);
   }
   __syncthreads();
-  for (int col = threadIdx.x; col < a.cols; col += blockDim.x) {
-    float v = 0.0f;
-    for (int j = 0; j < deep; ++j) v += fold[j * width + col];
-    a.parts[(int64_t)blockIdx.x * a.cols + col] = v;
+  for (int col = 4 * threadIdx.x; col < a.cols; col += 4 * blockDim.x) {
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int j = 0; j < deep; ++j) {
+      const float4 x = *reinterpret_cast<const float4*>(fold + j * width + col);
+      v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+    }
+    *reinterpret_cast<float4*>(a.parts + (int64_t)blockIdx.x * a.cols + col) = v;
   }
 }
 
@@ -525,6 +551,8 @@ mp_status launch_bwd_rows(NormBwd a, const RowShape& s, int* parts, cudaStream_t
   const int fold = (L ? kCta * kUnit : teams * a.cols) * 4;  // the join of the column sums
   if (smem < fold) smem = fold;
   if (!smem_ok(k_norm_bwd<XT, SAVED, L, U>, smem, opted)) return MP_ECUDA;
+  static std::atomic<uint64_t> split{0};
+  if (!carveout_opt_in(k_norm_bwd<XT, SAVED, L, U>, split)) return MP_ECUDA;
   const int grid = resident_grid((groups + teams - 1) / teams, L ? per_sm : 1);
   *parts = grid < kMaxParts ? grid : kMaxParts;
   launch_chained(k_norm_bwd<XT, SAVED, L, U>, dim3(*parts), dim3(teams * team), smem, st, a);
@@ -543,6 +571,10 @@ mp_status launch_bwd(const NormBwd& a, void* dweight, int32_t dt, cudaStream_t s
                                         : launch_bwd_rows<XT, SAVED, 0, 2>(a, s, &parts, st);
     if (r != MP_OK) return r;
   }
+  // The same split of L1 and shared memory as the kernel before: an SM changes
+  // it only when it is empty.
+  static std::atomic<uint64_t> split{0};
+  if (!carveout_opt_in(k_norm_dweight, split)) return MP_ECUDA;
   launch_chained(k_norm_dweight, dim3((a.cols + 31) / 32), dim3(32 * kFoldWarps), 0, st, (const float*)a.parts,
                  (int32_t)parts, a.cols, dweight, dt);
   note_launches(1);
