@@ -358,6 +358,7 @@ __global__ __maxnreg__(U == 2 ? 128 : 64) void k_norm_bwd(const __grid_constant_
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) acc[k][i] = both(0.0f);
   bool ok = true;
+  const bool second_unit = U > 1 && __any_sync(0xFFFFFFFFu, u + T < units);  // of any lane of the warp
   // The elements of a unit's half that this lane works on first, and second:
   // lanes 4 to 7 of eight begin with the other half, so that the 16-byte reads
   // of eight lanes, 32 bytes apart, cover all banks.
@@ -385,6 +386,7 @@ __global__ __maxnreg__(U == 2 ? 128 : 64) void k_norm_bwd(const __grid_constant_
     float dot = 0.0f;
 #pragma unroll
     for (int k = 0; k < U; ++k) {
+      if (k > 0 && !second_unit) break;
       float2 d = both(0.0f);
       Unit<XT> dy, v;
       Unit<XF32> w;
@@ -422,6 +424,7 @@ __global__ __maxnreg__(U == 2 ? 128 : 64) void k_norm_bwd(const __grid_constant_
     c *= -a.inv_cols * rstd;
 #pragma unroll
     for (int k = 0; k < U; ++k) {
+      if (k > 0 && !second_unit) break;
       const bool out = ok && live && u + k * T < units;
       const int64_t to = (int64_t)(row0 + sub) * a.cols + (u + k * T) * kUnit;
       Unit<XT> o, v;
@@ -486,10 +489,10 @@ __global__ __maxnreg__(U == 2 ? 128 : 64) void k_norm_bwd(const __grid_constant_
   }
 }
 
-// dweight[col] = sum over the partial rows: 32 columns a CTA, 8 warps that each
-// sum every 8th partial row, joined in a fixed order.
-constexpr int kFoldWarps = 8, kFoldLoads = 20;
-__global__ __launch_bounds__(32 * kFoldWarps, 8) void k_norm_dweight(const float* parts, int32_t nparts, int32_t cols,
+// dweight[col] = sum over the partial rows: 32 columns a CTA, 16 warps that each
+// sum every 16th partial row, joined in a fixed order.
+constexpr int kFoldWarps = 16, kFoldLoads = 20;
+__global__ __launch_bounds__(32 * kFoldWarps, 4) void k_norm_dweight(const float* parts, int32_t nparts, int32_t cols,
                                                                      void* dweight, int32_t dt) {
   __shared__ float s[kFoldWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
