@@ -31,7 +31,6 @@ constexpr int kCta = 256;           // threads of a CTA that takes several rows 
 constexpr int kMaxThreads = 1024;   // threads of a CTA that takes one row at a time
 constexpr int kMaxCols = kMaxThreads * kUnit;
 constexpr int64_t kMaxRows = (1ll << 31) - 32;  // a row's number and that of its group's last are 32-bit
-constexpr int kRegisters = 65536;   // of an SM
 constexpr int kMaxParts = 608;      // partial sums of dweight: four CTAs on each of 152 SMs
 
 // How a row is laid over threads, by its length alone: `lanes` of a warp (8,
@@ -109,9 +108,14 @@ struct NormFwd {
 };
 
 // A row lies in L lanes of a warp or (L = 0) in the CTA, U units a thread: unit
-// k of thread t is t + k * threads.
+// k of thread t is t + k * threads.  Rows of a CTA take two units a thread for
+// the 16-bit types: their weights are read after the row's sum, which leaves 64
+// registers and 2048 units, two rows of 16384, on an SM.  (With one unit a
+// thread half as many are there: [16384 x 5120] BF16 107.6 us against 99.0,
+// [7000 x 16384] 163.7 against 137.7.  For FP32 the two units' registers do not
+// leave room for more rows: [8192 x 4096] 73.2 us with one unit, 80.7 with two.)
 template <int XT, int L, int U, bool SAVE>
-__global__ __launch_bounds__(L ? kCta : kMaxThreads / U) void k_norm_fwd(const __grid_constant__ NormFwd a) {
+__global__ __launch_bounds__(L ? kCta : kMaxThreads / U, L ? 1 : U) void k_norm_fwd(const __grid_constant__ NormFwd a) {
   __shared__ float slots[32];
   chain_wait();
   chain_release();
@@ -121,7 +125,7 @@ __global__ __launch_bounds__(L ? kCta : kMaxThreads / U) void k_norm_fwd(const _
   const int64_t row = (int64_t)blockIdx.x * R + sub;
   Place p[U];
   Unit<XT> h[U][2], r[U];
-  Weights w[U];
+  Weights w;
 #pragma unroll
   for (int k = 0; k < U; ++k) {
     p[k].row = (int32_t)row;
@@ -134,7 +138,7 @@ __global__ __launch_bounds__(L ? kCta : kMaxThreads / U) void k_norm_fwd(const _
     if (p[k].in) {
       h[k][0].load(a.x, p[k].at);
       if (a.residual) r[k].load(a.residual, p[k].at);
-      w[k].load(a.weight, a.wt, p[k].u);
+      if constexpr (U == 1) w.load(a.weight, a.wt, p[k].u);
     }
   }
   float2 ss = both(0.0f);
@@ -157,8 +161,10 @@ __global__ __launch_bounds__(L ? kCta : kMaxThreads / U) void k_norm_fwd(const _
   if (u == 0 && row < a.rows && a.rstd) a.rstd[row] = rstd;
 #pragma unroll
   for (int k = 0; k < U; ++k) {
+    if (k > 0 && !__any_sync(0xFFFFFFFFu, p[k].in)) break;  // no lane of the warp has a second unit
     float2 y[kPairs];
-    w[k].floats(a.wt, y);
+    if constexpr (U > 1) w.load(a.weight, a.wt, min(p[k].u, units - 1));
+    w.floats(a.wt, y);
     h[k][0].forget();
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) y[i] = mul2(mul2(h[k][0].pair(i), both(rstd)), y[i]);
@@ -181,26 +187,13 @@ mp_status launch_fwd(const NormFwd& a, const RowShape& s, cudaStream_t st) {
   return launch_status();
 }
 
-// Whether a row's CTA takes two units a thread: where more rows are then on an
-// SM at a time, at 96 registers a thread (one unit: 64).  16-bit types; for
-// FP32 the two units' registers leave fewer.  [16384 x 5120] BF16 104.6 us
-// with two, 107.6 with one; [10240 x 8192], where as many are resident, 116.6
-// with two, 110.3 with one; FP32 [8192 x 4096] 80.7 and 73.2.
-template <int XT>
-bool two_units(const RowShape& s) {
-  if (XT == XF32) return false;
-  return kRegisters / 96 / team_of(s, 2) > kRegisters / 64 / s.threads;
-}
-
 template <int XT, bool SAVE>
 mp_status launch_fwd_shape(const NormFwd& a, cudaStream_t st) {
   const RowShape s = row_shape(a.cols);
   if (s.lanes == 8) return launch_fwd<XT, 8, 1, SAVE>(a, s, st);
   if (s.lanes == 16) return launch_fwd<XT, 16, 1, SAVE>(a, s, st);
   if (s.lanes == 32) return launch_fwd<XT, 32, 1, SAVE>(a, s, st);
-  if constexpr (XT != XF32)
-    if (two_units<XT>(s)) return launch_fwd<XT, 0, 2, SAVE>(a, s, st);
-  return launch_fwd<XT, 0, 1, SAVE>(a, s, st);
+  return launch_fwd<XT, 0, XT == XF32 ? 1 : 2, SAVE>(a, s, st);
 }
 template <int XT>
 mp_status launch_fwd_type(const NormFwd& a, cudaStream_t st) {

@@ -199,17 +199,20 @@ struct Unit {
 };
 
 // 16 weights of a vector of any of the three types (a uniform branch), as
-// stored.  The vector is read again for every row: default caching keeps it in L1.
+// stored.  The vector is read again for every row: default caching keeps it in
+// L1.  The loads are volatile so that they stay where they are written, early
+// to be in flight or late to be in registers only while they are used.
 struct Weights {
   uint4 v[4];
+  __device__ __forceinline__ static uint4 load16(const uint4* p) {
+    uint4 r;
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+  }
   __device__ __forceinline__ void load(const void* w, int wt, int u) {
-    const uint4* p = static_cast<const uint4*>(w);
-    if (wt == XF32) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = __ldg(p + u * 4 + i);
-    } else {
-      v[0] = __ldg(p + u * 2), v[1] = __ldg(p + u * 2 + 1);
-    }
+    const uint4* p = static_cast<const uint4*>(w) + u * (wt == XF32 ? 4 : 2);
+    v[0] = load16(p), v[1] = load16(p + 1);
+    if (wt == XF32) v[2] = load16(p + 2), v[3] = load16(p + 3);
   }
   __device__ __forceinline__ void floats(int wt, float2 (&f)[kPairs]) const {
     if (wt == XF32) {
