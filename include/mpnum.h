@@ -450,7 +450,8 @@ MP_API mp_status rmsnorm_residual_backward(const void* dy, const void* dh, mp_dt
  * one product have ld = 2 * cols): ld >= cols and rows 16-byte aligned where
  * rows > 1 (else MP_ESHAPE).  ckpt (may be NULL, with ckpt_scales): gate's
  * and then up's checkpoint, [2][rows][cols] codes and [2][rows][ceil(cols/128)]
- * scales.  rows, cols < 2^31.  One kernel launch. */
+ * scales.  rows < 2^31, cols <= 2^31 - 128, and below 2^31 - 32 tiles in all
+ * (else MP_ESHAPE).  One kernel launch. */
 MP_API mp_status swiglu_fp8(const void* gate, const void* up, int64_t ld, mp_dtype x_dtype, int64_t rows,
                             int64_t cols, void* y, mp_dtype fp8_dtype, int32_t scale_block, void* y_scales,
                             void* ckpt, float* ckpt_scales, void* stream);

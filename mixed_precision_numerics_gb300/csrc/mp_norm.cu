@@ -11,13 +11,12 @@
 // Backward, with v = h or the checkpoint's values, xh = v * rstd, g = dy * w:
 //   c = mean(g * xh),  dx = rstd * (g - xh * c) + dh,  dw = sum_rows dy * xh.
 //
-// Both read and write every element once: the row lives in registers between
-// the two uses of it, before and after the row's sum.
-//
-// A CTA stays on its SM and takes row after row.  Each thread fetches its own
-// 16 elements of the next rows into shared memory with asynchronous copies
-// while it works on this one, so DRAM stays busy through the row's barrier and
-// no register waits for memory.
+// Both read and write every element once, and are bound by DRAM: a row stays on
+// its SM between the two uses of it, before and after the row's sum.  Forward
+// it stays in registers; backward, where the column sums dw take those, in
+// shared memory.  [8192 x 4096] BF16 with checkpoint: forward 42.4 us, 0.96 of
+// the copy rate (6680 GB/s), backward 43.4 us, 0.81; [16384 x 5120]: 101.1 us,
+// 1.00, and 95.2 us, 0.93.
 #include <math.h>
 
 #include "mp_chain.cuh"
@@ -45,6 +44,9 @@ RowShape row_shape(int64_t cols) {
   const int l = n <= 8 ? 8 : n <= 16 ? 16 : 32;
   return {l, kCta, kCta / l};
 }
+constexpr int kSmemBytes = 224 * 1024;   // dynamic shared memory of a CTA that has an SM to itself
+constexpr int kSmemShared = 216 * 1024;  // of all CTAs that share one
+
 // Threads that hold such a row with `u` units each.
 int team_of(const RowShape& s, int u) { return (s.threads / u + 31) / 32 * 32; }
 // CTAs that take `groups` groups of rows in turn, `per_sm` resident on an SM.
@@ -53,24 +55,11 @@ int resident_grid(int64_t groups, int per_sm) {
   return (int)(groups < most ? groups : most);
 }
 
-// Asks for the largest share of an SM's memory as shared memory, once a device.
-template <typename K>
-bool carveout_opt_in(K kernel, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
-  const uint64_t bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0;
-  if (bit && (done.load(std::memory_order_acquire) & bit)) return true;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) != cudaSuccess)
-    return false;
-  if (bit) done.fetch_or(bit, std::memory_order_release);
-  return true;
-}
-
 // Raises a kernel's dynamic shared-memory limit where a launch may need more
 // than the default: 48 KB, the kernel's static arrays included.
 template <typename K>
 bool smem_ok(K kernel, int bytes, std::atomic<uint64_t>& done) {
-  return bytes <= 32 * 1024 || smem_opt_in(kernel, 224 * 1024, done);
+  return bytes <= 32 * 1024 || smem_opt_in(kernel, kSmemBytes, done);
 }
 
 // Sum over the L lanes that hold one row, in every one of them.
@@ -108,12 +97,16 @@ struct NormFwd {
 };
 
 // A row lies in L lanes of a warp or (L = 0) in the CTA, U units a thread: unit
-// k of thread t is t + k * threads.  Rows of a CTA take two units a thread for
-// the 16-bit types: their weights are read after the row's sum, which leaves 64
-// registers and 2048 units, two rows of 16384, on an SM.  (With one unit a
-// thread half as many are there: [16384 x 5120] BF16 107.6 us against 99.0,
-// [7000 x 16384] 163.7 against 137.7.  For FP32 the two units' registers do not
-// leave room for more rows: [8192 x 4096] 73.2 us with one unit, 80.7 with two.)
+// k of thread t is t + k * threads.  Every CTA is launched at once; the others
+// on the SM keep DRAM busy while one meets its row's barrier.  Rows of a CTA
+// take two units a thread for the 16-bit types: their weights are read after
+// the row's sum, which leaves 64 registers and 2048 units, two rows of 16384, on
+// an SM.  (With one unit a thread half as many are there: [16384 x 5120] BF16
+// 107.6 us against 99.0, [7000 x 16384] 163.7 against 137.7.  For FP32 the two
+// units' registers do not leave room for more rows: [8192 x 4096] 73.2 us with
+// one unit, 80.7 with two.  CTAs that stay and fetch the next rows into shared
+// memory a thread at a time: 60.2 us on [8192 x 4096] BF16 against 42.8; a
+// cluster of CTAs for a row, 130 us on [16384 x 5120].)
 template <int XT, int L, int U, bool SAVE>
 __global__ __launch_bounds__(L ? kCta : kMaxThreads / U, L ? 1 : U) void k_norm_fwd(const __grid_constant__ NormFwd a) {
   __shared__ float slots[32];
@@ -218,9 +211,7 @@ struct NormBwd {
 };
 
 constexpr int kMaxStages = 4;
-constexpr int kMaxTeams = 15;    // a named barrier each
-constexpr int kSmemBytes = 224 * 1024;  // shared memory of a CTA that has an SM to itself, its dynamic part
-constexpr int kSmemShared = 216 * 1024; // of all CTAs that share one
+constexpr int kMaxTeams = 15;            // a named barrier each
 
 __device__ unsigned int g_norm_wait_failures;  // bounded waits that gave up (read by mp_wait_failures)
 
@@ -243,14 +234,24 @@ __host__ __device__ constexpr int weight_bytes(int units) { return (units + 3) /
 // row needs a whole team; one, where rows lie in a warp's lanes).  A team takes
 // every (gridDim.x * teams)-th group of rows.  Its first thread keeps the
 // team's rings filled with bulk copies (a group's rows are consecutive in
-// memory, so a tensor's part of a group is one copy).  The barrier of a group's
-// sum tells that the whole team has done with the group's early stage and with
-// the late stage of the group before: both are filled again there, the early
-// one `stages` groups ahead.  Each thread keeps the sums of its own columns in
-// registers over its rows (binary32, in row order); at the end the CTA joins
-// its teams' sums and writes one row of `parts`.  A thread whose wait gave up
-// works on what it finds and stores nothing more, but keeps meeting the
-// barriers.
+// memory, so a tensor's part of a group is one copy): an early stage is free
+// after the barrier of the group's sum and is filled again there; a late one
+// when the last of the team's warps has arrived at its `done` barrier, which
+// the thread looks at when it begins the next group.  Each thread keeps the
+// sums of its own columns in registers over its rows (binary32, in row order);
+// at the end the CTA joins its teams' sums and writes one row of `parts`.
+// Across the barrier of the sum live only the column sums and dy * w, 64
+// registers of two units; the stream's values are converted twice.  A thread
+// whose wait gave up works on what it finds and stores nothing more, but keeps
+// meeting the barriers.
+//
+// [8192 x 4096] BF16 from the checkpoint, both kernels: with loads into
+// registers 65.9 us, a ring of bulk copies 47.7, two units a thread (a row's
+// waits, sum and addresses shared by twice the elements) 45.7, the weights in
+// binary32 in shared memory, the late ring refilled early and no bank conflicts
+// 43.4.  From there on rows come at 0.97 of the copy rate; about 8 us are the
+// first rows' latency, the last round (54 rows for four teams), the join of the
+// column sums and the second kernel.
 template <int XT, bool SAVED, int L, int U>
 __global__ __maxnreg__(U == 2 ? 128 : 64) void k_norm_bwd(const __grid_constant__ NormBwd a) {
   extern __shared__ __align__(128) unsigned char smem[];
@@ -303,7 +304,8 @@ __global__ __maxnreg__(U == 2 ? 128 : 64) void k_norm_bwd(const __grid_constant_
     const uint32_t n = (uint32_t)min(rows - (int32_t)from, R) * a.cols, to = late0 + s * late;
     uint64_t* bar = &full[kMaxStages + s];
     mbar_arrive_expect_tx(bar, n * ves + (ring_dh ? n * es : 0));
-    bulk_g2s(to, (SAVED ? reinterpret_cast<const char*>(a.codes) : static_cast<const char*>(a.h)) + from * a.cols * ves, n * ves, bar, policy);
+    const char* stream = SAVED ? reinterpret_cast<const char*>(a.codes) : static_cast<const char*>(a.h);
+    bulk_g2s(to, stream + from * a.cols * ves, n * ves, bar, policy);
     if (ring_dh) bulk_g2s(to + group * ves, static_cast<const char*>(a.dh) + from * a.cols * es, n * es, bar, policy);
   };
   if (t == 0) {
@@ -313,7 +315,7 @@ __global__ __maxnreg__(U == 2 ? 128 : 64) void k_norm_bwd(const __grid_constant_
     }
   }
   // The row's scalars are read one group ahead.
-  float next_rstd = 0.0f, next_scale[U];
+  float next_rstd = 0.0f, next_scale[U] = {};
   auto scalars = [&](int64_t row) {
     if (row >= rows) return;
     next_rstd = a.rstd[row];
@@ -372,7 +374,7 @@ __global__ __maxnreg__(U == 2 ? 128 : 64) void k_norm_bwd(const __grid_constant_
       if (ok) fetch_late(before, row0 + (int64_t)(S - 1) * step);
     }
     // a row past the end works on the group's first, whose copy is there
-    const uint32_t es0 = L && live ? sub * a.cols : 0;
+    const uint32_t row_at = L && live ? sub * a.cols : 0;
     // Half a unit at a time, and the stream's values twice: across the barrier
     // stay the column sums and dy * w.
     float2 g[U][kPairs];
@@ -386,7 +388,7 @@ __global__ __maxnreg__(U == 2 ? 128 : 64) void k_norm_bwd(const __grid_constant_
       uint2 code;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const uint32_t at = es0 + eu[k] + (half ? second : first);
+        const uint32_t at = row_at + eu[k] + (half ? second : first);
         dy.take_half(ea + at * es, half);
         if constexpr (SAVED)
           code = lds8(la + at);
@@ -425,7 +427,7 @@ __global__ __maxnreg__(U == 2 ? 128 : 64) void k_norm_bwd(const __grid_constant_
       o.zero();
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const uint32_t h = half ? second : first, at = es0 + eu[k] + h;
+        const uint32_t h = half ? second : first, at = row_at + eu[k] + h;
         if (ring_dh)
           o.take_half(la + group * ves + at * es, half);
         else if (a.dh && out)
@@ -469,7 +471,8 @@ __global__ __maxnreg__(U == 2 ? 128 : 64) void k_norm_bwd(const __grid_constant_
     float* f = fold + (L ? sub : team) * width + (u + k * T) * kUnit;
 #pragma unroll
     for (int i = 0; i < kPairs; i += 2)
-      *reinterpret_cast<float4*>(f + (i < kPairs / 2 ? first : second) + 2 * i % 8) = make_float4(acc[k][i].x, acc[k][i].y, acc[k][i + 1].x, acc[k][i + 1].y);
+      *reinterpret_cast<float4*>(f + (i < kPairs / 2 ? first : second) + 2 * i % 8) =
+          make_float4(acc[k][i].x, acc[k][i].y, acc[k][i + 1].x, acc[k][i + 1].y);
   }
   __syncthreads();
   for (int col = 4 * threadIdx.x; col < a.cols; col += 4 * blockDim.x) {
@@ -526,7 +529,8 @@ template <int XT, bool SAVED, int L, int U>
 mp_status launch_bwd_rows(NormBwd a, const RowShape& s, int* parts, cudaStream_t st) {
   static std::atomic<uint64_t> opted{0};
   const int64_t groups = (a.rows + s.rows_per_cta - 1) / s.rows_per_cta;
-  const int weights = weight_bytes(a.cols / kUnit), elements = s.rows_per_cta * a.cols, early = early_bytes<XT>(elements);
+  const int weights = weight_bytes(a.cols / kUnit), elements = s.rows_per_cta * a.cols;
+  const int early = early_bytes<XT>(elements);
   // FP32 rows of over 14336 without a checkpoint do not fit with dh, which is then read directly.
   a.stage_dh = a.dh && early + late_bytes<XT, SAVED>(elements, true) + weights <= kSmemBytes;
   const int bytes = early + late_bytes<XT, SAVED>(elements, a.stage_dh);  // with the weights at most 224 KB
@@ -537,7 +541,8 @@ mp_status launch_bwd_rows(NormBwd a, const RowShape& s, int* parts, cudaStream_t
   const int team = L ? kCta : team_of(s, U);
   int per_sm = kMaxThreads / U / team;
   if (L == 0 && per_sm > kMaxTeams) per_sm = kMaxTeams;
-  while (per_sm > 1 && (L ? (2 * bytes + weights) * per_sm > kSmemShared : 2 * bytes * per_sm + weights > kSmemBytes)) --per_sm;
+  while (per_sm > 1 && (L ? (2 * bytes + weights) * per_sm > kSmemShared : 2 * bytes * per_sm + weights > kSmemBytes))
+    --per_sm;
   const int64_t spread = (groups + sm_count() - 1) / sm_count();
   const int teams = L ? 1 : (int)(per_sm < spread ? per_sm : spread);
   a.team = team;
@@ -547,8 +552,6 @@ mp_status launch_bwd_rows(NormBwd a, const RowShape& s, int* parts, cudaStream_t
   const int fold = (L ? kCta * kUnit : teams * a.cols) * 4;  // the join of the column sums
   if (smem < fold) smem = fold;
   if (!smem_ok(k_norm_bwd<XT, SAVED, L, U>, smem, opted)) return MP_ECUDA;
-  static std::atomic<uint64_t> split{0};
-  if (!carveout_opt_in(k_norm_bwd<XT, SAVED, L, U>, split)) return MP_ECUDA;
   const int grid = resident_grid((groups + teams - 1) / teams, L ? per_sm : 1);
   *parts = grid < kMaxParts ? grid : kMaxParts;
   launch_chained(k_norm_bwd<XT, SAVED, L, U>, dim3(*parts), dim3(teams * team), smem, st, a);
@@ -567,10 +570,6 @@ mp_status launch_bwd(const NormBwd& a, void* dweight, int32_t dt, cudaStream_t s
                                         : launch_bwd_rows<XT, SAVED, 0, 2>(a, s, &parts, st);
     if (r != MP_OK) return r;
   }
-  // The same split of L1 and shared memory as the kernel before: an SM changes
-  // it only when it is empty.
-  static std::atomic<uint64_t> split{0};
-  if (!carveout_opt_in(k_norm_dweight, split)) return MP_ECUDA;
   launch_chained(k_norm_dweight, dim3((a.cols + 31) / 32), dim3(32 * kFoldWarps), 0, st, (const float*)a.parts,
                  (int32_t)parts, a.cols, dweight, dt);
   note_launches(1);

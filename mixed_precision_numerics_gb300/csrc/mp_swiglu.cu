@@ -7,9 +7,16 @@
 // Backward, with g and u as given or the checkpoint's values:
 //   du = dp * (g * s(g)),  dg = dp * u * (s(g) * (1 + g * (1 - s(g)))).
 //
-// One thread owns 16 elements end to end; every element is read and written
-// once.  gate and up (dgate and dup) may be column ranges of one wider matrix:
-// each pair has a row pitch.
+// One thread owns 16 elements end to end, with every CTA launched at once;
+// every element is read and written once.  gate and up (dgate and dup) may be
+// column ranges of one wider matrix: each pair has a row distance.
+//
+// Bound by DRAM.  Forward with the checkpoint, 7.1 bytes an element of 16 bits
+// and 400 instructions for 16: [8192 x 14336] BF16 131.5 us, 0.95 of the copy
+// rate (6680 GB/s); at 57 registers four CTAs share an SM.  (The tile's three
+// pairs of divisions one by one: 157 us; with launch bounds that make gate and
+// up spill: 172.)  Backward from the checkpoint, 8.1 bytes: 138.2 us, 1.02;
+// from gate and up, 10 bytes: [2048 x 12288] 39.6 us, 0.95.
 #include "mp_chain.cuh"
 #include "mp_internal.h"
 #include "mp_tile8.cuh"
@@ -158,7 +165,7 @@ mp_status launch_fwd(const SwigluFwd& a, cudaStream_t st) {
 }
 template <int XT>
 mp_status launch_bwd(const SwigluBwd& a, cudaStream_t st) {
-  const dim3 g((unsigned)ctas_of(a.rows, a.tiles)), b(kThreads);
+  const dim3 g(ctas_of(a.rows, a.tiles)), b(kThreads);
   if (a.codes)
     launch_chained(k_swiglu_bwd<XT, true>, g, b, 0, st, a);
   else
@@ -175,10 +182,10 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 bool pitch_ok(int64_t ld, int64_t cols, int64_t rows, mp_dtype t) {
   return rows <= 1 || (ld >= cols && ld < (1ll << 31) && ld % (t == MP_F32 ? 4 : 8) == 0);
 }
-// rows * tiles below 2^31 - 32, so that a tile's number is (2.7e11 elements:
-// more than the device's memory holds of any input)
+// Tile numbers (2.7e11 elements: more than the device's memory holds of any
+// input), rows and the columns up to the end of a row's last tile are 32-bit.
 bool shape_ok(int64_t rows, int64_t cols, int step) {
-  if (rows >= (1ll << 31) || cols >= (1ll << 31) || cols % step != 0) return false;
+  if (rows >= (1ll << 31) || cols > (1ll << 31) - kTile || cols % step != 0) return false;
   return rows * ((cols + kTile - 1) / kTile) < (1ll << 31) - kThreads / kTileLanes;
 }
 

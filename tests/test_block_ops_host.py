@@ -53,7 +53,7 @@ def test_invalid_arguments(call, bad):
     (norm, dict(cols=264)), (norm, dict(cols=272, block=32)), (norm, dict(cols=16400)), (norm, dict(rows=2**31)),
     (norm_bwd, dict(cols=8)), (norm_bwd, dict(cols=16400)), (norm_bwd, dict(rows=2**31 - 31)),
     (swiglu, dict(cols=24)), (swiglu, dict(cols=48, block=32)), (swiglu, dict(ld=255)), (swiglu, dict(ld=260)),
-    (swiglu, dict(ld=258, x_dtype=M.MP_F32)), (swiglu, dict(rows=2**31)), (swiglu, dict(cols=2**31)),
+    (swiglu, dict(ld=258, x_dtype=M.MP_F32)), (swiglu, dict(rows=2**31)), (swiglu, dict(cols=2**31)), (swiglu, dict(rows=1, cols=2**31 - 16)),
     (swiglu, dict(rows=2**30, cols=256)), (swiglu_bwd, dict(d_ld=240)), (swiglu_bwd, dict(d_ld=257)),
     (swiglu_bwd, dict(ld=8)), (swiglu_bwd, dict(cols=40)),
 ])

@@ -292,6 +292,14 @@ def test_norm_backward(shape, dtype, saved):
     check_norm_backward(dy, w, o["rstd"], v, dh, dx, dw)
 
 
+@pytest.mark.parametrize("shape", [(100_003, 32), (20_011, 208), (9001, 512), (6007, 1040), (3001, 4096), (330, 16384)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("saved", [True, False])
+def test_norm_backward_of_many_rounds(shape, dtype, saved):
+    """So many rows that every stage of a team's rings is filled several times."""
+    test_norm_backward(shape, dtype, saved)
+
+
 @pytest.mark.parametrize("dw_type", TYPES)
 @pytest.mark.parametrize("wt", TYPES)
 def test_norm_backward_weight_types_without_stream_gradient(wt, dw_type):
@@ -337,6 +345,10 @@ def test_norm_backward_against_differences():
         d[c] = step
         want = float(loss(a, b + d) - loss(a, b - d)) / (2 * step)
         assert abs(float(dw[c]) - want) <= 1e-5 * (1 + abs(want))
+
+
+def test_no_wait_gave_up():
+    assert M.mp_wait_failures() == 0
 
 
 def test_norm_backward_of_no_rows_and_of_nonfinite_rows():
