@@ -11,12 +11,14 @@
 // every element is read and written once.  gate and up (dgate and dup) may be
 // column ranges of one wider matrix: each pair has a row distance.
 //
-// Bound by DRAM.  Forward with the checkpoint, 7.1 bytes an element of 16 bits
-// and 400 instructions for 16: [8192 x 14336] BF16 131.5 us, 0.95 of the copy
-// rate (6680 GB/s); at 57 registers four CTAs share an SM.  (The tile's three
-// pairs of divisions one by one: 157 us; with launch bounds that make gate and
-// up spill: 172.)  Backward from the checkpoint, 8.1 bytes: 138.2 us, 1.02;
-// from gate and up, 10 bytes: [2048 x 12288] 39.6 us, 0.95.
+// Bound by DRAM.  [8192 x 14336] BF16 forward with the checkpoint, 7.1 bytes an
+// element and 400 instructions for 16: 123.9 us, 1.01 of the copy rate (6680
+// GB/s); backward from the checkpoint, 8.1 bytes: 136.0 us, 1.04; from gate and
+// up, 10 bytes: [2048 x 12288] 38.8 us, 0.97.  What counts is how many units are
+// on an SM: CTAs of 128 threads, nine of them (56 registers) forward and twelve
+// (40) backward for the 16-bit types.  (256 threads, four and six CTAs: 132.9 and
+// 138.9 us; 512 threads: 137.5 and 142.5; 36 registers backward, which spill:
+// 147.6.  The forward tile's three pairs of divisions one by one: 157.)
 #include "mp_chain.cuh"
 #include "mp_internal.h"
 #include "mp_tile8.cuh"
@@ -24,7 +26,7 @@
 namespace mp {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 // 1 / (1 + exp(-g)) through the hardware's base-2 exponential and reciprocal:
 // within (|g| + 8) * 2^-24, relative; 0 where exp(-g) overflows (g below -88,
@@ -64,7 +66,7 @@ struct SwigluFwd {
 };
 
 template <int XT, bool SAVE>
-__global__ __launch_bounds__(kThreads) void k_swiglu_fwd(const __grid_constant__ SwigluFwd a) {
+__global__ __launch_bounds__(kThreads, XT == XF32 ? 1 : 9) void k_swiglu_fwd(const __grid_constant__ SwigluFwd a) {
   chain_wait();
   chain_release();
   constexpr int N = SAVE ? 3 : 1;
@@ -109,7 +111,7 @@ struct SwigluBwd {
 };
 
 template <int XT, bool SAVED>
-__global__ __launch_bounds__(kThreads) void k_swiglu_bwd(const __grid_constant__ SwigluBwd a) {
+__global__ __launch_bounds__(kThreads, XT == XF32 ? 1 : 12) void k_swiglu_bwd(const __grid_constant__ SwigluBwd a) {
   chain_wait();
   chain_release();
   const Place p = place_of(a.rows, a.cols, a.tiles);
