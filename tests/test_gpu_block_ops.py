@@ -611,6 +611,66 @@ def test_offsets_beyond_32_bits():
     assert not dx[:-tail].any()
 
 
+def odd(t):
+    """The tensor in a buffer that starts 16 bytes past a multiple of 32."""
+    n, es = t.numel(), t.element_size()
+    buf = torch.empty(n * es + 64, dtype=torch.uint8, device="cuda")
+    at = (16 - buf.data_ptr()) % 32
+    v = buf[at:at + n * es].view(t.dtype).view(t.shape)
+    v.copy_(t)
+    assert v.data_ptr() % 32 == 16
+    return v
+
+
+@pytest.mark.parametrize("shape", [(9, 48), (70, 1040)])
+def test_pointers_aligned_to_16_bytes_only(shape):
+    rows, cols = shape
+    x, r, dy, dh = (odd(normal(100 + k, rows, cols, dtype=torch.bfloat16)) for k in range(4))
+    w = odd(normal(104, cols, dtype=torch.bfloat16))
+    ref = norm(x.clone(), w.clone(), residual=r.clone())
+    o = {k: odd(torch.zeros_like(v)) for k, v in ref.items()}
+    M.rmsnorm_residual_fp8(x, w, o["y"], o["y_scales"], residual=r, h=o["h"], rstd=o["rstd"], ckpt=o["ckpt"],
+                           ckpt_scales=o["ckpt_scales"])
+    for k in ref:
+        assert_bits(o[k], ref[k], k)
+    dx, dw = odd(torch.zeros_like(x)), odd(torch.zeros(cols, device="cuda"))
+    ws = odd(M.new_rmsnorm_workspace(rows, cols))
+    want = norm_backward(dy, w, ref["rstd"], ckpt=ref["ckpt"], scales=ref["ckpt_scales"], dh=dh)
+    M.rmsnorm_residual_backward(dy, w, o["rstd"], dx, dw, ws, ckpt=o["ckpt"], ckpt_scales=o["ckpt_scales"], dh=dh)
+    assert_bits(dx, want[0], "dx")
+    assert_bits(dw, want[1], "dweight")
+    ref = swiglu(x.clone(), r.clone())
+    o = {k: odd(torch.zeros_like(v)) for k, v in ref.items()}
+    M.swiglu_fp8(x, r, o["y"], o["y_scales"], ckpt=o["ckpt"], ckpt_scales=o["ckpt_scales"])
+    for k in ref:
+        assert_bits(o[k], ref[k], k)
+    want = swiglu_backward(dy, ckpt=ref["ckpt"], ckpt_scales=ref["ckpt_scales"])
+    dg, du = odd(torch.zeros_like(x)), odd(torch.zeros_like(x))
+    M.swiglu_backward(dy, dg, du, ckpt=o["ckpt"], ckpt_scales=o["ckpt_scales"])
+    assert_bits(dg, want[0], "dgate")
+    assert_bits(du, want[1], "dup")
+
+
+def test_calls_on_two_streams_at_once():
+    """Calls with their own buffers may run together: nothing of one waits for the other."""
+    rows, cols = 3000, 2048
+    x, dy, w = normal(110, rows, cols, dtype=torch.bfloat16), normal(111, rows, cols, dtype=torch.bfloat16), normal(112, cols)
+    rstd = norm(x, w)["rstd"]
+    want = norm_backward(dy, w, rstd, h=x)
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    outs = [(torch.empty_like(x), torch.empty(cols, device="cuda"), M.new_rmsnorm_workspace(rows, cols)) for _ in sides]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for side, (dx, dw, ws) in zip(sides, outs):
+            M.rmsnorm_residual_backward(dy, w, rstd, dx, dw, ws, h=x, stream=side)
+    torch.cuda.synchronize()
+    for dx, dw, _ in outs:
+        assert_bits(dx, want[0], "dx")
+        assert_bits(dw, want[1], "dweight")
+    assert M.mp_wait_failures() == 0
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 def test_every_nan_written_in_16_bits_is_the_canonical_one(dtype):
     dt = TYPES[dtype]
