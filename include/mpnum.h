@@ -9,6 +9,9 @@
  *   3. NVFP4 quantisation (E2M1 codes, E4M3 block scales, FP32 tensor scale,
  *      1x16 or 16x16 blocks, optional random Hadamard transform, round to
  *      nearest even or stochastic rounding), plus the standalone transform.
+ * Next to them: the MX block formats (section 4), and the norm and gated
+ * product of a transformer block with 8-bit outputs and checkpoints, forward
+ * and backward (section 5).
  *
  * Pages cited (title, then section):
  *   [MPT-ko] itwiki "혼합 정밀도 학습" (mixed precision training)
@@ -31,7 +34,8 @@
  *     be anything >= 0 unless stated.
  *   - Calls that share a state struct, meta struct or workspace must be
  *     ordered on one stream; calls with disjoint state may run concurrently.
- *   - The quantiser kernels (FP8, NVFP4, MX, the transform) are launched with
+ *   - The quantiser kernels (FP8, NVFP4, MX, the transform) and the block
+ *     operators' (section 5) are launched with
  *     programmatic stream serialization allowed: their blocks may be
  *     scheduled while the previous kernel in the stream finishes, but each
  *     waits for that kernel to complete (griddepcontrol.wait) before touching
@@ -413,7 +417,7 @@ MP_API mp_status mx_quantize(const void* x, mp_dtype x_dtype, int64_t rows, int6
  * x, residual, h, dy, dh, dx, gate, up, dp, dgate, dup has type x_dtype.
  * cols % 16 == 0 (else MP_ESHAPE); tensors 16-byte aligned, FP32 scales and
  * rstd 4-byte, UE8M0 bytes not at all.  Sums are binary32 in an order fixed
- * by the shape, so results repeat. */
+ * by the shape and the device, so results repeat. */
 
 /* rmsnorm_residual_fp8 — h = x + residual rounded to x_dtype (h = x if
  * residual is NULL); rstd = 1 / sqrt(mean(h^2) + eps) per row; y = the cast of

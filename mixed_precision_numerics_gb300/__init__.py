@@ -499,12 +499,17 @@ def _in(t, name: str, nbytes: int, like, dev: int, dtype=None, align: int = 16) 
     another 16-bit type has the right size).  A call has up to ten arguments and
     a one-token kernel takes two microseconds: what passes is seen in few steps,
     and _dev says what does not."""
-    if t is None or isinstance(t, int):
-        return t
-    p = t.data_ptr()
-    if t.get_device() != dev or not t.is_contiguous() or (t.nbytes < nbytes and p % align == 0):
+    if t is None:
+        return None
+    try:
+        p = t.data_ptr()
+    except AttributeError:
+        if isinstance(t, int):  # raw pointers pass unchecked
+            return t
+        raise ValueError(f"{name}: a CUDA tensor is required (the kernels read and write device memory)") from None
+    if t.nbytes < nbytes or not t.is_contiguous() or t.get_device() != dev:
         _dev(t, name, nbytes, like=None if t is like else like, align=align)
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name}: {t.dtype}, the call needs {dtype}")
     return p
 
