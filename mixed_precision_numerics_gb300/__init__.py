@@ -4,7 +4,9 @@ The functions below carry the C entry points' names and only marshal
 arguments (tensor data pointers, the current CUDA stream, host structs); every
 step of the computation runs in the library's CUDA kernels.  Importing this
 package fails loudly when ``libmpnum.so`` has not been built: there is no
-other implementation to fall back to.
+other implementation to fall back to.  The block operators, whose smallest
+calls take less time on the GPU than arguments take here, are marshalled
+natively first (``_mpcall.so``).
 
 PyTorch supplies device memory and streams.
 """
@@ -127,6 +129,12 @@ def _load() -> ctypes.CDLL:
 
 lib = _load()
 
+try:
+    from . import _mpcall
+except ImportError as e:
+    raise ImportError(f"{os.path.join(_PKG, '_mpcall.so')} cannot be loaded ({e}): build it with `python -c 'import "
+                      "__graft_entry__ as g; g.build()'`") from e
+
 
 class MpError(RuntimeError):
     def __init__(self, fn: str, status: int):
@@ -171,27 +179,13 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
-_CUDA: tuple = ()
-
-
-def _cuda() -> tuple:
-    """The functions that give the current device's number and a device's current
-    stream handle, and torch.float32.  The handle comes without a Stream object
-    around it, whose making takes longer than a small kernel."""
-    global _CUDA
+def _stream(stream) -> int | None:
     import torch
 
-    _CUDA = (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
-             getattr(torch._C, "_cuda_getCurrentRawStream", lambda d: torch.cuda.current_stream(d).cuda_stream),
-             torch.float32)
-    return _CUDA
-
-
-def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-
-        return (_CUDA or _cuda())[1](torch.cuda.current_device())
+        # the current stream's handle without a Stream object around it, whose making takes longer than a small kernel
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -493,58 +487,57 @@ def mx_quantize(x, codes, scales, elem_dtype: int = MP_E2M1, dequant=None, strea
 # ---- block operators with 8-bit outputs and 8-bit checkpoints ------------------------------
 
 
-def _in(t, name: str, nbytes: int, like, dev: int, dtype=None, align: int = 16) -> int | None:
-    """The pointer of an argument that passes _dev's checks on device number
-    `dev` and, where `dtype` is given, has that element type (a tensor of
-    another 16-bit type has the right size).  A call has up to ten arguments and
-    a one-token kernel takes two microseconds: what passes is seen in few steps,
-    and _dev says what does not."""
-    if t is None:
-        return None
-    try:
-        p = t.data_ptr()
-    except AttributeError:
-        if isinstance(t, int):  # raw pointers pass unchecked
-            return t
-        raise ValueError(f"{name}: a CUDA tensor is required (the kernels read and write device memory)") from None
-    if t.nbytes < nbytes or not t.is_contiguous() or t.get_device() != dev:
-        _dev(t, name, nbytes, like=None if t is like else like, align=align)
-    if dtype is not None and t.dtype is not dtype:
+# _mpcall makes the checks of these functions natively and calls the library.  What does not pass there
+# (None) comes to the Python checks, which say what is wrong, as does the first call of a process.
+
+
+def _bind() -> None:
+    import torch
+
+    names = ("rmsnorm_residual_fp8", "rmsnorm_residual_backward", "swiglu_fp8", "swiglu_backward")
+    _mpcall.bind(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names),
+                 (torch.float32, torch.float16, torch.bfloat16),
+                 getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+                 getattr(torch._C, "_cuda_getCurrentRawStream", lambda d: torch.cuda.current_stream(d).cuda_stream))
+
+
+def _in(t, name: str, nbytes: int, like=None, dtype=None, align: int = 16) -> int | None:
+    """The pointer of an argument after _dev's checks and, where `dtype` is given, that of the element
+    type: a tensor of another 16-bit type has the right size."""
+    _dev(t, name, nbytes, like=like, align=align)
+    if dtype is not None and t is not None and not isinstance(t, int) and t.dtype != dtype:
         raise ValueError(f"{name}: {t.dtype}, the call needs {dtype}")
-    return p
+    return _ptr(t)
 
 
-def _matrix(t, name: str, rows: int, cols: int, like, dev: int) -> tuple[int, int]:
-    """Pointer and row distance (in elements) of a [rows, cols] matrix of like's
-    type that may be a column range of a wider one."""
-    if t.get_device() != dev or t.shape != like.shape or t.dtype != like.dtype:
-        if not t.is_cuda:
-            raise ValueError(f"{name}: a CUDA tensor is required (the kernels read and write device memory)")
+def _matrix(t, name: str, like) -> tuple[int, int]:
+    """Pointer and row distance (in elements) of a matrix of like's shape and type that may be a column
+    range of a wider one."""
+    import torch
+
+    rows, cols = like.shape
+    if not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor is required (the kernels read and write device memory)")
+    want = torch.device("cuda", torch.cuda.current_device())
+    if t.device != want or t.shape != like.shape or t.dtype != like.dtype:
         raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, the call needs {(rows, cols)} {like.dtype} "
-                         f"on cuda:{dev}")
-    ld, one = t.stride()
-    if one != 1 and cols > 1:
+                         f"on {want}")
+    if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return t.data_ptr(), ld if rows > 1 else cols
+    return t.data_ptr(), t.stride(0) if rows > 1 else cols
 
 
-def _pair(a, b, names: tuple[str, str], rows: int, cols: int, like, dev: int) -> tuple[int, int, int]:
-    pa, ld = _matrix(a, names[0], rows, cols, like, dev)
-    pb, ld_b = _matrix(b, names[1], rows, cols, like, dev)
+def _pair(a, b, names: tuple[str, str], like) -> tuple[int, int, int]:
+    (pa, ld), (pb, ld_b) = _matrix(a, names[0], like), _matrix(b, names[1], like)
     if ld != ld_b:
         raise ValueError(f"{names[1]}: its rows lie {ld_b} elements apart, those of {names[0]} {ld}")
     return pa, pb, ld
 
 
-def _where(t, stream) -> tuple:
-    """(current device number, stream handle, torch.float32) of a call on `t`; for
-    a host tensor a device that no tensor is on, so that its check fails without
-    a GPU being needed."""
-    device, current, f32 = _CUDA or _cuda()
-    if not t.is_cuda:
-        return -2, None, f32
-    dev = device()
-    return dev, current(dev) if stream is None else _stream(stream), f32
+def _fp8_out(y, y_scales, scale_block: int, like) -> tuple[int, int]:
+    n, tile_bytes = like.numel(), 4 * like.shape[0] * -(-like.shape[1] // 128)
+    nbytes, align = (n // 32, 1) if scale_block == 32 else (tile_bytes, 4)
+    return _in(y, "y", n, like), _in(y_scales, "y_scales", nbytes, like, align=align)
 
 
 def rmsnorm_residual_fp8(x, weight, y, y_scales, *, residual=None, h=None, rstd=None, ckpt=None, ckpt_scales=None,
@@ -553,18 +546,22 @@ def rmsnorm_residual_fp8(x, weight, y, y_scales, *, residual=None, h=None, rstd=
     bytes; y_scales: float32 [rows, ceil(cols/128)], or with scale_block 32 one UE8M0 byte per 32
     elements.  h (as x), rstd (float32 [rows]) and ckpt (rows*cols bytes, with ckpt_scales float32
     [rows, ceil(cols/128)]) are outputs the backward pass reads; each may be None."""
-    rows, cols = x.shape
-    (dev, at, f32), dt, n = _where(x, stream), x.dtype, rows * cols
-    nb, tile_bytes = n * x.element_size(), 4 * rows * -(-cols // 128)
-    scale_bytes, scale_align = (n // 32, 1) if scale_block == 32 else (tile_bytes, 4)
-    _check("rmsnorm_residual_fp8",
-           lib.rmsnorm_residual_fp8(_in(x, "x", nb, x, dev), _in(residual, "residual", nb, x, dev, dt), _dtype_code(x),
-                                    rows, cols, _in(weight, "weight", cols * weight.element_size(), x, dev),
-                                    _dtype_code(weight), eps, _in(h, "h", nb, x, dev, dt), _in(y, "y", n, x, dev),
-                                    fp8_dtype, scale_block,
-                                    _in(y_scales, "y_scales", scale_bytes, x, dev, None, scale_align),
-                                    _in(rstd, "rstd", 4 * rows, x, dev, f32, 4), _in(ckpt, "ckpt", n, x, dev),
-                                    _in(ckpt_scales, "ckpt_scales", tile_bytes, x, dev, f32, 4), at))
+    status = _mpcall.rmsnorm_residual_fp8(x, weight, y, y_scales, residual, h, rstd, ckpt, ckpt_scales, eps, fp8_dtype,
+                                          scale_block, stream)
+    if status is None:
+        import torch
+
+        _bind()
+        rows, cols = x.shape
+        nb, tile_bytes, f32 = x.element_size() * rows * cols, 4 * rows * -(-cols // 128), torch.float32
+        px = _in(x, "x", nb)
+        py, ps = _fp8_out(y, y_scales, scale_block, x)
+        status = lib.rmsnorm_residual_fp8(
+            px, _in(residual, "residual", nb, x, x.dtype), _dtype_code(x), rows, cols,
+            _in(weight, "weight", cols * weight.element_size(), x), _dtype_code(weight), eps,
+            _in(h, "h", nb, x, x.dtype), py, fp8_dtype, scale_block, ps, _in(rstd, "rstd", 4 * rows, x, f32, 4),
+            _in(ckpt, "ckpt", rows * cols, x), _in(ckpt_scales, "ckpt_scales", tile_bytes, x, f32, 4), _stream(stream))
+    _check("rmsnorm_residual_fp8", status)
 
 
 def rmsnorm_workspace_size(rows: int, cols: int) -> int:
@@ -582,54 +579,65 @@ def rmsnorm_residual_backward(dy, weight, rstd, dx, dweight, workspace, *, h=Non
                               dh=None, stream=None) -> None:
     """dx (as dy) and dweight ([cols], any of the three float types) from dy, rstd and the stream: either h
     or its 8-bit checkpoint (ckpt, ckpt_scales).  dh: the gradient reaching the stream from above, or None."""
-    rows, cols = dy.shape
-    (dev, at, f32), dt, n = _where(dy, stream), dy.dtype, rows * cols
-    nb = n * dy.element_size()
-    _check("rmsnorm_residual_backward",
-           lib.rmsnorm_residual_backward(_in(dy, "dy", nb, dy, dev), _in(dh, "dh", nb, dy, dev, dt), _dtype_code(dy),
-                                         rows, cols, _in(h, "h", nb, dy, dev, dt), _in(ckpt, "ckpt", n, dy, dev),
-                                         _in(ckpt_scales, "ckpt_scales", 4 * rows * -(-cols // 128), dy, dev,
-                                             f32, 4),
-                                         _in(weight, "weight", cols * weight.element_size(), dy, dev),
-                                         _dtype_code(weight), _in(rstd, "rstd", 4 * rows, dy, dev, f32, 4),
-                                         _in(dx, "dx", nb, dy, dev, dt),
-                                         _in(dweight, "dweight", cols * dweight.element_size(), dy, dev),
-                                         _dtype_code(dweight), _in(workspace, "workspace", 0, dy, dev),
-                                         0 if workspace is None else workspace.nbytes, at))
+    status = _mpcall.rmsnorm_residual_backward(dy, weight, rstd, dx, dweight, workspace, h, ckpt, ckpt_scales, dh, stream)
+    if status is None:
+        import torch
+
+        _bind()
+        rows, cols = dy.shape
+        nb, dt, f32 = dy.element_size() * rows * cols, dy.dtype, torch.float32
+        pdy = _in(dy, "dy", nb)
+        status = lib.rmsnorm_residual_backward(
+            pdy, _in(dh, "dh", nb, dy, dt), _dtype_code(dy), rows, cols, _in(h, "h", nb, dy, dt),
+            _in(ckpt, "ckpt", rows * cols, dy),
+            _in(ckpt_scales, "ckpt_scales", 4 * rows * -(-cols // 128), dy, f32, 4),
+            _in(weight, "weight", cols * weight.element_size(), dy), _dtype_code(weight),
+            _in(rstd, "rstd", 4 * rows, dy, f32, 4), _in(dx, "dx", nb, dy, dt),
+            _in(dweight, "dweight", cols * dweight.element_size(), dy), _dtype_code(dweight),
+            _in(workspace, "workspace", 0, dy), _ws(workspace)[1], _stream(stream))
+    _check("rmsnorm_residual_backward", status)
 
 
 def swiglu_fp8(gate, up, y, y_scales, *, ckpt=None, ckpt_scales=None, fp8_dtype: int = MP_E4M3,
                scale_block: int = 128, stream=None) -> None:
     """y = FP8 of silu(gate) * up.  gate, up: [rows, cols], each may be a column range of one wider
     matrix; ckpt: 2*rows*cols bytes (gate's codes, then up's), ckpt_scales: float32 [2, rows, ceil(cols/128)]."""
-    rows, cols = gate.shape
-    (dev, at, f32), n = _where(gate, stream), rows * cols
-    tile_bytes = 4 * rows * -(-cols // 128)
-    scale_bytes, scale_align = (n // 32, 1) if scale_block == 32 else (tile_bytes, 4)
-    pg, pu, ld = _pair(gate, up, ("gate", "up"), rows, cols, gate, dev)
-    _check("swiglu_fp8",
-           lib.swiglu_fp8(pg, pu, ld, _dtype_code(gate), rows, cols, _in(y, "y", n, gate, dev), fp8_dtype, scale_block,
-                          _in(y_scales, "y_scales", scale_bytes, gate, dev, None, scale_align),
-                          _in(ckpt, "ckpt", 2 * n, gate, dev),
-                          _in(ckpt_scales, "ckpt_scales", 2 * tile_bytes, gate, dev, f32, 4), at))
+    status = _mpcall.swiglu_fp8(gate, up, y, y_scales, ckpt, ckpt_scales, fp8_dtype, scale_block, stream)
+    if status is None:
+        import torch
+
+        _bind()
+        rows, cols = gate.shape
+        pg, pu, ld = _pair(gate, up, ("gate", "up"), gate)
+        py, ps = _fp8_out(y, y_scales, scale_block, gate)
+        status = lib.swiglu_fp8(
+            pg, pu, ld, _dtype_code(gate), rows, cols, py, fp8_dtype, scale_block, ps,
+            _in(ckpt, "ckpt", 2 * rows * cols, gate),
+            _in(ckpt_scales, "ckpt_scales", 8 * rows * -(-cols // 128), gate, torch.float32, 4), _stream(stream))
+    _check("swiglu_fp8", status)
 
 
 def swiglu_backward(dp, dgate, dup, *, gate=None, up=None, ckpt=None, ckpt_scales=None, stream=None) -> None:
     """dgate, dup from dp and either gate and up or their 8-bit checkpoint of swiglu_fp8.  dgate and dup
     ([rows, cols]) may be column ranges of one wider matrix, as gate and up may."""
-    rows, cols = dp.shape
-    (dev, at, f32), n = _where(dp, stream), rows * cols
-    pg, pu, ld = None, None, cols
-    if gate is not None and up is not None:
-        pg, pu, ld = _pair(gate, up, ("gate", "up"), rows, cols, dp, dev)
-    elif gate is not None or up is not None:
-        raise ValueError("gate and up: both or neither")
-    pdg, pdu, d_ld = _pair(dgate, dup, ("dgate", "dup"), rows, cols, dp, dev)
-    _check("swiglu_backward",
-           lib.swiglu_backward(_in(dp, "dp", n * dp.element_size(), dp, dev), _dtype_code(dp), rows, cols, pg, pu, ld,
-                               _in(ckpt, "ckpt", 2 * n, dp, dev),
-                               _in(ckpt_scales, "ckpt_scales", 8 * rows * -(-cols // 128), dp, dev, f32, 4),
-                               pdg, pdu, d_ld, at))
+    status = _mpcall.swiglu_backward(dp, dgate, dup, gate, up, ckpt, ckpt_scales, stream)
+    if status is None:
+        import torch
+
+        _bind()
+        rows, cols = dp.shape
+        pdp = _in(dp, "dp", dp.element_size() * rows * cols)
+        pg, pu, ld = None, None, cols
+        if gate is not None and up is not None:
+            pg, pu, ld = _pair(gate, up, ("gate", "up"), dp)
+        elif gate is not None or up is not None:
+            raise ValueError("gate and up: both or neither")
+        pdg, pdu, d_ld = _pair(dgate, dup, ("dgate", "dup"), dp)
+        status = lib.swiglu_backward(
+            pdp, _dtype_code(dp), rows, cols, pg, pu, ld, _in(ckpt, "ckpt", 2 * rows * cols, dp),
+            _in(ckpt_scales, "ckpt_scales", 8 * rows * -(-cols // 128), dp, torch.float32, 4), pdg, pdu, d_ld,
+            _stream(stream))
+    _check("swiglu_backward", status)
 
 
 __all__ = [

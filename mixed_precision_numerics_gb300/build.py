@@ -1,16 +1,19 @@
-"""Build libmpnum.so in-tree: nvcc for sm_103a, one object per .cu, compiled in parallel."""
+"""Build in-tree: libmpnum.so (nvcc for sm_103a, one object per .cu, compiled in
+parallel) and _mpcall.so, the native argument marshalling of the block operators."""
 from __future__ import annotations
 
 import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmpnum.so")
+CALL = os.path.join(PKG, "_mpcall.so")
 HEADER = os.path.join(ROOT, "include", "mpnum.h")
 
 SOURCES = ["mp_common.cu", "mp_adamw.cu", "mp_fp8.cu", "mp_nvfp4.cu", "mp_mx.cu", "mp_norm.cu", "mp_swiglu.cu"]
@@ -43,13 +46,25 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _compile_call() -> None:
+    tmp = CALL + f".tmp{os.getpid()}"
+    p = subprocess.run(["gcc", "-O2", "-shared", "-fPIC", "-Wall", "-Wextra", "-I", os.path.join(ROOT, "include"), "-I",
+                        sysconfig.get_paths()["include"], os.path.join(CSRC, "mp_call.c"), "-o", tmp],
+                       capture_output=True, text=True)
+    if p.returncode != 0:
+        raise RuntimeError(f"gcc failed for mp_call.c:\n{p.stderr}")
+    os.replace(tmp, CALL)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/*.cu and link libmpnum.so next to this file; returns its path."""
-    if not force and not _stale(LIB):
+    """Compile csrc/*.cu and link libmpnum.so and _mpcall.so next to this file; returns the library's path."""
+    if not force and not _stale(LIB) and not _stale(CALL):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        call = ex.submit(_compile_call)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        call.result()
     tmp = LIB + f".tmp{os.getpid()}"
     p = subprocess.run(["nvcc", *GENCODE, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if p.returncode != 0:

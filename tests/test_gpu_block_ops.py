@@ -685,6 +685,56 @@ def test_every_nan_written_in_16_bits_is_the_canonical_one(dtype):
     assert int(bits(dg)[0, 3]) == 0x7FFF and int(bits(du)[1, 5]) == 0x7FFF
 
 
+def test_python_marshalling_gives_what_the_native_one_does():
+    """A raw pointer among the arguments is left to the Python marshalling: same call, same results."""
+    rows, cols = 33, 272
+    x, r, dy, dh = (normal(120 + k, rows, cols, dtype=torch.float16) for k in range(4))
+    w = normal(124, cols)
+    ref = norm(x, w, residual=r, fp8=M.MP_E5M2)
+    o = {k: torch.zeros_like(v) for k, v in ref.items()}
+    n0 = M.mp_launch_count()
+    M.rmsnorm_residual_fp8(x, w, o["y"].data_ptr(), o["y_scales"], residual=r, h=o["h"], rstd=o["rstd"], ckpt=o["ckpt"],
+                           ckpt_scales=o["ckpt_scales"], fp8_dtype=M.MP_E5M2, stream=torch.cuda.current_stream())
+    assert M.mp_launch_count() == n0 + 1
+    for k in ref:
+        assert_bits(o[k], ref[k], k)
+    want = norm_backward(dy, w, ref["rstd"], ckpt=ref["ckpt"], scales=ref["ckpt_scales"], dh=dh)
+    dx, dw = torch.zeros_like(x), torch.zeros(cols, device="cuda")
+    ws = M.new_rmsnorm_workspace(rows, cols)
+    M.rmsnorm_residual_backward(dy, w, o["rstd"].data_ptr(), dx, dw, ws, ckpt=o["ckpt"], ckpt_scales=o["ckpt_scales"], dh=dh,
+                                stream=torch.cuda.current_stream().cuda_stream)
+    assert_bits(dx, want[0], "dx")
+    assert_bits(dw, want[1], "dweight")
+    ref = swiglu(x, r)
+    o = {k: torch.zeros_like(v) for k, v in ref.items()}
+    M.swiglu_fp8(x, r, o["y"].data_ptr(), o["y_scales"], ckpt=o["ckpt"], ckpt_scales=o["ckpt_scales"])
+    for k in ref:
+        assert_bits(o[k], ref[k], k)
+    want = swiglu_backward(dy, ckpt=ref["ckpt"], ckpt_scales=ref["ckpt_scales"])
+    dg, du = torch.zeros_like(x), torch.zeros_like(x)
+    M.swiglu_backward(dy, dg, du, ckpt=o["ckpt"].data_ptr(), ckpt_scales=o["ckpt_scales"])
+    assert_bits(dg, want[0], "dgate")
+    assert_bits(du, want[1], "dup")
+
+
+def test_arguments_keep_their_reference_counts():
+    import sys
+
+    x, w = normal(130, 4, 256), normal(131, 256)
+    y, ys = torch.empty(4, 256, dtype=torch.uint8, device="cuda"), torch.empty(4, 2, device="cuda")
+    side = torch.cuda.Stream()
+    held = (x, w, y, ys, side, torch.float32)
+    before = [sys.getrefcount(t) for t in held]
+    for _ in range(100):
+        M.rmsnorm_residual_fp8(x, w, y, ys, stream=side)
+        M.swiglu_fp8(x, x, y, ys)
+        M.swiglu_backward(x, x, x, gate=x, up=x)
+        with pytest.raises(ValueError):
+            M.rmsnorm_residual_fp8(x, w, y, ys[:2])
+    torch.cuda.synchronize()
+    assert [sys.getrefcount(t) for t in held] == before
+
+
 def test_refusals_launch_nothing():
     x, w = normal(90, 4, 256, dtype=torch.bfloat16), normal(91, 256)
     y, ys, rstd = torch.empty(4, 256, dtype=torch.uint8, device="cuda"), torch.empty(4, 2, device="cuda"), torch.empty(4, device="cuda")
