@@ -102,13 +102,17 @@ struct NormFwd {
 // take two units a thread for the 16-bit types: their weights are read after
 // the row's sum, which leaves 64 registers and 2048 units, two rows of 16384, on
 // an SM.  (With one unit a thread half as many are there: [16384 x 5120] BF16
-// 107.6 us against 99.0, [7000 x 16384] 163.7 against 137.7.  For FP32 the two
-// units' registers do not leave room for more rows: [8192 x 4096] 73.2 us with
-// one unit, 80.7 with two.  CTAs that stay and fetch the next rows into shared
-// memory a thread at a time: 60.2 us on [8192 x 4096] BF16 against 42.8; a
-// cluster of CTAs for a row, 130 us on [16384 x 5120].)
+// 107.6 us against 99.0, [7000 x 16384] 163.7 against 137.7.)  For FP32 two
+// units take 80 registers and the weights' loads cost more than they give up to
+// 8192 columns ([7000 x 4096] 64.6 us with one unit, 70.6 with two); above, one
+// unit a thread would leave a single row on an SM ([7000 x 10816] 223.8 us and
+// 185.3).  Dropped: CTAs that stay and fetch the next rows into shared memory a
+// thread at a time, 60.2 us on [8192 x 4096] BF16 against 42.8; a cluster of
+// CTAs for a row, 130 us on [16384 x 5120].
+template <int XT, int L, int U>
+constexpr int fwd_threads() { return L ? kCta : U == 1 ? kMaxThreads : XT == XF32 ? 768 : kMaxThreads / 2; }
 template <int XT, int L, int U, bool SAVE>
-__global__ __launch_bounds__(L ? kCta : kMaxThreads / U, L ? 1 : U) void k_norm_fwd(const __grid_constant__ NormFwd a) {
+__global__ __launch_bounds__(fwd_threads<XT, L, U>(), XT != XF32 && U == 2 ? 2 : 1) void k_norm_fwd(const __grid_constant__ NormFwd a) {
   __shared__ float slots[32];
   chain_wait();
   chain_release();
@@ -186,7 +190,9 @@ mp_status launch_fwd_shape(const NormFwd& a, cudaStream_t st) {
   if (s.lanes == 8) return launch_fwd<XT, 8, 1, SAVE>(a, s, st);
   if (s.lanes == 16) return launch_fwd<XT, 16, 1, SAVE>(a, s, st);
   if (s.lanes == 32) return launch_fwd<XT, 32, 1, SAVE>(a, s, st);
-  return launch_fwd<XT, 0, XT == XF32 ? 1 : 2, SAVE>(a, s, st);
+  if constexpr (XT == XF32)
+    if (s.threads <= kMaxThreads / 2) return launch_fwd<XT, 0, 1, SAVE>(a, s, st);
+  return launch_fwd<XT, 0, 2, SAVE>(a, s, st);
 }
 template <int XT>
 mp_status launch_fwd_type(const NormFwd& a, cudaStream_t st) {

@@ -29,8 +29,8 @@ namespace {
 constexpr int kThreads = 128;
 
 // 1 / (1 + exp(-g)) through the hardware's base-2 exponential and reciprocal:
-// within (|g| + 8) * 2^-24, relative; 0 where exp(-g) overflows (g below -88,
-// where the exact value is below 2^-126 too), NaN for NaN.
+// within (|g| + 8) * 2^-24, relative; 0 where it is below 2^-126 (g below -87),
+// NaN for NaN.
 __device__ __forceinline__ float2 logistic2(float2 g) {
   const float2 t = mul2(g, both(-1.442695041f));
   float2 e, r;
