@@ -15,8 +15,8 @@
 // its SM between the two uses of it, before and after the row's sum.  Forward
 // it stays in registers; backward, where the column sums dw take those, in
 // shared memory.  [8192 x 4096] BF16 with checkpoint: forward 42.4 us, 0.96 of
-// the copy rate (6680 GB/s), backward 43.4 us, 0.81; [16384 x 5120]: 101.1 us,
-// 1.00, and 95.2 us, 0.93.
+// the copy rate (6680 GB/s), backward 42.1 us, 0.84; [16384 x 5120]: 101.1 us,
+// 1.00, and 95.0 us, 0.93.
 #include <math.h>
 
 #include "mp_chain.cuh"
@@ -79,6 +79,20 @@ __device__ __forceinline__ float team_sum(float v, float* slot, int barrier, int
   if (lane == 0) slot[t >> 5] = v;
   named_barrier(barrier, threads);
   return lane_sum<32>(lane < (threads >> 5) ? slot[lane] : 0.0f);
+}
+
+// The same of N sums at once; slot: N floats for each warp.
+template <int N>
+__device__ __forceinline__ void team_sums(float (&v)[N], float* slot, int barrier, int t, int threads) {
+  const int lane = t & 31;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    v[k] = lane_sum<32>(v[k]);
+    if (lane == 0) slot[(t >> 5) * N + k] = v[k];
+  }
+  named_barrier(barrier, threads);
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = lane_sum<32>(lane < (threads >> 5) ? slot[lane * N + k] : 0.0f);
 }
 
 // ---------------------------------------------------------------------------
@@ -246,8 +260,10 @@ __host__ __device__ constexpr int weight_bytes(int units) { return (units + 3) /
 // the thread looks at when it begins the next group.  Each thread keeps the
 // sums of its own columns in registers over its rows (binary32, in row order);
 // at the end the CTA joins its teams' sums and writes one row of `parts`.
-// Across the barrier of the sum live only the column sums and dy * w, 64
-// registers of two units; the stream's values are converted twice.  A thread
+// Where a row needs a team, each thread has two slots: two units of a row or,
+// with ROWS, one unit of two rows, which share the weights, the column sums and
+// all that comes once a group.  Across the barrier of the sum live only the
+// column sums and dy * w; the stream's values are converted twice.  A thread
 // whose wait gave up works on what it finds and stores nothing more, but keeps
 // meeting the barriers.
 //
@@ -255,25 +271,28 @@ __host__ __device__ constexpr int weight_bytes(int units) { return (units + 3) /
 // registers 65.9 us, a ring of bulk copies 47.7, two units a thread (a row's
 // waits, sum and addresses shared by twice the elements) 45.7, the weights in
 // binary32 in shared memory, the late ring refilled early and no bank conflicts
-// 43.4.  From there on rows come at 0.97 of the copy rate; about 8 us are the
-// first rows' latency, the last round (54 rows for four teams), the join of the
-// column sums and the second kernel.
-template <int XT, bool SAVED, int L, int U>
-__global__ __maxnreg__(U == 2 ? 128 : 64) void k_norm_bwd(const __grid_constant__ NormBwd a) {
+// 43.4, two rows a team
+// instead of two units 42.1 (38.1 within a graph).  Of the rest about 6 us are the
+// first rows' latency, the last round, the join of the column sums and the second
+// kernel (2.7).
+template <int XT, bool SAVED, int L, int U, bool ROWS>
+__global__ __maxnreg__(U == 1 ? 64 : ROWS ? 96 : 128) void k_norm_bwd(const __grid_constant__ NormBwd a) {
+  constexpr int NR = ROWS ? U : 1, NU = ROWS ? 1 : U;  // rows of a thread, and units in each
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ float slots[2 * 32];
+  __shared__ float slots[2 * 32 * NR];
   __shared__ uint64_t bars[kMaxTeams * 3 * kMaxStages];
-  constexpr int R = L ? kCta / L : 1, es = XT == XF32 ? 4 : 2, ves = SAVED ? 1 : es;
+  constexpr int R1 = L ? kCta / L : 1, R = R1 * NR, es = XT == XF32 ? 4 : 2, ves = SAVED ? 1 : es;
   const int units = a.cols / kUnit, S = a.stages;
   const int T = L ? kCta : a.team;
   const int team = L ? 0 : __shfl_sync(0xFFFFFFFFu, threadIdx.x / T, 0);  // the same in a warp, and known to be
   const int t = L ? threadIdx.x : threadIdx.x - team * T;
   const int u = L ? threadIdx.x % (L ? L : 1) : t, sub = L ? threadIdx.x / (L ? L : 1) : 0;
-  // Unit k of a thread is u + k * T; one past the row's end works on the row's
-  // last unit and stores nothing.
-  uint32_t eu[U];  // its first element
+  // Slot k of a thread is unit u + k * T of its row or, with ROWS, unit u of its
+  // row sub + k * R1.  A unit past the row's end works on the row's last one and
+  // stores nothing.
+  uint32_t eu[NU];  // a unit's first element
 #pragma unroll
-  for (int k = 0; k < U; ++k) eu[k] = min(u + k * T, units - 1) * kUnit;
+  for (int k = 0; k < NU; ++k) eu[k] = min(u + k * T, units - 1) * kUnit;
   const int group = R * a.cols;  // elements
   const bool ring_dh = a.dh && a.stage_dh;
   const uint32_t early = early_bytes<XT>(group), late = late_bytes<XT, SAVED>(group, ring_dh);
@@ -281,7 +300,7 @@ __global__ __maxnreg__(U == 2 ? 128 : 64) void k_norm_bwd(const __grid_constant_
   const uint32_t early0 = weights + weight_bytes(units) + team * S * (early + late), late0 = early0 + S * early;
   uint64_t* const full = bars + team * 3 * kMaxStages;  // [early or late][stage]
   uint64_t* const done = full + 2 * kMaxStages;         // [stage]: each warp has done with the late one
-  float* const slot = slots + team * (T >> 5);
+  float* const slot = slots + team * (T >> 5) * NR;
   if (t == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
@@ -293,7 +312,7 @@ __global__ __maxnreg__(U == 2 ? 128 : 64) void k_norm_bwd(const __grid_constant_
   __syncthreads();
   chain_wait();
   chain_release();
-  const int32_t rows = (int32_t)a.rows, step = gridDim.x * (L ? R : blockDim.x / T);
+  const int32_t rows = (int32_t)a.rows, step = gridDim.x * R * (L ? 1 : blockDim.x / T);
   int32_t row0 = (team * gridDim.x + blockIdx.x) * R;
   // One thread of the team: group of rows `from` (64 bits: it may lie past the
   // end, and then nothing is done) into stage s.
@@ -320,27 +339,29 @@ __global__ __maxnreg__(U == 2 ? 128 : 64) void k_norm_bwd(const __grid_constant_
       fetch_late(s, row0 + (int64_t)s * step);
     }
   }
-  // The row's scalars are read one group ahead.
-  float next_rstd = 0.0f, next_scale[U] = {};
+  // The rows' scalars are read one group ahead.
+  float next_rstd[NR] = {}, next_scale[U] = {};
   auto scalars = [&](int64_t row) {
-    if (row >= rows) return;
-    next_rstd = a.rstd[row];
 #pragma unroll
-    for (int k = 0; k < U; ++k)
-      if constexpr (SAVED) next_scale[k] = a.scales[row * a.tiles + eu[k] / kTile];
+    for (int k = 0; k < U; ++k) {
+      const int64_t r = row + (ROWS ? k * R1 : 0);
+      if (r >= rows) return;
+      if (ROWS || k == 0) next_rstd[ROWS ? k : 0] = a.rstd[r];
+      if constexpr (SAVED) next_scale[k] = a.scales[r * a.tiles + eu[ROWS ? 0 : k] / kTile];
+    }
   };
   scalars(row0 + sub);
   // The weights in shared memory, in binary32: 16-byte piece p of unit k at p * pieces + 16 * k.
   const uint32_t pieces = weight_bytes(units) / 4;
   {
-    Weights w[U];
+    Weights w[NU];
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
+    for (int j = 0; j < NU; ++j) {
       const int k = threadIdx.x + j * blockDim.x;
       if (k < units) w[j].load(a.weight, a.wt, k);
     }
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
+    for (int j = 0; j < NU; ++j) {
       const int k = threadIdx.x + j * blockDim.x;
       float2 f[kPairs];
       w[j].floats(a.wt, f);
@@ -353,25 +374,29 @@ __global__ __maxnreg__(U == 2 ? 128 : 64) void k_norm_bwd(const __grid_constant_
     }
   }
   __syncthreads();
-  float2 acc[U][kPairs];
+  float2 acc[NU][kPairs];
 #pragma unroll
-  for (int k = 0; k < U; ++k)
+  for (int k = 0; k < NU; ++k)
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) acc[k][i] = both(0.0f);
   bool ok = true;
-  const bool second_unit = U > 1 && __any_sync(0xFFFFFFFFu, u + T < units);  // of any lane of the warp
+  const bool second = ROWS || (U > 1 && __any_sync(0xFFFFFFFFu, u + T < units));  // slot, of any lane of the warp
   // The elements of a unit's half that this lane works on first, and second:
   // lanes 4 to 7 of eight begin with the other half, so that the 16-byte reads
   // of eight lanes, 32 bytes apart, cover all banks.
-  const uint32_t first = threadIdx.x & 4 ? 8 : 0, second = 8 - first;
+  const uint32_t half0 = threadIdx.x & 4 ? 8 : 0, half1 = 8 - half0;
   int s = 0;
   uint32_t phase = 0, ea = early0, la = late0;  // the stages of this group
   for (int it = 0; row0 < rows; ++it) {
-    const bool live = L == 0 || row0 + sub < rows;
-    const float rstd = next_rstd;
-    float vs[U];
+    bool live[NR];
+    float rstd[NR], vs[U];
 #pragma unroll
-    for (int k = 0; k < U; ++k) vs[k] = SAVED ? next_scale[k] * rstd : rstd;
+    for (int k = 0; k < NR; ++k) {
+      live[k] = (L == 0 && k == 0) || (int64_t)row0 + sub + k * R1 < rows;
+      rstd[k] = next_rstd[k];
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) vs[k] = SAVED ? next_scale[k] * rstd[ROWS ? k : 0] : rstd[ROWS ? k : 0];
     scalars((int64_t)row0 + step + sub);
     if (ok) ok = mbar_wait_bounded(&full[s], phase) && mbar_wait_bounded(&full[kMaxStages + s], phase);
     if (t == 0 && ok && S > 1 && it > 0) {  // the late stage of the group before
@@ -380,73 +405,91 @@ __global__ __maxnreg__(U == 2 ? 128 : 64) void k_norm_bwd(const __grid_constant_
       if (ok) fetch_late(before, row0 + (int64_t)(S - 1) * step);
     }
     // a row past the end works on the group's first, whose copy is there
-    const uint32_t row_at = L && live ? sub * a.cols : 0;
-    // Half a unit at a time, and the stream's values twice: across the barrier
-    // stay the column sums and dy * w.
-    float2 g[U][kPairs];
-    float dot = 0.0f;
+    uint32_t at[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      if (k > 0 && !second_unit) break;
-      float2 d = both(0.0f);
-      Unit<XT> dy, v;
-      Unit<XF32> w;
-      uint2 code;
+      const int r = ROWS ? k : 0;
+      at[k] = (live[r] ? (sub + r * R1) * a.cols : 0) + eu[ROWS ? 0 : k];
+    }
+    // Half a unit at a time, and the stream's values twice: across the barrier
+    // stay the column sums and dy * w.
+    float2 g[U][kPairs], d[NR];
+#pragma unroll
+    for (int k = 0; k < NR; ++k) d[k] = both(0.0f);
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+      if (j > 0 && !second) break;
+      float2 e[NR];
+#pragma unroll
+      for (int k = 0; k < NR; ++k) e[k] = both(0.0f);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const uint32_t at = row_at + eu[k] + (half ? second : first);
-        dy.take_half(ea + at * es, half);
-        if constexpr (SAVED)
-          code = lds8(la + at);
-        else
-          v.take_half(la + at * es, half);
-        const uint32_t wp = weights + (half ? second : first) / 4 * pieces + eu[k];
+        const uint32_t h = half ? half1 : half0, wp = weights + h / 4 * pieces + eu[j];
+        Unit<XF32> w;
         w.v[2 * half] = lds16(wp);
         w.v[2 * half + 1] = lds16(wp + pieces);
 #pragma unroll
-        for (int j = 0; j < kPairs / 2; ++j) {
-          const int i = half * (kPairs / 2) + j;
-          const float2 x = mul2(SAVED ? e4m3_floats(j < 2 ? code.x : code.y, j) : v.pair(i), both(vs[k]));
-          if (live) acc[k][i] = fma2(dy.pair(i), x, acc[k][i]);
-          g[k][i] = mul2(dy.pair(i), w.pair(i));
-          d = fma2(g[k][i], x, d);
+        for (int r = 0; r < NR; ++r) {
+          const int k = ROWS ? r : j;  // the slot
+          Unit<XT> dy, v;
+          uint2 code;
+          dy.take_half(ea + (at[k] + h) * es, half);
+          if constexpr (SAVED)
+            code = lds8(la + at[k] + h);
+          else
+            v.take_half(la + (at[k] + h) * es, half);
+#pragma unroll
+          for (int q = 0; q < kPairs / 2; ++q) {
+            const int i = half * (kPairs / 2) + q;
+            const float2 x = mul2(SAVED ? e4m3_floats(q < 2 ? code.x : code.y, q) : v.pair(i), both(vs[k]));
+            if (live[r]) acc[j][i] = fma2(dy.pair(i), x, acc[j][i]);
+            g[k][i] = mul2(dy.pair(i), w.pair(i));
+            e[r] = fma2(g[k][i], x, e[r]);
+          }
         }
       }
-      if (u + k * T < units) dot += d.x + d.y;
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+        if (u + j * T < units) d[r] = add2(d[r], e[r]);
     }
-    float c = dot;
+    float c[NR];
+#pragma unroll
+    for (int k = 0; k < NR; ++k) c[k] = d[k].x + d[k].y;
     if constexpr (L != 0) {
-      c = lane_sum<L>(c);
+#pragma unroll
+      for (int k = 0; k < NR; ++k) c[k] = lane_sum<L>(c[k]);
       __syncthreads();
     } else {
-      c = team_sum(c, slot + (it & 1) * 32, team + 1, t, T);
+      team_sums(c, slot + (it & 1) * 32 * NR, team + 1, t, T);
     }
     if (t == 0 && ok) fetch_early(s, row0 + (int64_t)S * step);
-    c *= -a.inv_cols * rstd;
+#pragma unroll
+    for (int k = 0; k < NR; ++k) c[k] *= -a.inv_cols * rstd[k];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      if (k > 0 && !second_unit) break;
-      const bool out = ok && live && u + k * T < units;
-      const int64_t to = (int64_t)(row0 + sub) * a.cols + (u + k * T) * kUnit;
+      if (k > 0 && !second) break;
+      const int r = ROWS ? k : 0, j = ROWS ? 0 : k;
+      const bool out = ok && live[r] && u + j * T < units;
+      const int64_t to = ((int64_t)row0 + sub + r * R1) * a.cols + (u + j * T) * kUnit;
       Unit<XT> o, v;
       uint2 code;
       o.zero();
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const uint32_t h = half ? second : first, at = row_at + eu[k] + h;
+        const uint32_t h = half ? half1 : half0;
         if (ring_dh)
-          o.take_half(la + group * ves + at * es, half);
+          o.take_half(la + group * ves + (at[k] + h) * es, half);
         else if (a.dh && out)
           o.load_half(static_cast<const char*>(a.dh) + (to + h) * es, half);
         if constexpr (SAVED)
-          code = lds8(la + at);
+          code = lds8(la + at[k] + h);
         else
-          v.take_half(la + at * es, half);
+          v.take_half(la + (at[k] + h) * es, half);
 #pragma unroll
-        for (int j = 0; j < kPairs / 2; ++j) {
-          const int i = half * (kPairs / 2) + j;
-          const float2 x = SAVED ? e4m3_floats(j < 2 ? code.x : code.y, j) : v.pair(i);
-          o.set_pair(i, fma2(g[k][i], both(rstd), fma2(x, both(c * vs[k]), o.pair(i))));
+        for (int q = 0; q < kPairs / 2; ++q) {
+          const int i = half * (kPairs / 2) + q;
+          const float2 x = SAVED ? e4m3_floats(q < 2 ? code.x : code.y, q) : v.pair(i);
+          o.set_pair(i, fma2(g[k][i], both(rstd[r]), fma2(x, both(c[r] * vs[k]), o.pair(i))));
         }
         if (out) o.store_half(static_cast<char*>(a.dx) + (to + h) * es, half);
       }
@@ -470,14 +513,14 @@ __global__ __maxnreg__(U == 2 ? 128 : 64) void k_norm_bwd(const __grid_constant_
   }
   __syncthreads();  // the rings are free: every team has done with its last row
   float* fold = reinterpret_cast<float*>(smem);  // [team or sub-row][columns]
-  const int width = L ? L * kUnit : a.cols, deep = L ? R : blockDim.x / T;
+  const int width = L ? L * kUnit : a.cols, deep = L ? R1 : blockDim.x / T;
 #pragma unroll
-  for (int k = 0; k < U; ++k) {
+  for (int k = 0; k < NU; ++k) {
     if (L == 0 && u + k * T >= units) break;
     float* f = fold + (L ? sub : team) * width + (u + k * T) * kUnit;
 #pragma unroll
     for (int i = 0; i < kPairs; i += 2)
-      *reinterpret_cast<float4*>(f + (i < kPairs / 2 ? first : second) + 2 * i % 8) =
+      *reinterpret_cast<float4*>(f + (i < kPairs / 2 ? half0 : half1) + 2 * i % 8) =
           make_float4(acc[k][i].x, acc[k][i].y, acc[k][i + 1].x, acc[k][i + 1].y);
   }
   __syncthreads();
@@ -531,11 +574,13 @@ int64_t parts_of(int64_t rows, int64_t cols) {
   return groups < kMaxParts ? groups : kMaxParts;
 }
 
-template <int XT, bool SAVED, int L, int U>
+template <int XT, bool SAVED, int L, int U, bool ROWS>
 mp_status launch_bwd_rows(NormBwd a, const RowShape& s, int* parts, cudaStream_t st) {
   static std::atomic<uint64_t> opted{0};
-  const int64_t groups = (a.rows + s.rows_per_cta - 1) / s.rows_per_cta;
-  const int weights = weight_bytes(a.cols / kUnit), elements = s.rows_per_cta * a.cols;
+  constexpr auto kernel = k_norm_bwd<XT, SAVED, L, U, ROWS>;
+  const int rows_per_group = s.rows_per_cta * (ROWS ? U : 1);
+  const int64_t groups = (a.rows + rows_per_group - 1) / rows_per_group;
+  const int weights = weight_bytes(a.cols / kUnit), elements = rows_per_group * a.cols;
   const int early = early_bytes<XT>(elements);
   // FP32 rows of over 14336 without a checkpoint do not fit with dh, which is then read directly.
   a.stage_dh = a.dh && early + late_bytes<XT, SAVED>(elements, true) + weights <= kSmemBytes;
@@ -544,8 +589,8 @@ mp_status launch_bwd_rows(NormBwd a, const RowShape& s, int* parts, cudaStream_t
   // teams: one CTA of as many teams, but of no more than spread the rows over
   // all SMs.  Either so many that each has two stages; then as many stages, up
   // to kMaxStages, as there is room.
-  const int team = L ? kCta : team_of(s, U);
-  int per_sm = kMaxThreads / U / team;
+  const int team = L ? kCta : team_of(s, ROWS ? 1 : U);
+  int per_sm = (U == 1 ? 1024 : ROWS ? 640 : 512) / team;  // threads of 64, 96 and 128 registers on an SM
   if (L == 0 && per_sm > kMaxTeams) per_sm = kMaxTeams;
   while (per_sm > 1 && (L ? (2 * bytes + weights) * per_sm > kSmemShared : 2 * bytes * per_sm + weights > kSmemBytes))
     --per_sm;
@@ -557,23 +602,34 @@ mp_status launch_bwd_rows(NormBwd a, const RowShape& s, int* parts, cudaStream_t
   int smem = weights + teams * a.stages * bytes;
   const int fold = (L ? kCta * kUnit : teams * a.cols) * 4;  // the join of the column sums
   if (smem < fold) smem = fold;
-  if (!smem_ok(k_norm_bwd<XT, SAVED, L, U>, smem, opted)) return MP_ECUDA;
+  if (!smem_ok(kernel, smem, opted)) return MP_ECUDA;
   const int grid = resident_grid((groups + teams - 1) / teams, L ? per_sm : 1);
   *parts = grid < kMaxParts ? grid : kMaxParts;
-  launch_chained(k_norm_bwd<XT, SAVED, L, U>, dim3(*parts), dim3(teams * team), smem, st, a);
+  launch_chained(kernel, dim3(*parts), dim3(teams * team), smem, st, a);
   note_launches(1);
   return launch_status();
 }
+
+// The row length, in threads of one unit, up to which a team takes two rows at a
+// time instead of two units of one.  Two rows need more of shared memory for each
+// team, so that of long rows fewer are in flight.  GPU time in us, with two rows
+// and with two units: BF16 from the checkpoint [16384 x 1040] 28.1 and 33.7,
+// [8192 x 4096] 38.1 and 40.2, [16384 x 5120] 93.0 and 92.0, [4096 x 8192] 41.9
+// and 40.4; F32 [4096 x 1040] 14.2 and 15.8, [16384 x 1536] 62.3 and 63.0,
+// [4096 x 2048] 23.9 and 22.7, [16384 x 2560] 108.7 and 98.7.
+template <int XT>
+constexpr int two_rows_up_to() { return XT == XF32 ? 96 : 256; }
 
 template <int XT, bool SAVED>
 mp_status launch_bwd(const NormBwd& a, void* dweight, int32_t dt, cudaStream_t st) {
   int parts = 0;
   if (a.rows > 0) {
     const RowShape s = row_shape(a.cols);
-    const mp_status r = s.lanes == 8    ? launch_bwd_rows<XT, SAVED, 8, 1>(a, s, &parts, st)
-                        : s.lanes == 16 ? launch_bwd_rows<XT, SAVED, 16, 1>(a, s, &parts, st)
-                        : s.lanes == 32 ? launch_bwd_rows<XT, SAVED, 32, 1>(a, s, &parts, st)
-                                        : launch_bwd_rows<XT, SAVED, 0, 2>(a, s, &parts, st);
+    const mp_status r = s.lanes == 8    ? launch_bwd_rows<XT, SAVED, 8, 1, false>(a, s, &parts, st)
+                        : s.lanes == 16 ? launch_bwd_rows<XT, SAVED, 16, 1, false>(a, s, &parts, st)
+                        : s.lanes == 32 ? launch_bwd_rows<XT, SAVED, 32, 1, false>(a, s, &parts, st)
+                        : s.threads <= two_rows_up_to<XT>() ? launch_bwd_rows<XT, SAVED, 0, 2, true>(a, s, &parts, st)
+                                                            : launch_bwd_rows<XT, SAVED, 0, 2, false>(a, s, &parts, st);
     if (r != MP_OK) return r;
   }
   launch_chained(k_norm_dweight, dim3((a.cols + 31) / 32), dim3(32 * kFoldWarps), 0, st, (const float*)a.parts,
