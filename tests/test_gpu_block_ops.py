@@ -347,6 +347,32 @@ def test_norm_backward_against_differences():
         assert abs(float(dw[c]) - want) <= 1e-5 * (1 + abs(want))
 
 
+@pytest.mark.parametrize("cols", [528, 1536, 1552, 2064, 4096, 4112])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_norm_backward_of_pairs_of_rows(dtype, cols):
+    """Rows that come to a team two at a time, and the lengths next to that rule; a last row alone."""
+    for rows in (1, 2, 3, 303, 304, 305, 1217):
+        for saved in (True, False):
+            test_norm_backward((rows, cols), dtype, saved)
+
+
+@pytest.mark.parametrize("cols", [256, 1040, 5120])
+@pytest.mark.parametrize("bad", [0, 7, 8, 610])
+def test_norm_backward_keeps_a_nonfinite_row_to_itself(cols, bad):
+    rows = 611
+    h, dy = normal(46, rows, cols, dtype=torch.bfloat16), normal(47, rows, cols, dtype=torch.bfloat16)
+    w = torch.ones(cols, device="cuda")
+    rstd = norm(h, w)["rstd"]
+    want, _ = norm_backward(dy, w, rstd, h=h)
+    want = want.clone()
+    dy[bad, 3] = float("inf")
+    dx, dw = norm_backward(dy, w, rstd, h=h)
+    keep = torch.arange(rows, device="cuda") != bad
+    assert_bits(dx[keep], want[keep], "dx of the other rows")
+    assert not bool(torch.isfinite(dx[bad]).any())
+    assert bool(torch.isfinite(dw).sum() == cols - 1)
+
+
 def test_no_wait_gave_up():
     assert M.mp_wait_failures() == 0
 
