@@ -417,7 +417,8 @@ MP_API mp_status mx_quantize(const void* x, mp_dtype x_dtype, int64_t rows, int6
  * x, residual, h, dy, dh, dx, gate, up, dp, dgate, dup has type x_dtype.
  * cols % 16 == 0 (else MP_ESHAPE); tensors 16-byte aligned, FP32 scales and
  * rstd 4-byte, UE8M0 bytes not at all.  Sums are binary32 in an order fixed
- * by the shape and the device, so results repeat. */
+ * by the shape and the device, so results repeat; a row's own results (all but
+ * dweight) do not depend on how many rows the call has. */
 
 /* rmsnorm_residual_fp8 — h = x + residual rounded to x_dtype (h = x if
  * residual is NULL); rstd = 1 / sqrt(mean(h^2) + eps) per row; y = the cast of

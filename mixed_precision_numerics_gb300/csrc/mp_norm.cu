@@ -14,8 +14,8 @@
 // Both read and write every element once, and are bound by DRAM: a row stays on
 // its SM between the two uses of it, before and after the row's sum.  Forward
 // it stays in registers; backward, where the column sums dw take those, in
-// shared memory.  [8192 x 4096] BF16 with checkpoint: forward 42.4 us, 0.96 of
-// the copy rate (6680 GB/s), backward 42.1 us, 0.84; [16384 x 5120]: 101.1 us,
+// shared memory.  [8192 x 4096] BF16 with checkpoint: forward 42.6 us, 0.95 of
+// the copy rate (6680 GB/s), backward 42.1 us, 0.84; [16384 x 5120]: 101.3 us,
 // 1.00, and 95.0 us, 0.93.
 #include <math.h>
 
@@ -69,19 +69,33 @@ __device__ __forceinline__ float lane_sum(float v) {
   for (int d = L / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
   return v;
 }
-// Sum over the `threads` of a team (whole warps; t the thread's place in it),
-// in a fixed order, in every one of them.  `slot` (a float for each warp) must
+// Sum over the row's tiles of eight lanes each, at most kTilesMax of them, in
+// every lane of the row; slot: a float for each.  All of the CTA's threads call.
+__device__ __forceinline__ float tiles_sum(float v, float* slot, int tiles, int u) {
+  v = lane_sum<8>(v);
+  const int i = u & 7;
+  if (i == 0) slot[u >> 3] = v;
+  __syncthreads();
+  return lane_sum<8>((i < tiles ? slot[i] : 0.0f) + (i + 8 < tiles ? slot[i + 8] : 0.0f));
+}
+// Sum over the CTA's threads and their U units, in every one of them.  Units 32 b
+// to 32 b + 31 are added up first, whatever U is, so that a row's sum does not
+// depend on how many rows the call has; slots: 32 floats.
+template <int U>
+__device__ __forceinline__ float cta_sum(float (&v)[U], float* slots) {
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    v[k] = lane_sum<32>(v[k]);
+    if (lane == 0) slots[(threadIdx.x >> 5) + k * warps] = v[k];
+  }
+  __syncthreads();
+  return lane_sum<32>(lane < U * warps ? slots[lane] : 0.0f);
+}
+// N sums over the `threads` of a team (whole warps; t the thread's place in it),
+// in a fixed order, in every one of them.  `slot` (N floats for each warp) must
 // not be written again before every thread has passed the next barrier:
 // callers alternate between two.
-__device__ __forceinline__ float team_sum(float v, float* slot, int barrier, int t, int threads) {
-  v = lane_sum<32>(v);
-  const int lane = t & 31;
-  if (lane == 0) slot[t >> 5] = v;
-  named_barrier(barrier, threads);
-  return lane_sum<32>(lane < (threads >> 5) ? slot[lane] : 0.0f);
-}
-
-// The same of N sums at once; slot: N floats for each warp.
 template <int N>
 __device__ __forceinline__ void team_sums(float (&v)[N], float* slot, int barrier, int t, int threads) {
   const int lane = t & 31;
@@ -98,6 +112,8 @@ __device__ __forceinline__ void team_sums(float (&v)[N], float* slot, int barrie
 // ---------------------------------------------------------------------------
 // Forward
 // ---------------------------------------------------------------------------
+constexpr int kInTiles = 1;    // a layout beside 8, 16 and 32 lanes: see in_tiles
+constexpr int kTilesMax = 16;  // tiles of its rows
 struct NormFwd {
   const void *x, *residual, *weight;
   void* h;
@@ -107,33 +123,37 @@ struct NormFwd {
   float* ckpt_scales;
   int64_t rows;
   int32_t cols, tiles, wt;
+  int32_t group;  // rows of a CTA, where L is kInTiles
   float eps, inv_cols;
 };
 
-// A row lies in L lanes of a warp or (L = 0) in the CTA, U units a thread: unit
-// k of thread t is t + k * threads.  Every CTA is launched at once; the others
-// on the SM keep DRAM busy while one meets its row's barrier.  Rows of a CTA
-// take two units a thread for the 16-bit types: their weights are read after
-// the row's sum, which leaves 64 registers and 2048 units, two rows of 16384, on
-// an SM.  (With one unit a thread half as many are there: [16384 x 5120] BF16
-// 107.6 us against 99.0, [7000 x 16384] 163.7 against 137.7.)  For FP32 two
-// units take 80 registers and the weights' loads cost more than they give up to
-// 8192 columns ([7000 x 4096] 64.6 us with one unit, 70.6 with two); above, one
-// unit a thread would leave a single row on an SM ([7000 x 10816] 223.8 us and
-// 185.3).  Dropped: CTAs that stay and fetch the next rows into shared memory a
-// thread at a time, 60.2 us on [8192 x 4096] BF16 against 42.8; a cluster of
-// CTAs for a row, 130 us on [16384 x 5120].
+// A row lies in L lanes of a warp, in tiles of eight lanes of a CTA that holds
+// `group` rows (L = kInTiles) or in the whole CTA (L = 0), U units a thread:
+// unit k of thread t is t + k * threads.  Every CTA is launched at once; the
+// others on the SM keep DRAM busy while one meets its row's barrier.
+// Dropped: CTAs that stay and fetch the next rows into shared memory a thread
+// at a time, 60.2 us on [8192 x 4096] BF16 against 42.8; a cluster of CTAs for a
+// row, 130 us on [16384 x 5120].
 template <int XT, int L, int U>
-constexpr int fwd_threads() { return L ? kCta : U == 1 ? kMaxThreads : XT == XF32 ? 768 : kMaxThreads / 2; }
+constexpr int fwd_threads() { return L == kInTiles ? 512 : L ? kCta : U == 1 ? kMaxThreads : XT == XF32 ? 768 : kMaxThreads / 2; }
 template <int XT, int L, int U, bool SAVE>
 __global__ __launch_bounds__(fwd_threads<XT, L, U>(), XT != XF32 && U == 2 ? 2 : 1) void k_norm_fwd(const __grid_constant__ NormFwd a) {
-  __shared__ float slots[32];
+  __shared__ float slots[L == kInTiles ? 5 * kTilesMax : 32];
   chain_wait();
   chain_release();
-  constexpr int R = L ? kCta / L : 1;
   const int units = a.cols / kUnit, T = blockDim.x;
-  const int u = L ? threadIdx.x % (L ? L : 1) : threadIdx.x, sub = L ? threadIdx.x / (L ? L : 1) : 0;
-  const int64_t row = (int64_t)blockIdx.x * R + sub;
+  int u = threadIdx.x, sub = 0, R = 1;  // the thread's unit, its row among the CTA's, their number
+  if constexpr (L == kInTiles) {
+    sub = u / (a.tiles * 8);
+    u -= sub * a.tiles * 8;
+    R = a.group;
+  } else if constexpr (L > 0) {
+    sub = u / L;
+    u %= L;
+    R = kCta / L;
+  }
+  // Threads past the last of `group` rows, less than a row of them, have none.
+  const int64_t row = L == kInTiles && sub >= R ? a.rows : (int64_t)blockIdx.x * R + sub;
   Place p[U];
   Unit<XT> h[U][2], r[U];
   Weights w;
@@ -152,12 +172,12 @@ __global__ __launch_bounds__(fwd_threads<XT, L, U>(), XT != XF32 && U == 2 ? 2 :
       if constexpr (U == 1) w.load(a.weight, a.wt, p[k].u);
     }
   }
-  float2 ss = both(0.0f);
-  float amax[U];
+  float part[U], amax[U];
 #pragma unroll
   for (int k = 0; k < U; ++k) {
     if (a.residual) h[k][0].add(r[k]);
     if (p[k].in && a.h) h[k][0].store(a.h, p[k].at);
+    float2 ss = both(0.0f);
     amax[k] = 0.0f;
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
@@ -165,9 +185,11 @@ __global__ __launch_bounds__(fwd_threads<XT, L, U>(), XT != XF32 && U == 2 ? 2 :
       ss = fma2(f, f, ss);
       if constexpr (SAVE) amax[k] = max3_abs_nan(amax[k], f.x, f.y);
     }
+    part[k] = ss.x + ss.y;
   }
-  const float part = ss.x + ss.y;
-  const float sum = L ? lane_sum<L ? L : 1>(part) : team_sum(part, slots, 1, threadIdx.x, T);
+  const float sum = L == kInTiles ? tiles_sum(part[0], slots + sub * kTilesMax, a.tiles, u)
+                    : L           ? lane_sum<L ? L : 1>(part[0])
+                                  : cta_sum(part, slots);
   const float rstd = rsqrtf(fmaf(sum, a.inv_cols, a.eps));
   if (u == 0 && row < a.rows && a.rstd) a.rstd[row] = rstd;
 #pragma unroll
@@ -192,21 +214,60 @@ __global__ __launch_bounds__(fwd_threads<XT, L, U>(), XT != XF32 && U == 2 ? 2 :
 
 template <int XT, int L, int U, bool SAVE>
 mp_status launch_fwd(const NormFwd& a, const RowShape& s, cudaStream_t st) {
-  const int64_t groups = (a.rows + s.rows_per_cta - 1) / s.rows_per_cta;  // below 2^31
-  launch_chained(k_norm_fwd<XT, L, U, SAVE>, dim3((unsigned)groups), dim3(L ? kCta : team_of(s, U)), 0, st, a);
+  const int rows = L == kInTiles ? a.group : s.rows_per_cta;
+  const int threads = L == kInTiles ? (rows * a.tiles + 3) / 4 * 32 : L ? kCta : team_of(s, U);
+  const int64_t groups = (a.rows + rows - 1) / rows;  // below 2^31
+  launch_chained(k_norm_fwd<XT, L, U, SAVE>, dim3((unsigned)groups), dim3(threads), 0, st, a);
   note_launches(1);
   return launch_status();
 }
 
+// Rows that do not fill their warps, in tiles instead.  BF16, GPU time in us
+// with this layout and with whole warps: [16384 x 576] 12.9 and 18.3, [1024 x
+// 768] 2.7 and 3.7, [16384 x 1280] 28.2 and 31.2, [16384 x 384] 8.0 and 9.1; the
+// same at 1536 and 2048 columns, and 40.4 and 38.2 at 1792.  Four tiles are a
+// warp, whose rows need no barrier: [16384 x 512] 9.8, and 17.3 in this layout.
+// FP32 is nearer to DRAM: [16384 x 576] 23.4 and 25.2, but [4096 x 896] 11.1 and
+// 10.3, [16384 x 384] 16.6 and 15.8.
+template <int XT>
+bool in_tiles(int tiles) {
+  return XT == XF32 ? tiles == 5 || tiles == 6 : tiles >= 3 && tiles <= kTilesMax && tiles != 4;
+}
+// Rows of a CTA in that layout: as many as let the most tiles be on an SM.
+int rows_in_tiles(int tiles) {
+  int best = 1, most = 0;
+  for (int rows = 1; rows <= 4; ++rows) {  // with four no lane is idle
+    const int warps = (rows * tiles + 3) / 4, held = kMaxThreads / 32 / warps * rows;
+    if (held > most) most = held, best = rows;
+  }
+  return best;
+}
+// Whether a CTA that takes one row holds one unit a thread, and not two.  One
+// has its weights by the row's sum, where two (in the 16-bit types) read them
+// after it, to be 64 registers and to have twice the rows on an SM.  That counts
+// once the rows come in several waves, the earlier the fewer fit on an SM.  BF16,
+// us with one and with two: one row of 4096 2.2 and 3.0, [37 x 5120] 2.4 and 3.2,
+// [1024 x 4096] 5.8 and 6.5, [304 x 16384] 7.8 and 6.8, [8192 x 4096] 42.7 and
+// 43.4, [16384 x 5120] 107.2 and 100.4.  FP32 has 80 registers with two, and is
+// better off with one up to 8192 columns ([7000 x 4096] 64.6 and 70.6; [7000 x
+// 10816] 223.8 and 185.3).
+template <int XT>
+bool one_unit(const RowShape& s, int64_t rows) {
+  const int held = kMaxThreads / s.threads;
+  return (XT == XF32 && held > 1) || rows <= (int64_t)sm_count() * held * (held < 3 ? held : 3);
+}
+
 template <int XT, bool SAVE>
-mp_status launch_fwd_shape(const NormFwd& a, cudaStream_t st) {
+mp_status launch_fwd_shape(NormFwd a, cudaStream_t st) {
   const RowShape s = row_shape(a.cols);
+  if (in_tiles<XT>(a.tiles)) {
+    a.group = rows_in_tiles(a.tiles);
+    return launch_fwd<XT, kInTiles, 1, SAVE>(a, s, st);
+  }
   if (s.lanes == 8) return launch_fwd<XT, 8, 1, SAVE>(a, s, st);
   if (s.lanes == 16) return launch_fwd<XT, 16, 1, SAVE>(a, s, st);
   if (s.lanes == 32) return launch_fwd<XT, 32, 1, SAVE>(a, s, st);
-  if constexpr (XT == XF32)
-    if (s.threads <= kMaxThreads / 2) return launch_fwd<XT, 0, 1, SAVE>(a, s, st);
-  return launch_fwd<XT, 0, 2, SAVE>(a, s, st);
+  return one_unit<XT>(s, a.rows) ? launch_fwd<XT, 0, 1, SAVE>(a, s, st) : launch_fwd<XT, 0, 2, SAVE>(a, s, st);
 }
 template <int XT>
 mp_status launch_fwd_type(const NormFwd& a, cudaStream_t st) {

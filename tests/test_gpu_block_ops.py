@@ -163,6 +163,33 @@ def test_norm_weight_types_and_optional_outputs(dtype, wt):
     assert_bits(y, o["y"], "codes without rstd")
 
 
+@pytest.mark.parametrize("cols", [272, 512, 576, 1040, 2064, 4096, 5120, 8208, 16384])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_a_row_does_not_depend_on_the_number_of_rows(dtype, cols):
+    """Layouts that are chosen by the number of rows give the same bits, forward and for dx."""
+    rows, few = 2800 if cols < 4096 else 1900, 5
+    x, dy = normal(50, rows, cols, dtype=TYPES[dtype]), normal(51, rows, cols, dtype=TYPES[dtype])
+    w = (1.0 + normal(52, cols, sigma=0.3)).to(TYPES[dtype])
+    a = norm(x, w, residual=dy)
+    da, _ = norm_backward(dy, w, a["rstd"], ckpt=a["ckpt"], scales=a["ckpt_scales"], dh=x)
+    for part in (slice(0, few), slice(rows - few, rows)):
+        xs, dys = x[part].clone(), dy[part].clone()
+        b = norm(xs, w, residual=dys)
+        for k in ("h", "rstd", "y", "y_scales", "ckpt", "ckpt_scales"):
+            assert_bits(a[k][part], b[k], k)
+        db, _ = norm_backward(dys, w, b["rstd"], ckpt=b["ckpt"], scales=b["ckpt_scales"], dh=xs)
+        assert_bits(da[part], db, "dx")
+
+
+@pytest.mark.parametrize("cols", [272, 384, 528, 640, 768, 896, 1152, 1280, 1408, 1664, 1792, 1920, 2048])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_norm_of_rows_of_whole_tiles(dtype, cols):
+    """Rows that share a CTA, and numbers of them that end inside one."""
+    for rows in (1, 2, 3, 5, 163):
+        for block in (128, 32) if cols % 32 == 0 else (128,):
+            test_norm_forward((rows, cols), dtype, block)
+
+
 def test_norm_writes_the_stream_over_its_input():
     x, r = normal(9, 13, 1040, dtype=torch.bfloat16), normal(10, 13, 1040, dtype=torch.bfloat16)
     w = normal(11, 1040)
