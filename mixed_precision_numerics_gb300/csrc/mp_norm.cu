@@ -34,7 +34,8 @@ constexpr int kMaxParts = 608;      // partial sums of dweight: four CTAs on eac
 
 // How a row is laid over threads, by its length alone: `lanes` of a warp (8,
 // 16 or 32) and kCta / lanes rows a CTA, or (lanes 0) a CTA of `threads`, one
-// 16-element unit a thread.
+// 16-element unit a thread.  Instead of either, a row may lie in whole tiles (of
+// eight lanes) of a CTA or team: in_tiles, tiles_save_lanes.
 struct RowShape {
   int lanes, threads, rows_per_cta;
 };
@@ -91,6 +92,24 @@ __device__ __forceinline__ float cta_sum(float (&v)[U], float* slots) {
   }
   __syncthreads();
   return lane_sum<32>(lane < U * warps ? slots[lane] : 0.0f);
+}
+// The same of N sums, in a team of `threads`; slot: N floats for each tile of the
+// team.  It must not be written again before every thread has passed the next
+// barrier: callers alternate between two.
+template <int N>
+__device__ __forceinline__ void tiles_sums(float (&v)[N], float* slot, int barrier, int t, int threads, int tiles,
+                                           int sub) {
+  const int i = t & 7;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    v[k] = lane_sum<8>(v[k]);
+    if (i == 0) slot[(t >> 3) * N + k] = v[k];
+  }
+  named_barrier(barrier, threads);
+  const float* row = slot + sub * tiles * N;
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    v[k] = lane_sum<8>((i < tiles ? row[i * N + k] : 0.0f) + (i + 8 < tiles ? row[(i + 8) * N + k] : 0.0f));
 }
 // N sums over the `threads` of a team (whole warps; t the thread's place in it),
 // in a fixed order, in every one of them.  `slot` (N floats for each warp) must
@@ -286,6 +305,7 @@ struct NormBwd {
   int64_t rows;
   int32_t cols, tiles, wt;
   int32_t team;     // threads of a team
+  int32_t group;    // of its rows, one unit a thread, where L is kInTiles
   int32_t stages;   // of its ring
   bool stage_dh;    // whether dh comes through it
   float inv_cols;
@@ -293,6 +313,7 @@ struct NormBwd {
 
 constexpr int kMaxStages = 4;
 constexpr int kMaxTeams = 15;            // a named barrier each
+constexpr int kRowsThreads = 640;        // threads of 96 registers on an SM
 
 __device__ unsigned int g_norm_wait_failures;  // bounded waits that gave up (read by mp_wait_failures)
 
@@ -323,31 +344,35 @@ __host__ __device__ constexpr int weight_bytes(int units) { return (units + 3) /
 // at the end the CTA joins its teams' sums and writes one row of `parts`.
 // Where a row needs a team, each thread has two slots: two units of a row or,
 // with ROWS, one unit of two rows, which share the weights, the column sums and
-// all that comes once a group.  Across the barrier of the sum live only the
-// column sums and dy * w; the stream's values are converted twice.  A thread
-// whose wait gave up works on what it finds and stores nothing more, but keeps
-// meeting the barriers.
+// all that comes once a group.  With L = kInTiles a team has `group` rows beside
+// each other, in tiles of eight lanes (and as many more in the second slots).
+// Across the barrier of the sum live only the column sums and dy * w; the
+// stream's values are converted twice.  A thread whose wait gave up works on what
+// it finds and stores nothing more, but keeps meeting the barriers.
 //
 // [8192 x 4096] BF16 from the checkpoint, both kernels: with loads into
 // registers 65.9 us, a ring of bulk copies 47.7, two units a thread (a row's
 // waits, sum and addresses shared by twice the elements) 45.7, the weights in
 // binary32 in shared memory, the late ring refilled early and no bank conflicts
-// 43.4, two rows a team
-// instead of two units 42.1 (38.1 within a graph).  Of the rest about 6 us are the
-// first rows' latency, the last round, the join of the column sums and the second
-// kernel (2.7).
+// 43.4, two rows a team instead of two units 42.1 (38.1 within a
+// graph).  Of the rest about 6 us are the first rows' latency, the last round, the
+// join of the column sums and the second kernel (2.7).
 template <int XT, bool SAVED, int L, int U, bool ROWS>
 __global__ __maxnreg__(U == 1 ? 64 : ROWS ? 96 : 128) void k_norm_bwd(const __grid_constant__ NormBwd a) {
   constexpr int NR = ROWS ? U : 1, NU = ROWS ? 1 : U;  // rows of a thread, and units in each
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ float slots[2 * 32 * NR];
+  constexpr bool kLanes = L > kInTiles, kTiles = L == kInTiles;
+  constexpr int kSlots = kTiles ? kRowsThreads / 8 + kTilesMax : 32;  // a thread without a row reads up to a row past
+  __shared__ float slots[2 * kSlots * NR];
   __shared__ uint64_t bars[kMaxTeams * 3 * kMaxStages];
-  constexpr int R1 = L ? kCta / L : 1, R = R1 * NR, es = XT == XF32 ? 4 : 2, ves = SAVED ? 1 : es;
+  constexpr int es = XT == XF32 ? 4 : 2, ves = SAVED ? 1 : es;
+  const int R1 = kTiles ? a.group : kLanes ? kCta / (L ? L : 1) : 1, R = R1 * NR;
   const int units = a.cols / kUnit, S = a.stages;
-  const int T = L ? kCta : a.team;
-  const int team = L ? 0 : __shfl_sync(0xFFFFFFFFu, threadIdx.x / T, 0);  // the same in a warp, and known to be
-  const int t = L ? threadIdx.x : threadIdx.x - team * T;
-  const int u = L ? threadIdx.x % (L ? L : 1) : t, sub = L ? threadIdx.x / (L ? L : 1) : 0;
+  const int T = kLanes ? kCta : a.team;
+  const int team = kLanes ? 0 : __shfl_sync(0xFFFFFFFFu, threadIdx.x / T, 0);  // the same in a warp, and known to be
+  const int t = kLanes ? threadIdx.x : threadIdx.x - team * T;
+  const int lanes = kTiles ? a.tiles * 8 : kLanes ? L : T;  // of a row
+  const int sub = L ? t / lanes : 0, u = t - sub * lanes;
   // Slot k of a thread is unit u + k * T of its row or, with ROWS, unit u of its
   // row sub + k * R1.  A unit past the row's end works on the row's last one and
   // stores nothing.
@@ -361,7 +386,7 @@ __global__ __maxnreg__(U == 1 ? 64 : ROWS ? 96 : 128) void k_norm_bwd(const __gr
   const uint32_t early0 = weights + weight_bytes(units) + team * S * (early + late), late0 = early0 + S * early;
   uint64_t* const full = bars + team * 3 * kMaxStages;  // [early or late][stage]
   uint64_t* const done = full + 2 * kMaxStages;         // [stage]: each warp has done with the late one
-  float* const slot = slots + team * (T >> 5) * NR;
+  float* const slot = slots + team * (T >> (kTiles ? 3 : 5)) * NR;
   if (t == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
@@ -373,7 +398,7 @@ __global__ __maxnreg__(U == 1 ? 64 : ROWS ? 96 : 128) void k_norm_bwd(const __gr
   __syncthreads();
   chain_wait();
   chain_release();
-  const int32_t rows = (int32_t)a.rows, step = gridDim.x * R * (L ? 1 : blockDim.x / T);
+  const int32_t rows = (int32_t)a.rows, step = gridDim.x * R * (kLanes ? 1 : blockDim.x / T);
   int32_t row0 = (team * gridDim.x + blockIdx.x) * R;
   // One thread of the team: group of rows `from` (64 bits: it may lie past the
   // end, and then nothing is done) into stage s.
@@ -453,7 +478,7 @@ __global__ __maxnreg__(U == 1 ? 64 : ROWS ? 96 : 128) void k_norm_bwd(const __gr
     float rstd[NR], vs[U];
 #pragma unroll
     for (int k = 0; k < NR; ++k) {
-      live[k] = (L == 0 && k == 0) || (int64_t)row0 + sub + k * R1 < rows;
+      live[k] = (L == 0 && k == 0) || ((!kTiles || sub < R1) && (int64_t)row0 + sub + k * R1 < rows);
       rstd[k] = next_rstd[k];
     }
 #pragma unroll
@@ -516,12 +541,14 @@ __global__ __maxnreg__(U == 1 ? 64 : ROWS ? 96 : 128) void k_norm_bwd(const __gr
     float c[NR];
 #pragma unroll
     for (int k = 0; k < NR; ++k) c[k] = d[k].x + d[k].y;
-    if constexpr (L != 0) {
+    if constexpr (kLanes) {
 #pragma unroll
       for (int k = 0; k < NR; ++k) c[k] = lane_sum<L>(c[k]);
       __syncthreads();
+    } else if constexpr (kTiles) {
+      tiles_sums(c, slot + (it & 1) * kSlots * NR, team + 1, t, T, a.tiles, sub);
     } else {
-      team_sums(c, slot + (it & 1) * 32 * NR, team + 1, t, T);
+      team_sums(c, slot + (it & 1) * kSlots * NR, team + 1, t, T);
     }
     if (t == 0 && ok) fetch_early(s, row0 + (int64_t)S * step);
 #pragma unroll
@@ -574,11 +601,11 @@ __global__ __maxnreg__(U == 1 ? 64 : ROWS ? 96 : 128) void k_norm_bwd(const __gr
   }
   __syncthreads();  // the rings are free: every team has done with its last row
   float* fold = reinterpret_cast<float*>(smem);  // [team or sub-row][columns]
-  const int width = L ? L * kUnit : a.cols, deep = L ? R1 : blockDim.x / T;
+  const int width = kLanes ? L * kUnit : a.cols, deep = kLanes ? R1 : blockDim.x / T * R1;
 #pragma unroll
   for (int k = 0; k < NU; ++k) {
-    if (L == 0 && u + k * T >= units) break;
-    float* f = fold + (L ? sub : team) * width + (u + k * T) * kUnit;
+    if (!kLanes && (u + k * T >= units || sub >= R1)) break;
+    float* f = fold + (team * R1 + sub) * width + (u + k * T) * kUnit;
 #pragma unroll
     for (int i = 0; i < kPairs; i += 2)
       *reinterpret_cast<float4*>(f + (i < kPairs / 2 ? half0 : half1) + 2 * i % 8) =
@@ -639,7 +666,8 @@ template <int XT, bool SAVED, int L, int U, bool ROWS>
 mp_status launch_bwd_rows(NormBwd a, const RowShape& s, int* parts, cudaStream_t st) {
   static std::atomic<uint64_t> opted{0};
   constexpr auto kernel = k_norm_bwd<XT, SAVED, L, U, ROWS>;
-  const int rows_per_group = s.rows_per_cta * (ROWS ? U : 1);
+  constexpr bool kLanes = L > kInTiles;
+  const int rows_per_group = (L == kInTiles ? a.group : s.rows_per_cta) * (ROWS ? U : 1);
   const int64_t groups = (a.rows + rows_per_group - 1) / rows_per_group;
   const int weights = weight_bytes(a.cols / kUnit), elements = rows_per_group * a.cols;
   const int early = early_bytes<XT>(elements);
@@ -650,22 +678,23 @@ mp_status launch_bwd_rows(NormBwd a, const RowShape& s, int* parts, cudaStream_t
   // teams: one CTA of as many teams, but of no more than spread the rows over
   // all SMs.  Either so many that each has two stages; then as many stages, up
   // to kMaxStages, as there is room.
-  const int team = L ? kCta : team_of(s, ROWS ? 1 : U);
-  int per_sm = (U == 1 ? 1024 : ROWS ? 640 : 512) / team;  // threads of 64, 96 and 128 registers on an SM
-  if (L == 0 && per_sm > kMaxTeams) per_sm = kMaxTeams;
-  while (per_sm > 1 && (L ? (2 * bytes + weights) * per_sm > kSmemShared : 2 * bytes * per_sm + weights > kSmemBytes))
+  const int team = kLanes ? kCta : L == kInTiles ? (a.group * a.tiles + 3) / 4 * 32 : team_of(s, ROWS ? 1 : U);
+  int per_sm = (U == 1 ? 1024 : ROWS ? kRowsThreads : 512) / team;  // threads of 64, 96 and 128 registers on an SM
+  if (!kLanes && per_sm > kMaxTeams) per_sm = kMaxTeams;
+  while (per_sm > 1 && (kLanes ? (2 * bytes + weights) * per_sm > kSmemShared : 2 * bytes * per_sm + weights > kSmemBytes))
     --per_sm;
   const int64_t spread = (groups + sm_count() - 1) / sm_count();
-  const int teams = L ? 1 : (int)(per_sm < spread ? per_sm : spread);
+  const int teams = kLanes ? 1 : (int)(per_sm < spread ? per_sm : spread);
   a.team = team;
-  a.stages = ((L ? kSmemShared / per_sm : kSmemBytes) - weights) / (bytes * teams);
+  a.stages = ((kLanes ? kSmemShared / per_sm : kSmemBytes) - weights) / (bytes * teams);
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   int smem = weights + teams * a.stages * bytes;
-  const int fold = (L ? kCta * kUnit : teams * a.cols) * 4;  // the join of the column sums
+  const int fold = (kLanes ? kCta * kUnit : teams * (L == kInTiles ? a.group : 1) * a.cols) * 4;  // the join of the column sums
   if (smem < fold) smem = fold;
   if (!smem_ok(kernel, smem, opted)) return MP_ECUDA;
-  const int grid = resident_grid((groups + teams - 1) / teams, L ? per_sm : 1);
-  *parts = grid < kMaxParts ? grid : kMaxParts;
+  const int grid = resident_grid((groups + teams - 1) / teams, kLanes ? per_sm : 1);
+  const int64_t room = parts_of(a.rows, a.cols);  // partial rows in the workspace
+  *parts = (int)(grid < room ? grid : room);
   launch_chained(kernel, dim3(*parts), dim3(teams * team), smem, st, a);
   note_launches(1);
   return launch_status();
@@ -681,16 +710,45 @@ mp_status launch_bwd_rows(NormBwd a, const RowShape& s, int* parts, cudaStream_t
 template <int XT>
 constexpr int two_rows_up_to() { return XT == XF32 ? 96 : 256; }
 
+// Rows (of 5 to 16 tiles) that would leave a sixth of whole warps idle lie in
+// tiles of a team that takes twice `group` of them.  GPU time in us with this
+// layout and without, BF16 from the checkpoint: [4096 x 640] 7.1 and 9.4, [16384 x
+// 528] 15.4 and 19.3, [16384 x 768] 19.5 and 21.0, [16384 x 1040] 25.2 and 28.3,
+// [16384 x 1664] 33.2 and 35.4; where fewer lanes are idle it lost ([16384 x 896]
+// 22.9 and 22.0, [16384 x 1792] 37.7 and 36.0).
+// FP32 was as often slower as faster ([16384 x 640] 31.1 and 29.6, [16384 x 576]
+// 25.0 and 29.3).
+bool tiles_save_lanes(int tiles) { return tiles > 4 && tiles <= kTilesMax && 6 * tiles <= 5 * ((tiles + 3) / 4 * 4); }
+// Such rows of a team, for each of a thread's two: as many as let the most be on
+// an SM, by its registers and by shared memory for two stages of `bytes` each.
+int rows_of_team(const NormBwd& a, int bytes) {
+  int best = 1, most = 0;
+  for (int rows = 1; rows <= 4; ++rows) {
+    const int by_regs = kRowsThreads / 32 / ((rows * a.tiles + 3) / 4);
+    const int by_smem = (kSmemBytes - weight_bytes(a.cols / kUnit)) / (2 * rows * bytes);
+    int teams = by_regs < by_smem ? by_regs : by_smem;
+    if (teams > kMaxTeams) teams = kMaxTeams;
+    if (teams * rows > most) most = teams * rows, best = rows;
+  }
+  return best;
+}
+
 template <int XT, bool SAVED>
-mp_status launch_bwd(const NormBwd& a, void* dweight, int32_t dt, cudaStream_t st) {
+mp_status launch_bwd(NormBwd a, void* dweight, int32_t dt, cudaStream_t st) {
   int parts = 0;
   if (a.rows > 0) {
     const RowShape s = row_shape(a.cols);
-    const mp_status r = s.lanes == 8    ? launch_bwd_rows<XT, SAVED, 8, 1, false>(a, s, &parts, st)
-                        : s.lanes == 16 ? launch_bwd_rows<XT, SAVED, 16, 1, false>(a, s, &parts, st)
-                        : s.lanes == 32 ? launch_bwd_rows<XT, SAVED, 32, 1, false>(a, s, &parts, st)
-                        : s.threads <= two_rows_up_to<XT>() ? launch_bwd_rows<XT, SAVED, 0, 2, true>(a, s, &parts, st)
-                                                            : launch_bwd_rows<XT, SAVED, 0, 2, false>(a, s, &parts, st);
+    mp_status r;
+    if (XT != XF32 && tiles_save_lanes(a.tiles)) {
+      a.group = rows_of_team(a, 2 * (early_bytes<XT>(a.cols) + late_bytes<XT, SAVED>(a.cols, a.dh)));
+      r = launch_bwd_rows<XT, SAVED, XT == XF32 ? 0 : kInTiles, 2, true>(a, s, &parts, st);
+    } else {
+      r = s.lanes == 8    ? launch_bwd_rows<XT, SAVED, 8, 1, false>(a, s, &parts, st)
+          : s.lanes == 16 ? launch_bwd_rows<XT, SAVED, 16, 1, false>(a, s, &parts, st)
+          : s.lanes == 32 ? launch_bwd_rows<XT, SAVED, 32, 1, false>(a, s, &parts, st)
+          : s.threads <= two_rows_up_to<XT>() ? launch_bwd_rows<XT, SAVED, 0, 2, true>(a, s, &parts, st)
+                                              : launch_bwd_rows<XT, SAVED, 0, 2, false>(a, s, &parts, st);
+    }
     if (r != MP_OK) return r;
   }
   launch_chained(k_norm_dweight, dim3((a.cols + 31) / 32), dim3(32 * kFoldWarps), 0, st, (const float*)a.parts,

@@ -374,7 +374,7 @@ def test_norm_backward_against_differences():
         assert abs(float(dw[c]) - want) <= 1e-5 * (1 + abs(want))
 
 
-@pytest.mark.parametrize("cols", [528, 1536, 1552, 2064, 4096, 4112])
+@pytest.mark.parametrize("cols", [528, 640, 768, 1152, 1280, 1536, 1552, 2064, 4096, 4112])
 @pytest.mark.parametrize("dtype", TYPES)
 def test_norm_backward_of_pairs_of_rows(dtype, cols):
     """Rows that come to a team two at a time, and the lengths next to that rule; a last row alone."""
