@@ -63,6 +63,11 @@ bool smem_ok(K kernel, int bytes, std::atomic<uint64_t>& done) {
   return bytes <= 32 * 1024 || smem_opt_in(kernel, kSmemBytes, done);
 }
 
+// Brings bytes (a multiple of 16, as their address is) into L2.
+__device__ __forceinline__ void prefetch_l2(const void* at, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(__cvta_generic_to_global(at)), "r"(bytes) : "memory");
+}
+
 // Sum over the L lanes that hold one row, in every one of them.
 template <int L>
 __device__ __forceinline__ float lane_sum(float v) {
@@ -357,7 +362,13 @@ __host__ __device__ constexpr int weight_bytes(int units) { return (units + 3) /
 // 43.4, two rows a team instead of two units 42.1 (38.1 within a
 // graph).  Of the rest about 6 us are the first rows' latency, the last round, the
 // join of the column sums and the second kernel (2.7).
-template <int XT, bool SAVED, int L, int U, bool ROWS>
+//
+// ONE: rows so long that there is room for one stage (FP32 of over 10500 columns
+// from the checkpoint, and of over 8900 without) would meet all of DRAM's latency
+// each time; so the next group's bytes are sent for as far as L2.  FP32 [7000 x
+// 12288] from the checkpoint 191 us, without the prefetch 225; [7000 x 9216] 164
+// and 201.
+template <int XT, bool SAVED, int L, int U, bool ROWS, bool ONE>
 __global__ __maxnreg__(U == 1 ? 64 : ROWS ? 96 : 128) void k_norm_bwd(const __grid_constant__ NormBwd a) {
   constexpr int NR = ROWS ? U : 1, NU = ROWS ? 1 : U;  // rows of a thread, and units in each
   extern __shared__ __align__(128) unsigned char smem[];
@@ -367,7 +378,7 @@ __global__ __maxnreg__(U == 1 ? 64 : ROWS ? 96 : 128) void k_norm_bwd(const __gr
   __shared__ uint64_t bars[kMaxTeams * 3 * kMaxStages];
   constexpr int es = XT == XF32 ? 4 : 2, ves = SAVED ? 1 : es;
   const int R1 = kTiles ? a.group : kLanes ? kCta / (L ? L : 1) : 1, R = R1 * NR;
-  const int units = a.cols / kUnit, S = a.stages;
+  const int units = a.cols / kUnit, S = ONE ? 1 : a.stages;
   const int T = kLanes ? kCta : a.team;
   const int team = kLanes ? 0 : __shfl_sync(0xFFFFFFFFu, threadIdx.x / T, 0);  // the same in a warp, and known to be
   const int t = kLanes ? threadIdx.x : threadIdx.x - team * T;
@@ -418,6 +429,15 @@ __global__ __maxnreg__(U == 1 ? 64 : ROWS ? 96 : 128) void k_norm_bwd(const __gr
     const char* stream = SAVED ? reinterpret_cast<const char*>(a.codes) : static_cast<const char*>(a.h);
     bulk_g2s(to, stream + from * a.cols * ves, n * ves, bar, policy);
     if (ring_dh) bulk_g2s(to + group * ves, static_cast<const char*>(a.dh) + from * a.cols * es, n * es, bar, policy);
+  };
+  // With one stage (ONE), the next group's bytes come as far as L2 meanwhile.
+  auto ahead = [&](int64_t from) {
+    if (from >= rows) return;
+    const uint32_t n = (uint32_t)min(rows - (int32_t)from, R) * a.cols;
+    const int64_t at = from * a.cols;
+    prefetch_l2(static_cast<const char*>(a.dy) + at * es, n * es);
+    prefetch_l2((SAVED ? reinterpret_cast<const char*>(a.codes) : static_cast<const char*>(a.h)) + at * ves, n * ves);
+    if (a.dh) prefetch_l2(static_cast<const char*>(a.dh) + at * es, n * es);
   };
   if (t == 0) {
     for (int s = 0; s < S; ++s) {
@@ -484,6 +504,7 @@ __global__ __maxnreg__(U == 1 ? 64 : ROWS ? 96 : 128) void k_norm_bwd(const __gr
 #pragma unroll
     for (int k = 0; k < U; ++k) vs[k] = SAVED ? next_scale[k] * rstd[ROWS ? k : 0] : rstd[ROWS ? k : 0];
     scalars((int64_t)row0 + step + sub);
+    if (ONE && t == 0) ahead((int64_t)row0 + step);
     if (ok) ok = mbar_wait_bounded(&full[s], phase) && mbar_wait_bounded(&full[kMaxStages + s], phase);
     if (t == 0 && ok && S > 1 && it > 0) {  // the late stage of the group before
       const int before = s == 0 ? S - 1 : s - 1;
@@ -664,8 +685,7 @@ int64_t parts_of(int64_t rows, int64_t cols) {
 
 template <int XT, bool SAVED, int L, int U, bool ROWS>
 mp_status launch_bwd_rows(NormBwd a, const RowShape& s, int* parts, cudaStream_t st) {
-  static std::atomic<uint64_t> opted{0};
-  constexpr auto kernel = k_norm_bwd<XT, SAVED, L, U, ROWS>;
+  static std::atomic<uint64_t> opted[2] = {0, 0};
   constexpr bool kLanes = L > kInTiles;
   const int rows_per_group = (L == kInTiles ? a.group : s.rows_per_cta) * (ROWS ? U : 1);
   const int64_t groups = (a.rows + rows_per_group - 1) / rows_per_group;
@@ -691,7 +711,10 @@ mp_status launch_bwd_rows(NormBwd a, const RowShape& s, int* parts, cudaStream_t
   int smem = weights + teams * a.stages * bytes;
   const int fold = (kLanes ? kCta * kUnit : teams * (L == kInTiles ? a.group : 1) * a.cols) * 4;  // the join of the column sums
   if (smem < fold) smem = fold;
-  if (!smem_ok(kernel, smem, opted)) return MP_ECUDA;
+  const bool one = a.stages == 1;  // only rows of whole teams and two units a thread are that long
+  const auto kernel = one ? k_norm_bwd<XT, SAVED, L, U, ROWS, L == 0 && U == 2 && !ROWS>
+                          : k_norm_bwd<XT, SAVED, L, U, ROWS, false>;
+  if (!smem_ok(kernel, smem, opted[one])) return MP_ECUDA;
   const int grid = resident_grid((groups + teams - 1) / teams, kLanes ? per_sm : 1);
   const int64_t room = parts_of(a.rows, a.cols);  // partial rows in the workspace
   *parts = (int)(grid < room ? grid : room);
