@@ -451,6 +451,8 @@ MP_API mp_status rmsnorm_residual_backward(const void* dy, const void* dh, mp_dt
                                            size_t workspace_bytes, void* stream);
 
 /* swiglu_fp8 — y = the cast of (gate * s(gate)) * up, s the logistic function.
+ * Relative error of s: 6.2 * 2^-24 in MP_F32, (1.25 |gate| + 6) * 2^-24 in the
+ * 16-bit types, whose s is 0 for a gate below -87 (-88.7 in MP_F32).
  * gate and up [rows, cols] with rows `ld` elements apart (the two halves of
  * one product have ld = 2 * cols): ld >= cols and rows 16-byte aligned where
  * rows > 1 (else MP_ESHAPE).  ckpt (may be NULL, with ckpt_scales): gate's

@@ -16,9 +16,16 @@
 // GB/s); backward from the checkpoint, 8.1 bytes: 136.0 us, 1.04; from gate and
 // up, 10 bytes: [2048 x 12288] 38.8 us, 0.97.  What counts is how many units are
 // on an SM: CTAs of 128 threads, nine of them (56 registers) forward and twelve
-// (40) backward for the 16-bit types.  (256 threads, four and six CTAs: 132.9 and
-// 138.9 us; 512 threads: 137.5 and 142.5; 36 registers backward, which spill:
-// 147.6.  The forward tile's three pairs of divisions one by one: 157.)
+// (40, which spill 20 to 24 bytes a thread) backward for the 16-bit types.  (256
+// threads, four and six CTAs: 132.9 and 138.9 us; 512 threads: 137.5 and 142.5; 36
+// registers backward, which spill more: 147.6.  The forward tile's three pairs of
+// divisions one by one: 157.)
+//
+// FP32 [8192 x 8192], us by CTAs an SM: forward, with the checkpoint and without,
+// four 111.7 and 90.6, six 107.5 and 86.4, seven 106.1 and 85.4, nine 110.8 and 85.5;
+// backward from the checkpoint four 158.7, six 152.3, seven 148.6, ten 155.0; from
+// gate and up, more bytes of which are in flight a thread, four 185.8, six 188.6,
+// seven 190.1.
 #include "mp_chain.cuh"
 #include "mp_internal.h"
 #include "mp_tile8.cuh"
@@ -28,18 +35,46 @@ namespace {
 
 constexpr int kThreads = 128;
 
-// 1 / (1 + exp(-g)) through the hardware's base-2 exponential and reciprocal:
-// within (|g| + 8) * 2^-24, relative; 0 where it is below 2^-126 (g below -87),
-// NaN for NaN.
+// 1 / (1 + exp(-g)) through the hardware's base-2 exponential and reciprocal,
+// which over every argument are within 2.45 and 1.65 times 2^-24, relative.
+//
+// 16-bit types: the exponent -g * log2(e) is rounded once, and the constant before
+// it, so the error grows with |g|: within (1.25 |g| + 6) * 2^-24, relative.  What
+// leaves in 8 or 16 bits hides it (a sixtieth of a step at most); an FP32 scale
+// has it in full.  0 where it is below 2^-126 (g below -87).
+//
+// FP32, whose gradients hide nothing: within 6.2 * 2^-24 whatever g is.  With t
+// the rounded exponent, exp(-g) = 2^t * exp(r) for r = -g - t * ln(2), which the
+// fused multiply-adds give almost exactly (the first cancels; ln(2) is taken in two
+// parts), and 1 + r stands for exp(r): r is below 2^-16.  |g| is limited to 128,
+// where the result is 0 or 1, so that t is finite.  Sum and reciprocal are taken an
+// eighth as large, so that a result down to 2^-128 (g down to -88.7, then 0) is
+// rounded to a subnormal number instead of flushed.  That is six instructions a
+// pair more than the 16-bit form, and no time; expf and a correctly rounded
+// reciprocal took 1 to 12 % more ([8192 x 8192] with the checkpoints 119.2 us
+// forward and 162.5 backward, one row of 14336 2.3).
+//
+// A NaN g may give any number: every result has a factor g besides.
+template <int XT>
 __device__ __forceinline__ float2 logistic2(float2 g) {
-  const float2 t = mul2(g, both(-1.442695041f));
   float2 e, r;
+  if constexpr (XT == XF32) {  // min(|g|, 128) with g's sign
+    asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(g.x) : "f"(g.x), "f"(128.0f));
+    asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(g.y) : "f"(g.y), "f"(128.0f));
+  }
+  const float2 t = mul2(g, both(-1.442695041f));
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
-  e = add2(e, both(1.0f));
+  if constexpr (XT == XF32) {
+    float2 rest = fma2(t, both(-0.693147182f), make_float2(-g.x, -g.y));
+    rest = fma2(t, both(1.904654323e-9f), rest);
+    e = fma2(mul2(e, both(0.125f)), add2(rest, both(1.0f)), both(0.125f));
+  } else {
+    e = add2(e, both(1.0f));
+  }
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
-  return r;
+  return XT == XF32 ? mul2(r, both(0.125f)) : r;
 }
 
 // Thread q holds lane q % 8 of tile q / 8; tiles run along rows.
@@ -66,7 +101,7 @@ struct SwigluFwd {
 };
 
 template <int XT, bool SAVE>
-__global__ __launch_bounds__(kThreads, XT == XF32 ? 1 : 9) void k_swiglu_fwd(const __grid_constant__ SwigluFwd a) {
+__global__ __launch_bounds__(kThreads, XT == XF32 ? 7 : 9) void k_swiglu_fwd(const __grid_constant__ SwigluFwd a) {
   chain_wait();
   chain_release();
   constexpr int N = SAVE ? 3 : 1;
@@ -88,7 +123,7 @@ __global__ __launch_bounds__(kThreads, XT == XF32 ? 1 : 9) void k_swiglu_fwd(con
       ag = max3_abs_nan(ag, g.x, g.y);
       au = max3_abs_nan(au, u.x, u.y);
     }
-    y[k] = mul2(mul2(g, logistic2(g)), u);
+    y[k] = mul2(mul2(g, logistic2<XT>(g)), u);
   }
   if constexpr (SAVE) {
     const uint32_t mc[N] = {tile_max(__float_as_uint(ag)), tile_max(__float_as_uint(au)), 0u};
@@ -111,7 +146,7 @@ struct SwigluBwd {
 };
 
 template <int XT, bool SAVED>
-__global__ __launch_bounds__(kThreads, XT == XF32 ? 1 : 12) void k_swiglu_bwd(const __grid_constant__ SwigluBwd a) {
+__global__ __launch_bounds__(kThreads, XT != XF32 ? 12 : SAVED ? 7 : 4) void k_swiglu_bwd(const __grid_constant__ SwigluBwd a) {
   chain_wait();
   chain_release();
   const Place p = place_of(a.rows, a.cols, a.tiles);
@@ -141,7 +176,7 @@ __global__ __launch_bounds__(kThreads, XT == XF32 ? 1 : 12) void k_swiglu_bwd(co
   Unit<XT> dg, du;
 #pragma unroll
   for (int k = 0; k < kPairs; ++k) {
-    const float2 d = dr.pair(k), s = logistic2(g[k]), xs = mul2(g[k], s);
+    const float2 d = dr.pair(k), s = logistic2<XT>(g[k]), xs = mul2(g[k], s);
     du.set_pair(k, mul2(d, xs));
     const float2 one_s = fma2(s, both(-1.0f), both(1.0f));
     dg.set_pair(k, mul2(mul2(d, u[k]), fma2(xs, one_s, s)));
