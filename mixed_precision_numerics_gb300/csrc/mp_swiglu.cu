@@ -215,9 +215,9 @@ bool float_type(mp_dtype t) { return t == MP_F32 || t == MP_F16 || t == MP_BF16;
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Whether a matrix of `cols` columns may have rows `ld` elements apart: they
-// must not overlap, and each has to start on 16 bytes.
+// must not overlap, and each has to start on 16 bytes.  Byte offsets are 64-bit.
 bool pitch_ok(int64_t ld, int64_t cols, int64_t rows, mp_dtype t) {
-  return rows <= 1 || (ld >= cols && ld < (1ll << 31) && ld % (t == MP_F32 ? 4 : 8) == 0);
+  return rows <= 1 || (ld >= cols && ld < (1ll << 61) / rows && ld % (t == MP_F32 ? 4 : 8) == 0);
 }
 // Tile numbers (2.7e11 elements: more than the device's memory holds of any
 // input), rows and the columns up to the end of a row's last tile are 32-bit.
