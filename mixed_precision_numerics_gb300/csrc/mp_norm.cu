@@ -599,7 +599,13 @@ __global__ __maxnreg__(U == 1 ? 64 : ROWS ? 96 : 128) void k_norm_bwd(const __gr
         for (int q = 0; q < kPairs / 2; ++q) {
           const int i = half * (kPairs / 2) + q;
           const float2 x = SAVED ? e4m3_floats(q < 2 ? code.x : code.y, q) : v.pair(i);
-          o.set_pair(i, fma2(g[k][i], both(rstd[r]), fma2(x, both(c[r] * vs[k]), o.pair(i))));
+          const float2 f = both(c[r] * vs[k]);
+          // FP32: dh, mostly the largest term, is added last and rounded once; a 16-bit result hides the
+          // rounding that one instruction less costs.
+          if constexpr (XT == XF32)
+            o.set_pair(i, add2(fma2(g[k][i], both(rstd[r]), mul2(x, f)), o.pair(i)));
+          else
+            o.set_pair(i, fma2(g[k][i], both(rstd[r]), fma2(x, f, o.pair(i))));
         }
         if (out) o.store_half(static_cast<char*>(a.dx) + (to + h) * es, half);
       }
