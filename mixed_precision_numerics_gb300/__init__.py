@@ -6,13 +6,16 @@ step of the computation runs in the library's CUDA kernels.  Importing this
 package fails loudly when ``libmpnum.so`` has not been built: there is no
 other implementation to fall back to.  The block operators, whose smallest
 calls take less time on the GPU than arguments take here, are marshalled
-natively first (``_mpcall.so``).
+natively first where the extension ``_mpcall`` has been built for the running
+interpreter; without it the functions below make the same calls.
 
 PyTorch supplies device memory and streams.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 from dataclasses import dataclass
 from typing import Sequence
@@ -129,11 +132,18 @@ def _load() -> ctypes.CDLL:
 
 lib = _load()
 
-try:
-    from . import _mpcall
-except ImportError as e:
-    raise ImportError(f"{os.path.join(_PKG, '_mpcall.so')} cannot be loaded ({e}): build it with `python -c 'import "
-                      "__graft_entry__ as g; g.build()'`") from e
+def _load_native():
+    """The native marshalling built for this very interpreter (its ABI tag is in the file's name), or None."""
+    path = os.path.join(_PKG, "_mpcall" + importlib.machinery.EXTENSION_SUFFIXES[0])
+    if not os.path.exists(path):
+        return None
+    spec = importlib.util.spec_from_file_location(__name__ + "._mpcall", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+_mpcall = _load_native()
 
 
 class MpError(RuntimeError):
@@ -488,10 +498,13 @@ def mx_quantize(x, codes, scales, elem_dtype: int = MP_E2M1, dequant=None, strea
 
 
 # _mpcall makes the checks of these functions natively and calls the library.  What does not pass there
-# (None) comes to the Python checks, which say what is wrong, as does the first call of a process.
+# (None) comes to the Python checks, which say what is wrong, as does the first call of a process and, where
+# the extension has not been built, every call.
 
 
 def _bind() -> None:
+    if _mpcall is None:
+        return
     import torch
 
     names = ("rmsnorm_residual_fp8", "rmsnorm_residual_backward", "swiglu_fp8", "swiglu_backward")
@@ -546,8 +559,8 @@ def rmsnorm_residual_fp8(x, weight, y, y_scales, *, residual=None, h=None, rstd=
     bytes; y_scales: float32 [rows, ceil(cols/128)], or with scale_block 32 one UE8M0 byte per 32
     elements.  h (as x), rstd (float32 [rows]) and ckpt (rows*cols bytes, with ckpt_scales float32
     [rows, ceil(cols/128)]) are outputs the backward pass reads; each may be None."""
-    status = _mpcall.rmsnorm_residual_fp8(x, weight, y, y_scales, residual, h, rstd, ckpt, ckpt_scales, eps, fp8_dtype,
-                                          scale_block, stream)
+    status = _mpcall and _mpcall.rmsnorm_residual_fp8(x, weight, y, y_scales, residual, h, rstd, ckpt, ckpt_scales, eps,
+                                                      fp8_dtype, scale_block, stream)
     if status is None:
         import torch
 
@@ -579,7 +592,8 @@ def rmsnorm_residual_backward(dy, weight, rstd, dx, dweight, workspace, *, h=Non
                               dh=None, stream=None) -> None:
     """dx (as dy) and dweight ([cols], any of the three float types) from dy, rstd and the stream: either h
     or its 8-bit checkpoint (ckpt, ckpt_scales).  dh: the gradient reaching the stream from above, or None."""
-    status = _mpcall.rmsnorm_residual_backward(dy, weight, rstd, dx, dweight, workspace, h, ckpt, ckpt_scales, dh, stream)
+    status = _mpcall and _mpcall.rmsnorm_residual_backward(dy, weight, rstd, dx, dweight, workspace, h, ckpt, ckpt_scales,
+                                                           dh, stream)
     if status is None:
         import torch
 
@@ -602,7 +616,7 @@ def swiglu_fp8(gate, up, y, y_scales, *, ckpt=None, ckpt_scales=None, fp8_dtype:
                scale_block: int = 128, stream=None) -> None:
     """y = FP8 of silu(gate) * up.  gate, up: [rows, cols], each may be a column range of one wider
     matrix; ckpt: 2*rows*cols bytes (gate's codes, then up's), ckpt_scales: float32 [2, rows, ceil(cols/128)]."""
-    status = _mpcall.swiglu_fp8(gate, up, y, y_scales, ckpt, ckpt_scales, fp8_dtype, scale_block, stream)
+    status = _mpcall and _mpcall.swiglu_fp8(gate, up, y, y_scales, ckpt, ckpt_scales, fp8_dtype, scale_block, stream)
     if status is None:
         import torch
 
@@ -620,7 +634,7 @@ def swiglu_fp8(gate, up, y, y_scales, *, ckpt=None, ckpt_scales=None, fp8_dtype:
 def swiglu_backward(dp, dgate, dup, *, gate=None, up=None, ckpt=None, ckpt_scales=None, stream=None) -> None:
     """dgate, dup from dp and either gate and up or their 8-bit checkpoint of swiglu_fp8.  dgate and dup
     ([rows, cols]) may be column ranges of one wider matrix, as gate and up may."""
-    status = _mpcall.swiglu_backward(dp, dgate, dup, gate, up, ckpt, ckpt_scales, stream)
+    status = _mpcall and _mpcall.swiglu_backward(dp, dgate, dup, gate, up, ckpt, ckpt_scales, stream)
     if status is None:
         import torch
 

@@ -1,8 +1,12 @@
 """Build in-tree: libmpnum.so (nvcc for sm_103a, one object per .cu, compiled in
-parallel) and _mpcall.so, the native argument marshalling of the block operators."""
+parallel) and _mpcall, the native argument marshalling of the block operators: an
+extension of the running interpreter, named with its ABI tag so that another one
+neither loads it nor takes it as up to date.  Where that interpreter's headers are
+missing it is left out, and the package marshals in Python."""
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.machinery
 import os
 import subprocess
 import sys
@@ -13,7 +17,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmpnum.so")
-CALL = os.path.join(PKG, "_mpcall.so")
+CALL = os.path.join(PKG, "_mpcall" + importlib.machinery.EXTENSION_SUFFIXES[0])
+UNTAGGED = os.path.join(PKG, "_mpcall.so")  # the extension's name in earlier builds
+PYTHON_H = os.path.join(sysconfig.get_paths()["include"], "Python.h")
 HEADER = os.path.join(ROOT, "include", "mpnum.h")
 
 SOURCES = ["mp_common.cu", "mp_adamw.cu", "mp_fp8.cu", "mp_nvfp4.cu", "mp_mx.cu", "mp_norm.cu", "mp_swiglu.cu"]
@@ -46,10 +52,21 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _call_stale() -> bool:
+    return os.path.exists(UNTAGGED) or ((os.path.exists(PYTHON_H) or os.path.exists(CALL)) and _stale(CALL))
+
+
 def _compile_call() -> None:
+    without = not os.path.exists(PYTHON_H)
+    for old in (UNTAGGED, CALL) if without else (UNTAGGED,):  # nothing out of date stays to be loaded
+        if os.path.exists(old):
+            os.remove(old)
+    if without:
+        sys.stderr.write(f"{PYTHON_H} is missing: {os.path.basename(CALL)} is not built\n")
+        return
     tmp = CALL + f".tmp{os.getpid()}"
     p = subprocess.run(["gcc", "-O2", "-shared", "-fPIC", "-Wall", "-Wextra", "-I", os.path.join(ROOT, "include"), "-I",
-                        sysconfig.get_paths()["include"], os.path.join(CSRC, "mp_call.c"), "-o", tmp],
+                        os.path.dirname(PYTHON_H), os.path.join(CSRC, "mp_call.c"), "-o", tmp],
                        capture_output=True, text=True)
     if p.returncode != 0:
         raise RuntimeError(f"gcc failed for mp_call.c:\n{p.stderr}")
@@ -57,8 +74,10 @@ def _compile_call() -> None:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/*.cu and link libmpnum.so and _mpcall.so next to this file; returns the library's path."""
-    if not force and not _stale(LIB) and not _stale(CALL):
+    """Compile csrc/*.cu and link libmpnum.so and _mpcall next to this file; returns the library's path."""
+    if not force and not _stale(LIB):
+        if _call_stale():
+            _compile_call()
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
