@@ -407,8 +407,8 @@ MP_API mp_status mx_quantize(const void* x, mp_dtype x_dtype, int64_t rows, int6
  * in E4M3 with one FP32 scale per 1x128 tile of a row: the bytes and scales
  * of fp8_quantize_blockwise(1, 128, MP_E4M3), written by the forward pass from
  * the same read and taken by the backward pass in place of the tensor.  One
- * difference from that call: a tile with 0 < amax < fp8_max / FLT_MAX (below
- * 2^-112) becomes zeros.
+ * difference from that call: a tile with 0 < amax < fp8_max / FLT_MAX (2^-119 in
+ * E4M3, 2^-112 in E5M2) becomes zeros.
  * FP8 outputs (fp8_dtype MP_E4M3 or MP_E5M2) take scale_block 128 (FP32
  * scales [rows][ceil(cols/128)], the rule of fp8_quantize_blockwise applied
  * to the binary32 result) or 32 (UE8M0 bytes [rows][cols/32], the rule of
@@ -421,7 +421,7 @@ MP_API mp_status mx_quantize(const void* x, mp_dtype x_dtype, int64_t rows, int6
  * dweight) do not depend on how many rows the call has. */
 
 /* rmsnorm_residual_fp8 — h = x + residual rounded to x_dtype (h = x if
- * residual is NULL); rstd = 1 / sqrt(mean(h^2) + eps) per row; y = the cast of
+ * residual is NULL); rstd = 1 / sqrt(mean(h^2) + eps) per row, in binary32; y = the cast of
  * (h * rstd) * weight.  h, rstd and the checkpoint of h (ckpt [rows, cols],
  * ckpt_scales) may be NULL; a checkpoint needs both its pointers.  h may be x
  * or residual.  weight [cols].  eps finite and >= 0; a row of zeros with eps 0

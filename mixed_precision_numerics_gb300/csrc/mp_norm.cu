@@ -14,9 +14,9 @@
 // Both read and write every element once, and are bound by DRAM: a row stays on
 // its SM between the two uses of it, before and after the row's sum.  Forward
 // it stays in registers; backward, where the column sums dw take those, in
-// shared memory.  [8192 x 4096] BF16 with checkpoint: forward 42.6 us, 0.95 of
-// the copy rate (6680 GB/s), backward 42.1 us, 0.84; [16384 x 5120]: 101.3 us,
-// 1.00, and 95.0 us, 0.93.
+// shared memory.  [8192 x 4096] BF16 with checkpoint: forward 42.6 us, 0.94 of
+// the copy rate (6793 GB/s), backward 42.1 us, 0.82; [16384 x 5120]: 101.4 us,
+// 0.98, and 94.8 us, 0.92.
 #include <math.h>
 
 #include "mp_chain.cuh"
@@ -215,6 +215,8 @@ __global__ __launch_bounds__(fwd_threads<XT, L, U>(), XT != XF32 && U == 2 ? 2 :
   const float sum = L == kInTiles ? tiles_sum(part[0], slots + sub * kTilesMax, a.tiles, u)
                     : L           ? lane_sum<L ? L : 1>(part[0])
                                   : cta_sum(part, slots);
+  // In binary32: within 3 * 2^-24 of 1 / sqrt(mean + eps) on random rows, as a correctly rounded division and root
+  // of the same sum are (the sum's own error is the larger part).
   const float rstd = rsqrtf(fmaf(sum, a.inv_cols, a.eps));
   if (u == 0 && row < a.rows && a.rstd) a.rstd[row] = rstd;
 #pragma unroll
@@ -247,10 +249,11 @@ mp_status launch_fwd(const NormFwd& a, const RowShape& s, cudaStream_t st) {
   return launch_status();
 }
 
-// Rows that do not fill their warps, in tiles instead.  BF16, GPU time in us
-// with this layout and with whole warps: [16384 x 576] 12.9 and 18.3, [1024 x
-// 768] 2.7 and 3.7, [16384 x 1280] 28.2 and 31.2, [16384 x 384] 8.0 and 9.1; the
-// same at 1536 and 2048 columns, and 40.4 and 38.2 at 1792.  Four tiles are a
+// Rows that do not fill their warps, in tiles instead.  BF16 with the checkpoint,
+// GPU time in us over inputs beyond L2 with this layout and with whole warps: [16384
+// x 576] 15.3 and 19.0, [1024 x 768] 3.1 and 3.3, [16384 x 1040] 27.1 and 30.1,
+// [16384 x 1280] 28.3 and 31.8, [16384 x 384] 10.2 and 11.7, [16384 x 1536] 32.2 and
+// 33.4, [16384 x 2048] 41.3 and 42.3, but 40.4 and 38.2 at 1792.  Four tiles are a
 // warp, whose rows need no barrier: [16384 x 512] 9.8, and 17.3 in this layout.
 // FP32 is nearer to DRAM: [16384 x 576] 23.4 and 25.2, but [4096 x 896] 11.1 and
 // 10.3, [16384 x 384] 16.6 and 15.8.
@@ -269,13 +272,14 @@ int rows_in_tiles(int tiles) {
 }
 // Whether a CTA that takes one row holds one unit a thread, and not two.  One
 // has its weights by the row's sum, where two (in the 16-bit types) read them
-// after it, to be 64 registers and to have twice the rows on an SM.  That counts
+// after it, to be 64 registers (with 8 bytes a thread spilled, and with the
+// checkpoint 28) and to have twice the rows on an SM.  That counts
 // once the rows come in several waves, the earlier the fewer fit on an SM.  BF16,
-// us with one and with two: one row of 4096 2.2 and 3.0, [37 x 5120] 2.4 and 3.2,
-// [1024 x 4096] 5.8 and 6.5, [304 x 16384] 7.8 and 6.8, [8192 x 4096] 42.7 and
-// 43.4, [16384 x 5120] 107.2 and 100.4.  FP32 has 80 registers with two, and is
-// better off with one up to 8192 columns ([7000 x 4096] 64.6 and 70.6; [7000 x
-// 10816] 223.8 and 185.3).
+// us with one and with two: one row of 4096 2.1 and 2.8, [37 x 5120] 2.1 and 2.9,
+// [1024 x 4096] 7.8 and 8.3, [304 x 16384] 10.2 and 9.1, [8192 x 4096] 42.5 and
+// 42.4, [16384 x 5120] 107.2 and 101.1.  FP32 has 80 registers with two, and is
+// better off with one up to 8192 columns ([7000 x 4096] 64.3 and 71.5; [7000 x
+// 10816] 223.7 and 188.4).
 template <int XT>
 bool one_unit(const RowShape& s, int64_t rows) {
   const int held = kMaxThreads / s.threads;
@@ -364,11 +368,18 @@ __host__ __device__ constexpr int weight_bytes(int units) { return (units + 3) /
 // graph).  Of the rest about 6 us are the first rows' latency, the last round, the
 // join of the column sums and the second kernel (2.7).
 //
-// ONE: rows so long that there is room for one stage (FP32 of over 10500 columns
-// from the checkpoint, and of over 8900 without) would meet all of DRAM's latency
-// each time; so the next group's bytes are sent for as far as L2.  FP32 [7000 x
-// 12288] from the checkpoint 191 us, without the prefetch 225; [7000 x 9216] 164
-// and 201.
+// From the kept BF16 stream, within a graph: [8192 x 4096] 45.6 us, [16384 x 5120]
+// 104.0 (floors 39.5 and 98.8).
+//
+// ONE: rows so long that there is room for one stage would meet all of DRAM's
+// latency each time; so the next group's bytes are sent for as far as L2.  Those are
+// FP32 rows from 8208 columns on from the stream and from 10432 on from the
+// checkpoint, without dh from 11472 on from the stream, and 16-bit rows with dh from
+// 14352 on from the stream.  FP32 [7000 x 12288] from the checkpoint 191 us, without
+// the prefetch 225; [7000 x 9216] from the stream 164 and 201.
+//
+// Rows in lanes of a warp, from the checkpoint, spill 4 bytes a thread in the 16-bit
+// types and 16 in FP32 at their 64 registers.
 template <int XT, bool SAVED, int L, int U, bool ROWS, bool ONE>
 __global__ __maxnreg__(U == 1 ? 64 : ROWS ? 96 : 128) void k_norm_bwd(const __grid_constant__ NormBwd a) {
   constexpr int NR = ROWS ? U : 1, NU = ROWS ? 1 : U;  // rows of a thread, and units in each
@@ -734,18 +745,30 @@ mp_status launch_bwd_rows(NormBwd a, const RowShape& s, int* parts, cudaStream_t
 // time instead of two units of one.  Two rows need more of shared memory for each
 // team, so that of long rows fewer are in flight.  GPU time in us, with two rows
 // and with two units: BF16 from the checkpoint [16384 x 1040] 28.1 and 33.7,
-// [8192 x 4096] 38.1 and 40.2, [16384 x 5120] 93.0 and 92.0, [4096 x 8192] 41.9
-// and 40.4; F32 [4096 x 1040] 14.2 and 15.8, [16384 x 1536] 62.3 and 63.0,
-// [4096 x 2048] 23.9 and 22.7, [16384 x 2560] 108.7 and 98.7.
+// [8192 x 2560] 29.6 and 30.6, [8192 x 3072] 34.2 and 34.0, [8192 x 4096] 38.1 and
+// 40.2, [16384 x 5120] 93.0 and 92.0, [4096 x 8192] 41.9 and 40.4; F32 [4096 x 1040]
+// 14.2 and 15.8, [16384 x 1536] 62.3 and 63.0, [4096 x 2048] 23.9 and 22.7,
+// [16384 x 2560] 108.7 and 98.7.
+// BF16 from the stream, whose stage is a fifth larger: from 2048 to 3072 columns an
+// SM then holds one team fewer, and two rows are still as fast or faster.  [16384 x
+// 2048] 46.7 and 47.7, [8192 x 2304] 28.4 and 30.6, [8192 x 2560] 30.8 and 32.1,
+// [8192 x 3072] 37.2 and 37.2, [8192 x 3584] 40.8 and 41.8, [8192 x 4096] 45.6 and
+// 47.0, [16384 x 5120] 113.8 and 104.0; without dh 38.9 and 40.0 at 2048 columns,
+// 26.5 and 28.0 at 2560, 30.9 and 31.6 at 3072, but 40.8 and 39.8 at 4096.  F32 from
+// the stream [4096 x 1040] 16.3 and 18.1, [16384 x 1536] 63.6 and 64.7.
 template <int XT>
 constexpr int two_rows_up_to() { return XT == XF32 ? 96 : 256; }
 
 // Rows (of 5 to 16 tiles) that would leave a sixth of whole warps idle lie in
-// tiles of a team that takes twice `group` of them.  GPU time in us with this
-// layout and without, BF16 from the checkpoint: [4096 x 640] 7.1 and 9.4, [16384 x
-// 528] 15.4 and 19.3, [16384 x 768] 19.5 and 21.0, [16384 x 1040] 25.2 and 28.3,
-// [16384 x 1664] 33.2 and 35.4; where fewer lanes are idle it lost ([16384 x 896]
-// 22.9 and 22.0, [16384 x 1792] 37.7 and 36.0).
+// tiles of a team that takes twice `group` of them.  GPU time in us over inputs
+// beyond L2 with this layout and without, BF16 from the checkpoint: [4096 x 640] 8.3
+// and 10.7, [16384 x 528] 18.0 and 22.9, [16384 x 576] 18.4 and 22.4, [16384 x 768]
+// 21.4 and 22.5, [16384 x 1040] 26.1 and 29.2, [16384 x 1280] 30.1 and 30.1, [16384 x
+// 1664] 35.9 and 36.8; where fewer lanes are idle it lost ([16384 x 896] 22.9 and
+// 22.0, [16384 x 1792] 37.7 and 36.0).
+// From the stream: [16384 x 528] 18.0 and 23.0, [4096 x 640] 10.5 and 11.2, [16384 x
+// 768] 22.9 and 23.7, [16384 x 1040] 27.6 and 30.7, [16384 x 1280] 32.8 and 33.3,
+// [16384 x 1664] 40.3 and 41.0.
 // FP32 was as often slower as faster ([16384 x 640] 31.1 and 29.6, [16384 x 576]
 // 25.0 and 29.3).
 bool tiles_save_lanes(int tiles) { return tiles > 4 && tiles <= kTilesMax && 6 * tiles <= 5 * ((tiles + 3) / 4 * 4); }

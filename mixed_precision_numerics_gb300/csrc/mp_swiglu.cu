@@ -12,9 +12,9 @@
 // column ranges of one wider matrix: each pair has a row distance.
 //
 // Bound by DRAM.  [8192 x 14336] BF16 forward with the checkpoint, 7.1 bytes an
-// element and 400 instructions for 16: 123.9 us, 1.01 of the copy rate (6680
-// GB/s); backward from the checkpoint, 8.1 bytes: 136.0 us, 1.04; from gate and
-// up, 10 bytes: [2048 x 12288] 38.8 us, 0.97.  What counts is how many units are
+// element and 400 instructions for 16: 124.0 us, 0.99 of the copy rate (6793
+// GB/s); backward from the checkpoint, 8.1 bytes: 135.8 us, 1.03; from gate and
+// up, 10 bytes: [2048 x 12288] 38.8 us, 0.95.  What counts is how many units are
 // on an SM: CTAs of 128 threads, nine of them (56 registers) forward and twelve
 // (40, which spill 20 to 24 bytes a thread) backward for the 16-bit types.  (256
 // threads, four and six CTAs: 132.9 and 138.9 us; 512 threads: 137.5 and 142.5; 36

@@ -267,8 +267,8 @@ constexpr uint32_t kInfBits = 0x7F800000u;
 // 2k of the tile's eight does tile k's multiplier and lane 2k + 1 its scale, so
 // one division serves them all.  mul[k] is valid in every lane, *scale in lane
 // 2k + 1.  The multiplier is 0 for a tile of zeros, with a non-finite element,
-// or with an amax below top / FLT_MAX (about 2^-112), where top / amax would be
-// infinite: its elements become zeros instead of the NaN that 0 * inf would give.
+// or with an amax below top / FLT_MAX (2^-119 in E4M3, 2^-112 in E5M2), where top /
+// amax would be infinite: its elements become zeros instead of the NaN that 0 * inf would give.
 template <int N, int M>
 __device__ __forceinline__ void tile_scales(const uint32_t (&m)[N], float top, float (&mul)[N], float* scale) {
   const int lane = threadIdx.x & 7;
