@@ -472,6 +472,90 @@ MP_API mp_status swiglu_backward(const void* dp, mp_dtype x_dtype, int64_t rows,
                                  const void* up, int64_t ld, const void* ckpt, const float* ckpt_scales, void* dgate,
                                  void* dup, int64_t d_ld, void* stream);
 
+/* =========================================================================
+ * 6. Matrix products of a gated feed-forward block
+ * ========================================================================= */
+
+/* linear_swiglu — both projections of a gated feed-forward block, the SwiGLU
+ * activation and the product, in one kernel: g = x w_gate^T, u = x w_up^T,
+ * p = (g * s(g)) * u, s the logistic function (within 6.2 * 2^-24, relative).
+ * x [rows, width], w_gate and w_up [hidden, width], of one type, MP_F16 or
+ * MP_BF16.  Sums are binary32: within a run of 512 terms they are the tensor
+ * core's, which truncates; runs are added rounded to nearest.
+ * p [rows, hidden]: of x's type (p_dtype = x_dtype, p_scales NULL), or FP8
+ * (p_dtype MP_E4M3 or MP_E5M2) with scale_block 128 (FP32) or 32 (UE8M0) and
+ * p_scales, by the rules of section 5 applied to the binary32 product.
+ * Written on the way if not NULL: gate and up (g and u in x's type, rows `ld`
+ * elements apart: ld >= hidden and a multiple of 8 where rows > 1, else
+ * MP_ESHAPE), or ckpt with ckpt_scales (g's and then u's 8-bit checkpoint as
+ * swiglu_fp8 has it); not both (MP_EINVAL).  No output may overlap an input.
+ * width % 16 == 0, hidden % 16 == 0 (32 with scale_block 32), both at most
+ * 2^20, rows < 2^31 - 256 (else MP_ESHAPE); tensors 16-byte aligned, FP32
+ * scales 4-byte.  rows or hidden 0: nothing is written; width 0 otherwise:
+ * MP_ESHAPE.  A row's results do not depend on the other rows' values.  One kernel
+ * launch, reading its operands through tile copies: MP_ECUDA if the driver's
+ * tensor-map encoder is unavailable. */
+MP_API mp_status linear_swiglu(const void* x, mp_dtype x_dtype, int64_t rows, int64_t width, int64_t hidden,
+                               const void* w_gate, const void* w_up, void* p, mp_dtype p_dtype, int32_t scale_block,
+                               void* p_scales, void* gate, void* up, int64_t ld, void* ckpt, float* ckpt_scales,
+                               void* stream);
+
+/* linear_swiglu_backward — from dp [rows, hidden] (the gradient of the
+ * unquantised product), x, the weights and what the forward call has saved:
+ * gate and up with row distance ld, or their checkpoint, or neither (both
+ * products are formed again):
+ *     dg = dp * u * (s + g * s * (1 - s)),   du = dp * (g * s)
+ *     dx = dg w_gate + du w_up               [rows, width]
+ *     dw_gate = dg^T x,  dw_up = du^T x      [hidden, width], overwritten
+ * all of x_dtype.  dg and du are rounded to it once, as operands; sums as in
+ * the forward call, in an order fixed by the shape and the device.  dx may be
+ * NULL, and dw_gate and dw_up together.  No output may overlap an input.
+ * d_workspace: linear_swiglu_workspace_size(rows, width, hidden) bytes, 16-byte
+ * aligned, any contents (else MP_EWORKSPACE).  Limits as in the forward call.
+ * rows 0 writes zeros to the weights' gradients, hidden 0 to dx.  At most
+ * five kernel launches. */
+MP_API size_t linear_swiglu_workspace_size(int64_t rows, int64_t width, int64_t hidden);
+MP_API mp_status linear_swiglu_backward(const void* dp, mp_dtype x_dtype, int64_t rows, int64_t width, int64_t hidden,
+                                        const void* x, const void* w_gate, const void* w_up, const void* gate,
+                                        const void* up, int64_t ld, const void* ckpt, const float* ckpt_scales,
+                                        void* dx, void* dw_gate, void* dw_up, void* d_workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/* =========================================================================
+ * 7. Gradient norm and clipping of a list of tensors
+ * ========================================================================= */
+
+/* One gradient: numel >= 0 elements of grad_dtype and, for mp_grad_clip, where
+ * the clipped ones go (out may be grad if out_dtype is grad_dtype).  Both types
+ * MP_F32, MP_F16 or MP_BF16; pointers 16-byte aligned. */
+typedef struct {
+  const void* grad;
+  void* out;
+  int64_t numel;
+  mp_dtype grad_dtype, out_dtype;
+} mp_grad;
+
+/* mp_grad_norm — *d_norm = the global L2 norm of n gradients, divided by
+ * *d_loss_scale (a device float; NULL for 1): that of the unscaled gradients,
+ * as mp_adamw_check forms it for its own list.  Squares neither overflow nor
+ * underflow; sums are binary32 over 64 elements (32 in FP32) and binary64 above, in an order
+ * fixed by the list and the device.  An infinite or NaN gradient gives an infinite or
+ * NaN norm; an empty list 0.  out and out_dtype are not read.  d_workspace:
+ * mp_grad_norm_workspace_size(grads, n) bytes, 16-byte aligned, zero-filled
+ * before its first use; every completed call leaves what it needs zero.  One
+ * kernel launch for up to 512 tensors with elements, one more for each 512 further.
+ *
+ * mp_grad_clip — out = grad * c, c = min(1, max_norm / (*d_norm + 1e-6)) in
+ * binary32 (formed in binary64), rounded once to out_dtype.  If *d_norm is not
+ * finite c is NaN, so that every list clipped by it is seen as bad by the check
+ * of a step.  c = 1 leaves gradients clipped in place untouched.  max_norm
+ * finite and > 0 (else MP_EINVAL).  The gradients keep their loss scale.
+ * Tensors may not overlap but for out = grad.  Launches as above. */
+MP_API size_t mp_grad_norm_workspace_size(const mp_grad* grads, int32_t n);
+MP_API mp_status mp_grad_norm(const mp_grad* grads, int32_t n, const float* d_loss_scale, float* d_norm,
+                              void* d_workspace, size_t workspace_bytes, void* stream);
+MP_API mp_status mp_grad_clip(const mp_grad* grads, int32_t n, const float* d_norm, float max_norm, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -38,6 +38,16 @@ class MpParam(ctypes.Structure):
     ]
 
 
+class MpGrad(ctypes.Structure):
+    _fields_ = [
+        ("grad", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("numel", ctypes.c_int64),
+        ("grad_dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+    ]
+
+
 class AdamwHparams(ctypes.Structure):
     _fields_ = [(n, ctypes.c_float) for n in ("lr", "beta1", "beta2", "eps", "weight_decay", "max_grad_norm")]
 
@@ -82,7 +92,7 @@ class Fp8Meta(ctypes.Structure):
     ]
 
 
-assert ctypes.sizeof(ScalerState) == 88 and ctypes.sizeof(Fp8Meta) == 32 and ctypes.sizeof(MpParam) == 48
+assert ctypes.sizeof(ScalerState) == 88 and ctypes.sizeof(Fp8Meta) == 32 and ctypes.sizeof(MpParam) == 48 and ctypes.sizeof(MpGrad) == 32
 
 
 def _load() -> ctypes.CDLL:
@@ -122,6 +132,12 @@ def _load() -> ctypes.CDLL:
         "rmsnorm_residual_backward": (I32, [P, P, I32, I64, I64, P, P, P, P, I32, P, P, P, I32, P, S, P]),
         "swiglu_fp8": (I32, [P, P, I64, I32, I64, I64, P, I32, I32, P, P, P, P]),
         "swiglu_backward": (I32, [P, I32, I64, I64, P, P, I64, P, P, P, P, I64, P]),
+        "mp_grad_norm_workspace_size": (S, [P, I32]),
+        "mp_grad_norm": (I32, [P, I32, P, P, P, S, P]),
+        "mp_grad_clip": (I32, [P, I32, P, F, P]),
+        "linear_swiglu": (I32, [P, I32, I64, I64, I64, P, P, P, I32, I32, P, P, P, I64, P, P, P]),
+        "linear_swiglu_workspace_size": (S, [I64, I64, I64]),
+        "linear_swiglu_backward": (I32, [P, I32, I64, I64, I64, P, P, P, P, P, I64, P, P, P, P, P, P, S, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -654,7 +670,153 @@ def swiglu_backward(dp, dgate, dup, *, gate=None, up=None, ckpt=None, ckpt_scale
     _check("swiglu_backward", status)
 
 
+# ---- matrix products of a gated feed-forward block ------------------------------------------
+
+
+def _products(x, w_gate, w_up, gate, up) -> tuple:
+    """What both calls begin with: rows, width, hidden and the pointers of x, the weights, gate and up."""
+    rows, width = x.shape
+    hidden = w_gate.shape[0]
+    for name, w in (("w_gate", w_gate), ("w_up", w_up)):
+        if tuple(w.shape) != (hidden, width):
+            raise ValueError(f"{name}: {tuple(w.shape)}, the call needs {(hidden, width)}")
+    nb, dt = 2 * hidden * width, x.dtype
+    px = _in(x, "x", 2 * rows * width)
+    pw = _in(w_gate, "w_gate", nb, x, dt), _in(w_up, "w_up", nb, x, dt)
+    if gate is None and up is None:
+        return rows, width, hidden, px, *pw, None, None, hidden
+    if gate is None or up is None:
+        raise ValueError("gate and up: both or neither")
+    if tuple(gate.shape) != (rows, hidden) or gate.dtype != dt:
+        raise ValueError(f"gate: {tuple(gate.shape)} {gate.dtype}, the call needs {(rows, hidden)} {dt}")
+    return rows, width, hidden, px, *pw, *_pair(gate, up, ("gate", "up"), gate)
+
+
+def linear_swiglu(x, w_gate, w_up, p, *, p_scales=None, gate=None, up=None, ckpt=None, ckpt_scales=None,
+                  fp8_dtype: int = MP_E4M3, scale_block: int = 128, stream=None) -> None:
+    """p = silu(x @ w_gate.T) * (x @ w_up.T) in one kernel.  x: [rows, width], w_gate and w_up: [hidden, width],
+    all FP16 or all BF16.  p: [rows, hidden] of that type, or with p_scales FP8 codes and scales as swiglu_fp8
+    writes them.  What the backward pass can read is written on the way: gate and up (both products, [rows,
+    hidden] as x, each may be a column range of one wider matrix), or their 8-bit checkpoint ckpt with
+    ckpt_scales as swiglu_fp8 has it; or neither."""
+    rows, width, hidden, px, pg, pu, gp, up_, ld = _products(x, w_gate, w_up, gate, up)
+    if p_scales is None:
+        code, pp, ps = _dtype_code(x), _in(p, "p", 2 * rows * hidden, x, x.dtype), None
+    else:
+        nbytes, align = (rows * (hidden // 32), 1) if scale_block == 32 else (4 * rows * -(-hidden // 128), 4)
+        code, pp, ps = fp8_dtype, _in(p, "p", rows * hidden, x), _in(p_scales, "p_scales", nbytes, x, align=align)
+    _check("linear_swiglu", lib.linear_swiglu(
+        px, _dtype_code(x), rows, width, hidden, pg, pu, pp, code, scale_block, ps, gp, up_, ld,
+        _in(ckpt, "ckpt", 2 * rows * hidden, x),
+        _in(ckpt_scales, "ckpt_scales", 8 * rows * -(-hidden // 128), x, _f32(), 4), _stream(stream)))
+
+
+def _f32():
+    import torch
+
+    return torch.float32
+
+
+def linear_swiglu_workspace_size(rows: int, width: int, hidden: int) -> int:
+    return int(lib.linear_swiglu_workspace_size(rows, width, hidden))
+
+
+def new_linear_swiglu_workspace(rows: int, width: int, hidden: int, device="cuda"):
+    """Scratch of linear_swiglu_backward for these sizes."""
+    import torch
+
+    return torch.empty(linear_swiglu_workspace_size(rows, width, hidden), dtype=torch.uint8, device=device)
+
+
+def linear_swiglu_backward(dp, x, w_gate, w_up, dx, dw_gate, dw_up, workspace, *, gate=None, up=None, ckpt=None,
+                           ckpt_scales=None, stream=None) -> None:
+    """Gradients of linear_swiglu from dp ([rows, hidden], that of the unquantised product) and what was saved:
+    gate and up, their 8-bit checkpoint, or neither, when both products are formed again.  dx: [rows, width];
+    dw_gate, dw_up: [hidden, width]; all as x.  dx may be None, and both weights' gradients may."""
+    rows, width, hidden, px, pg, pu, gp, up_, ld = _products(x, w_gate, w_up, gate, up)
+    dt, nb = x.dtype, 2 * hidden * width
+    _check("linear_swiglu_backward", lib.linear_swiglu_backward(
+        _in(dp, "dp", 2 * rows * hidden, x, dt), _dtype_code(x), rows, width, hidden, px, pg, pu, gp, up_, ld,
+        _in(ckpt, "ckpt", 2 * rows * hidden, x),
+        _in(ckpt_scales, "ckpt_scales", 8 * rows * -(-hidden // 128), x, _f32(), 4),
+        _in(dx, "dx", 2 * rows * width, x, dt), _in(dw_gate, "dw_gate", nb, x, dt), _in(dw_up, "dw_up", nb, x, dt),
+        _in(workspace, "workspace", 0, x), _ws(workspace)[1], _stream(stream)))
+
+
+# ---- gradient norm and clipping ---------------------------------------------------------------
+
+
+def make_grad_array(grads, out=None):
+    """The list that mp_grad_norm and mp_grad_clip take, made once for tensors that stay where they are.
+    out: where the clipped gradients go, tensors of the same sizes in any of the three types; None: in place."""
+    outs = grads if out is None else out
+    if len(outs) != len(grads):
+        raise ValueError(f"out: {len(outs)} tensors, the call needs {len(grads)}")
+    arr = (MpGrad * max(1, len(grads)))()
+    arr.count = len(grads)
+    seen = set()
+    for i, (g, o) in enumerate(zip(grads, outs)):
+        _dev(g, f"grads[{i}]", like=grads[0])
+        if o is not g:
+            _dev(o, f"out[{i}]", like=grads[0])
+            if o.numel() != g.numel():
+                raise ValueError(f"out[{i}]: {o.numel()} elements, the call needs {g.numel()}")
+        if g.dtype not in _dtypes() or o.dtype not in _dtypes():
+            raise ValueError(f"grads[{i}]: {g.dtype} into {o.dtype}; FP32, FP16 and BF16 are taken")
+        if o.numel() and o.data_ptr() in seen:
+            raise ValueError(f"out[{i}]: listed before")
+        seen.add(o.data_ptr())
+        arr[i] = MpGrad(g.data_ptr(), o.data_ptr(), g.numel(), _dtype_code(g), _dtype_code(o))
+    return arr
+
+
+def _dtypes() -> dict:
+    if not _CODES:
+        import torch
+
+        _dtype_code(torch.empty(0))
+    return _CODES
+
+
+def _grads(grads, out=None):
+    arr = grads if isinstance(grads, ctypes.Array) else make_grad_array(grads, out)
+    return arr, getattr(arr, "count", len(arr))
+
+
+def mp_grad_norm_workspace_size(grads) -> int:
+    return int(lib.mp_grad_norm_workspace_size(*_grads(grads)))
+
+
+def new_grad_norm_workspace(grads, device="cuda"):
+    """Scratch of mp_grad_norm for that list or a shorter one, zero-filled."""
+    import torch
+
+    return torch.zeros(mp_grad_norm_workspace_size(grads), dtype=torch.uint8, device=device)
+
+
+def mp_grad_norm(grads, norm, workspace, loss_scale=None, stream=None) -> None:
+    """norm (float32, one element) = the global L2 norm of the gradients, divided by loss_scale (a float32 device
+    tensor of one element, such as new_scaler_state()[:4].view(torch.float32)) if that is given.  grads: tensors,
+    or the array of make_grad_array."""
+    arr, n = _grads(grads)
+    pn = _in(norm, "norm", 4, dtype=_f32(), align=4)
+    _check("mp_grad_norm", lib.mp_grad_norm(arr, n, _in(loss_scale, "loss_scale", 4, norm, _f32(), 4), pn,
+                                            _in(workspace, "workspace", 0, norm), _ws(workspace)[1], _stream(stream)))
+
+
+def mp_grad_clip(grads, norm, max_norm: float, out=None, stream=None) -> None:
+    """The gradients times min(1, max_norm / (norm + 1e-6)), in place or into the tensors `out`.  grads: tensors, or
+    the array of make_grad_array (which has `out` in it)."""
+    if out is not None and isinstance(grads, ctypes.Array):
+        raise ValueError("out: a prebuilt list has its own")
+    arr, n = _grads(grads, out)
+    _check("mp_grad_clip", lib.mp_grad_clip(arr, n, _in(norm, "norm", 4, dtype=_f32(), align=4), float(max_norm),
+                                            _stream(stream)))
+
+
 __all__ = [
+    "MpGrad", "make_grad_array", "mp_grad_norm", "mp_grad_clip", "mp_grad_norm_workspace_size", "new_grad_norm_workspace",
+    "linear_swiglu", "linear_swiglu_backward", "linear_swiglu_workspace_size", "new_linear_swiglu_workspace",
     "rmsnorm_residual_fp8", "rmsnorm_residual_backward", "rmsnorm_workspace_size", "new_rmsnorm_workspace",
     "swiglu_fp8", "swiglu_backward",
     "AdamwHparams", "Fp8Meta", "MpError", "MpParam", "Param", "ScalerCfg", "ScalerState",

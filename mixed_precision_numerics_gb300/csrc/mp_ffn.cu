@@ -1,0 +1,676 @@
+// mp_ffn.cu — the gated feed-forward block's matrix products: both projections
+// with the SwiGLU product formed on them in one kernel, and their backward pass.
+//
+// Forward: g = x Wg^T, u = x Wu^T, p = (g * s(g)) * u; g and u never reach
+// memory unless asked for.  Backward, with g and u as saved (16 bits, or the
+// 8-bit checkpoint) or formed again from x by the forward kernel's main loop:
+//   dg = dp * u * (s + g * s * (1 - s)),  du = dp * g * s,
+//   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x.
+// dg and du go through a 16-bit workspace: they are the operands of 16-bit
+// matrix instructions, which is the one rounding inside the backward pass.
+//
+// One kernel does all of it: 256 x 256 tiles of a product on pairs of CTAs
+// (tcgen05, 128 rows of the tile in each CTA's TMEM), persistent, with roles by
+// warp: one copies operand tiles (TMA, six stages of 64 steps of the
+// contraction), one issues the matrix instructions, eight form the results.
+// The forward tile's 256 columns are 128 of g and the same 128 of u: the pair's
+// first CTA holds the gate weights' half of the operand and the second the up
+// weights', so the thread that has an element of g has that of u.
+//
+// Sums: the tensor core adds to its binary32 accumulator by truncation, which
+// over a contraction of 4096 leaves results 4e-6 too small.  So every kChunk
+// blocks the sums so far leave TMEM and are added to registers with correct
+// rounding, while the next chunk goes into the other half of TMEM.
+#include <new>
+
+#include "mp_chain.cuh"
+#include "mp_internal.h"
+#include "mp_mma.cuh"
+#include "mp_tile8.cuh"
+
+namespace mp {
+namespace {
+
+constexpr int kBlockK = 64;        // steps of the contraction in a stage: 128 bytes
+constexpr int kChunk = 8;          // stages added up inside the tensor core
+constexpr int kStages = 6;
+constexpr int kHalf = 128;         // rows of a tile, and of its other operand, in one CTA
+constexpr int kOperandBytes = kHalf * kBlockK * 2;
+constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kResultWarps = 8;
+constexpr int kStagingBytes = 4096;  // 32 rows of 128 bytes, for each of those warps
+// Three warpgroups: two form results, with 128 sums a thread, one copies and
+// issues.  384 threads start with 168 registers each; the split adds up to that.
+constexpr int kThreads = (kResultWarps + 4) * 32;
+constexpr int kResultRegisters = 232, kOtherRegisters = 40;
+static_assert(kResultWarps * kResultRegisters + 4 * kOtherRegisters <= (kResultWarps + 4) * 168, "registers of a CTA");
+constexpr int kTmemColumns = 512;
+constexpr int kBarrierBytes = 256;
+constexpr int kSmem = kStages * kStageBytes + kResultWarps * kStagingBytes + 2 * 2 * kHalf * 4 + kBarrierBytes;
+static_assert(kSmem <= 232448, "227 KB a CTA");
+static_assert((2 * kStages + 4) * 8 + 8 <= kBarrierBytes, "barriers and the TMEM address");
+
+// What the result warps do with a tile.
+enum {
+  FWD16 = 0,  // p in 16 bits
+  FWD8,       // p in FP8
+  AGAIN,      // g and u formed again: dg and du
+  STORE       // the product itself
+};
+
+struct Ffn {
+  CUtensorMap a[2], b[2], out[3];
+  int32_t items, tiles_m, tiles_n, group;  // work items = tiles * splits; rows of tiles walked together
+  int32_t per_matrix;                      // STORE of two matrices: rows of tiles in each, else tiles_m
+  int32_t blocks0, blocks, splits;         // blocks of the contraction in the first operand pair, and in all
+  int32_t rows, cols;                      // of a result matrix
+  // FWD
+  bool e5m2, mx, keep16, ckpt;
+  void* p_scales;
+  float* ckpt_scales;  // [2][rows][tiles]
+  int32_t per_row, tiles;
+  // AGAIN
+  const void* dp;
+  // STORE in parts: [splits][matrices][rows][cols]
+  float* parts;
+};
+
+__device__ unsigned int g_ffn_wait_failures;  // bounded waits that gave up (read by mp_wait_failures)
+
+struct Tile {
+  int32_t m, n, k0, k1, split;
+};
+// Items walk the tiles in bands of `group` rows of tiles, column by column, so
+// that those in flight together share operands in L2; all tiles of a split first.
+__device__ __forceinline__ Tile tile_of(const Ffn& f, int item) {
+  const int all = f.tiles_m * f.tiles_n;
+  Tile t;
+  t.split = item / all;
+  item -= t.split * all;
+  const int band = item / (f.group * f.tiles_n), first = band * f.group;
+  const int high = min(f.group, f.tiles_m - first);
+  item -= band * f.group * f.tiles_n;
+  t.n = item / high;
+  t.m = first + item - t.n * high;
+  t.k0 = (int)((int64_t)f.blocks * t.split / f.splits);
+  t.k1 = (int)((int64_t)f.blocks * (t.split + 1) / f.splits);
+  return t;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float2 v) {  // a NaN gives 0x7FFF
+  uint32_t r;
+  if constexpr (BF16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
+  return r;
+}
+
+// 32 accumulators as 16 pairs.
+__device__ __forceinline__ float2 pair_of(const uint32_t (&r)[32], int k) {
+  return make_float2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
+}
+__device__ __forceinline__ void set_pair(uint32_t (&r)[32], int k, float2 v) {
+  r[2 * k] = __float_as_uint(v.x), r[2 * k + 1] = __float_as_uint(v.y);
+}
+
+// One warp's way out: 32 rows of 64 16-bit elements (or of 64 bytes) through
+// its staging buffer, swizzled as the map's box is.
+struct Way {
+  uint32_t stage;
+  int lane;
+  __device__ __forceinline__ void free_stage() const {
+    if (lane == 0) store_wait_read();
+    __syncwarp();
+  }
+  __device__ __forceinline__ void send(const CUtensorMap* map, uint32_t at, int32_t x, int32_t y) const {
+    fence_async_shared();
+    __syncwarp();
+    if (lane == 0) tma_store_2d(map, at, x, y);
+  }
+  // 64 values of this lane's row
+  template <bool BF16>
+  __device__ __forceinline__ void row16(const uint32_t (&lo)[32], const uint32_t (&hi)[32]) const {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const uint32_t(&r)[32] = c < 4 ? lo : hi;
+      const int k = (c & 3) * 4;
+      sts16(stage + lane * 128 + ((c ^ (lane & 7)) << 4), pack16<BF16>(pair_of(r, k)), pack16<BF16>(pair_of(r, k + 1)),
+            pack16<BF16>(pair_of(r, k + 2)), pack16<BF16>(pair_of(r, k + 3)));
+    }
+  }
+};
+
+// |values| of 32 columns: NaN-propagating maximum as bits that order as integers.
+__device__ __forceinline__ uint32_t amax32(const uint32_t (&r)[32]) {
+  float a = 0.0f, b = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 32; k += 4) {
+    a = max3_abs_nan(a, __uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+    b = max3_abs_nan(b, __uint_as_float(r[k + 2]), __uint_as_float(r[k + 3]));
+  }
+  return __float_as_uint(max3_abs_nan(a, b, b));
+}
+
+// Scale and multiplier of a 1x128 tile by the rule of the other block operators
+// (tile_scales), one thread for the tile.
+__device__ __forceinline__ float tile_scale(uint32_t m, float top, float* mul) {
+  const float amax = __uint_as_float(m), r = __fdiv_rn(top, amax);
+  *mul = (r < INFINITY && m < kInfBits) ? r : 0.0f;
+  return m > kInfBits ? __uint_as_float(0x7FC00000u) : __fdiv_rn(amax, top);
+}
+
+// Codes of 32 columns of this lane's row into its 64-byte row of staging, at
+// 16-byte unit `unit`.
+__device__ __forceinline__ void codes32(const uint32_t (&r)[32], uint32_t stage, int lane, int unit, uint32_t m,
+                                        float mul, bool e5m2, bool mx) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float2 v[kPairs];
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) v[k] = pair_of(r, h * kPairs + k);
+    uint4 c;
+    if (__builtin_expect(m >= kInfBits, 0))
+      c = mx ? make_uint4(0u, 0u, 0u, 0u) : nonfinite_unit(v, [&](int i) { return float_sign80(v, i); });
+    else
+      c = e5m2 ? cast_unit<true>(v, mul) : cast_unit<false>(v, mul);
+    sts16(stage + lane * 64 + (((unit + h) ^ ((lane >> 1) & 3)) << 4), c.x, c.y, c.z, c.w);
+  }
+}
+
+// A row's 128 columns are in two threads, `half` 0 and 1: the larger of both.
+__device__ __forceinline__ uint32_t both_halves(uint32_t m, uint32_t* slot, int half, int row, int quad) {
+  slot[half * kHalf + row] = m;
+  named_barrier(1 + quad, 64);
+  return max(m, slot[(half ^ 1) * kHalf + row]);
+}
+
+template <bool BF16, bool A_MN, bool B_MN, int EP>
+__global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn f) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  unsigned char* const staging = smem + kStages * kStageBytes;
+  uint32_t* const red = reinterpret_cast<uint32_t*>(staging + kResultWarps * kStagingBytes);  // [2][2][128]
+  uint64_t* const full = reinterpret_cast<uint64_t*>(red + 2 * 2 * kHalf);
+  uint64_t *const empty = full + kStages, *const tfull = empty + kStages, *const tempty = tfull + 2;
+  uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(tempty + 2);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+
+  if (warp == kResultWarps && lane == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
+    for (int b = 0; b < 2; ++b) mbar_init(tfull + b, 1), mbar_init(tempty + b, 2 * kResultWarps);
+    fence_mbar_init();
+  }
+  if (warp == kResultWarps + 1) tmem_alloc<2>(smem_u32(tmem_at), kTmemColumns);
+  tmem_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers stand
+  tmem_fence_after();
+  const uint32_t tmem = *tmem_at;
+  chain_wait();
+  chain_release();
+
+  bool ok = true;
+  if (warp >= kResultWarps) {
+    fewer_registers<kOtherRegisters>();
+    if (warp == kResultWarps && lane == 0) {  // operand tiles
+      const uint64_t keep = policy_evict_last();
+      uint32_t it = 0;
+      for (int item = pair; item < f.items && ok; item += pairs) {
+        const Tile t = tile_of(f, item);
+        for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
+          const int s = it % kStages;
+          if (!(ok = mbar_wait_bounded(empty + s, ((it / kStages) & 1) ^ 1))) break;
+          if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * kStageBytes);
+          const uint32_t bar = map_rank(smem_u32(full + s), 0);
+          const uint32_t pa = smem_u32(smem + s * kStageBytes), pb = pa + kOperandBytes;
+          const int second = kb >= f.blocks0;  // the other operand pair's turn
+          const int k = (second ? kb - f.blocks0 : kb) * kBlockK;
+          const int of = t.m / f.per_matrix;   // 0 unless two matrices are stored
+          const int m = (t.m - of * f.per_matrix) * 2 * kHalf + rank * kHalf;
+          const CUtensorMap* ma = f.a + (second | of);
+          if constexpr (A_MN) {
+            tma_load_2d_pair(pa, ma, m, k, bar, keep);
+            tma_load_2d_pair(pa + kMnBlockBytes, ma, m + 64, k, bar, keep);
+          } else {
+            tma_load_2d_pair(pa, ma, k, m, bar, keep);
+          }
+          if constexpr (EP == STORE) {
+            const int n = t.n * 2 * kHalf + rank * kHalf;
+            const CUtensorMap* mb = f.b + second;
+            if constexpr (B_MN) {
+              tma_load_2d_pair(pb, mb, n, k, bar, keep);
+              tma_load_2d_pair(pb + kMnBlockBytes, mb, n + 64, k, bar, keep);
+            } else {
+              tma_load_2d_pair(pb, mb, k, n, bar, keep);
+            }
+          } else {
+            tma_load_2d_pair(pb, f.b + rank, k, t.n * kHalf, bar, keep);
+          }
+        }
+      }
+      // The last arrivals at `empty` come from the other CTA: wait for them.
+      for (uint32_t j = it > kStages ? it - kStages : 0; j < it && ok; ++j)
+        ok = mbar_wait_bounded(empty + j % kStages, (j / kStages) & 1);
+    } else if (warp == kResultWarps + 1 && lane == 0 && rank == 0) {  // matrix instructions
+      constexpr uint32_t idesc = instr_desc<BF16, A_MN, B_MN>(2 * kHalf, 2 * kHalf);
+      uint32_t it = 0, chunk = 0;
+      for (int item = pair; item < f.items && ok; item += pairs) {
+        const Tile t = tile_of(f, item);
+        for (int k0 = t.k0; k0 < t.k1 && ok; k0 += kChunk, ++chunk) {
+          const uint32_t b = chunk & 1, d = tmem + b * 2 * kHalf;
+          if (!(ok = mbar_wait_bounded(tempty + b, ((chunk >> 1) & 1) ^ 1))) break;
+          tmem_fence_after();
+          const int k1 = min(t.k1, k0 + kChunk);
+          for (int kb = k0; kb < k1; ++kb, ++it) {
+            const int s = it % kStages;
+            if (!(ok = mbar_wait_bounded(full + s, (it / kStages) & 1))) break;
+            tmem_fence_after();
+            const uint32_t pa = smem_u32(smem + s * kStageBytes);
+            const uint64_t da = operand_desc<A_MN>(pa), db = operand_desc<B_MN>(pa + kOperandBytes);
+#pragma unroll
+            for (int j = 0; j < kBlockK / 16; ++j)
+              mma_f16<2>(d, da + j * kDescStep<A_MN>, db + j * kDescStep<B_MN>, idesc, kb != k0 || j != 0);
+            mma_commit<2>(empty + s);
+          }
+          if (ok) mma_commit<2>(tfull + b);
+        }
+      }
+      if (!ok) for (int s = 0; s < kStages; ++s) mbar_drain(full + s);
+    }
+  } else {  // results
+    more_registers<kResultRegisters>();
+    const int quad = warp & 3, half = warp >> 2, in_cta = quad * 32 + lane;
+    const Way way{smem_u32(staging + warp * kStagingBytes), lane};
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    uint32_t chunk = 0;
+    for (int item = pair; item < f.items; item += pairs) {
+      const Tile t = tile_of(f, item);
+      const int of = t.m / f.per_matrix;
+      const int row0 = (t.m - of * f.per_matrix) * 2 * kHalf + rank * kHalf + quad * 32, row = row0 + lane;
+      // FWD, AGAIN: acc[0..1] are 64 columns of g, acc[2..3] of u.  STORE: 128 columns.
+      uint32_t acc[4][32];
+      for (int k0 = t.k0; k0 < t.k1; k0 += kChunk, ++chunk) {
+        const uint32_t b = chunk & 1;
+        // After a wait that gave up, the warp goes through its steps (others
+        // may wait for it at a barrier) without waiting or storing.
+        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(tfull + b, (chunk >> 1) & 1));
+        tmem_fence_after();
+        const uint32_t at = lanes + b * 2 * kHalf;
+        auto column = [&](int j) { return EP == STORE ? half * 128 + j * 32 : (j >> 1) * 128 + half * 64 + (j & 1) * 32; };
+        if (k0 == t.k0) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) tmem_load32(acc[j], at + column(j));
+          tmem_wait_loads();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t r[32];
+            tmem_load32(r, at + column(j));
+            tmem_wait_loads();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) set_pair(acc[j], k, add2(pair_of(acc[j], k), pair_of(r, k)));
+          }
+        }
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(map_rank(smem_u32(tempty + b), 0));
+      }
+      const int rows = ok ? f.rows : 0;
+
+      if constexpr (EP == STORE) {
+        const int col0 = t.n * 2 * kHalf + half * 128;
+        if (f.splits > 1) {
+          if (row < rows) {
+            const int matrices = f.tiles_m / f.per_matrix;
+            float* to = f.parts + (((int64_t)t.split * matrices + of) * f.rows + row) * f.cols + col0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int k = 0; k < 32; k += 4)
+                if (col0 + j * 32 + k < f.cols)
+                  *reinterpret_cast<uint4*>(to + j * 32 + k) =
+                      make_uint4(acc[j][k], acc[j][k + 1], acc[j][k + 2], acc[j][k + 3]);
+          }
+        } else if (row0 < rows) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (col0 + j * 64 < f.cols) {
+              way.free_stage();
+              way.row16<BF16>(acc[2 * j], acc[2 * j + 1]);
+              way.send(f.out + of, way.stage, col0 + j * 64, row0);
+            }
+        }
+      } else {
+        const int col0 = t.n * kHalf + half * 64;
+        const bool in = row0 < rows && col0 < f.cols;
+        if (col0 + 64 > f.cols) {  // columns past the end: 0 * inf has made NaN of them in a row with infinities
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int k = 0; k < 32; ++k) acc[j][k] = col0 + (j & 1) * 32 + k < f.cols ? acc[j][k] : 0u;
+        }
+        if constexpr (EP == AGAIN) {
+          const uint4* from = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(f.dp) +
+                                                              ((int64_t)row * f.cols + col0));
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint4 q = make_uint4(0u, 0u, 0u, 0u);
+            if (row < rows && col0 + c * 8 < f.cols) q = ld_plain(from + c);
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int j = c >> 2, k = (c & 3) * 4 + i;
+              const float2 d = BF16 ? make_float2(bf16lo(w[i]), bf16hi(w[i])) : make_float2(f16lo(w[i]), f16hi(w[i]));
+              const float2 g = pair_of(acc[j], k), s = logistic2<XF32>(g), xs = mul2(g, s);
+              const float2 one_s = fma2(s, both(-1.0f), both(1.0f));
+              const float2 du = mul2(d, xs);
+              set_pair(acc[j], k, mul2(mul2(d, pair_of(acc[2 + j], k)), fma2(xs, one_s, s)));
+              set_pair(acc[2 + j], k, du);
+            }
+          }
+          if (in) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              way.free_stage();
+              way.row16<BF16>(acc[2 * j], acc[2 * j + 1]);
+              way.send(f.out + j, way.stage, col0, row0);
+            }
+          }
+        } else {
+          const int tile = t.n;  // 128 columns are a tile of scales
+          if (f.keep16 && in) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              way.free_stage();
+              way.row16<BF16>(acc[2 * j], acc[2 * j + 1]);
+              way.send(f.out + 1 + j, way.stage, col0, row0);
+            }
+          }
+          if (f.ckpt) {
+            way.free_stage();
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t m = both_halves(max(amax32(acc[2 * j]), amax32(acc[2 * j + 1])), red + j * 2 * kHalf, half,
+                                             in_cta, quad);
+              float mul;
+              const float scale = tile_scale(m, 448.0f, &mul);
+              if (half == 0 && row < rows) f.ckpt_scales[((int64_t)j * f.rows + row) * f.tiles + tile] = scale;
+              codes32(acc[2 * j], way.stage + j * 2048, lane, 0, m, mul, false, false);
+              codes32(acc[2 * j + 1], way.stage + j * 2048, lane, 2, m, mul, false, false);
+              if (in) way.send(f.out + 1 + j, way.stage + j * 2048, col0, row0);
+            }
+            named_barrier(1 + quad, 64);  // the slots have been read
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float2 g = pair_of(acc[j], k);
+              set_pair(acc[j], k, mul2(mul2(g, logistic2<XF32>(g)), pair_of(acc[2 + j], k)));
+            }
+          if constexpr (EP == FWD16) {
+            if (in) {
+              way.free_stage();
+              way.row16<BF16>(acc[0], acc[1]);
+              way.send(f.out, way.stage, col0, row0);
+            }
+          } else {
+            uint32_t m[2] = {amax32(acc[0]), amax32(acc[1])};
+            float mul[2];
+            if (f.mx) {
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                uint32_t byte;
+                mx_scale(m[j], f.e5m2 ? 15u : 8u, &mul[j], &byte);
+                if (row < rows && col0 + j * 32 < f.cols)
+                  static_cast<uint8_t*>(f.p_scales)[(int64_t)row * f.per_row + (col0 >> 5) + j] = (uint8_t)byte;
+              }
+            } else {
+              m[0] = m[1] = both_halves(max(m[0], m[1]), red, half, in_cta, quad);
+              const float scale = tile_scale(m[0], f.e5m2 ? 57344.0f : 448.0f, &mul[0]);
+              mul[1] = mul[0];
+              if (half == 0 && row < rows) static_cast<float*>(f.p_scales)[(int64_t)row * f.per_row + tile] = scale;
+              named_barrier(1 + quad, 64);  // the slot has been read
+            }
+            way.free_stage();
+            codes32(acc[0], way.stage, lane, 0, m[0], mul[0], f.e5m2, f.mx);
+            codes32(acc[1], way.stage, lane, 2, m[1], mul[1], f.e5m2, f.mx);
+            if (in) way.send(f.out, way.stage, col0, row0);
+          }
+        }
+      }
+    }
+    if (lane == 0) store_wait_all();
+  }
+  if (!ok) atomicAdd(&g_ffn_wait_failures, 1u);
+  tmem_fence_before();
+  __syncthreads();
+  cluster_sync();  // no CTA leaves while the other's instructions may read or signal it
+  tmem_fence_after();
+  if (warp == kResultWarps + 1) tmem_free<2>(tmem, kTmemColumns);
+}
+
+// Adds the parts of a product split along its contraction, in order, and
+// rounds once.  One thread: 8 elements.
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_ffn_join(const float* parts, int splits, int64_t n, void* out0, void* out1,
+                                                  int64_t n0) {
+  chain_wait();
+  chain_release();
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (i >= n) return;
+  float2 v[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = make_float2(0.0f, 0.0f);
+  for (int s = 0; s < splits; ++s) {
+    const float4* p = reinterpret_cast<const float4*>(parts + s * n + i);
+    const float4 a = __ldcg(p), b = __ldcg(p + 1);
+    v[0] = add2(v[0], make_float2(a.x, a.y)), v[1] = add2(v[1], make_float2(a.z, a.w));
+    v[2] = add2(v[2], make_float2(b.x, b.y)), v[3] = add2(v[3], make_float2(b.z, b.w));
+  }
+  uint16_t* to = i < n0 ? static_cast<uint16_t*>(out0) + i : static_cast<uint16_t*>(out1) + (i - n0);
+  *reinterpret_cast<uint4*>(to) = make_uint4(pack16<BF16>(v[0]), pack16<BF16>(v[1]), pack16<BF16>(v[2]), pack16<BF16>(v[3]));
+}
+
+template <bool BF16, bool A_MN, bool B_MN, int EP>
+mp_status launch(Ffn& f, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  const auto kernel = k_ffn<BF16, A_MN, B_MN, EP>;
+  if (!smem_opt_in(kernel, kSmem, done)) return MP_ECUDA;
+  const int most = sm_count() / 2;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * (f.items < most ? f.items : most));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, kernel, f) != cudaSuccess) {
+    cudaGetLastError();
+    return MP_ECUDA;
+  }
+  note_launches(1);
+  return MP_OK;
+}
+
+bool type16(mp_dtype t) { return t == MP_F16 || t == MP_BF16; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+int32_t ceil_div(int64_t a, int64_t b) { return (int32_t)((a + b - 1) / b); }
+
+// A dense (or `pitch` elements a row) matrix of 16-bit elements, boxes of 64 x box_rows.
+bool map16(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t pitch, int box_rows) {
+  return encode_swizzled_map_2d(m, p, 2, rows, cols, pitch * 2, box_rows, 64);
+}
+bool map8(CUtensorMap* m, const void* p, int64_t rows, int64_t cols) {
+  return encode_swizzled_map_2d(m, p, 1, rows, cols, cols, 32, 64);
+}
+
+// Tiles, and the walk over them.
+void lay_out(Ffn& f, int tiles_m, int tiles_n, int splits) {
+  f.tiles_m = f.per_matrix = tiles_m;
+  f.tiles_n = tiles_n;
+  f.splits = splits;
+  f.items = tiles_m * tiles_n * splits;
+  f.group = 8;
+}
+
+// Rows, columns and row lengths that both calls take.
+bool shape_ok(int64_t rows, int64_t width, int64_t hidden, int step) {
+  if (rows >= (1ll << 31) - 256 || width > (1 << 20) || hidden > (1 << 20)) return false;
+  if (width % 16 != 0 || hidden % step != 0) return false;
+  return ceil_div(rows, 256) * (int64_t)ceil_div(2 * hidden + width, 128) < (1ll << 30);
+}
+bool pitch_ok(int64_t ld, int64_t cols, int64_t rows) {
+  return rows <= 1 || (ld >= cols && ld < (1ll << 38) && ld % 8 == 0);
+}
+
+// Forms g and u (FWD16, FWD8, AGAIN).
+template <int EP>
+mp_status project(Ffn& f, mp_dtype t, const void* x, const void* w_gate, const void* w_up, int64_t rows, int64_t width,
+                  int64_t hidden, cudaStream_t st) {
+  if (!map16(&f.a[0], x, rows, width, width, kHalf) || !map16(&f.b[0], w_gate, hidden, width, width, kHalf) ||
+      !map16(&f.b[1], w_up, hidden, width, width, kHalf))
+    return MP_ECUDA;
+  f.blocks = f.blocks0 = ceil_div(width, kBlockK);
+  f.rows = (int32_t)rows, f.cols = (int32_t)hidden;
+  lay_out(f, ceil_div(rows, 2 * kHalf), ceil_div(hidden, kHalf), 1);
+  return t == MP_BF16 ? launch<true, false, false, EP>(f, st) : launch<false, false, false, EP>(f, st);
+}
+
+}  // namespace
+
+uint32_t ffn_wait_failures() {
+  uint32_t v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_ffn_wait_failures, sizeof(v)) != cudaSuccess) return 0xFFFFFFFFu;
+  return v;
+}
+
+}  // namespace mp
+
+extern "C" MP_API mp_status linear_swiglu(const void* x, mp_dtype x_dtype, int64_t rows, int64_t width, int64_t hidden,
+                                          const void* w_gate, const void* w_up, void* p, mp_dtype p_dtype,
+                                          int32_t scale_block, void* p_scales, void* gate, void* up, int64_t ld,
+                                          void* ckpt, float* ckpt_scales, void* stream) {
+  using namespace mp;
+  if (rows < 0 || width < 0 || hidden < 0 || !type16(x_dtype)) return MP_EINVAL;
+  const bool fp8 = p_dtype == MP_E4M3 || p_dtype == MP_E5M2;
+  if (!fp8 && p_dtype != x_dtype) return MP_EINVAL;
+  if (fp8 && scale_block != 128 && scale_block != 32) return MP_EINVAL;
+  if (!shape_ok(rows, width, hidden, fp8 && scale_block == 32 ? 32 : 16)) return MP_ESHAPE;
+  if (rows == 0 || hidden == 0) return MP_OK;
+  if (width == 0) return MP_ESHAPE;
+  if (!x || !w_gate || !w_up || !p || fp8 != (p_scales != nullptr) || (!gate != !up) || (!ckpt != !ckpt_scales) ||
+      (gate && ckpt))
+    return MP_EINVAL;
+  if (gate && !pitch_ok(ld, hidden, rows)) return MP_ESHAPE;
+  if (!aligned16(x) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(p) || !aligned16(gate) || !aligned16(up) ||
+      !aligned16(ckpt) || !aligned4(ckpt_scales) || (fp8 && scale_block == 128 && !aligned4(p_scales)))
+    return MP_EALIGN;
+  Ffn f;
+  f.e5m2 = p_dtype == MP_E5M2, f.mx = scale_block == 32;
+  f.keep16 = gate != nullptr, f.ckpt = ckpt != nullptr;
+  f.p_scales = p_scales, f.ckpt_scales = ckpt_scales;
+  f.tiles = ceil_div(hidden, 128);
+  f.per_row = f.mx ? (int32_t)(hidden / 32) : f.tiles;
+  bool ok = fp8 ? map8(&f.out[0], p, rows, hidden) : map16(&f.out[0], p, rows, hidden, hidden, 32);
+  if (gate) {
+    const int64_t pitch = rows > 1 ? ld : hidden;
+    ok = ok && map16(&f.out[1], gate, rows, hidden, pitch, 32) && map16(&f.out[2], up, rows, hidden, pitch, 32);
+  } else if (ckpt) {
+    ok = ok && map8(&f.out[1], ckpt, rows, hidden) &&
+         map8(&f.out[2], static_cast<uint8_t*>(ckpt) + rows * hidden, rows, hidden);
+  }
+  if (!ok) return MP_ECUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return fp8 ? project<FWD8>(f, x_dtype, x, w_gate, w_up, rows, width, hidden, st)
+             : project<FWD16>(f, x_dtype, x, w_gate, w_up, rows, width, hidden, st);
+}
+
+namespace mp {
+namespace {
+
+// The workspace: dg and du [2][rows][hidden] in 16 bits, then the parts of split products.
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+}  // namespace
+}  // namespace mp
+
+extern "C" MP_API size_t linear_swiglu_workspace_size(int64_t rows, int64_t width, int64_t hidden) {
+  using namespace mp;
+  if (rows <= 0 || width <= 0 || hidden <= 0 || !shape_ok(rows, width, hidden, 16)) return 0;
+  return up256((size_t)rows * hidden * 4);
+}
+
+extern "C" MP_API mp_status linear_swiglu_backward(const void* dp, mp_dtype x_dtype, int64_t rows, int64_t width,
+                                                   int64_t hidden, const void* x, const void* w_gate, const void* w_up,
+                                                   const void* gate, const void* up, int64_t ld, const void* ckpt,
+                                                   const float* ckpt_scales, void* dx, void* dw_gate, void* dw_up,
+                                                   void* d_workspace, size_t workspace_bytes, void* stream) {
+  using namespace mp;
+  if (rows < 0 || width < 0 || hidden < 0 || !type16(x_dtype)) return MP_EINVAL;
+  if (!shape_ok(rows, width, hidden, 16)) return MP_ESHAPE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (width == 0) return rows == 0 || hidden == 0 ? MP_OK : MP_ESHAPE;
+  if ((!dw_gate != !dw_up) || (!gate != !up) || (!ckpt != !ckpt_scales) || (gate && ckpt)) return MP_EINVAL;
+  if (!aligned16(dx) || !aligned16(dw_gate) || !aligned16(dw_up)) return MP_EALIGN;
+  if (rows == 0 || hidden == 0) {  // empty sums
+    if (rows > 0 && dx && cudaMemsetAsync(dx, 0, (size_t)rows * width * 2, st) != cudaSuccess) return MP_ECUDA;
+    const size_t n = (size_t)hidden * width * 2;
+    if (n && dw_gate && (cudaMemsetAsync(dw_gate, 0, n, st) != cudaSuccess || cudaMemsetAsync(dw_up, 0, n, st) != cudaSuccess))
+      return MP_ECUDA;
+    return MP_OK;
+  }
+  if (!dx && !dw_gate) return MP_OK;
+  if (!dp || !w_gate || !w_up || !x) return MP_EINVAL;
+  if (gate && !pitch_ok(ld, hidden, rows)) return MP_ESHAPE;
+  if (!aligned16(dp) || !aligned16(x) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(gate) || !aligned16(up) ||
+      !aligned16(ckpt) || !aligned4(ckpt_scales) || !aligned16(d_workspace))
+    return MP_EALIGN;
+  if (!d_workspace || workspace_bytes < linear_swiglu_workspace_size(rows, width, hidden)) return MP_EWORKSPACE;
+  uint16_t* const dg = static_cast<uint16_t*>(d_workspace);
+  uint16_t* const du = dg + rows * hidden;
+  const bool bf16 = x_dtype == MP_BF16;
+  Ffn f;
+  if (gate || ckpt) {
+    const mp_status s = swiglu_backward(dp, x_dtype, rows, hidden, gate, up, ld, ckpt, ckpt_scales, dg, du, hidden, stream);
+    if (s != MP_OK) return s;
+  } else {
+    f.dp = dp;
+    if (!map16(&f.out[0], dg, rows, hidden, hidden, 32) || !map16(&f.out[1], du, rows, hidden, hidden, 32)) return MP_ECUDA;
+    const mp_status s = project<AGAIN>(f, x_dtype, x, w_gate, w_up, rows, width, hidden, st);
+    if (s != MP_OK) return s;
+  }
+  if (dx) {
+    if (!map16(&f.a[0], dg, rows, hidden, hidden, kHalf) || !map16(&f.a[1], du, rows, hidden, hidden, kHalf) ||
+        !map16(&f.b[0], w_gate, hidden, width, width, 64) || !map16(&f.b[1], w_up, hidden, width, width, 64) ||
+        !map16(&f.out[0], dx, rows, width, width, 32))
+      return MP_ECUDA;
+    f.blocks0 = ceil_div(hidden, kBlockK), f.blocks = 2 * f.blocks0;
+    f.rows = (int32_t)rows, f.cols = (int32_t)width;
+    lay_out(f, ceil_div(rows, 2 * kHalf), ceil_div(width, 2 * kHalf), 1);
+    const mp_status s = bf16 ? launch<true, false, true, STORE>(f, st) : launch<false, false, true, STORE>(f, st);
+    if (s != MP_OK) return s;
+  }
+  if (dw_gate) {
+    if (!map16(&f.a[0], dg, rows, hidden, hidden, 64) || !map16(&f.a[1], du, rows, hidden, hidden, 64) ||
+        !map16(&f.b[0], x, rows, width, width, 64) || !map16(&f.out[0], dw_gate, hidden, width, width, 32) ||
+        !map16(&f.out[1], dw_up, hidden, width, width, 32))
+      return MP_ECUDA;
+    f.blocks0 = f.blocks = ceil_div(rows, kBlockK);
+    f.rows = (int32_t)hidden, f.cols = (int32_t)width;
+    const int per = ceil_div(hidden, 2 * kHalf);
+    lay_out(f, 2 * per, ceil_div(width, 2 * kHalf), 1);
+    f.per_matrix = per;
+    const mp_status s = bf16 ? launch<true, true, true, STORE>(f, st) : launch<false, true, true, STORE>(f, st);
+    if (s != MP_OK) return s;
+  }
+  return MP_OK;
+}
