@@ -18,9 +18,9 @@
 // weights', so the thread that has an element of g has that of u.
 //
 // Sums: the tensor core adds to its binary32 accumulator by truncation, which
-// over a contraction of 4096 leaves results 4e-6 too small.  So every kChunk
-// blocks the sums so far leave TMEM and are added to registers with correct
-// rounding, while the next chunk goes into the other half of TMEM.
+// over a contraction of 4096 leaves results 4e-6 too small.  So every kRun
+// stages the sums so far leave TMEM and are added to registers with correct
+// rounding, while the next run goes into the other half of TMEM.
 #include <new>
 
 #include "mp_chain.cuh"
@@ -32,7 +32,6 @@ namespace mp {
 namespace {
 
 constexpr int kBlockK = 64;        // steps of the contraction in a stage: 128 bytes
-constexpr int kChunk = 8;          // stages added up inside the tensor core
 constexpr int kStages = 6;
 constexpr int kHalf = 128;         // rows of a tile, and of its other operand, in one CTA
 constexpr int kOperandBytes = kHalf * kBlockK * 2;
@@ -42,7 +41,7 @@ constexpr int kStagingBytes = 4096;  // 32 rows of 128 bytes, for each of those 
 // Three warpgroups: two form results, with 128 sums a thread, one copies and
 // issues.  384 threads start with 168 registers each; the split adds up to that.
 constexpr int kThreads = (kResultWarps + 4) * 32;
-constexpr int kResultRegisters = 232, kOtherRegisters = 40;
+constexpr int kResultRegisters = 224, kOtherRegisters = 56;
 static_assert(kResultWarps * kResultRegisters + 4 * kOtherRegisters <= (kResultWarps + 4) * 168, "registers of a CTA");
 constexpr int kTmemColumns = 512;
 constexpr int kBarrierBytes = 256;
@@ -57,6 +56,12 @@ enum {
   AGAIN,      // g and u formed again: dg and du
   STORE       // the product itself
 };
+
+// Stages added up inside the tensor core before the sums move on to registers:
+// 512 terms where FP32 scales show the truncation (1024 would save 4 % of the
+// time), 2048 where results are rounded to 16 bits.
+template <int EP>
+constexpr int kRun = EP == FWD8 ? 8 : 32;
 
 struct Ffn {
   CUtensorMap a[2], b[2], out[3];
@@ -215,39 +220,41 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
   bool ok = true;
   if (warp >= kResultWarps) {
     fewer_registers<kOtherRegisters>();
-    if (warp == kResultWarps && lane == 0) {  // operand tiles
-      const uint64_t keep = policy_evict_last();
+    if ((warp == kResultWarps || warp == kResultWarps + 2) && lane == 0) {
+      // Operand tiles: one warp copies A's, another B's.  (One for both issued
+      // up to four copies a stage and held the MN-major products back: the
+      // weights' gradients of 2048 x 4096 x 14336 took 366 us.)
+      const bool is_b = warp != kResultWarps;
+      const uint32_t bars = map_rank(smem_u32(full), 0), tiles = smem_u32(smem) + (is_b ? kOperandBytes : 0);
       uint32_t it = 0;
       for (int item = pair; item < f.items && ok; item += pairs) {
         const Tile t = tile_of(f, item);
+        const int of = t.m / f.per_matrix;  // 0 unless two matrices are stored
+        int at;                             // the first of the tile's 128 rows of this operand in this CTA
+        const CUtensorMap *map0, *map1;     // of the first operand pair and of the second
+        if (!is_b) {
+          at = (t.m - of * f.per_matrix) * 2 * kHalf + rank * kHalf;
+          map0 = f.a + of, map1 = f.a + 1;
+        } else if (EP == STORE) {
+          at = t.n * 2 * kHalf + rank * kHalf;
+          map0 = f.b, map1 = f.b + 1;
+        } else {
+          at = t.n * kHalf;
+          map0 = map1 = f.b + rank;
+        }
         for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
           const int s = it % kStages;
           if (!(ok = mbar_wait_bounded(empty + s, ((it / kStages) & 1) ^ 1))) break;
-          if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * kStageBytes);
-          const uint32_t bar = map_rank(smem_u32(full + s), 0);
-          const uint32_t pa = smem_u32(smem + s * kStageBytes), pb = pa + kOperandBytes;
-          const int second = kb >= f.blocks0;  // the other operand pair's turn
+          if (rank == 0 && !is_b) mbar_arrive_expect_tx(full + s, 2 * kStageBytes);
+          const uint32_t bar = bars + s * 8, to = tiles + s * kStageBytes;
+          const bool second = kb >= f.blocks0;
           const int k = (second ? kb - f.blocks0 : kb) * kBlockK;
-          const int of = t.m / f.per_matrix;   // 0 unless two matrices are stored
-          const int m = (t.m - of * f.per_matrix) * 2 * kHalf + rank * kHalf;
-          const CUtensorMap* ma = f.a + (second | of);
-          if constexpr (A_MN) {
-            tma_load_2d_pair(pa, ma, m, k, bar, keep);
-            tma_load_2d_pair(pa + kMnBlockBytes, ma, m + 64, k, bar, keep);
+          const CUtensorMap* map = second ? map1 : map0;
+          if (is_b ? B_MN : A_MN) {
+            tma_load_2d_pair(to, map, at, k, bar);
+            tma_load_2d_pair(to + kMnBlockBytes, map, at + 64, k, bar);
           } else {
-            tma_load_2d_pair(pa, ma, k, m, bar, keep);
-          }
-          if constexpr (EP == STORE) {
-            const int n = t.n * 2 * kHalf + rank * kHalf;
-            const CUtensorMap* mb = f.b + second;
-            if constexpr (B_MN) {
-              tma_load_2d_pair(pb, mb, n, k, bar, keep);
-              tma_load_2d_pair(pb + kMnBlockBytes, mb, n + 64, k, bar, keep);
-            } else {
-              tma_load_2d_pair(pb, mb, k, n, bar, keep);
-            }
-          } else {
-            tma_load_2d_pair(pb, f.b + rank, k, t.n * kHalf, bar, keep);
+            tma_load_2d_pair(to, map, k, at, bar);
           }
         }
       }
@@ -259,11 +266,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
       uint32_t it = 0, chunk = 0;
       for (int item = pair; item < f.items && ok; item += pairs) {
         const Tile t = tile_of(f, item);
-        for (int k0 = t.k0; k0 < t.k1 && ok; k0 += kChunk, ++chunk) {
+        for (int k0 = t.k0; k0 < t.k1 && ok; k0 += kRun<EP>, ++chunk) {
           const uint32_t b = chunk & 1, d = tmem + b * 2 * kHalf;
           if (!(ok = mbar_wait_bounded(tempty + b, ((chunk >> 1) & 1) ^ 1))) break;
           tmem_fence_after();
-          const int k1 = min(t.k1, k0 + kChunk);
+          const int k1 = min(t.k1, k0 + kRun<EP>);
           for (int kb = k0; kb < k1; ++kb, ++it) {
             const int s = it % kStages;
             if (!(ok = mbar_wait_bounded(full + s, (it / kStages) & 1))) break;
@@ -292,7 +299,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
       const int row0 = (t.m - of * f.per_matrix) * 2 * kHalf + rank * kHalf + quad * 32, row = row0 + lane;
       // FWD, AGAIN: acc[0..1] are 64 columns of g, acc[2..3] of u.  STORE: 128 columns.
       uint32_t acc[4][32];
-      for (int k0 = t.k0; k0 < t.k1; k0 += kChunk, ++chunk) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < 32; ++k) acc[j][k] = 0u;
+      for (int k0 = t.k0; k0 < t.k1; k0 += kRun<EP>, ++chunk) {
         const uint32_t b = chunk & 1;
         // After a wait that gave up, the warp goes through its steps (others
         // may wait for it at a barrier) without waiting or storing.
@@ -300,18 +311,18 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
         tmem_fence_after();
         const uint32_t at = lanes + b * 2 * kHalf;
         auto column = [&](int j) { return EP == STORE ? half * 128 + j * 32 : (j >> 1) * 128 + half * 64 + (j & 1) * 32; };
-        if (k0 == t.k0) {
+        // the next 16 columns on their way while 16 are added
+        uint32_t r[2][16];
+        tmem_load16(r[0], at + column(0));
 #pragma unroll
-          for (int j = 0; j < 4; ++j) tmem_load32(acc[j], at + column(j));
-          tmem_wait_loads();
-        } else {
+        for (int j = 0; j < 8; ++j) {
+          tmem_wait(r[j & 1]);
+          if (j < 7) tmem_load16(r[(j + 1) & 1], at + column((j + 1) >> 1) + ((j + 1) & 1) * 16);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t r[32];
-            tmem_load32(r, at + column(j));
-            tmem_wait_loads();
-#pragma unroll
-            for (int k = 0; k < 16; ++k) set_pair(acc[j], k, add2(pair_of(acc[j], k), pair_of(r, k)));
+          for (int k = 0; k < 8; ++k) {
+            const float2 v = make_float2(__uint_as_float(r[j & 1][2 * k]), __uint_as_float(r[j & 1][2 * k + 1]));
+            const int to = (j & 1) * 8 + k;
+            set_pair(acc[j >> 1], to, add2(pair_of(acc[j >> 1], to), v));
           }
         }
         tmem_fence_before();
