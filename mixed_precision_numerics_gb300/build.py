@@ -22,7 +22,7 @@ UNTAGGED = os.path.join(PKG, "_mpcall.so")  # the extension's name in earlier bu
 PYTHON_H = os.path.join(sysconfig.get_paths()["include"], "Python.h")
 HEADER = os.path.join(ROOT, "include", "mpnum.h")
 
-SOURCES = ["mp_common.cu", "mp_adamw.cu", "mp_fp8.cu", "mp_nvfp4.cu", "mp_mx.cu", "mp_norm.cu", "mp_swiglu.cu", "mp_ffn.cu", "mp_grads.cu"]
+SOURCES = ["mp_common.cu", "mp_adamw.cu", "mp_fp8.cu", "mp_nvfp4.cu", "mp_mx.cu", "mp_norm.cu", "mp_swiglu.cu", "mp_ffn.cu", "mp_ffn_few.cu", "mp_grads.cu"]
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = GENCODE + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
                         "-I", os.path.join(ROOT, "include")]

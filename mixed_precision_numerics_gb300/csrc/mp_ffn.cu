@@ -24,14 +24,11 @@
 #include <new>
 
 #include "mp_chain.cuh"
-#include "mp_internal.h"
-#include "mp_mma.cuh"
-#include "mp_tile8.cuh"
+#include "mp_ffn.cuh"
 
 namespace mp {
 namespace {
 
-constexpr int kBlockK = 64;        // steps of the contraction in a stage: 128 bytes
 constexpr int kStages = 6;
 constexpr int kHalf = 128;         // rows of a tile, and of its other operand, in one CTA
 constexpr int kOperandBytes = kHalf * kBlockK * 2;
@@ -44,72 +41,49 @@ constexpr int kThreads = (kResultWarps + 4) * 32;
 constexpr int kResultRegisters = 224, kOtherRegisters = 56;
 static_assert(kResultWarps * kResultRegisters + 4 * kOtherRegisters <= (kResultWarps + 4) * 168, "registers of a CTA");
 constexpr int kTmemColumns = 512;
+constexpr int kBand = 8;
 constexpr int kBarrierBytes = 256;
 constexpr int kSmem = kStages * kStageBytes + kResultWarps * kStagingBytes + 2 * 2 * kHalf * 4 + kBarrierBytes;
 static_assert(kSmem <= 232448, "227 KB a CTA");
 static_assert((2 * kStages + 4) * 8 + 8 <= kBarrierBytes, "barriers and the TMEM address");
 
-// What the result warps do with a tile.
-enum {
-  FWD16 = 0,  // p in 16 bits
-  FWD8,       // p in FP8
-  AGAIN,      // g and u formed again: dg and du
-  STORE       // the product itself
-};
-
-// Stages added up inside the tensor core before the sums move on to registers:
-// 512 terms where FP32 scales show the truncation (1024 would save 4 % of the
-// time), 2048 where results are rounded to 16 bits.
-template <int EP>
-constexpr int kRun = EP == FWD8 ? 8 : 32;
-
 struct Ffn {
-  CUtensorMap a[2], b[2], out[3];
-  int32_t items, tiles_m, tiles_n, group;  // work items = tiles * splits; rows of tiles walked together
-  int32_t per_matrix;                      // STORE of two matrices: rows of tiles in each, else tiles_m
-  int32_t blocks0, blocks, splits;         // blocks of the contraction in the first operand pair, and in all
+  CUtensorMap a[2], b[2];
+  int32_t items, tiles_m;  // work items = tiles * splits
+  FastDiv tiles, band, last, per_matrix;  // tiles of a split, of a band; rows of tiles in the last band, in a matrix
+  int32_t blocks0, blocks, splits, matrices;  // blocks of the contraction in the first operand pair, and in all
   int32_t rows, cols;                      // of a result matrix
-  // FWD
-  bool e5m2, mx, keep16, ckpt;
-  void* p_scales;
-  float* ckpt_scales;  // [2][rows][tiles]
-  int32_t per_row, tiles;
-  // AGAIN
-  const void* dp;
-  // STORE in parts: [splits][matrices][rows][cols]
-  float* parts;
+  FfnOut o;
+  void* result[2];  // STORE: the matrices
+  float* parts;     // STORE of a split product: [splits][matrices][rows][cols]
 };
 
 __device__ unsigned int g_ffn_wait_failures;  // bounded waits that gave up (read by mp_wait_failures)
 
 struct Tile {
-  int32_t m, n, k0, k1, split;
+  int32_t m, n, k0, k1, split, of;  // row and column of tiles, stages from k0 to k1, which matrix
 };
-// Items walk the tiles in bands of `group` rows of tiles, column by column, so
-// that those in flight together share operands in L2; all tiles of a split first.
-__device__ __forceinline__ Tile tile_of(const Ffn& f, int item) {
-  const int all = f.tiles_m * f.tiles_n;
+// Items walk the tiles in bands of kBand rows of tiles, column by column, so
+// that those in flight together share operands in L2; all tiles of a split
+// first.  (Every role does this for every tile, one thread after another: with
+// plain divisions the tiles of short contractions waited for it.)
+__device__ __forceinline__ Tile tile_of(const Ffn& f, uint32_t item) {
   Tile t;
-  t.split = item / all;
-  item -= t.split * all;
-  const int band = item / (f.group * f.tiles_n), first = band * f.group;
-  const int high = min(f.group, f.tiles_m - first);
-  item -= band * f.group * f.tiles_n;
-  t.n = item / high;
-  t.m = first + item - t.n * high;
-  t.k0 = (int)((int64_t)f.blocks * t.split / f.splits);
-  t.k1 = (int)((int64_t)f.blocks * (t.split + 1) / f.splits);
+  t.split = 0, t.k0 = 0, t.k1 = f.blocks;
+  if (f.splits > 1) {
+    t.split = div_by(item, f.tiles);
+    item -= t.split * f.tiles.d;
+    t.k0 = f.blocks * t.split / f.splits;  // below 2^30
+    t.k1 = f.blocks * (t.split + 1) / f.splits;
+  }
+  const uint32_t band = div_by(item, f.band);
+  item -= band * f.band.d;
+  const bool whole = (int)(band + 1) * kBand <= f.tiles_m;
+  t.n = whole ? item / kBand : div_by(item, f.last);
+  t.m = band * kBand + item - t.n * (whole ? kBand : f.last.d);
+  t.of = div_by(t.m, f.per_matrix);  // 0 unless two matrices are stored
+  t.m -= t.of * f.per_matrix.d;
   return t;
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack16(float2 v) {  // a NaN gives 0x7FFF
-  uint32_t r;
-  if constexpr (BF16)
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
-  else
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
-  return r;
 }
 
 // 32 accumulators as 16 pairs.
@@ -120,30 +94,48 @@ __device__ __forceinline__ void set_pair(uint32_t (&r)[32], int k, float2 v) {
   r[2 * k] = __float_as_uint(v.x), r[2 * k + 1] = __float_as_uint(v.y);
 }
 
-// One warp's way out: 32 rows of 64 16-bit elements (or of 64 bytes) through
-// its staging buffer, swizzled as the map's box is.
+// One warp's way out: 32 rows of 128 or 64 bytes through its staging buffer,
+// so that eight or four lanes store a row's bytes together.  Unit c of 16 bytes
+// of row r lies at unit c ^ (r % 8), or c ^ (r / 2 % 4) of the shorter rows,
+// which spreads writes and reads over the banks.  (Tile copies out of the
+// buffer need a fence after the writes that took longer than the tile of a
+// short contraction: dw of one row 69 us, .)
 struct Way {
   uint32_t stage;
   int lane;
-  __device__ __forceinline__ void free_stage() const {
-    if (lane == 0) store_wait_read();
+  __device__ __forceinline__ void put128(int c, uint4 v) const {
+    sts16(stage + lane * 128 + ((c ^ (lane & 7)) << 4), v.x, v.y, v.z, v.w);
+  }
+  __device__ __forceinline__ void put64(int c, uint4 v) const {
+    sts16(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), v.x, v.y, v.z, v.w);
+  }
+  // Rows `pitch` bytes apart from `to`; `rows` of them and `bytes` of each are in the matrix.
+  template <int BYTES>
+  __device__ __forceinline__ void send(void* to, int64_t pitch, int rows, int bytes) const {
+    constexpr int U = BYTES / 16;  // lanes to a row
+    __syncwarp();
+    const int u = lane % U, r0 = lane / U;
+    unsigned char* at = static_cast<unsigned char*>(to) + r0 * pitch + u * 16;
+#pragma unroll
+    for (int i = 0; i < U; ++i, at += pitch * (32 / U)) {
+      const int r = i * (32 / U) + r0, swizzled = U == 8 ? u ^ (r & 7) : u ^ ((r >> 1) & 3);
+      const uint4 v = lds16(stage + r * BYTES + (swizzled << 4));
+      if (r < rows && u * 16 < bytes) *reinterpret_cast<uint4*>(at) = v;
+    }
     __syncwarp();
   }
-  __device__ __forceinline__ void send(const CUtensorMap* map, uint32_t at, int32_t x, int32_t y) const {
-    fence_async_shared();
-    __syncwarp();
-    if (lane == 0) tma_store_2d(map, at, x, y);
-  }
-  // 64 values of this lane's row
+  // 64 values of each row, rounded
   template <bool BF16>
-  __device__ __forceinline__ void row16(const uint32_t (&lo)[32], const uint32_t (&hi)[32]) const {
+  __device__ __forceinline__ void send16(const uint32_t (&lo)[32], const uint32_t (&hi)[32], void* to, int64_t pitch,
+                                         int rows, int cols) const {
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
       const uint32_t(&r)[32] = c < 4 ? lo : hi;
       const int k = (c & 3) * 4;
-      sts16(stage + lane * 128 + ((c ^ (lane & 7)) << 4), pack16<BF16>(pair_of(r, k)), pack16<BF16>(pair_of(r, k + 1)),
-            pack16<BF16>(pair_of(r, k + 2)), pack16<BF16>(pair_of(r, k + 3)));
+      put128(c, make_uint4(pack16<BF16>(pair_of(r, k)), pack16<BF16>(pair_of(r, k + 1)), pack16<BF16>(pair_of(r, k + 2)),
+                           pack16<BF16>(pair_of(r, k + 3))));
     }
+    send<128>(to, pitch * 2, rows, cols * 2);
   }
 };
 
@@ -158,18 +150,9 @@ __device__ __forceinline__ uint32_t amax32(const uint32_t (&r)[32]) {
   return __float_as_uint(max3_abs_nan(a, b, b));
 }
 
-// Scale and multiplier of a 1x128 tile by the rule of the other block operators
-// (tile_scales), one thread for the tile.
-__device__ __forceinline__ float tile_scale(uint32_t m, float top, float* mul) {
-  const float amax = __uint_as_float(m), r = __fdiv_rn(top, amax);
-  *mul = (r < INFINITY && m < kInfBits) ? r : 0.0f;
-  return m > kInfBits ? __uint_as_float(0x7FC00000u) : __fdiv_rn(amax, top);
-}
-
-// Codes of 32 columns of this lane's row into its 64-byte row of staging, at
-// 16-byte unit `unit`.
-__device__ __forceinline__ void codes32(const uint32_t (&r)[32], uint32_t stage, int lane, int unit, uint32_t m,
-                                        float mul, bool e5m2, bool mx) {
+// Codes of 32 columns of this lane's row of 64 bytes, at 16-byte unit `unit`.
+__device__ __forceinline__ void codes32(const uint32_t (&r)[32], const Way& way, int unit, uint32_t m, float mul,
+                                        bool e5m2, bool mx) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     float2 v[kPairs];
@@ -180,7 +163,7 @@ __device__ __forceinline__ void codes32(const uint32_t (&r)[32], uint32_t stage,
       c = mx ? make_uint4(0u, 0u, 0u, 0u) : nonfinite_unit(v, [&](int i) { return float_sign80(v, i); });
     else
       c = e5m2 ? cast_unit<true>(v, mul) : cast_unit<false>(v, mul);
-    sts16(stage + lane * 64 + (((unit + h) ^ ((lane >> 1) & 3)) << 4), c.x, c.y, c.z, c.w);
+    way.put64(unit + h, c);
   }
 }
 
@@ -229,12 +212,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
       uint32_t it = 0;
       for (int item = pair; item < f.items && ok; item += pairs) {
         const Tile t = tile_of(f, item);
-        const int of = t.m / f.per_matrix;  // 0 unless two matrices are stored
         int at;                             // the first of the tile's 128 rows of this operand in this CTA
         const CUtensorMap *map0, *map1;     // of the first operand pair and of the second
         if (!is_b) {
-          at = (t.m - of * f.per_matrix) * 2 * kHalf + rank * kHalf;
-          map0 = f.a + of, map1 = f.a + 1;
+          at = t.m * 2 * kHalf + rank * kHalf;
+          map0 = f.a + t.of, map1 = f.a + 1;
         } else if (EP == STORE) {
           at = t.n * 2 * kHalf + rank * kHalf;
           map0 = f.b, map1 = f.b + 1;
@@ -295,28 +277,42 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
     uint32_t chunk = 0;
     for (int item = pair; item < f.items; item += pairs) {
       const Tile t = tile_of(f, item);
-      const int of = t.m / f.per_matrix;
-      const int row0 = (t.m - of * f.per_matrix) * 2 * kHalf + rank * kHalf + quad * 32, row = row0 + lane;
+      const int row0 = t.m * 2 * kHalf + rank * kHalf + quad * 32, row = row0 + lane;
       // FWD, AGAIN: acc[0..1] are 64 columns of g, acc[2..3] of u.  STORE: 128 columns.
       uint32_t acc[4][32];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int k = 0; k < 32; ++k) acc[j][k] = 0u;
-      for (int k0 = t.k0; k0 < t.k1; k0 += kRun<EP>, ++chunk) {
-        const uint32_t b = chunk & 1;
-        // After a wait that gave up, the warp goes through its steps (others
-        // may wait for it at a barrier) without waiting or storing.
-        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(tfull + b, (chunk >> 1) & 1));
+      auto column = [&](int j) { return EP == STORE ? half * 128 + j * 32 : (j >> 1) * 128 + half * 64 + (j & 1) * 32; };
+      // Waits for a run's sums; where they are.  After a wait that gave up, the
+      // warp goes through its steps (others may wait for it at a barrier)
+      // without waiting or storing.
+      auto run_done = [&]() {
+        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(tfull + (chunk & 1), (chunk >> 1) & 1));
         tmem_fence_after();
-        const uint32_t at = lanes + b * 2 * kHalf;
-        auto column = [&](int j) { return EP == STORE ? half * 128 + j * 32 : (j >> 1) * 128 + half * 64 + (j & 1) * 32; };
+        return lanes + (chunk & 1) * 2 * kHalf;
+      };
+      auto run_read = [&]() {  // their place is free
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(map_rank(smem_u32(tempty + (chunk & 1)), 0));
+        ++chunk;
+      };
+      {  // the first run's sums straight to where they stay
+        const uint32_t at = run_done();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tmem_load32(acc[j], at + column(j));
+        tmem_wait();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) loaded(acc[j]);
+        run_read();
+      }
+      for (int k0 = t.k0 + kRun<EP>; k0 < t.k1; k0 += kRun<EP>) {
+        const uint32_t at = run_done();
         // the next 16 columns on their way while 16 are added
         uint32_t r[2][16];
         tmem_load16(r[0], at + column(0));
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          tmem_wait(r[j & 1]);
+          tmem_wait();
+          loaded(r[j & 1]);
           if (j < 7) tmem_load16(r[(j + 1) & 1], at + column((j + 1) >> 1) + ((j + 1) & 1) * 16);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
@@ -325,38 +321,32 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
             set_pair(acc[j >> 1], to, add2(pair_of(acc[j >> 1], to), v));
           }
         }
-        tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(map_rank(smem_u32(tempty + b), 0));
+        run_read();
       }
       const int rows = ok ? f.rows : 0;
 
       if constexpr (EP == STORE) {
         const int col0 = t.n * 2 * kHalf + half * 128;
         if (f.splits > 1) {
-          if (row < rows) {
-            const int matrices = f.tiles_m / f.per_matrix;
-            float* to = f.parts + (((int64_t)t.split * matrices + of) * f.rows + row) * f.cols + col0;
+          float* const to = f.parts + ((int64_t)t.split * f.matrices + t.of) * f.rows * f.cols +
+                            (int64_t)row0 * f.cols + col0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < 4; ++j) {
 #pragma unroll
-              for (int k = 0; k < 32; k += 4)
-                if (col0 + j * 32 + k < f.cols)
-                  *reinterpret_cast<uint4*>(to + j * 32 + k) =
-                      make_uint4(acc[j][k], acc[j][k + 1], acc[j][k + 2], acc[j][k + 3]);
+            for (int c = 0; c < 8; ++c)
+              way.put128(c, make_uint4(acc[j][4 * c], acc[j][4 * c + 1], acc[j][4 * c + 2], acc[j][4 * c + 3]));
+            way.send<128>(to + j * 32, (int64_t)f.cols * 4, rows - row0, (f.cols - col0 - j * 32) * 4);
           }
-        } else if (row0 < rows) {
+        } else {
+          uint16_t* const to = static_cast<uint16_t*>(f.result[t.of]) + (int64_t)row0 * f.cols + col0;
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            if (col0 + j * 64 < f.cols) {
-              way.free_stage();
-              way.row16<BF16>(acc[2 * j], acc[2 * j + 1]);
-              way.send(f.out + of, way.stage, col0 + j * 64, row0);
-            }
+            way.send16<BF16>(acc[2 * j], acc[2 * j + 1], to + j * 64, f.cols, rows - row0, f.cols - col0 - j * 64);
         }
       } else {
         const int col0 = t.n * kHalf + half * 64;
-        const bool in = row0 < rows && col0 < f.cols;
+        const int down = rows - row0, across = f.cols - col0;  // what is left of the matrix
+        const int64_t at = (int64_t)row0 * f.cols + col0;
         if (col0 + 64 > f.cols) {  // columns past the end: 0 * inf has made NaN of them in a row with infinities
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -364,7 +354,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
             for (int k = 0; k < 32; ++k) acc[j][k] = col0 + (j & 1) * 32 + k < f.cols ? acc[j][k] : 0u;
         }
         if constexpr (EP == AGAIN) {
-          const uint4* from = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(f.dp) +
+          const uint4* from = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(f.o.dp) +
                                                               ((int64_t)row * f.cols + col0));
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
@@ -374,87 +364,69 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int j = c >> 2, k = (c & 3) * 4 + i;
-              const float2 d = BF16 ? make_float2(bf16lo(w[i]), bf16hi(w[i])) : make_float2(f16lo(w[i]), f16hi(w[i]));
-              const float2 g = pair_of(acc[j], k), s = logistic2<XF32>(g), xs = mul2(g, s);
-              const float2 one_s = fma2(s, both(-1.0f), both(1.0f));
-              const float2 du = mul2(d, xs);
-              set_pair(acc[j], k, mul2(mul2(d, pair_of(acc[2 + j], k)), fma2(xs, one_s, s)));
+              float2 dg, du;
+              slopes(pair16<BF16>(w[i]), pair_of(acc[j], k), pair_of(acc[2 + j], k), &dg, &du);
+              set_pair(acc[j], k, dg);
               set_pair(acc[2 + j], k, du);
             }
           }
-          if (in) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              way.free_stage();
-              way.row16<BF16>(acc[2 * j], acc[2 * j + 1]);
-              way.send(f.out + j, way.stage, col0, row0);
-            }
-          }
+          for (int j = 0; j < 2; ++j)
+            way.send16<BF16>(acc[2 * j], acc[2 * j + 1], static_cast<uint16_t*>(j ? f.o.du : f.o.dg) + at, f.cols, down, across);
         } else {
           const int tile = t.n;  // 128 columns are a tile of scales
-          if (f.keep16 && in) {
+          if (f.o.gate) {
+            const int64_t kept = (int64_t)row0 * f.o.ld + col0;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              way.free_stage();
-              way.row16<BF16>(acc[2 * j], acc[2 * j + 1]);
-              way.send(f.out + 1 + j, way.stage, col0, row0);
-            }
+            for (int j = 0; j < 2; ++j)
+              way.send16<BF16>(acc[2 * j], acc[2 * j + 1], static_cast<uint16_t*>(j ? f.o.up : f.o.gate) + kept, f.o.ld, down,
+                               across);
           }
-          if (f.ckpt) {
-            way.free_stage();
+          if (f.o.ckpt) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const uint32_t m = both_halves(max(amax32(acc[2 * j]), amax32(acc[2 * j + 1])), red + j * 2 * kHalf, half,
                                              in_cta, quad);
               float mul;
               const float scale = tile_scale(m, 448.0f, &mul);
-              if (half == 0 && row < rows) f.ckpt_scales[((int64_t)j * f.rows + row) * f.tiles + tile] = scale;
-              codes32(acc[2 * j], way.stage + j * 2048, lane, 0, m, mul, false, false);
-              codes32(acc[2 * j + 1], way.stage + j * 2048, lane, 2, m, mul, false, false);
-              if (in) way.send(f.out + 1 + j, way.stage + j * 2048, col0, row0);
+              if (half == 0 && row < rows) f.o.ckpt_scales[((int64_t)j * f.rows + row) * f.o.tiles + tile] = scale;
+              codes32(acc[2 * j], way, 0, m, mul, false, false);
+              codes32(acc[2 * j + 1], way, 2, m, mul, false, false);
+              way.send<64>(f.o.ckpt + (int64_t)j * f.rows * f.cols + at, f.cols, down, across);
             }
             named_barrier(1 + quad, 64);  // the slots have been read
           }
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float2 g = pair_of(acc[j], k);
-              set_pair(acc[j], k, mul2(mul2(g, logistic2<XF32>(g)), pair_of(acc[2 + j], k)));
-            }
+            for (int k = 0; k < 16; ++k) set_pair(acc[j], k, gated(pair_of(acc[j], k), pair_of(acc[2 + j], k)));
           if constexpr (EP == FWD16) {
-            if (in) {
-              way.free_stage();
-              way.row16<BF16>(acc[0], acc[1]);
-              way.send(f.out, way.stage, col0, row0);
-            }
+            way.send16<BF16>(acc[0], acc[1], static_cast<uint16_t*>(f.o.p) + at, f.cols, down, across);
           } else {
             uint32_t m[2] = {amax32(acc[0]), amax32(acc[1])};
             float mul[2];
-            if (f.mx) {
+            if (f.o.mx) {
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
                 uint32_t byte;
-                mx_scale(m[j], f.e5m2 ? 15u : 8u, &mul[j], &byte);
+                mx_scale(m[j], f.o.e5m2 ? 15u : 8u, &mul[j], &byte);
                 if (row < rows && col0 + j * 32 < f.cols)
-                  static_cast<uint8_t*>(f.p_scales)[(int64_t)row * f.per_row + (col0 >> 5) + j] = (uint8_t)byte;
+                  static_cast<uint8_t*>(f.o.p_scales)[(int64_t)row * f.o.per_row + (col0 >> 5) + j] = (uint8_t)byte;
               }
             } else {
               m[0] = m[1] = both_halves(max(m[0], m[1]), red, half, in_cta, quad);
-              const float scale = tile_scale(m[0], f.e5m2 ? 57344.0f : 448.0f, &mul[0]);
+              const float scale = tile_scale(m[0], f.o.e5m2 ? 57344.0f : 448.0f, &mul[0]);
               mul[1] = mul[0];
-              if (half == 0 && row < rows) static_cast<float*>(f.p_scales)[(int64_t)row * f.per_row + tile] = scale;
+              if (half == 0 && row < rows) static_cast<float*>(f.o.p_scales)[(int64_t)row * f.o.per_row + tile] = scale;
               named_barrier(1 + quad, 64);  // the slot has been read
             }
-            way.free_stage();
-            codes32(acc[0], way.stage, lane, 0, m[0], mul[0], f.e5m2, f.mx);
-            codes32(acc[1], way.stage, lane, 2, m[1], mul[1], f.e5m2, f.mx);
-            if (in) way.send(f.out, way.stage, col0, row0);
+            codes32(acc[0], way, 0, m[0], mul[0], f.o.e5m2, f.o.mx);
+            codes32(acc[1], way, 2, m[1], mul[1], f.o.e5m2, f.o.mx);
+            way.send<64>(static_cast<uint8_t*>(f.o.p) + at, f.cols, down, across);
           }
         }
       }
     }
-    if (lane == 0) store_wait_all();
   }
   if (!ok) atomicAdd(&g_ffn_wait_failures, 1u);
   tmem_fence_before();
@@ -514,23 +486,47 @@ mp_status launch(Ffn& f, cudaStream_t st) {
 
 bool type16(mp_dtype t) { return t == MP_F16 || t == MP_BF16; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-int32_t ceil_div(int64_t a, int64_t b) { return (int32_t)((a + b - 1) / b); }
-
-// A dense (or `pitch` elements a row) matrix of 16-bit elements, boxes of 64 x box_rows.
-bool map16(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t pitch, int box_rows) {
-  return encode_swizzled_map_2d(m, p, 2, rows, cols, pitch * 2, box_rows, 64);
-}
-bool map8(CUtensorMap* m, const void* p, int64_t rows, int64_t cols) {
-  return encode_swizzled_map_2d(m, p, 1, rows, cols, cols, 32, 64);
-}
-
 // Tiles, and the walk over them.
-void lay_out(Ffn& f, int tiles_m, int tiles_n, int splits) {
-  f.tiles_m = f.per_matrix = tiles_m;
-  f.tiles_n = tiles_n;
-  f.splits = splits;
-  f.items = tiles_m * tiles_n * splits;
-  f.group = 8;
+void lay_out(Ffn& f, int matrices, int rows_of_tiles, int tiles_n, int splits) {
+  f.matrices = matrices, f.splits = splits;
+  f.tiles_m = matrices * rows_of_tiles;
+  f.items = f.tiles_m * tiles_n * splits;
+  f.tiles = fast_div(f.tiles_m * tiles_n), f.band = fast_div(kBand * tiles_n);
+  f.last = fast_div(f.tiles_m % kBand ? f.tiles_m % kBand : kBand), f.per_matrix = fast_div(rows_of_tiles);
+}
+
+// Into how many parts a product of so many tiles and stages is split along its
+// contraction: one wave of pairs, where the tiles fill less than half of one;
+// four stages a part at least.  (More tiles would split with a remainder; what
+// that saves goes into writing and reading the parts.)
+int splits_of(int64_t tiles, int blocks) {
+  const int64_t pairs = sm_count() / 2;
+  int64_t s = tiles > 0 ? pairs / tiles : 1;
+  if (s > blocks / 4) s = blocks / 4;
+  if (s > 16) s = 16;
+  return s < 1 ? 1 : (int)s;
+}
+int64_t dx_tiles(int64_t rows, int64_t width) { return (int64_t)ceil_div(rows, 2 * kHalf) * ceil_div(width, 2 * kHalf); }
+int64_t dw_tiles(int64_t width, int64_t hidden) { return 2ll * ceil_div(hidden, 2 * kHalf) * ceil_div(width, 2 * kHalf); }
+int dx_splits(int64_t rows, int64_t width, int64_t hidden) {
+  return rows <= kFewRows ? 1 : splits_of(dx_tiles(rows, width), 2 * ceil_div(hidden, kBlockK));
+}
+int dw_splits(int64_t rows, int64_t width, int64_t hidden) {
+  return splits_of(dw_tiles(width, hidden), ceil_div(rows, kBlockK));
+}
+
+// A stored product and, where it is split, the joining of its parts.
+template <bool A_MN>
+mp_status multiply(bool bf16, Ffn& f, void* out0, void* out1, cudaStream_t st) {
+  f.result[0] = out0, f.result[1] = out1;
+  const mp_status s = bf16 ? launch<true, A_MN, true, STORE>(f, st) : launch<false, A_MN, true, STORE>(f, st);
+  if (s != MP_OK || f.splits == 1) return s;
+  const int64_t one = (int64_t)f.rows * f.cols, n = f.matrices * one;
+  const dim3 grid((unsigned)((n / 8 + 255) / 256));
+  launch_chained(bf16 ? k_ffn_join<true> : k_ffn_join<false>, grid, dim3(256), 0, st, (const float*)f.parts, f.splits, n,
+                 out0, out1, one);
+  note_launches(1);
+  return launch_status();
 }
 
 // Rows, columns and row lengths that both calls take.
@@ -545,23 +541,27 @@ bool pitch_ok(int64_t ld, int64_t cols, int64_t rows) {
 
 // Forms g and u (FWD16, FWD8, AGAIN).
 template <int EP>
-mp_status project(Ffn& f, mp_dtype t, const void* x, const void* w_gate, const void* w_up, int64_t rows, int64_t width,
-                  int64_t hidden, cudaStream_t st) {
+mp_status project(bool bf16, const void* x, const void* w_gate, const void* w_up, int64_t rows, int64_t width,
+                  int64_t hidden, const FfnOut& o, cudaStream_t st) {
+  if (rows <= kFewRows) return ffn_few_project(EP, bf16, x, w_gate, w_up, rows, width, hidden, o, st);
+  Ffn f;
   if (!map16(&f.a[0], x, rows, width, width, kHalf) || !map16(&f.b[0], w_gate, hidden, width, width, kHalf) ||
       !map16(&f.b[1], w_up, hidden, width, width, kHalf))
     return MP_ECUDA;
+  f.o = o;
   f.blocks = f.blocks0 = ceil_div(width, kBlockK);
   f.rows = (int32_t)rows, f.cols = (int32_t)hidden;
-  lay_out(f, ceil_div(rows, 2 * kHalf), ceil_div(hidden, kHalf), 1);
-  return t == MP_BF16 ? launch<true, false, false, EP>(f, st) : launch<false, false, false, EP>(f, st);
+  lay_out(f, 1, ceil_div(rows, 2 * kHalf), ceil_div(hidden, kHalf), 1);
+  return bf16 ? launch<true, false, false, EP>(f, st) : launch<false, false, false, EP>(f, st);
 }
 
 }  // namespace
 
-uint32_t ffn_wait_failures() {
+uint32_t ffn_wait_failures() {  // of both kernels
   uint32_t v = 0;
   if (cudaMemcpyFromSymbol(&v, g_ffn_wait_failures, sizeof(v)) != cudaSuccess) return 0xFFFFFFFFu;
-  return v;
+  const uint32_t w = ffn_few_wait_failures();
+  return v > UINT32_MAX - w ? UINT32_MAX : v + w;
 }
 
 }  // namespace mp
@@ -585,24 +585,16 @@ extern "C" MP_API mp_status linear_swiglu(const void* x, mp_dtype x_dtype, int64
   if (!aligned16(x) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(p) || !aligned16(gate) || !aligned16(up) ||
       !aligned16(ckpt) || !aligned4(ckpt_scales) || (fp8 && scale_block == 128 && !aligned4(p_scales)))
     return MP_EALIGN;
-  Ffn f;
-  f.e5m2 = p_dtype == MP_E5M2, f.mx = scale_block == 32;
-  f.keep16 = gate != nullptr, f.ckpt = ckpt != nullptr;
-  f.p_scales = p_scales, f.ckpt_scales = ckpt_scales;
-  f.tiles = ceil_div(hidden, 128);
-  f.per_row = f.mx ? (int32_t)(hidden / 32) : f.tiles;
-  bool ok = fp8 ? map8(&f.out[0], p, rows, hidden) : map16(&f.out[0], p, rows, hidden, hidden, 32);
-  if (gate) {
-    const int64_t pitch = rows > 1 ? ld : hidden;
-    ok = ok && map16(&f.out[1], gate, rows, hidden, pitch, 32) && map16(&f.out[2], up, rows, hidden, pitch, 32);
-  } else if (ckpt) {
-    ok = ok && map8(&f.out[1], ckpt, rows, hidden) &&
-         map8(&f.out[2], static_cast<uint8_t*>(ckpt) + rows * hidden, rows, hidden);
-  }
-  if (!ok) return MP_ECUDA;
+  FfnOut o = {};
+  o.p = p, o.p_scales = p_scales, o.e5m2 = p_dtype == MP_E5M2, o.mx = scale_block == 32;
+  o.tiles = ceil_div(hidden, 128);
+  o.per_row = o.mx ? (int32_t)(hidden / 32) : o.tiles;
+  o.gate = gate, o.up = up, o.ld = rows > 1 ? ld : hidden;
+  o.ckpt = static_cast<uint8_t*>(ckpt), o.ckpt_scales = ckpt_scales;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return fp8 ? project<FWD8>(f, x_dtype, x, w_gate, w_up, rows, width, hidden, st)
-             : project<FWD16>(f, x_dtype, x, w_gate, w_up, rows, width, hidden, st);
+  const bool bf16 = x_dtype == MP_BF16;
+  return fp8 ? project<FWD8>(bf16, x, w_gate, w_up, rows, width, hidden, o, st)
+             : project<FWD16>(bf16, x, w_gate, w_up, rows, width, hidden, o, st);
 }
 
 namespace mp {
@@ -617,7 +609,9 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 extern "C" MP_API size_t linear_swiglu_workspace_size(int64_t rows, int64_t width, int64_t hidden) {
   using namespace mp;
   if (rows <= 0 || width <= 0 || hidden <= 0 || !shape_ok(rows, width, hidden, 16)) return 0;
-  return up256((size_t)rows * hidden * 4);
+  const int64_t dx = dx_splits(rows, width, hidden), dw = dw_splits(rows, width, hidden);
+  const int64_t parts = dx > 1 ? dx * rows * width * 4 : 0, more = dw > 1 ? dw * 2 * hidden * width * 4 : 0;
+  return up256((size_t)rows * hidden * 4) + (size_t)(parts > more ? parts : more);
 }
 
 extern "C" MP_API mp_status linear_swiglu_backward(const void* dp, mp_dtype x_dtype, int64_t rows, int64_t width,
@@ -648,39 +642,40 @@ extern "C" MP_API mp_status linear_swiglu_backward(const void* dp, mp_dtype x_dt
   if (!d_workspace || workspace_bytes < linear_swiglu_workspace_size(rows, width, hidden)) return MP_EWORKSPACE;
   uint16_t* const dg = static_cast<uint16_t*>(d_workspace);
   uint16_t* const du = dg + rows * hidden;
+  float* const parts = reinterpret_cast<float*>(static_cast<unsigned char*>(d_workspace) + up256((size_t)rows * hidden * 4));
   const bool bf16 = x_dtype == MP_BF16;
   Ffn f;
+  f.parts = parts;
   if (gate || ckpt) {
     const mp_status s = swiglu_backward(dp, x_dtype, rows, hidden, gate, up, ld, ckpt, ckpt_scales, dg, du, hidden, stream);
     if (s != MP_OK) return s;
   } else {
-    f.dp = dp;
-    if (!map16(&f.out[0], dg, rows, hidden, hidden, 32) || !map16(&f.out[1], du, rows, hidden, hidden, 32)) return MP_ECUDA;
-    const mp_status s = project<AGAIN>(f, x_dtype, x, w_gate, w_up, rows, width, hidden, st);
+    FfnOut o = {};
+    o.dp = dp, o.dg = dg, o.du = du;
+    const mp_status s = project<AGAIN>(bf16, x, w_gate, w_up, rows, width, hidden, o, st);
     if (s != MP_OK) return s;
   }
-  if (dx) {
+  if (dx && rows <= kFewRows) {
+    const mp_status s = ffn_few_dx(bf16, dg, du, w_gate, w_up, rows, width, hidden, dx, st);
+    if (s != MP_OK) return s;
+  } else if (dx) {
     if (!map16(&f.a[0], dg, rows, hidden, hidden, kHalf) || !map16(&f.a[1], du, rows, hidden, hidden, kHalf) ||
-        !map16(&f.b[0], w_gate, hidden, width, width, 64) || !map16(&f.b[1], w_up, hidden, width, width, 64) ||
-        !map16(&f.out[0], dx, rows, width, width, 32))
+        !map16(&f.b[0], w_gate, hidden, width, width, 64) || !map16(&f.b[1], w_up, hidden, width, width, 64))
       return MP_ECUDA;
     f.blocks0 = ceil_div(hidden, kBlockK), f.blocks = 2 * f.blocks0;
     f.rows = (int32_t)rows, f.cols = (int32_t)width;
-    lay_out(f, ceil_div(rows, 2 * kHalf), ceil_div(width, 2 * kHalf), 1);
-    const mp_status s = bf16 ? launch<true, false, true, STORE>(f, st) : launch<false, false, true, STORE>(f, st);
+    lay_out(f, 1, ceil_div(rows, 2 * kHalf), ceil_div(width, 2 * kHalf), dx_splits(rows, width, hidden));
+    const mp_status s = multiply<false>(bf16, f, dx, nullptr, st);
     if (s != MP_OK) return s;
   }
   if (dw_gate) {
     if (!map16(&f.a[0], dg, rows, hidden, hidden, 64) || !map16(&f.a[1], du, rows, hidden, hidden, 64) ||
-        !map16(&f.b[0], x, rows, width, width, 64) || !map16(&f.out[0], dw_gate, hidden, width, width, 32) ||
-        !map16(&f.out[1], dw_up, hidden, width, width, 32))
+        !map16(&f.b[0], x, rows, width, width, 64))
       return MP_ECUDA;
     f.blocks0 = f.blocks = ceil_div(rows, kBlockK);
     f.rows = (int32_t)hidden, f.cols = (int32_t)width;
-    const int per = ceil_div(hidden, 2 * kHalf);
-    lay_out(f, 2 * per, ceil_div(width, 2 * kHalf), 1);
-    f.per_matrix = per;
-    const mp_status s = bf16 ? launch<true, true, true, STORE>(f, st) : launch<false, true, true, STORE>(f, st);
+    lay_out(f, 2, ceil_div(hidden, 2 * kHalf), ceil_div(width, 2 * kHalf), dw_splits(rows, width, hidden));
+    const mp_status s = multiply<true>(bf16, f, dw_gate, dw_up, st);
     if (s != MP_OK) return s;
   }
   return MP_OK;

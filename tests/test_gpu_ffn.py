@@ -7,7 +7,8 @@ from . import ffn_util as U
 pytestmark = pytest.mark.gpu
 BF16, F16 = torch.bfloat16, torch.float16
 SIZES = [(1, 16, 16), (1, 4096, 512), (3, 64, 128), (17, 80, 144), (37, 1040, 272), (64, 512, 1456), (129, 48, 400),
-         (256, 256, 688), (257, 5120, 96), (301, 1040, 1456), (513, 592, 16), (4113, 32, 48)]
+         (256, 256, 688), (257, 5120, 96), (301, 1040, 1456), (513, 592, 16), (4113, 32, 48),
+         (2, 8192, 160), (16, 1552, 4112), (33, 272, 128), (100, 4096, 528), (128, 2064, 256)]
 
 
 @pytest.fixture
