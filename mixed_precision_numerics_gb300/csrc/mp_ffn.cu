@@ -47,15 +47,50 @@ constexpr int kSmem = kStages * kStageBytes + kResultWarps * kStagingBytes + 2 *
 static_assert(kSmem <= 232448, "227 KB a CTA");
 static_assert((2 * kStages + 4) * 8 + 8 <= kBarrierBytes, "barriers and the TMEM address");
 
-struct Ffn {
+// One product in tiles.
+struct Product {
   CUtensorMap a[2], b[2];
   int32_t items, tiles_m;  // work items = tiles * splits
   FastDiv tiles, band, last, per_matrix;  // tiles of a split, of a band; rows of tiles in the last band, in a matrix
-  int32_t blocks0, blocks, splits, matrices;  // blocks of the contraction in the first operand pair, and in all
-  int32_t rows, cols;                      // of a result matrix
+  int32_t blocks0, blocks, splits, matrices;  // stages of the contraction in the first operand pair, and in all
+  int32_t rows, cols;      // of a result matrix
+  bool a_mn;               // STORE: A is MN-major
+  void* result[2];         // STORE: the matrices
+  float* parts;            // STORE of a split product: [splits][matrices][rows][cols]
+};
+
+// FWD, AGAIN: one product.  STORE: dx's and then the weights' gradients', or one of them.
+struct Ffn {
+  Product p[2];
+  int32_t long_pairs, ahead;  // see Walk
   FfnOut o;
-  void* result[2];  // STORE: the matrices
-  float* parts;     // STORE of a split product: [splits][matrices][rows][cols]
+};
+
+// The order in which a pair takes items: the first product's in turn with the
+// other pairs, then the second's.  The first `long_pairs` pairs have one more
+// of the first product's; the others make up for it with `ahead` of the second
+// product's before all take turns again.
+struct Walk {
+  int32_t i0, i1, taken, pair, pairs;
+  int which, item;
+  __device__ __forceinline__ Walk(const Ffn& f) {
+    pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+    i0 = pair, taken = pair < f.long_pairs ? f.ahead : 0;
+    i1 = f.ahead * (pairs - f.long_pairs) + (pair < f.long_pairs ? pair + pairs : pair) - f.long_pairs;
+  }
+  __device__ __forceinline__ bool next(const Ffn& f) {
+    which = i0 >= f.p[0].items;
+    if (!which) {
+      item = i0, i0 += pairs;
+      return true;
+    }
+    if (taken < f.ahead) {
+      item = pair - f.long_pairs + taken++ * (pairs - f.long_pairs);
+      return true;
+    }
+    item = i1, i1 += pairs;
+    return item < f.p[1].items;
+  }
 };
 
 __device__ unsigned int g_ffn_wait_failures;  // bounded waits that gave up (read by mp_wait_failures)
@@ -67,7 +102,7 @@ struct Tile {
 // that those in flight together share operands in L2; all tiles of a split
 // first.  (Every role does this for every tile, one thread after another: with
 // plain divisions the tiles of short contractions waited for it.)
-__device__ __forceinline__ Tile tile_of(const Ffn& f, uint32_t item) {
+__device__ __forceinline__ Tile tile_of(const Product& f, uint32_t item) {
   Tile t;
   t.split = 0, t.k0 = 0, t.k1 = f.blocks;
   if (f.splits > 1) {
@@ -174,7 +209,7 @@ __device__ __forceinline__ uint32_t both_halves(uint32_t m, uint32_t* slot, int 
   return max(m, slot[(half ^ 1) * kHalf + row]);
 }
 
-template <bool BF16, bool A_MN, bool B_MN, int EP>
+template <bool BF16, int EP>
 __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn f) {
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* const staging = smem + kStages * kStageBytes;
@@ -184,7 +219,6 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
   uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(tempty + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
-  const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
 
   if (warp == kResultWarps && lane == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
@@ -210,29 +244,31 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
       const bool is_b = warp != kResultWarps;
       const uint32_t bars = map_rank(smem_u32(full), 0), tiles = smem_u32(smem) + (is_b ? kOperandBytes : 0);
       uint32_t it = 0;
-      for (int item = pair; item < f.items && ok; item += pairs) {
-        const Tile t = tile_of(f, item);
+      for (Walk w(f); ok && w.next(f);) {
+        const Product& q = f.p[w.which];
+        const Tile t = tile_of(q, w.item);
+        const bool mn = EP == STORE && (is_b || q.a_mn);
         int at;                             // the first of the tile's 128 rows of this operand in this CTA
         const CUtensorMap *map0, *map1;     // of the first operand pair and of the second
         if (!is_b) {
           at = t.m * 2 * kHalf + rank * kHalf;
-          map0 = f.a + t.of, map1 = f.a + 1;
+          map0 = q.a + t.of, map1 = q.a + 1;
         } else if (EP == STORE) {
           at = t.n * 2 * kHalf + rank * kHalf;
-          map0 = f.b, map1 = f.b + 1;
+          map0 = q.b, map1 = q.b + 1;
         } else {
           at = t.n * kHalf;
-          map0 = map1 = f.b + rank;
+          map0 = map1 = q.b + rank;
         }
         for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
           const int s = it % kStages;
           if (!(ok = mbar_wait_bounded(empty + s, ((it / kStages) & 1) ^ 1))) break;
           if (rank == 0 && !is_b) mbar_arrive_expect_tx(full + s, 2 * kStageBytes);
           const uint32_t bar = bars + s * 8, to = tiles + s * kStageBytes;
-          const bool second = kb >= f.blocks0;
-          const int k = (second ? kb - f.blocks0 : kb) * kBlockK;
+          const bool second = kb >= q.blocks0;
+          const int k = (second ? kb - q.blocks0 : kb) * kBlockK;
           const CUtensorMap* map = second ? map1 : map0;
-          if (is_b ? B_MN : A_MN) {
+          if (mn) {
             tma_load_2d_pair(to, map, at, k, bar);
             tma_load_2d_pair(to + kMnBlockBytes, map, at + 64, k, bar);
           } else {
@@ -244,10 +280,15 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
       for (uint32_t j = it > kStages ? it - kStages : 0; j < it && ok; ++j)
         ok = mbar_wait_bounded(empty + j % kStages, (j / kStages) & 1);
     } else if (warp == kResultWarps + 1 && lane == 0 && rank == 0) {  // matrix instructions
-      constexpr uint32_t idesc = instr_desc<BF16, A_MN, B_MN>(2 * kHalf, 2 * kHalf);
       uint32_t it = 0, chunk = 0;
-      for (int item = pair; item < f.items && ok; item += pairs) {
-        const Tile t = tile_of(f, item);
+      for (Walk w(f); ok && w.next(f);) {
+        const Product& q = f.p[w.which];
+        const Tile t = tile_of(q, w.item);
+        constexpr bool B_MN = EP == STORE;
+        const bool a_mn = B_MN && q.a_mn;
+        const uint32_t idesc = a_mn ? instr_desc<BF16, true, B_MN>(2 * kHalf, 2 * kHalf)
+                                    : instr_desc<BF16, false, B_MN>(2 * kHalf, 2 * kHalf);
+        const uint32_t step = a_mn ? kDescStep<true> : kDescStep<false>;
         for (int k0 = t.k0; k0 < t.k1 && ok; k0 += kRun<EP>, ++chunk) {
           const uint32_t b = chunk & 1, d = tmem + b * 2 * kHalf;
           if (!(ok = mbar_wait_bounded(tempty + b, ((chunk >> 1) & 1) ^ 1))) break;
@@ -258,10 +299,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
             if (!(ok = mbar_wait_bounded(full + s, (it / kStages) & 1))) break;
             tmem_fence_after();
             const uint32_t pa = smem_u32(smem + s * kStageBytes);
-            const uint64_t da = operand_desc<A_MN>(pa), db = operand_desc<B_MN>(pa + kOperandBytes);
+            const uint64_t da = a_mn ? operand_desc<true>(pa) : operand_desc<false>(pa);
+            const uint64_t db = operand_desc<B_MN>(pa + kOperandBytes);
 #pragma unroll
             for (int j = 0; j < kBlockK / 16; ++j)
-              mma_f16<2>(d, da + j * kDescStep<A_MN>, db + j * kDescStep<B_MN>, idesc, kb != k0 || j != 0);
+              mma_f16<2>(d, da + j * step, db + j * kDescStep<B_MN>, idesc, kb != k0 || j != 0);
             mma_commit<2>(empty + s);
           }
           if (ok) mma_commit<2>(tfull + b);
@@ -275,8 +317,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
     const Way way{smem_u32(staging + warp * kStagingBytes), lane};
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     uint32_t chunk = 0;
-    for (int item = pair; item < f.items; item += pairs) {
-      const Tile t = tile_of(f, item);
+    for (Walk w(f); w.next(f);) {
+      const Product& q = f.p[w.which];
+      const Tile t = tile_of(q, w.item);
       const int row0 = t.m * 2 * kHalf + rank * kHalf + quad * 32, row = row0 + lane;
       // FWD, AGAIN: acc[0..1] are 64 columns of g, acc[2..3] of u.  STORE: 128 columns.
       uint32_t acc[4][32];
@@ -323,44 +366,44 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
         }
         run_read();
       }
-      const int rows = ok ? f.rows : 0;
+      const int rows = ok ? q.rows : 0;
 
       if constexpr (EP == STORE) {
         const int col0 = t.n * 2 * kHalf + half * 128;
-        if (f.splits > 1) {
-          float* const to = f.parts + ((int64_t)t.split * f.matrices + t.of) * f.rows * f.cols +
-                            (int64_t)row0 * f.cols + col0;
+        if (q.splits > 1) {
+          float* const to = q.parts + ((int64_t)t.split * q.matrices + t.of) * q.rows * q.cols +
+                            (int64_t)row0 * q.cols + col0;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
 #pragma unroll
             for (int c = 0; c < 8; ++c)
               way.put128(c, make_uint4(acc[j][4 * c], acc[j][4 * c + 1], acc[j][4 * c + 2], acc[j][4 * c + 3]));
-            way.send<128>(to + j * 32, (int64_t)f.cols * 4, rows - row0, (f.cols - col0 - j * 32) * 4);
+            way.send<128>(to + j * 32, (int64_t)q.cols * 4, rows - row0, (q.cols - col0 - j * 32) * 4);
           }
         } else {
-          uint16_t* const to = static_cast<uint16_t*>(f.result[t.of]) + (int64_t)row0 * f.cols + col0;
+          uint16_t* const to = static_cast<uint16_t*>(q.result[t.of]) + (int64_t)row0 * q.cols + col0;
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            way.send16<BF16>(acc[2 * j], acc[2 * j + 1], to + j * 64, f.cols, rows - row0, f.cols - col0 - j * 64);
+            way.send16<BF16>(acc[2 * j], acc[2 * j + 1], to + j * 64, q.cols, rows - row0, q.cols - col0 - j * 64);
         }
       } else {
         const int col0 = t.n * kHalf + half * 64;
-        const int down = rows - row0, across = f.cols - col0;  // what is left of the matrix
-        const int64_t at = (int64_t)row0 * f.cols + col0;
-        if (col0 + 64 > f.cols) {  // columns past the end: 0 * inf has made NaN of them in a row with infinities
+        const int down = rows - row0, across = q.cols - col0;  // what is left of the matrix
+        const int64_t at = (int64_t)row0 * q.cols + col0;
+        if (col0 + 64 > q.cols) {  // columns past the end: 0 * inf has made NaN of them in a row with infinities
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int k = 0; k < 32; ++k) acc[j][k] = col0 + (j & 1) * 32 + k < f.cols ? acc[j][k] : 0u;
+            for (int k = 0; k < 32; ++k) acc[j][k] = col0 + (j & 1) * 32 + k < q.cols ? acc[j][k] : 0u;
         }
         if constexpr (EP == AGAIN) {
           const uint4* from = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(f.o.dp) +
-                                                              ((int64_t)row * f.cols + col0));
+                                                              ((int64_t)row * q.cols + col0));
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            uint4 q = make_uint4(0u, 0u, 0u, 0u);
-            if (row < rows && col0 + c * 8 < f.cols) q = ld_plain(from + c);
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (row < rows && col0 + c * 8 < q.cols) v = ld_plain(from + c);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int j = c >> 2, k = (c & 3) * 4 + i;
@@ -372,7 +415,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
           }
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            way.send16<BF16>(acc[2 * j], acc[2 * j + 1], static_cast<uint16_t*>(j ? f.o.du : f.o.dg) + at, f.cols, down, across);
+            way.send16<BF16>(acc[2 * j], acc[2 * j + 1], static_cast<uint16_t*>(j ? f.o.du : f.o.dg) + at, q.cols, down, across);
         } else {
           const int tile = t.n;  // 128 columns are a tile of scales
           if (f.o.gate) {
@@ -389,10 +432,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
                                              in_cta, quad);
               float mul;
               const float scale = tile_scale(m, 448.0f, &mul);
-              if (half == 0 && row < rows) f.o.ckpt_scales[((int64_t)j * f.rows + row) * f.o.tiles + tile] = scale;
+              if (half == 0 && row < rows) f.o.ckpt_scales[((int64_t)j * q.rows + row) * f.o.tiles + tile] = scale;
               codes32(acc[2 * j], way, 0, m, mul, false, false);
               codes32(acc[2 * j + 1], way, 2, m, mul, false, false);
-              way.send<64>(f.o.ckpt + (int64_t)j * f.rows * f.cols + at, f.cols, down, across);
+              way.send<64>(f.o.ckpt + (int64_t)j * q.rows * q.cols + at, q.cols, down, across);
             }
             named_barrier(1 + quad, 64);  // the slots have been read
           }
@@ -401,7 +444,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
 #pragma unroll
             for (int k = 0; k < 16; ++k) set_pair(acc[j], k, gated(pair_of(acc[j], k), pair_of(acc[2 + j], k)));
           if constexpr (EP == FWD16) {
-            way.send16<BF16>(acc[0], acc[1], static_cast<uint16_t*>(f.o.p) + at, f.cols, down, across);
+            way.send16<BF16>(acc[0], acc[1], static_cast<uint16_t*>(f.o.p) + at, q.cols, down, across);
           } else {
             uint32_t m[2] = {amax32(acc[0]), amax32(acc[1])};
             float mul[2];
@@ -410,7 +453,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
               for (int j = 0; j < 2; ++j) {
                 uint32_t byte;
                 mx_scale(m[j], f.o.e5m2 ? 15u : 8u, &mul[j], &byte);
-                if (row < rows && col0 + j * 32 < f.cols)
+                if (row < rows && col0 + j * 32 < q.cols)
                   static_cast<uint8_t*>(f.o.p_scales)[(int64_t)row * f.o.per_row + (col0 >> 5) + j] = (uint8_t)byte;
               }
             } else {
@@ -422,7 +465,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
             }
             codes32(acc[0], way, 0, m[0], mul[0], f.o.e5m2, f.o.mx);
             codes32(acc[1], way, 2, m[1], mul[1], f.o.e5m2, f.o.mx);
-            way.send<64>(static_cast<uint8_t*>(f.o.p) + at, f.cols, down, across);
+            way.send<64>(static_cast<uint8_t*>(f.o.p) + at, q.cols, down, across);
           }
         }
       }
@@ -436,41 +479,66 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
   if (warp == kResultWarps + 1) tmem_free<2>(tmem, kTmemColumns);
 }
 
-// Adds the parts of a product split along its contraction, in order, and
-// rounds once.  One thread: 8 elements.
+// Adds the parts of up to two products split along their contraction, in order,
+// and rounds once.  One thread: 8 elements.
+struct Join {
+  const float* parts[2];
+  int32_t splits[2];
+  int64_t n[2], one[2];  // elements of all matrices of a product, and of one
+  void* out[2][2];
+  unsigned first;        // CTAs of the first
+};
 template <bool BF16>
-__global__ __launch_bounds__(256) void k_ffn_join(const float* parts, int splits, int64_t n, void* out0, void* out1,
-                                                  int64_t n0) {
+__global__ __launch_bounds__(256) void k_ffn_join(const __grid_constant__ Join f) {
   chain_wait();
   chain_release();
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  const int w = blockIdx.x >= f.first;
+  const int64_t i = ((int64_t)(blockIdx.x - (w ? f.first : 0)) * 256 + threadIdx.x) * 8, n = f.n[w], one = f.one[w];
   if (i >= n) return;
   float2 v[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) v[j] = make_float2(0.0f, 0.0f);
-  for (int s = 0; s < splits; ++s) {
-    const float4* p = reinterpret_cast<const float4*>(parts + s * n + i);
+#pragma unroll 4
+  for (int s = 0; s < f.splits[w]; ++s) {
+    const float4* p = reinterpret_cast<const float4*>(f.parts[w] + s * n + i);
     const float4 a = __ldcg(p), b = __ldcg(p + 1);
     v[0] = add2(v[0], make_float2(a.x, a.y)), v[1] = add2(v[1], make_float2(a.z, a.w));
     v[2] = add2(v[2], make_float2(b.x, b.y)), v[3] = add2(v[3], make_float2(b.z, b.w));
   }
-  uint16_t* to = i < n0 ? static_cast<uint16_t*>(out0) + i : static_cast<uint16_t*>(out1) + (i - n0);
+  uint16_t* to = i < one ? static_cast<uint16_t*>(f.out[w][0]) + i : static_cast<uint16_t*>(f.out[w][1]) + (i - one);
   *reinterpret_cast<uint4*>(to) = make_uint4(pack16<BF16>(v[0]), pack16<BF16>(v[1]), pack16<BF16>(v[2]), pack16<BF16>(v[3]));
 }
 
-template <bool BF16, bool A_MN, bool B_MN, int EP>
+// What a tile costs, in stages: a short one waits for its results' way out.
+int64_t cost_of(int blocks) { return blocks > 10 ? blocks : 10; }
+
+// Evens out what the pairs have to do (Walk): those without the last turn's
+// item of the first product take as many stages of the second product ahead.
+void share(Ffn& f, int pairs) {
+  const Product &a = f.p[0], &b = f.p[1];
+  f.long_pairs = a.items % pairs, f.ahead = 0;
+  const int others = pairs - f.long_pairs;
+  if (f.long_pairs == 0 || b.items == 0) return;
+  const int64_t one = cost_of(b.blocks / b.splits);
+  const int longer = (int)((cost_of(a.blocks / a.splits) + one / 2) / one);
+  f.ahead = longer < b.items / others ? longer : b.items / others;
+}
+
+template <bool BF16, int EP>
 mp_status launch(Ffn& f, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  const auto kernel = k_ffn<BF16, A_MN, B_MN, EP>;
+  const auto kernel = k_ffn<BF16, EP>;
   if (!smem_opt_in(kernel, kSmem, done)) return MP_ECUDA;
-  const int most = sm_count() / 2;
+  const int64_t items = (int64_t)f.p[0].items + f.p[1].items, most = sm_count() / 2;
+  const int pairs = (int)(items < most ? items : most);
+  share(f, pairs);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * (f.items < most ? f.items : most));
+  cfg.gridDim = dim3(2 * pairs);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
@@ -487,7 +555,7 @@ mp_status launch(Ffn& f, cudaStream_t st) {
 bool type16(mp_dtype t) { return t == MP_F16 || t == MP_BF16; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 // Tiles, and the walk over them.
-void lay_out(Ffn& f, int matrices, int rows_of_tiles, int tiles_n, int splits) {
+void lay_out(Product& f, int matrices, int rows_of_tiles, int tiles_n, int splits) {
   f.matrices = matrices, f.splits = splits;
   f.tiles_m = matrices * rows_of_tiles;
   f.items = f.tiles_m * tiles_n * splits;
@@ -495,36 +563,56 @@ void lay_out(Ffn& f, int matrices, int rows_of_tiles, int tiles_n, int splits) {
   f.last = fast_div(f.tiles_m % kBand ? f.tiles_m % kBand : kBand), f.per_matrix = fast_div(rows_of_tiles);
 }
 
-// Into how many parts a product of so many tiles and stages is split along its
-// contraction: one wave of pairs, where the tiles fill less than half of one;
-// four stages a part at least.  (More tiles would split with a remainder; what
-// that saves goes into writing and reading the parts.)
-int splits_of(int64_t tiles, int blocks) {
-  const int64_t pairs = sm_count() / 2;
-  int64_t s = tiles > 0 ? pairs / tiles : 1;
+// The gradients' products: tiles and stages of the contraction of dx (none up to
+// kFewRows rows, which have a kernel of their own) and of the weights' gradients,
+// and into how many parts each is split along its contraction.  With all pairs
+// at work on both products each would have `even` stages to do; a tile longer
+// than that by a quarter or more is split into parts of at most about that length,
+// of four stages at least, if that saves more than the parts' way through memory
+// costs (16 stages take 4 us).  Whichever gradients are asked for, the parts are
+// these, so that results do not depend on that.
+struct Plan {
+  int64_t dx_tiles, dw_tiles;
+  int dx_blocks, dw_blocks, dx_splits, dw_splits;
+  size_t dx_parts, dw_parts;  // bytes
+};
+int splits_of(int64_t tiles, int blocks, int64_t even) {
+  int64_t s = blocks / even;
+  if (s == 1 && blocks > even + even / 4) s = 2;
   if (s > blocks / 4) s = blocks / 4;
-  if (s > 16) s = 16;
-  return s < 1 ? 1 : (int)s;
+  return s < 2 || tiles == 0 || blocks - blocks / s < 16 ? 1 : s < 16 ? (int)s : 16;
 }
-int64_t dx_tiles(int64_t rows, int64_t width) { return (int64_t)ceil_div(rows, 2 * kHalf) * ceil_div(width, 2 * kHalf); }
-int64_t dw_tiles(int64_t width, int64_t hidden) { return 2ll * ceil_div(hidden, 2 * kHalf) * ceil_div(width, 2 * kHalf); }
-int dx_splits(int64_t rows, int64_t width, int64_t hidden) {
-  return rows <= kFewRows ? 1 : splits_of(dx_tiles(rows, width), 2 * ceil_div(hidden, kBlockK));
-}
-int dw_splits(int64_t rows, int64_t width, int64_t hidden) {
-  return splits_of(dw_tiles(width, hidden), ceil_div(rows, kBlockK));
+Plan plan_of(int64_t rows, int64_t width, int64_t hidden) {
+  Plan p;
+  const int64_t tiles_n = ceil_div(width, 2 * kHalf);
+  p.dx_tiles = rows <= kFewRows ? 0 : ceil_div(rows, 2 * kHalf) * tiles_n;
+  p.dw_tiles = 2 * ceil_div(hidden, 2 * kHalf) * tiles_n;
+  p.dx_blocks = 2 * ceil_div(hidden, kBlockK), p.dw_blocks = ceil_div(rows, kBlockK);
+  const int64_t pairs = sm_count() / 2 < 1 ? 1 : sm_count() / 2;
+  const int64_t even = (p.dx_tiles * cost_of(p.dx_blocks) + p.dw_tiles * cost_of(p.dw_blocks) + pairs - 1) / pairs;
+  p.dx_splits = splits_of(p.dx_tiles, p.dx_blocks, even), p.dw_splits = splits_of(p.dw_tiles, p.dw_blocks, even);
+  p.dx_parts = p.dx_splits > 1 ? (size_t)p.dx_splits * rows * width * 4 : 0;
+  p.dw_parts = p.dw_splits > 1 ? (size_t)p.dw_splits * 2 * hidden * width * 4 : 0;
+  return p;
 }
 
-// A stored product and, where it is split, the joining of its parts.
-template <bool A_MN>
-mp_status multiply(bool bf16, Ffn& f, void* out0, void* out1, cudaStream_t st) {
-  f.result[0] = out0, f.result[1] = out1;
-  const mp_status s = bf16 ? launch<true, A_MN, true, STORE>(f, st) : launch<false, A_MN, true, STORE>(f, st);
-  if (s != MP_OK || f.splits == 1) return s;
-  const int64_t one = (int64_t)f.rows * f.cols, n = f.matrices * one;
-  const dim3 grid((unsigned)((n / 8 + 255) / 256));
-  launch_chained(bf16 ? k_ffn_join<true> : k_ffn_join<false>, grid, dim3(256), 0, st, (const float*)f.parts, f.splits, n,
-                 out0, out1, one);
+// The products of f, and the joining of those that are split.
+mp_status multiply(bool bf16, Ffn& f, cudaStream_t st) {
+  const mp_status s = bf16 ? launch<true, STORE>(f, st) : launch<false, STORE>(f, st);
+  if (s != MP_OK) return s;
+  Join j = {};
+  unsigned ctas[2] = {0, 0};
+  for (int w = 0; w < 2; ++w) {
+    const Product& q = f.p[w];
+    if (q.items == 0 || q.splits == 1) continue;
+    j.parts[w] = q.parts, j.splits[w] = q.splits;
+    j.one[w] = (int64_t)q.rows * q.cols, j.n[w] = q.matrices * j.one[w];
+    j.out[w][0] = q.result[0], j.out[w][1] = q.result[1];
+    ctas[w] = (unsigned)((j.n[w] / 8 + 255) / 256);
+  }
+  if (ctas[0] + ctas[1] == 0) return MP_OK;
+  j.first = ctas[0];
+  launch_chained(bf16 ? k_ffn_join<true> : k_ffn_join<false>, dim3(ctas[0] + ctas[1]), dim3(256), 0, st, j);
   note_launches(1);
   return launch_status();
 }
@@ -544,15 +632,16 @@ template <int EP>
 mp_status project(bool bf16, const void* x, const void* w_gate, const void* w_up, int64_t rows, int64_t width,
                   int64_t hidden, const FfnOut& o, cudaStream_t st) {
   if (rows <= kFewRows) return ffn_few_project(EP, bf16, x, w_gate, w_up, rows, width, hidden, o, st);
-  Ffn f;
-  if (!map16(&f.a[0], x, rows, width, width, kHalf) || !map16(&f.b[0], w_gate, hidden, width, width, kHalf) ||
-      !map16(&f.b[1], w_up, hidden, width, width, kHalf))
+  Ffn f = {};
+  Product& q = f.p[0];
+  if (!map16(&q.a[0], x, rows, width, width, kHalf) || !map16(&q.b[0], w_gate, hidden, width, width, kHalf) ||
+      !map16(&q.b[1], w_up, hidden, width, width, kHalf))
     return MP_ECUDA;
   f.o = o;
-  f.blocks = f.blocks0 = ceil_div(width, kBlockK);
-  f.rows = (int32_t)rows, f.cols = (int32_t)hidden;
-  lay_out(f, 1, ceil_div(rows, 2 * kHalf), ceil_div(hidden, kHalf), 1);
-  return bf16 ? launch<true, false, false, EP>(f, st) : launch<false, false, false, EP>(f, st);
+  q.blocks = q.blocks0 = ceil_div(width, kBlockK);
+  q.rows = (int32_t)rows, q.cols = (int32_t)hidden;
+  lay_out(q, 1, ceil_div(rows, 2 * kHalf), ceil_div(hidden, kHalf), 1);
+  return bf16 ? launch<true, EP>(f, st) : launch<false, EP>(f, st);
 }
 
 }  // namespace
@@ -609,9 +698,8 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 extern "C" MP_API size_t linear_swiglu_workspace_size(int64_t rows, int64_t width, int64_t hidden) {
   using namespace mp;
   if (rows <= 0 || width <= 0 || hidden <= 0 || !shape_ok(rows, width, hidden, 16)) return 0;
-  const int64_t dx = dx_splits(rows, width, hidden), dw = dw_splits(rows, width, hidden);
-  const int64_t parts = dx > 1 ? dx * rows * width * 4 : 0, more = dw > 1 ? dw * 2 * hidden * width * 4 : 0;
-  return up256((size_t)rows * hidden * 4) + (size_t)(parts > more ? parts : more);
+  const Plan p = plan_of(rows, width, hidden);
+  return up256((size_t)rows * hidden * 4) + up256(p.dx_parts) + p.dw_parts;
 }
 
 extern "C" MP_API mp_status linear_swiglu_backward(const void* dp, mp_dtype x_dtype, int64_t rows, int64_t width,
@@ -642,10 +730,8 @@ extern "C" MP_API mp_status linear_swiglu_backward(const void* dp, mp_dtype x_dt
   if (!d_workspace || workspace_bytes < linear_swiglu_workspace_size(rows, width, hidden)) return MP_EWORKSPACE;
   uint16_t* const dg = static_cast<uint16_t*>(d_workspace);
   uint16_t* const du = dg + rows * hidden;
-  float* const parts = reinterpret_cast<float*>(static_cast<unsigned char*>(d_workspace) + up256((size_t)rows * hidden * 4));
+  unsigned char* const parts = static_cast<unsigned char*>(d_workspace) + up256((size_t)rows * hidden * 4);
   const bool bf16 = x_dtype == MP_BF16;
-  Ffn f;
-  f.parts = parts;
   if (gate || ckpt) {
     const mp_status s = swiglu_backward(dp, x_dtype, rows, hidden, gate, up, ld, ckpt, ckpt_scales, dg, du, hidden, stream);
     if (s != MP_OK) return s;
@@ -657,26 +743,29 @@ extern "C" MP_API mp_status linear_swiglu_backward(const void* dp, mp_dtype x_dt
   }
   if (dx && rows <= kFewRows) {
     const mp_status s = ffn_few_dx(bf16, dg, du, w_gate, w_up, rows, width, hidden, dx, st);
-    if (s != MP_OK) return s;
-  } else if (dx) {
-    if (!map16(&f.a[0], dg, rows, hidden, hidden, kHalf) || !map16(&f.a[1], du, rows, hidden, hidden, kHalf) ||
-        !map16(&f.b[0], w_gate, hidden, width, width, 64) || !map16(&f.b[1], w_up, hidden, width, width, 64))
+    if (s != MP_OK || !dw_gate) return s;
+  }
+  const Plan plan = plan_of(rows, width, hidden);
+  Ffn f = {};
+  if (dx && rows > kFewRows) {
+    Product& q = f.p[0];
+    if (!map16(&q.a[0], dg, rows, hidden, hidden, kHalf) || !map16(&q.a[1], du, rows, hidden, hidden, kHalf) ||
+        !map16(&q.b[0], w_gate, hidden, width, width, 64) || !map16(&q.b[1], w_up, hidden, width, width, 64))
       return MP_ECUDA;
-    f.blocks0 = ceil_div(hidden, kBlockK), f.blocks = 2 * f.blocks0;
-    f.rows = (int32_t)rows, f.cols = (int32_t)width;
-    lay_out(f, 1, ceil_div(rows, 2 * kHalf), ceil_div(width, 2 * kHalf), dx_splits(rows, width, hidden));
-    const mp_status s = multiply<false>(bf16, f, dx, nullptr, st);
-    if (s != MP_OK) return s;
+    q.blocks0 = plan.dx_blocks / 2, q.blocks = plan.dx_blocks;
+    q.rows = (int32_t)rows, q.cols = (int32_t)width;
+    q.result[0] = dx, q.parts = reinterpret_cast<float*>(parts);
+    lay_out(q, 1, ceil_div(rows, 2 * kHalf), ceil_div(width, 2 * kHalf), plan.dx_splits);
   }
   if (dw_gate) {
-    if (!map16(&f.a[0], dg, rows, hidden, hidden, 64) || !map16(&f.a[1], du, rows, hidden, hidden, 64) ||
-        !map16(&f.b[0], x, rows, width, width, 64))
+    Product& q = f.p[1];
+    if (!map16(&q.a[0], dg, rows, hidden, hidden, 64) || !map16(&q.a[1], du, rows, hidden, hidden, 64) ||
+        !map16(&q.b[0], x, rows, width, width, 64))
       return MP_ECUDA;
-    f.blocks0 = f.blocks = ceil_div(rows, kBlockK);
-    f.rows = (int32_t)hidden, f.cols = (int32_t)width;
-    lay_out(f, 2, ceil_div(hidden, 2 * kHalf), ceil_div(width, 2 * kHalf), dw_splits(rows, width, hidden));
-    const mp_status s = multiply<true>(bf16, f, dw_gate, dw_up, st);
-    if (s != MP_OK) return s;
+    q.blocks0 = q.blocks = plan.dw_blocks, q.a_mn = true;
+    q.rows = (int32_t)hidden, q.cols = (int32_t)width;
+    q.result[0] = dw_gate, q.result[1] = dw_up, q.parts = reinterpret_cast<float*>(parts + up256(plan.dx_parts));
+    lay_out(q, 2, ceil_div(hidden, 2 * kHalf), ceil_div(width, 2 * kHalf), plan.dw_splits);
   }
-  return MP_OK;
+  return multiply(bf16, f, st);
 }
