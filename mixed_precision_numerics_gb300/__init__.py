@@ -523,7 +523,8 @@ def _bind() -> None:
         return
     import torch
 
-    names = ("rmsnorm_residual_fp8", "rmsnorm_residual_backward", "swiglu_fp8", "swiglu_backward")
+    names = ("rmsnorm_residual_fp8", "rmsnorm_residual_backward", "swiglu_fp8", "swiglu_backward", "linear_swiglu",
+             "linear_swiglu_backward", "mp_grad_norm", "mp_grad_clip")
     _mpcall.bind(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names),
                  (torch.float32, torch.float16, torch.bfloat16),
                  getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
@@ -699,16 +700,21 @@ def linear_swiglu(x, w_gate, w_up, p, *, p_scales=None, gate=None, up=None, ckpt
     writes them.  What the backward pass can read is written on the way: gate and up (both products, [rows,
     hidden] as x, each may be a column range of one wider matrix), or their 8-bit checkpoint ckpt with
     ckpt_scales as swiglu_fp8 has it; or neither."""
-    rows, width, hidden, px, pg, pu, gp, up_, ld = _products(x, w_gate, w_up, gate, up)
-    if p_scales is None:
-        code, pp, ps = _dtype_code(x), _in(p, "p", 2 * rows * hidden, x, x.dtype), None
-    else:
-        nbytes, align = (rows * (hidden // 32), 1) if scale_block == 32 else (4 * rows * -(-hidden // 128), 4)
-        code, pp, ps = fp8_dtype, _in(p, "p", rows * hidden, x), _in(p_scales, "p_scales", nbytes, x, align=align)
-    _check("linear_swiglu", lib.linear_swiglu(
-        px, _dtype_code(x), rows, width, hidden, pg, pu, pp, code, scale_block, ps, gp, up_, ld,
-        _in(ckpt, "ckpt", 2 * rows * hidden, x),
-        _in(ckpt_scales, "ckpt_scales", 8 * rows * -(-hidden // 128), x, _f32(), 4), _stream(stream)))
+    status = _mpcall and _mpcall.linear_swiglu(x, w_gate, w_up, p, p_scales, gate, up, ckpt, ckpt_scales, fp8_dtype,
+                                               scale_block, stream)
+    if status is None:
+        _bind()
+        rows, width, hidden, px, pg, pu, gp, up_, ld = _products(x, w_gate, w_up, gate, up)
+        if p_scales is None:
+            code, pp, ps = _dtype_code(x), _in(p, "p", 2 * rows * hidden, x, x.dtype), None
+        else:
+            nbytes, align = (rows * (hidden // 32), 1) if scale_block == 32 else (4 * rows * -(-hidden // 128), 4)
+            code, pp, ps = fp8_dtype, _in(p, "p", rows * hidden, x), _in(p_scales, "p_scales", nbytes, x, align=align)
+        status = lib.linear_swiglu(
+            px, _dtype_code(x), rows, width, hidden, pg, pu, pp, code, scale_block, ps, gp, up_, ld,
+            _in(ckpt, "ckpt", 2 * rows * hidden, x),
+            _in(ckpt_scales, "ckpt_scales", 8 * rows * -(-hidden // 128), x, _f32(), 4), _stream(stream))
+    _check("linear_swiglu", status)
 
 
 def _f32():
@@ -733,27 +739,32 @@ def linear_swiglu_backward(dp, x, w_gate, w_up, dx, dw_gate, dw_up, workspace, *
     """Gradients of linear_swiglu from dp ([rows, hidden], that of the unquantised product) and what was saved:
     gate and up, their 8-bit checkpoint, or neither, when both products are formed again.  dx: [rows, width];
     dw_gate, dw_up: [hidden, width]; all as x.  dx may be None, and both weights' gradients may."""
-    rows, width, hidden, px, pg, pu, gp, up_, ld = _products(x, w_gate, w_up, gate, up)
-    dt, nb = x.dtype, 2 * hidden * width
-    _check("linear_swiglu_backward", lib.linear_swiglu_backward(
-        _in(dp, "dp", 2 * rows * hidden, x, dt), _dtype_code(x), rows, width, hidden, px, pg, pu, gp, up_, ld,
-        _in(ckpt, "ckpt", 2 * rows * hidden, x),
-        _in(ckpt_scales, "ckpt_scales", 8 * rows * -(-hidden // 128), x, _f32(), 4),
-        _in(dx, "dx", 2 * rows * width, x, dt), _in(dw_gate, "dw_gate", nb, x, dt), _in(dw_up, "dw_up", nb, x, dt),
-        _in(workspace, "workspace", 0, x), _ws(workspace)[1], _stream(stream)))
+    status = _mpcall and _mpcall.linear_swiglu_backward(dp, x, w_gate, w_up, dx, dw_gate, dw_up, workspace, gate, up, ckpt,
+                                                        ckpt_scales, stream)
+    if status is None:
+        _bind()
+        rows, width, hidden, px, pg, pu, gp, up_, ld = _products(x, w_gate, w_up, gate, up)
+        dt, nb = x.dtype, 2 * hidden * width
+        status = lib.linear_swiglu_backward(
+            _in(dp, "dp", 2 * rows * hidden, x, dt), _dtype_code(x), rows, width, hidden, px, pg, pu, gp, up_, ld,
+            _in(ckpt, "ckpt", 2 * rows * hidden, x),
+            _in(ckpt_scales, "ckpt_scales", 8 * rows * -(-hidden // 128), x, _f32(), 4),
+            _in(dx, "dx", 2 * rows * width, x, dt), _in(dw_gate, "dw_gate", nb, x, dt), _in(dw_up, "dw_up", nb, x, dt),
+            _in(workspace, "workspace", 0, x), _ws(workspace)[1], _stream(stream))
+    _check("linear_swiglu_backward", status)
 
 
 # ---- gradient norm and clipping ---------------------------------------------------------------
 
 
 def make_grad_array(grads, out=None):
-    """The list that mp_grad_norm and mp_grad_clip take, made once for tensors that stay where they are.
-    out: where the clipped gradients go, tensors of the same sizes in any of the three types; None: in place."""
+    """The list that mp_grad_norm and mp_grad_clip take, made once for tensors that stay where they are and
+    are kept by the caller.  out: where the clipped gradients go, tensors of the same sizes in any of the three types; None: in place."""
     outs = grads if out is None else out
     if len(outs) != len(grads):
         raise ValueError(f"out: {len(outs)} tensors, the call needs {len(grads)}")
     arr = (MpGrad * max(1, len(grads)))()
-    arr.count = len(grads)
+    arr.count, arr.device = len(grads), grads[0].get_device() if len(grads) else -1
     seen = set()
     for i, (g, o) in enumerate(zip(grads, outs)):
         _dev(g, f"grads[{i}]", like=grads[0])
@@ -778,9 +789,12 @@ def _dtypes() -> dict:
     return _CODES
 
 
-def _grads(grads, out=None):
+def _grads(grads, out=None, like=None):
     arr = grads if isinstance(grads, ctypes.Array) else make_grad_array(grads, out)
-    return arr, getattr(arr, "count", len(arr))
+    n, device = getattr(arr, "count", len(arr)), getattr(arr, "device", -1)
+    if device >= 0 and getattr(like, "is_cuda", False) and like.get_device() != device:
+        raise ValueError(f"grads: on device {device}, the call runs on {like.get_device()}")
+    return arr, n
 
 
 def mp_grad_norm_workspace_size(grads) -> int:
@@ -798,10 +812,14 @@ def mp_grad_norm(grads, norm, workspace, loss_scale=None, stream=None) -> None:
     """norm (float32, one element) = the global L2 norm of the gradients, divided by loss_scale (a float32 device
     tensor of one element, such as new_scaler_state()[:4].view(torch.float32)) if that is given.  grads: tensors,
     or the array of make_grad_array."""
-    arr, n = _grads(grads)
-    pn = _in(norm, "norm", 4, dtype=_f32(), align=4)
-    _check("mp_grad_norm", lib.mp_grad_norm(arr, n, _in(loss_scale, "loss_scale", 4, norm, _f32(), 4), pn,
-                                            _in(workspace, "workspace", 0, norm), _ws(workspace)[1], _stream(stream)))
+    status = _mpcall and _mpcall.mp_grad_norm(grads, norm, workspace, loss_scale, stream)
+    if status is None:
+        _bind()
+        arr, n = _grads(grads, like=norm)
+        pn = _in(norm, "norm", 4, dtype=_f32(), align=4)
+        status = lib.mp_grad_norm(arr, n, _in(loss_scale, "loss_scale", 4, norm, _f32(), 4), pn,
+                                  _in(workspace, "workspace", 0, norm), _ws(workspace)[1], _stream(stream))
+    _check("mp_grad_norm", status)
 
 
 def mp_grad_clip(grads, norm, max_norm: float, out=None, stream=None) -> None:
@@ -809,9 +827,12 @@ def mp_grad_clip(grads, norm, max_norm: float, out=None, stream=None) -> None:
     the array of make_grad_array (which has `out` in it)."""
     if out is not None and isinstance(grads, ctypes.Array):
         raise ValueError("out: a prebuilt list has its own")
-    arr, n = _grads(grads, out)
-    _check("mp_grad_clip", lib.mp_grad_clip(arr, n, _in(norm, "norm", 4, dtype=_f32(), align=4), float(max_norm),
-                                            _stream(stream)))
+    status = _mpcall and _mpcall.mp_grad_clip(grads, norm, max_norm, stream)
+    if status is None:
+        _bind()
+        arr, n = _grads(grads, out, norm)
+        status = lib.mp_grad_clip(arr, n, _in(norm, "norm", 4, dtype=_f32(), align=4), float(max_norm), _stream(stream))
+    _check("mp_grad_clip", status)
 
 
 __all__ = [
