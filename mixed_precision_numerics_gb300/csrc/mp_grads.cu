@@ -30,7 +30,7 @@ constexpr int kThreads = 256;
 constexpr int kVecs = 8;                             // 16-byte loads in flight a thread
 constexpr int kTileElems = kThreads * kVecs * 8;     // of a CTA's step
 constexpr int kCap = 512, kFew = 32;                 // tensors a launch
-constexpr int kNormCtas = 4, kClipCtas = 4;          // an SM
+constexpr int kNormCtas = 3, kClipCtas = 3;          // an SM
 
 struct Grad {
   const void* g;
@@ -45,9 +45,11 @@ struct List {
   int32_t count;
 };
 
+// The tensor of a tile, from that of an earlier one (every listed tensor has a tile).
 template <int CAP>
-__device__ __forceinline__ int tensor_of(const List<CAP>& L, int64_t tile) {  // every listed tensor has a tile
-  int lo = 0, hi = L.count - 1;
+__device__ __forceinline__ int tensor_of(const List<CAP>& L, int64_t tile, int i) {
+  if (tile < L.start[i + 1]) return i;
+  int lo = i + 1, hi = L.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (L.start[mid] <= tile) lo = mid;
@@ -59,22 +61,32 @@ __device__ __forceinline__ int tensor_of(const List<CAP>& L, int64_t tile) {  //
 template <int XT>
 constexpr int kVecElems = XT == XF32 ? 4 : 8;
 
-// 16 bytes at element e of a tensor of n; zeros past its end.
+// A thread's vectors of one of a tile's kGroups<XT> parts, from element `at`.
 template <int XT>
-__device__ __forceinline__ uint4 load_vec(const void* g, int64_t e, int64_t n) {
-  constexpr int V = kVecElems<XT>, B = XT == XF32 ? 4 : 2;
-  const unsigned char* p = static_cast<const unsigned char*>(g) + e * B;
-  if (e + V <= n) return *reinterpret_cast<const uint4*>(p);
-  uint32_t w[4] = {0u, 0u, 0u, 0u};
+constexpr int kGroups = kTileElems / (kThreads * kVecs * kVecElems<XT>);
+template <int XT>
+__device__ __forceinline__ void load_vecs(uint4 (&v)[kVecs], const void* g, int64_t at, int64_t n, bool whole) {
+  constexpr int V = kVecElems<XT>;
+  const uint4* p = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(g) + at * (16 / V));
+  if (whole) {
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (e + i < n) {
-      if constexpr (XT == XF32)
-        w[i] = reinterpret_cast<const uint32_t*>(p)[i];
-      else
-        w[i >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
-    }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+    for (int u = 0; u < kVecs; ++u) v[u] = p[u * kThreads];
+  } else {  // the tensor's last tile: zeros from its last whole vector on
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) v[u] = at + u * kThreads * V + V <= n ? p[u * kThreads] : make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+// The elements behind a tensor's last whole vector are a thread's each: its number, or -1.
+template <int XT>
+__device__ __forceinline__ int64_t end_of(int64_t n, bool whole) {
+  const int rest = (int)(n & (kVecElems<XT> - 1));
+  return !whole && threadIdx.x < rest ? n - rest + threadIdx.x : -1;
+}
+template <int XT>
+__device__ __forceinline__ float element(const void* g, int64_t e) {
+  if constexpr (XT == XF32) return static_cast<const float*>(g)[e];
+  const uint32_t w = static_cast<const uint16_t*>(g)[e];
+  return XT == XF16 ? f16lo(w) : bf16lo(w);
 }
 
 // Element pairs of 16 bytes.
@@ -129,15 +141,19 @@ __device__ __forceinline__ double squares(const uint4 (&v)[kVecs]) {
 
 template <int XT>
 __device__ __forceinline__ double tile_squares(const Grad& t, int64_t base) {
-  constexpr int V = kVecElems<XT>, G = kTileElems / (kThreads * kVecs * V);
+  constexpr int V = kVecElems<XT>;
+  const bool whole = base + kTileElems <= t.n;
   double s = 0.0;
 #pragma unroll
-  for (int h = 0; h < G; ++h) {
+  for (int h = 0; h < kGroups<XT>; ++h) {
     uint4 v[kVecs];
     const int64_t at = base + (int64_t)h * kThreads * kVecs * V + threadIdx.x * V;
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u) v[u] = load_vec<XT>(t.g, at + u * kThreads * V, t.n);
+    load_vecs<XT>(v, t.g, at, t.n, whole);
     s += squares<XT>(v);
+  }
+  if (const int64_t e = end_of<XT>(t.n, whole); e >= 0) {
+    const double x = element<XT>(t.g, e);
+    s += x * x;
   }
   return s;
 }
@@ -171,8 +187,9 @@ __global__ __launch_bounds__(kThreads, kNormCtas) void k_grad_norm(const __grid_
   chain_release();
   const int64_t total = L.start[L.count];
   double s = 0.0;
+  int i = 0;
   for (int64_t tile = blockIdx.x; tile < total; tile += gridDim.x) {
-    const int i = tensor_of(L, tile);
+    i = tensor_of(L, tile, i);
     const Grad& t = L.t[i];
     const int64_t base = (tile - L.start[i]) * kTileElems;
     s += t.gt == XF32 ? tile_squares<XF32>(t, base)
@@ -201,13 +218,13 @@ __global__ __launch_bounds__(kThreads, kNormCtas) void k_grad_norm(const __grid_
 
 template <int XT, int OT>
 __device__ __forceinline__ void clip_tile(const Grad& t, int64_t base, float c) {
-  constexpr int V = kVecElems<XT>, G = kTileElems / (kThreads * kVecs * V);
+  constexpr int V = kVecElems<XT>;
+  const bool whole = base + kTileElems <= t.n;
 #pragma unroll
-  for (int h = 0; h < G; ++h) {
+  for (int h = 0; h < kGroups<XT>; ++h) {
     uint4 v[kVecs];
     const int64_t at = base + (int64_t)h * kThreads * kVecs * V + threadIdx.x * V;
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u) v[u] = load_vec<XT>(t.g, at + u * kThreads * V, t.n);
+    load_vecs<XT>(v, t.g, at, t.n, whole);
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
       const int64_t e = at + u * kThreads * V;
@@ -224,7 +241,7 @@ __device__ __forceinline__ void clip_tile(const Grad& t, int64_t base, float c) 
           asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[k]) : "f"(x.y), "f"(x.x));
         }
       }
-      if (e + V <= t.n) {
+      if (whole || e + V <= t.n) {
         uint32_t* to = static_cast<uint32_t*>(t.out) + e * W / V;
         if constexpr (W == 2) {
           __stcs(reinterpret_cast<uint2*>(to), make_uint2(w[0], w[1]));
@@ -232,17 +249,15 @@ __device__ __forceinline__ void clip_tile(const Grad& t, int64_t base, float c) 
 #pragma unroll
           for (int i = 0; i < W; i += 4) st_cs(to + i, make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]));
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (e + i < t.n) {
-            if constexpr (OT == XF32)
-              static_cast<uint32_t*>(t.out)[e + i] = w[i];
-            else
-              static_cast<uint16_t*>(t.out)[e + i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
-          }
       }
     }
+  }
+  if (const int64_t e = end_of<XT>(t.n, whole); e >= 0) {
+    const float x = element<XT>(t.g, e) * c;
+    if constexpr (OT == XF32)
+      static_cast<float*>(t.out)[e] = x;
+    else
+      static_cast<uint16_t*>(t.out)[e] = (uint16_t)(OT == XF16 ? pack_f16x2(x, 0.0f) : pack_bf16x2(x, 0.0f));
   }
 }
 template <int XT>
@@ -266,8 +281,9 @@ __global__ __launch_bounds__(kThreads, kClipCtas) void k_grad_clip(const __grid_
   __syncthreads();
   const float c = factor;
   const int64_t total = L.start[L.count];
+  int i = 0;
   for (int64_t tile = blockIdx.x; tile < total; tile += gridDim.x) {
-    const int i = tensor_of(L, tile);
+    i = tensor_of(L, tile, i);
     const Grad& t = L.t[i];
     if (c == 1.0f && t.g == t.out) continue;  // nothing changes
     const int64_t base = (L.start[i + 1] - 1 - tile) * kTileElems;  // from the tensor's end
