@@ -4,14 +4,17 @@
 
 Each block adds the branch of the block before it to the residual stream and
 norms the sum straight to FP8 (rmsnorm_residual_fp8), multiplies it by the gate
-and up weights, forms the gated product straight to FP8 (swiglu_fp8) and
-multiplies that by the down weights.  What the backward pass reads of the stream,
-the gate and the up values are the 8-bit checkpoints that the two calls write on
-the way; rmsnorm_residual_backward and swiglu_backward take them as they are.
-The update is mp_adamw_step on FP32 masters under a dynamic loss scale.
+and up weights and forms the gated product of both straight to FP8 in one call
+(linear_swiglu), and multiplies that by the down weights.  What the backward pass
+reads of the stream, the gate and the up values are the 8-bit checkpoints that the
+two calls write on the way; rmsnorm_residual_backward and linear_swiglu_backward
+take them as they are.  The gradients of all blocks are clipped by one norm
+(mp_grad_norm, mp_grad_clip), and the update is mp_adamw_step on FP32 masters under
+a dynamic loss scale: one call for the matrices, one for the norms' weights, which
+do not decay.
 
-The library has no matrix product: here torch multiplies the dequantised FP8
-operands in BF16, where a training program has its FP8 GEMMs.
+The products of linear_swiglu are of 16-bit operands, so its input is the FP8
+norm dequantised to BF16; the down projection is torch's.
 """
 from __future__ import annotations
 
@@ -62,30 +65,28 @@ class Block:
         self.h_saved, self.h_scales = torch.empty_like(self.y), torch.empty_like(self.y_scales)
         self.p, self.p_scales = empty(tokens, hidden, dtype=u8), empty(tokens, tiles(hidden), dtype=f32)
         self.gu_saved, self.gu_scales = empty(2, tokens, hidden, dtype=u8), empty(2, tokens, tiles(hidden), dtype=f32)
-        self.d_gate_up, self.dx = empty(tokens, 2 * hidden, dtype=BF16), empty(tokens, width, dtype=BF16)
+        self.dy, self.dx = empty(tokens, width, dtype=BF16), empty(tokens, width, dtype=BF16)
         self.workspace = M.new_rmsnorm_workspace(tokens, width)
+        self.products = M.new_linear_swiglu_workspace(tokens, width, hidden)
 
-    def weights(self):
-        return [self.norm, self.gate_up, self.down]
+    def halves(self, gate_up):
+        return gate_up[:self.hidden], gate_up[self.hidden:]
 
     def forward(self, branch, stream):
         """(the block's branch, the stream it is to be added to)"""
         M.rmsnorm_residual_fp8(branch, self.norm.work, self.y, self.y_scales, residual=stream, h=self.h, rstd=self.rstd,
                                ckpt=self.h_saved, ckpt_scales=self.h_scales)
-        gate_up = dequantise(self.y, self.y_scales) @ self.gate_up.work.t()
-        M.swiglu_fp8(gate_up[:, :self.hidden], gate_up[:, self.hidden:], self.p, self.p_scales, ckpt=self.gu_saved,
-                     ckpt_scales=self.gu_scales)
+        M.linear_swiglu(dequantise(self.y, self.y_scales), *self.halves(self.gate_up.work), self.p, p_scales=self.p_scales,
+                        ckpt=self.gu_saved, ckpt_scales=self.gu_scales)
         return dequantise(self.p, self.p_scales) @ self.down.work.t(), self.h
 
     def backward(self, d_branch, d_stream):
         """Gradient of the branch and of the stream that came in (one tensor: they were added)."""
         torch.matmul(d_branch.t(), dequantise(self.p, self.p_scales), out=self.down.grad)
         dp = d_branch @ self.down.work
-        M.swiglu_backward(dp, self.d_gate_up[:, :self.hidden], self.d_gate_up[:, self.hidden:], ckpt=self.gu_saved,
-                          ckpt_scales=self.gu_scales)
-        torch.matmul(self.d_gate_up.t(), dequantise(self.y, self.y_scales), out=self.gate_up.grad)
-        dy = self.d_gate_up @ self.gate_up.work
-        M.rmsnorm_residual_backward(dy, self.norm.work, self.rstd, self.dx, self.norm.grad, self.workspace,
+        M.linear_swiglu_backward(dp, dequantise(self.y, self.y_scales), *self.halves(self.gate_up.work), self.dy,
+                                 *self.halves(self.gate_up.grad), self.products, ckpt=self.gu_saved, ckpt_scales=self.gu_scales)
+        M.rmsnorm_residual_backward(self.dy, self.norm.work, self.rstd, self.dx, self.norm.grad, self.workspace,
                                     ckpt=self.h_saved, ckpt_scales=self.h_scales, dh=d_stream)
         return self.dx
 
@@ -94,12 +95,16 @@ def train(steps: int = 200, tokens: int = 2048, blocks: int = 4, width: int = 25
           log=print) -> list[float]:
     gen = torch.Generator(device="cuda").manual_seed(seed)
     stack = [Block(tokens, width, hidden, gen) for _ in range(blocks)]
-    params = [w.param for b in stack for w in b.weights()]
+    matrices, norms = [w for b in stack for w in (b.gate_up, b.down)], [b.norm for b in stack]
+    groups = [([w.param for w in matrices], M.AdamwHparams(2e-3, 0.9, 0.95, 1e-8, 0.01, 0.0), M.new_scaler_state(1024.0)),
+              ([w.param for w in norms], M.AdamwHparams(2e-3, 0.9, 0.95, 1e-8, 0.0, 0.0), M.new_scaler_state(1024.0))]
+    grads = M.make_grad_array([w.grad for w in matrices + norms])
+    norm, norm_workspace = empty(1, dtype=torch.float32), M.new_grad_norm_workspace(grads)
     mix = torch.randn(width, width, generator=gen, device="cuda") * width**-0.5
-    hp, cfg = M.AdamwHparams(2e-3, 0.9, 0.95, 1e-8, 0.01, 1.0), M.ScalerCfg(2.0, 0.5, 100, 1)
-    state = M.new_scaler_state(1024.0)
-    workspace = empty(M.mp_adamw_workspace_size(params), dtype=torch.uint8)
-    scale = state[:4].view(torch.float32)  # the loss scale, on the device
+    cfg = M.ScalerCfg(2.0, 0.5, 100, 1)
+    # the loss scale, on the device: a norm that is not finite makes every gradient NaN, so both groups see the
+    # same bad steps and their scales stay the same
+    scale = groups[0][2][:4].view(torch.float32)
     losses = []
     for step in range(steps):
         x = torch.randn(tokens, width, generator=gen, device="cuda")
@@ -113,11 +118,14 @@ def train(steps: int = 200, tokens: int = 2048, blocks: int = 4, width: int = 25
         d_branch, d_stream = d, d
         for b in reversed(stack):
             d_branch = d_stream = b.backward(d_branch, d_stream)
-        M.mp_adamw_step(params, hp, state, workspace=workspace)
-        M.loss_scale_update(state, cfg)
+        M.mp_grad_norm(grads, norm, norm_workspace, loss_scale=scale)
+        M.mp_grad_clip(grads, norm, 1.0)
+        for params, hp, state in groups:
+            M.mp_adamw_step(params, hp, state)
+            M.loss_scale_update(state, cfg)
         if log and (step % 20 == 0 or step == steps - 1):
             log(f"step {step:4d}  loss {float(losses[-1]):.4f}")
-    s = M.read_scaler_state(state)
+    s = M.read_scaler_state(groups[0][2])
     if log:
         saved = sum(t.nbytes for b in stack for t in (b.h_saved, b.h_scales, b.gu_saved, b.gu_scales))
         kept = sum(2 * tokens * (width + 2 * hidden) for _ in stack)

@@ -41,7 +41,7 @@ constexpr int kThreads = (kResultWarps + 4) * 32;
 constexpr int kResultRegisters = 224, kOtherRegisters = 56;
 static_assert(kResultWarps * kResultRegisters + 4 * kOtherRegisters <= (kResultWarps + 4) * 168, "registers of a CTA");
 constexpr int kTmemColumns = 512;
-constexpr int kBand = 8;
+constexpr int kBand = 16;
 constexpr int kBarrierBytes = 256;
 constexpr int kSmem = kStages * kStageBytes + kResultWarps * kStagingBytes + 2 * 2 * kHalf * 4 + kBarrierBytes;
 static_assert(kSmem <= 232448, "227 KB a CTA");
@@ -510,7 +510,7 @@ __global__ __launch_bounds__(256) void k_ffn_join(const __grid_constant__ Join f
 }
 
 // What a tile costs, in stages: a short one waits for its results' way out.
-int64_t cost_of(int blocks) { return blocks > 10 ? blocks : 10; }
+int64_t cost_of(int blocks) { return blocks > 6 ? blocks : 6; }
 
 // Evens out what the pairs have to do (Walk): those without the last turn's
 // item of the first product take as many stages of the second product ahead.
