@@ -21,8 +21,6 @@
 // over a contraction of 4096 leaves results 4e-6 too small.  So every kRun
 // stages the sums so far leave TMEM and are added to registers with correct
 // rounding, while the next run goes into the other half of TMEM.
-#include <new>
-
 #include "mp_chain.cuh"
 #include "mp_ffn.cuh"
 
@@ -529,7 +527,7 @@ mp_status launch(Ffn& f, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   const auto kernel = k_ffn<BF16, EP>;
   if (!smem_opt_in(kernel, kSmem, done)) return MP_ECUDA;
-  const int64_t items = (int64_t)f.p[0].items + f.p[1].items, most = sm_count() / 2;
+  const int64_t items = (int64_t)f.p[0].items + f.p[1].items, most = sm_count() < 2 ? 1 : sm_count() / 2;
   const int pairs = (int)(items < most ? items : most);
   share(f, pairs);
   cudaLaunchAttribute attr[2];
@@ -624,7 +622,7 @@ bool shape_ok(int64_t rows, int64_t width, int64_t hidden, int step) {
   return ceil_div(rows, 256) * (int64_t)ceil_div(2 * hidden + width, 128) < (1ll << 30);
 }
 bool pitch_ok(int64_t ld, int64_t cols, int64_t rows) {
-  return rows <= 1 || (ld >= cols && ld < (1ll << 38) && ld % 8 == 0);
+  return rows <= 1 || (ld >= cols && ld < (1ll << 61) / rows && ld % 8 == 0);
 }
 
 // Forms g and u (FWD16, FWD8, AGAIN).

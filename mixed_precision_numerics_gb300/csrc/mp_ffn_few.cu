@@ -11,8 +11,6 @@
 //
 // Bound by DRAM: the stages of the CTAs on an SM, some 190 KB, are its bytes in
 // flight.
-#include <new>
-
 #include "mp_chain.cuh"
 #include "mp_ffn.cuh"
 

@@ -1,10 +1,11 @@
 """The gated feed-forward products and their gradients in binary64, with bounds on how far the
 kernels may be from them.
 
-Sums.  Within a run of 512 terms the tensor core adds 16 products at a time to a binary32 sum and
-truncates: 17 numbers are aligned to the largest of them, each cut by less than a step 2^-23 of a
-magnitude no larger than A = sum |a||b|.  32 such additions: 32 * 17 * 2^-23 * A < 2^-13.9 * A,
-and the runs' sums are added with half a step each, fewer than 64 of them here: SUM = 2^-13.8.
+Sums.  The tensor core adds 16 products at a time to a binary32 sum and truncates: 17 numbers are
+aligned to the largest and each is cut by half a step 2^-23 of the running sum's magnitude on
+average, which grows to A = sum |a||b| and is half of that on average.  A run of 2048 terms is 128
+such additions: 128 * 17 / 4 * 2^-23 * A = 2^-13.9 * A; runs (of a part of it each) are added with
+half a step each, fewer than 64 of them here: SUM = 2^-13.8.
 The logistic function is within 6.2 * 2^-24, products and sums of a few rounded factors within
 16 * 2^-24 of the magnitudes that go in: FEW = 2^-20.
 """

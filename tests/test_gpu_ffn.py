@@ -247,3 +247,62 @@ def test_captured_and_on_two_streams(M):
     for k, o in zip("ab", outs):
         assert all(torch.equal(p, q) for p, q in zip(o[:4], want[k]))
     assert M.mp_wait_failures() == 0
+
+
+def sampled(n, seed):
+    """Places on both sides of tile edges, the ends, and some others."""
+    gen = torch.Generator().manual_seed(seed)
+    edges = [i for e in range(0, n, max(256, n // 12 // 256 * 256)) for i in (e - 1, e, e + 127, e + 128) if 0 <= i < n]
+    return torch.tensor(sorted({*edges, n - 1, *torch.randint(0, n, (24,), generator=gen).tolist()}), device="cuda")
+
+
+def test_many_tiles_for_every_pair(M):
+    """More tiles than pairs of CTAs, ragged at every edge: sampled rows and columns of every result."""
+    rows, width, hidden = 4100, 2064, 5520
+    x, wg, wu, dp = U.inputs(rows, width, hidden, BF16, seed=8)
+    r = run_forward(M, x, wg, wu, 128, 16)
+    at = sampled(rows, 1)
+    (g, eg), (u, eu), (p, ep) = U.gated(x[at], wg, wu)
+    U.check("gate", r["gate"][at], g, eg)
+    U.check("up", r["up"][at], u, eu)
+    U.close_codes("p", r["p"][at], r["p_scales"][at], p, ep, 128)
+    dx, dw = empty(rows, width, dtype=BF16), empty(2, hidden, width, dtype=BF16)
+    M.linear_swiglu_backward(dp, x, wg, wu, dx, dw[0], dw[1], M.new_linear_swiglu_workspace(rows, width, hidden),
+                             gate=r["gate"], up=r["up"])
+    v, e = U.gradients(dp[at], x[at], wg, wu, U.d(r["gate"][at]), U.d(r["up"][at]))["dx"]
+    U.check("dx", dx[at], v, e)
+    cut = sampled(hidden, 2)
+    out = U.gradients(dp[:, cut], x, wg[cut], wu[cut], U.d(r["gate"][:, cut]), U.d(r["up"][:, cut]))
+    U.check("dw_gate", dw[0][cut], *out["dw_gate"])
+    U.check("dw_up", dw[1][cut], *out["dw_up"])
+
+
+@pytest.mark.parametrize("out,save", [(16, 16), (128, 8)])
+def test_more_than_2_to_31_elements(M, out, save):
+    width, hidden = 64, 14336
+    rows = 2**31 // hidden + 700
+    x, wg, wu, _ = U.inputs(rows, width, hidden, F16, seed=9)
+    at = torch.tensor([0, 1, 255, 256, 2**31 // hidden - 1, 2**31 // hidden, 2**31 // hidden + 1, rows - 257, rows - 1], device="cuda")
+    (g, eg), (u, eu), (p, ep) = U.gated(x[at], wg, wu)
+    r = run_forward(M, x, wg, wu, out, save)
+    if out == 16:
+        U.check("p", r["p"][at], p, ep)
+        U.check("gate", r["gate"][at], g, eg)
+        U.check("up", r["up"][at], u, eu)
+        del r["p"]
+    else:
+        U.close_codes("p", r["p"][at], r["p_scales"][at], p, ep, 128)
+        for k, (v, e) in enumerate(((g, eg), (u, eu))):
+            U.close_codes(f"ckpt {k}", r["ckpt"][k][at], r["ckpt_scales"][k][at], v, e, 128)
+    dp = torch.randn(rows, 1, device="cuda").to(F16).expand(rows, hidden).contiguous()
+    dx = empty(rows, width, dtype=F16)
+    ws = M.new_linear_swiglu_workspace(rows, width, hidden)
+    saved = {k: r[k] for k in ("gate", "up", "ckpt", "ckpt_scales") if k in r}
+    M.linear_swiglu_backward(dp, x, wg, wu, dx, None, None, ws, **saved)
+    if save == 16:
+        g, u, eg, eu = U.d(r["gate"][at]), U.d(r["up"][at]), 0.0, 0.0
+    else:
+        g, u = (U.d(r["ckpt"][k][at].view(torch.float8_e4m3fn).float()) * U.d(r["ckpt_scales"][k][at]).repeat_interleave(128, 1)
+                for k in (0, 1))
+        eg, eu = 2.0**-24 * g.abs(), 2.0**-24 * u.abs()
+    U.check("dx", dx[at], *U.gradients(dp[at], x[at], wg, wu, g, u, eg, eu)["dx"])

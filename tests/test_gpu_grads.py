@@ -158,3 +158,19 @@ def test_guard_bands(M):
     check_clipped([g], [out], norm, 1.0)
     M.mp_grad_clip([g], norm, 1.0)
     assert (raw[:4096] == 0x3C).all() and (raw[-4096:] == 0x3C).all()
+
+
+def test_more_than_2_to_31_elements(M):
+    n = 2**31 + 100003
+    g = torch.empty(n, dtype=F16, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    parts = g.split(1 << 28)
+    for p in parts:
+        p.copy_(torch.randn(p.numel(), generator=gen, device="cuda", dtype=F16) * 1e-2)
+    want = math.sqrt(sum(float(p.double().square().sum()) for p in parts))
+    norm = norm_of(M, [g])
+    assert abs(float(norm) - want) <= NORM * want
+    ends = torch.cat([torch.arange(0, 70000), torch.arange(2**31 - 70000, n)]).cuda()
+    first = g[ends]
+    M.mp_grad_clip([g], norm, 0.5 * want)
+    check_clipped([first], [g[ends]], norm, 0.5 * want)
