@@ -39,7 +39,6 @@ constexpr int kThreads = (kResultWarps + 4) * 32;
 constexpr int kResultRegisters = 224, kOtherRegisters = 56;
 static_assert(kResultWarps * kResultRegisters + 4 * kOtherRegisters <= (kResultWarps + 4) * 168, "registers of a CTA");
 constexpr int kTmemColumns = 512;
-constexpr int kBand = 16;
 constexpr int kBarrierBytes = 256;
 constexpr int kSmem = kStages * kStageBytes + kResultWarps * kStagingBytes + 2 * 2 * kHalf * 4 + kBarrierBytes;
 static_assert(kSmem <= 232448, "227 KB a CTA");
@@ -48,7 +47,7 @@ static_assert((2 * kStages + 4) * 8 + 8 <= kBarrierBytes, "barriers and the TMEM
 // One product in tiles.
 struct Product {
   CUtensorMap a[2], b[2];
-  int32_t items, tiles_m;  // work items = tiles * splits
+  int32_t items, tiles_m, shift;  // work items = tiles * splits; 2^shift rows of tiles to a band
   FastDiv tiles, band, last, per_matrix;  // tiles of a split, of a band; rows of tiles in the last band, in a matrix
   int32_t blocks0, blocks, splits, matrices;  // stages of the contraction in the first operand pair, and in all
   int32_t rows, cols;      // of a result matrix
@@ -96,7 +95,7 @@ __device__ unsigned int g_ffn_wait_failures;  // bounded waits that gave up (rea
 struct Tile {
   int32_t m, n, k0, k1, split, of;  // row and column of tiles, stages from k0 to k1, which matrix
 };
-// Items walk the tiles in bands of kBand rows of tiles, column by column, so
+// Items walk the tiles in bands of 2^shift rows of tiles, column by column, so
 // that those in flight together share operands in L2; all tiles of a split
 // first.  (Every role does this for every tile, one thread after another: with
 // plain divisions the tiles of short contractions waited for it.)
@@ -111,9 +110,9 @@ __device__ __forceinline__ Tile tile_of(const Product& f, uint32_t item) {
   }
   const uint32_t band = div_by(item, f.band);
   item -= band * f.band.d;
-  const bool whole = (int)(band + 1) * kBand <= f.tiles_m;
-  t.n = whole ? item / kBand : div_by(item, f.last);
-  t.m = band * kBand + item - t.n * (whole ? kBand : f.last.d);
+  const bool whole = (int)((band + 1) << f.shift) <= f.tiles_m;
+  t.n = whole ? item >> f.shift : div_by(item, f.last);
+  t.m = (band << f.shift) + item - t.n * (whole ? 1 << f.shift : f.last.d);
   t.of = div_by(t.m, f.per_matrix);  // 0 unless two matrices are stored
   t.m -= t.of * f.per_matrix.d;
   return t;
@@ -553,12 +552,21 @@ mp_status launch(Ffn& f, cudaStream_t st) {
 bool type16(mp_dtype t) { return t == MP_F16 || t == MP_BF16; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 // Tiles, and the walk over them.
-void lay_out(Product& f, int matrices, int rows_of_tiles, int tiles_n, int splits) {
+//
+// How high a band is: 16 rows of tiles in the forward product and 8 in the
+// gradients'.  A wave of 76 tiles that is 8 x 9.5 has the fewest different
+// operand rows; twice as high a band reads the weights half as often, which pays
+// where the band's rows of x stay in L2 (8192 x 4096 x 14336: 16 rows 1057 us, 8
+// 1083, 32 1131; gradients 8 rows 2410 us, 16 2445, 32 2522).
+constexpr int kForwardShift = 4, kGradientShift = 3;
+void lay_out(Product& f, int matrices, int rows_of_tiles, int tiles_n, int splits, int shift) {
   f.matrices = matrices, f.splits = splits;
   f.tiles_m = matrices * rows_of_tiles;
   f.items = f.tiles_m * tiles_n * splits;
-  f.tiles = fast_div(f.tiles_m * tiles_n), f.band = fast_div(kBand * tiles_n);
-  f.last = fast_div(f.tiles_m % kBand ? f.tiles_m % kBand : kBand), f.per_matrix = fast_div(rows_of_tiles);
+  f.shift = shift;
+  const int high = 1 << shift;
+  f.tiles = fast_div(f.tiles_m * tiles_n), f.band = fast_div(high * tiles_n);
+  f.last = fast_div(f.tiles_m % high ? f.tiles_m % high : high), f.per_matrix = fast_div(rows_of_tiles);
 }
 
 // The gradients' products: tiles and stages of the contraction of dx (none up to
@@ -638,7 +646,7 @@ mp_status project(bool bf16, const void* x, const void* w_gate, const void* w_up
   f.o = o;
   q.blocks = q.blocks0 = ceil_div(width, kBlockK);
   q.rows = (int32_t)rows, q.cols = (int32_t)hidden;
-  lay_out(q, 1, ceil_div(rows, 2 * kHalf), ceil_div(hidden, kHalf), 1);
+  lay_out(q, 1, ceil_div(rows, 2 * kHalf), ceil_div(hidden, kHalf), 1, kForwardShift);
   return bf16 ? launch<true, EP>(f, st) : launch<false, EP>(f, st);
 }
 
@@ -753,7 +761,7 @@ extern "C" MP_API mp_status linear_swiglu_backward(const void* dp, mp_dtype x_dt
     q.blocks0 = plan.dx_blocks / 2, q.blocks = plan.dx_blocks;
     q.rows = (int32_t)rows, q.cols = (int32_t)width;
     q.result[0] = dx, q.parts = reinterpret_cast<float*>(parts);
-    lay_out(q, 1, ceil_div(rows, 2 * kHalf), ceil_div(width, 2 * kHalf), plan.dx_splits);
+    lay_out(q, 1, ceil_div(rows, 2 * kHalf), ceil_div(width, 2 * kHalf), plan.dx_splits, kGradientShift);
   }
   if (dw_gate) {
     Product& q = f.p[1];
@@ -763,7 +771,7 @@ extern "C" MP_API mp_status linear_swiglu_backward(const void* dp, mp_dtype x_dt
     q.blocks0 = q.blocks = plan.dw_blocks, q.a_mn = true;
     q.rows = (int32_t)hidden, q.cols = (int32_t)width;
     q.result[0] = dw_gate, q.result[1] = dw_up, q.parts = reinterpret_cast<float*>(parts + up256(plan.dx_parts));
-    lay_out(q, 2, ceil_div(hidden, 2 * kHalf), ceil_div(width, 2 * kHalf), plan.dw_splits);
+    lay_out(q, 2, ceil_div(hidden, 2 * kHalf), ceil_div(width, 2 * kHalf), plan.dw_splits, kGradientShift);
   }
   return multiply(bf16, f, st);
 }
