@@ -9,9 +9,10 @@
  *   3. NVFP4 quantisation (E2M1 codes, E4M3 block scales, FP32 tensor scale,
  *      1x16 or 16x16 blocks, optional random Hadamard transform, round to
  *      nearest even or stochastic rounding), plus the standalone transform.
- * Next to them: the MX block formats (section 4), and the norm and gated
+ * Next to them: the MX block formats (section 4), the norm and gated
  * product of a transformer block with 8-bit outputs and checkpoints, forward
- * and backward (section 5).
+ * and backward (section 5), the matrix products of a gated feed-forward block
+ * (section 6), and the norm and clipping of a list of gradients (section 7).
  *
  * Pages cited (title, then section):
  *   [MPT-ko] itwiki "혼합 정밀도 학습" (mixed precision training)
@@ -34,8 +35,8 @@
  *     be anything >= 0 unless stated.
  *   - Calls that share a state struct, meta struct or workspace must be
  *     ordered on one stream; calls with disjoint state may run concurrently.
- *   - The quantiser kernels (FP8, NVFP4, MX, the transform) and the block
- *     operators' (section 5) are launched with
+ *   - The quantiser kernels (FP8, NVFP4, MX, the transform) and those of
+ *     sections 5 to 7 are launched with
  *     programmatic stream serialization allowed: their blocks may be
  *     scheduled while the previous kernel in the stream finishes, but each
  *     waits for that kernel to complete (griddepcontrol.wait) before touching
@@ -75,7 +76,7 @@ MP_API int32_t mp_version(void);
 /* Number of kernels this library has launched in this process (diagnostic). */
 MP_API uint64_t mp_launch_count(void);
 /* Number of bounded waits on a tile copy that gave up inside this library's
- * FP8 casts and norm backward kernel since it was loaded (0 in normal operation).  A kernel whose
+ * FP8 casts, norm backward kernel and feed-forward products since it was loaded (0 in normal operation).  A kernel whose
  * copy engine stopped answering waits about two seconds per wait, counts the
  * failure here and returns; the outputs of that call are then incomplete.
  * Reads device memory synchronously: call it after synchronising the streams
@@ -480,8 +481,10 @@ MP_API mp_status swiglu_backward(const void* dp, mp_dtype x_dtype, int64_t rows,
  * activation and the product, in one kernel: g = x w_gate^T, u = x w_up^T,
  * p = (g * s(g)) * u, s the logistic function (within 6.2 * 2^-24, relative).
  * x [rows, width], w_gate and w_up [hidden, width], of one type, MP_F16 or
- * MP_BF16.  Sums are binary32: within a run of 512 terms they are the tensor
- * core's, which truncates; runs are added rounded to nearest.
+ * MP_BF16.  Sums are binary32: within a run of terms they are the tensor core's,
+ * which truncates, and runs are added rounded to nearest.  A run has 512 terms
+ * where p is FP8, 2048 otherwise; up to 128 rows have room for two to eight runs in
+ * each of up to eight parts of the contraction, and longer ones where that is too few.
  * p [rows, hidden]: of x's type (p_dtype = x_dtype, p_scales NULL), or FP8
  * (p_dtype MP_E4M3 or MP_E5M2) with scale_block 128 (FP32) or 32 (UE8M0) and
  * p_scales, by the rules of section 5 applied to the binary32 product.
@@ -492,8 +495,8 @@ MP_API mp_status swiglu_backward(const void* dp, mp_dtype x_dtype, int64_t rows,
  * width % 16 == 0, hidden % 16 == 0 (32 with scale_block 32), both at most
  * 2^20, rows < 2^31 - 256 (else MP_ESHAPE); tensors 16-byte aligned, FP32
  * scales 4-byte.  rows or hidden 0: nothing is written; width 0 otherwise:
- * MP_ESHAPE.  A row's results do not depend on the other rows' values.  One kernel
- * launch, reading its operands through tile copies: MP_ECUDA if the driver's
+ * MP_ESHAPE.  A row's results do not depend on the other rows' values (they do on
+ * whether there are more than 128).  One kernel launch, reading its operands through tile copies: MP_ECUDA if the driver's
  * tensor-map encoder is unavailable. */
 MP_API mp_status linear_swiglu(const void* x, mp_dtype x_dtype, int64_t rows, int64_t width, int64_t hidden,
                                const void* w_gate, const void* w_up, void* p, mp_dtype p_dtype, int32_t scale_block,
@@ -509,11 +512,12 @@ MP_API mp_status linear_swiglu(const void* x, mp_dtype x_dtype, int64_t rows, in
  *     dw_gate = dg^T x,  dw_up = du^T x      [hidden, width], overwritten
  * all of x_dtype.  dg and du are rounded to it once, as operands; sums as in
  * the forward call, in an order fixed by the shape and the device.  dx may be
- * NULL, and dw_gate and dw_up together.  No output may overlap an input.
- * d_workspace: linear_swiglu_workspace_size(rows, width, hidden) bytes, 16-byte
- * aligned, any contents (else MP_EWORKSPACE).  Limits as in the forward call.
- * rows 0 writes zeros to the weights' gradients, hidden 0 to dx.  At most
- * five kernel launches. */
+ * NULL, and dw_gate and dw_up together; what the others are does not depend on
+ * that.  No output may overlap an input.
+ * d_workspace: linear_swiglu_workspace_size(rows, width, hidden) bytes (for the
+ * current device), 16-byte aligned, any contents (else MP_EWORKSPACE).  Limits as
+ * in the forward call.  rows 0 writes zeros to the weights' gradients, hidden 0 to
+ * dx.  At most four kernel launches. */
 MP_API size_t linear_swiglu_workspace_size(int64_t rows, int64_t width, int64_t hidden);
 MP_API mp_status linear_swiglu_backward(const void* dp, mp_dtype x_dtype, int64_t rows, int64_t width, int64_t hidden,
                                         const void* x, const void* w_gate, const void* w_up, const void* gate,

@@ -11,16 +11,25 @@
 //
 // One kernel does all of it: 256 x 256 tiles of a product on pairs of CTAs
 // (tcgen05, 128 rows of the tile in each CTA's TMEM), persistent, with roles by
-// warp: one copies operand tiles (TMA, six stages of 64 steps of the
-// contraction), one issues the matrix instructions, eight form the results.
-// The forward tile's 256 columns are 128 of g and the same 128 of u: the pair's
-// first CTA holds the gate weights' half of the operand and the second the up
-// weights', so the thread that has an element of g has that of u.
+// warp: two copy operand tiles (TMA, six stages of 64 steps of the contraction),
+// one issues the matrix instructions, eight form the results.  The forward
+// tile's 256 columns are 128 of g and the same 128 of u: the pair's first CTA
+// holds the gate weights' half of the operand and the second the up weights', so
+// the thread that has an element of g has that of u.  Backward, dx and the
+// weights' gradients are one launch, so that no pair waits between them.
 //
 // Sums: the tensor core adds to its binary32 accumulator by truncation, which
 // over a contraction of 4096 leaves results 4e-6 too small.  So every kRun
 // stages the sums so far leave TMEM and are added to registers with correct
 // rounding, while the next run goes into the other half of TMEM.
+//
+// Bound by the tensor pipe, which is active 89 % of the cycles of [2048 x 4096 x
+// 14336], and in a warm loop by the power limit: [8192 x 4096 x 14336] BF16
+// forward 972 us cold and 1060 warm (the library product of the same shape
+// without the activation 1030 and 1090), with an FP8 product and the 8-bit
+// checkpoint 1010 and 1150, whose runs are shorter; dx and the weights' gradients
+// 2260 and 2330 (2145 and 2240).  Small products are a chain of latencies: 12,600
+// cycles for one tile, half of them before and after its work.
 #include "mp_chain.cuh"
 #include "mp_ffn.cuh"
 
@@ -129,9 +138,7 @@ __device__ __forceinline__ void set_pair(uint32_t (&r)[32], int k, float2 v) {
 // One warp's way out: 32 rows of 128 or 64 bytes through its staging buffer,
 // so that eight or four lanes store a row's bytes together.  Unit c of 16 bytes
 // of row r lies at unit c ^ (r % 8), or c ^ (r / 2 % 4) of the shorter rows,
-// which spreads writes and reads over the banks.  (Tile copies out of the
-// buffer need a fence after the writes that took longer than the tile of a
-// short contraction: dw of one row 69 us, .)
+// which spreads writes and reads over the banks.
 struct Way {
   uint32_t stage;
   int lane;
@@ -237,7 +244,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
     if ((warp == kResultWarps || warp == kResultWarps + 2) && lane == 0) {
       // Operand tiles: one warp copies A's, another B's.  (One for both issued
       // up to four copies a stage and held the MN-major products back: the
-      // weights' gradients of 2048 x 4096 x 14336 took 366 us.)
+      // weights' gradients of 8192 x 4096 x 14336 took 1280 us, then 1125.)
       const bool is_b = warp != kResultWarps;
       const uint32_t bars = map_rank(smem_u32(full), 0), tiles = smem_u32(smem) + (is_b ? kOperandBytes : 0);
       uint32_t it = 0;

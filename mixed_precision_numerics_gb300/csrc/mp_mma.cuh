@@ -25,17 +25,13 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Orders nothing but tensor-memory accesses fenced before it (a release would
-// wait for the warp's global stores).
+// Orders nothing but tensor-memory accesses fenced before it.  A release would
+// wait for the warp's global stores: handing a run's tensor memory back took 2250
+// cycles that way and takes 310 (weights' gradients of one row of 4096 x 14336: 60
+// us and 41).
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
-  return p != 0;
-}
-
 // Registers of a warpgroup's threads from here on; the block's warpgroups
 // together stay within what it was launched with.
 template <int N>
