@@ -229,6 +229,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
     for (int b = 0; b < 2; ++b) mbar_init(tfull + b, 1), mbar_init(tempty + b, 2 * kResultWarps);
     fence_mbar_init();
   }
+  if (warp >= kResultWarps + 2) {  // the maps are on their way meanwhile
+    const Product& q = f.p[f.p[0].items == 0];
+    const bool of_a = warp & 1;
+    if (lane < (of_a ? (EP == STORE ? 2 : 1) : (EP == STORE && q.a_mn ? 1 : 2))) prefetch_tensor_map((of_a ? q.a : q.b) + lane);
+  }
   if (warp == kResultWarps + 1) tmem_alloc<2>(smem_u32(tmem_at), kTmemColumns);
   tmem_fence_before();
   __syncthreads();
@@ -577,7 +582,7 @@ void lay_out(Product& f, int matrices, int rows_of_tiles, int tiles_n, int split
 }
 
 // The gradients' products: tiles and stages of the contraction of dx (none up to
-// kFewRows rows, which have a kernel of their own) and of the weights' gradients,
+// kFewDxRows rows, which have a kernel of their own) and of the weights' gradients,
 // and into how many parts each is split along its contraction.  With all pairs
 // at work on both products each would have `even` stages to do; a tile longer
 // than that by a quarter or more is split into parts of at most about that length,
@@ -598,7 +603,7 @@ int splits_of(int64_t tiles, int blocks, int64_t even) {
 Plan plan_of(int64_t rows, int64_t width, int64_t hidden) {
   Plan p;
   const int64_t tiles_n = ceil_div(width, 2 * kHalf);
-  p.dx_tiles = rows <= kFewRows ? 0 : ceil_div(rows, 2 * kHalf) * tiles_n;
+  p.dx_tiles = rows <= kFewDxRows ? 0 : ceil_div(rows, 2 * kHalf) * tiles_n;
   p.dw_tiles = 2 * ceil_div(hidden, 2 * kHalf) * tiles_n;
   p.dx_blocks = 2 * ceil_div(hidden, kBlockK), p.dw_blocks = ceil_div(rows, kBlockK);
   const int64_t pairs = sm_count() / 2 < 1 ? 1 : sm_count() / 2;
@@ -754,13 +759,13 @@ extern "C" MP_API mp_status linear_swiglu_backward(const void* dp, mp_dtype x_dt
     const mp_status s = project<AGAIN>(bf16, x, w_gate, w_up, rows, width, hidden, o, st);
     if (s != MP_OK) return s;
   }
-  if (dx && rows <= kFewRows) {
+  if (dx && rows <= kFewDxRows) {
     const mp_status s = ffn_few_dx(bf16, dg, du, w_gate, w_up, rows, width, hidden, dx, st);
     if (s != MP_OK || !dw_gate) return s;
   }
   const Plan plan = plan_of(rows, width, hidden);
   Ffn f = {};
-  if (dx && rows > kFewRows) {
+  if (dx && rows > kFewDxRows) {
     Product& q = f.p[0];
     if (!map16(&q.a[0], dg, rows, hidden, hidden, kHalf) || !map16(&q.a[1], du, rows, hidden, hidden, kHalf) ||
         !map16(&q.b[0], w_gate, hidden, width, width, 64) || !map16(&q.b[1], w_up, hidden, width, width, 64))

@@ -17,7 +17,12 @@ enum {
 };
 
 constexpr int kBlockK = 64;    // steps of the contraction in a stage: 128 bytes
-constexpr int kFewRows = 128;
+// Up to this many rows the products have the kernel of few rows.  (Its time grows
+// with them: 128 rows of 4096 x 14336 47 us, the other kernel's 129 rows 49; of
+// 2048 x 5504 16.1 and 15.4.  dx has it up to fewer: above, it shares the launch of
+// the weights' gradients; 100 rows of 2048 x 5504 backward 39.6 us with a kernel
+// of its own, 129 rows without 33.8, 37 rows of 4096 x 14336 98 and 105.)
+constexpr int kFewRows = 128, kFewDxRows = 64;
 
 // Stages added up inside the tensor core before the sums move on to registers:
 // 512 terms where FP32 scales show the truncation (1024 would save 4 % of the
@@ -80,7 +85,7 @@ struct FfnOut {
 // x [rows, width] and the weights [hidden, width]: FWD16, FWD8 or AGAIN for up to kFewRows rows.
 mp_status ffn_few_project(int ep, bool bf16, const void* x, const void* w_gate, const void* w_up, int64_t rows,
                           int64_t width, int64_t hidden, const FfnOut& out, cudaStream_t st);
-// dx = dg w_gate + du w_up for up to kFewRows rows.
+// dx = dg w_gate + du w_up for up to kFewDxRows rows.
 mp_status ffn_few_dx(bool bf16, const void* dg, const void* du, const void* w_gate, const void* w_up, int64_t rows,
                      int64_t width, int64_t hidden, void* dx, cudaStream_t st);
 

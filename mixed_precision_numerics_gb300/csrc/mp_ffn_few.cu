@@ -35,7 +35,7 @@ struct Shape {
   static constexpr int kSumBytes = N * kMatrices * kTileRows * 4;
   // Two CTAs an SM have 113 KB each: two stages of 64 or more columns and two
   // matrices, and then one CTA with five is faster (1024 x 2816 for 64 rows 7.3
-  // us instead of 11.3); dx of 65 to 128 rows is not (2048 x 5504 44.8, 51.3).
+  // us instead of 11.3).
   static constexpr int kCtas = kMatrices == 2 && N >= 64 ? 1 : 2;
   static constexpr int kStages = ((kCtas == 2 ? 113 : 226) * 1024 - kBarrierBytes) / kStageBytes;
   static constexpr int kRing = kStages * kStageBytes;
@@ -167,6 +167,8 @@ __global__ __launch_bounds__(kThreads, Shape<N, EP>::kCtas) void k_ffn_few(const
     mbar_init(done, 1);
     fence_mbar_init();
   }
+  if (warp == 0 && lane < 2) prefetch_tensor_map(f.w + lane);
+  if (warp == 1 && lane < (EP == STORE ? 2 : 1)) prefetch_tensor_map(f.x + lane);
   if (warp == kResultWarps + 1) tmem_alloc<1>(smem_u32(tmem_at), S::kColumns);
   tmem_fence_before();
   __syncthreads();
@@ -315,8 +317,8 @@ template <bool BF16, int EP>
 mp_status by_rows(Few& f, int tiles, cudaStream_t st) {
   if (f.rows <= 16) return launch<BF16, 16, EP>(f, tiles, st);
   if (f.rows <= 32) return launch<BF16, 32, EP>(f, tiles, st);
-  if (f.rows <= 64) return launch<BF16, 64, EP>(f, tiles, st);
-  return launch<BF16, 128, EP>(f, tiles, st);
+  if (EP == STORE || f.rows <= 64) return launch<BF16, 64, EP>(f, tiles, st);  // dx: kFewDxRows
+  if constexpr (EP != STORE) return launch<BF16, 128, EP>(f, tiles, st);
 }
 template <int EP>
 mp_status by_type(bool bf16, Few& f, int tiles, cudaStream_t st) {
