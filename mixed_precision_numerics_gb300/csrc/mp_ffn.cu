@@ -30,28 +30,38 @@
 // checkpoint 1010 and 1150, whose runs are shorter; dx and the weights' gradients
 // 2260 and 2330 (2145 and 2240).  Small products are a chain of latencies: 12,600
 // cycles for one tile, half of them before and after its work.
+#include <type_traits>
+
 #include "mp_chain.cuh"
 #include "mp_ffn.cuh"
 
 namespace mp {
 namespace {
 
-constexpr int kStages = 6;
-constexpr int kHalf = 128;         // rows of a tile, and of its other operand, in one CTA
+constexpr int kHalf = 128;         // rows of a tile in one CTA
 constexpr int kOperandBytes = kHalf * kBlockK * 2;
-constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kResultWarps = 8;
+constexpr int kRingBytes = 192 * 1024;
 constexpr int kStagingBytes = 4096;  // 32 rows of 128 bytes, for each of those warps
 // Three warpgroups: two form results, with 128 sums a thread, one copies and
 // issues.  384 threads start with 168 registers each; the split adds up to that.
 constexpr int kThreads = (kResultWarps + 4) * 32;
 constexpr int kResultRegisters = 224, kOtherRegisters = 56;
 static_assert(kResultWarps * kResultRegisters + 4 * kOtherRegisters <= (kResultWarps + 4) * 168, "registers of a CTA");
-constexpr int kTmemColumns = 512;
+// A tile has W = 256 columns, or 128 where there are few tiles.
+template <int W>
+struct Wide {
+  static constexpr int kStageBytes = kOperandBytes + W / 2 * kBlockK * 2;  // half the columns' operand in each CTA
+  static constexpr int kStages = kRingBytes / kStageBytes;
+  static constexpr int kTmemColumns = 2 * W;
+  static constexpr int kChunks = W / 64;  // of 32 columns, in a thread
+  static constexpr int kHidden = W / 2;   // columns of g, and of u, in a forward tile
+};
+constexpr int kMostStages = Wide<128>::kStages;
 constexpr int kBarrierBytes = 256;
-constexpr int kSmem = kStages * kStageBytes + kResultWarps * kStagingBytes + 2 * 2 * kHalf * 4 + kBarrierBytes;
+constexpr int kSmem = kRingBytes + kResultWarps * kStagingBytes + 2 * 2 * kHalf * 4 + kBarrierBytes;
 static_assert(kSmem <= 232448, "227 KB a CTA");
-static_assert((2 * kStages + 4) * 8 + 8 <= kBarrierBytes, "barriers and the TMEM address");
+static_assert((2 * kMostStages + 4) * 8 + 8 <= kBarrierBytes, "barriers and the TMEM address");
 
 // One product in tiles.
 struct Product {
@@ -163,7 +173,15 @@ struct Way {
     }
     __syncwarp();
   }
-  // 64 values of each row, rounded
+  // 32 or 64 values of each row, rounded
+  template <bool BF16>
+  __device__ __forceinline__ void send16(const uint32_t (&r)[32], void* to, int64_t pitch, int rows, int cols) const {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      put64(c, make_uint4(pack16<BF16>(pair_of(r, 4 * c)), pack16<BF16>(pair_of(r, 4 * c + 1)),
+                          pack16<BF16>(pair_of(r, 4 * c + 2)), pack16<BF16>(pair_of(r, 4 * c + 3))));
+    send<64>(to, pitch * 2, rows, cols * 2);
+  }
   template <bool BF16>
   __device__ __forceinline__ void send16(const uint32_t (&lo)[32], const uint32_t (&hi)[32], void* to, int64_t pitch,
                                          int rows, int cols) const {
@@ -213,10 +231,13 @@ __device__ __forceinline__ uint32_t both_halves(uint32_t m, uint32_t* slot, int 
   return max(m, slot[(half ^ 1) * kHalf + row]);
 }
 
-template <bool BF16, int EP>
+template <bool BF16, int EP, int W>
 __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn f) {
+  using G = Wide<W>;
+  constexpr int kStages = G::kStages, kStageBytes = G::kStageBytes, N = G::kChunks, H = N / 2;
+  static_assert(EP != FWD8 || W == 256, "a tile of scales has 128 columns");
   extern __shared__ __align__(1024) unsigned char smem[];
-  unsigned char* const staging = smem + kStages * kStageBytes;
+  unsigned char* const staging = smem + kRingBytes;
   uint32_t* const red = reinterpret_cast<uint32_t*>(staging + kResultWarps * kStagingBytes);  // [2][2][128]
   uint64_t* const full = reinterpret_cast<uint64_t*>(red + 2 * 2 * kHalf);
   uint64_t *const empty = full + kStages, *const tfull = empty + kStages, *const tempty = tfull + 2;
@@ -234,7 +255,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
     const bool of_a = warp & 1;
     if (lane < (of_a ? (EP == STORE ? 2 : 1) : (EP == STORE && q.a_mn ? 1 : 2))) prefetch_tensor_map((of_a ? q.a : q.b) + lane);
   }
-  if (warp == kResultWarps + 1) tmem_alloc<2>(smem_u32(tmem_at), kTmemColumns);
+  if (warp == kResultWarps + 1) tmem_alloc<2>(smem_u32(tmem_at), G::kTmemColumns);
   tmem_fence_before();
   __syncthreads();
   cluster_sync();  // both CTAs' barriers stand
@@ -263,10 +284,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
           at = t.m * 2 * kHalf + rank * kHalf;
           map0 = q.a + t.of, map1 = q.a + 1;
         } else if (EP == STORE) {
-          at = t.n * 2 * kHalf + rank * kHalf;
+          at = t.n * W + rank * (W / 2);
           map0 = q.b, map1 = q.b + 1;
         } else {
-          at = t.n * kHalf;
+          at = t.n * G::kHidden;
           map0 = map1 = q.b + rank;
         }
         for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
@@ -279,7 +300,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
           const CUtensorMap* map = second ? map1 : map0;
           if (mn) {
             tma_load_2d_pair(to, map, at, k, bar);
-            tma_load_2d_pair(to + kMnBlockBytes, map, at + 64, k, bar);
+            if (W == 256 || !is_b) tma_load_2d_pair(to + kMnBlockBytes, map, at + 64, k, bar);
           } else {
             tma_load_2d_pair(to, map, k, at, bar);
           }
@@ -295,11 +316,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
         const Tile t = tile_of(q, w.item);
         constexpr bool B_MN = EP == STORE;
         const bool a_mn = B_MN && q.a_mn;
-        const uint32_t idesc = a_mn ? instr_desc<BF16, true, B_MN>(2 * kHalf, 2 * kHalf)
-                                    : instr_desc<BF16, false, B_MN>(2 * kHalf, 2 * kHalf);
+        const uint32_t idesc = a_mn ? instr_desc<BF16, true, B_MN>(2 * kHalf, W)
+                                    : instr_desc<BF16, false, B_MN>(2 * kHalf, W);
         const uint32_t step = a_mn ? kDescStep<true> : kDescStep<false>;
         for (int k0 = t.k0; k0 < t.k1 && ok; k0 += kRun<EP>, ++chunk) {
-          const uint32_t b = chunk & 1, d = tmem + b * 2 * kHalf;
+          const uint32_t b = chunk & 1, d = tmem + b * W;
           if (!(ok = mbar_wait_bounded(tempty + b, ((chunk >> 1) & 1) ^ 1))) break;
           tmem_fence_after();
           const int k1 = min(t.k1, k0 + kRun<EP>);
@@ -330,16 +351,18 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
       const Product& q = f.p[w.which];
       const Tile t = tile_of(q, w.item);
       const int row0 = t.m * 2 * kHalf + rank * kHalf + quad * 32, row = row0 + lane;
-      // FWD, AGAIN: acc[0..1] are 64 columns of g, acc[2..3] of u.  STORE: 128 columns.
-      uint32_t acc[4][32];
-      auto column = [&](int j) { return EP == STORE ? half * 128 + j * 32 : (j >> 1) * 128 + half * 64 + (j & 1) * 32; };
+      // FWD, AGAIN: acc[j] are 32 columns of g and acc[H + j] the same of u.  STORE: half of the tile's columns.
+      uint32_t acc[N][32];
+      auto column = [&](int j) {
+        return EP == STORE ? half * (W / 2) + j * 32 : j / H * G::kHidden + half * (W / 4) + j % H * 32;
+      };
       // Waits for a run's sums; where they are.  After a wait that gave up, the
       // warp goes through its steps (others may wait for it at a barrier)
       // without waiting or storing.
       auto run_done = [&]() {
         ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(tfull + (chunk & 1), (chunk >> 1) & 1));
         tmem_fence_after();
-        return lanes + (chunk & 1) * 2 * kHalf;
+        return lanes + (chunk & 1) * W;
       };
       auto run_read = [&]() {  // their place is free
         tmem_fence_before();
@@ -350,10 +373,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
       {  // the first run's sums straight to where they stay
         const uint32_t at = run_done();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) tmem_load32(acc[j], at + column(j));
+        for (int j = 0; j < N; ++j) tmem_load32(acc[j], at + column(j));
         tmem_wait();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) loaded(acc[j]);
+        for (int j = 0; j < N; ++j) loaded(acc[j]);
         run_read();
       }
       for (int k0 = t.k0 + kRun<EP>; k0 < t.k1; k0 += kRun<EP>) {
@@ -362,10 +385,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
         uint32_t r[2][16];
         tmem_load16(r[0], at + column(0));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 2 * N; ++j) {
           tmem_wait();
           loaded(r[j & 1]);
-          if (j < 7) tmem_load16(r[(j + 1) & 1], at + column((j + 1) >> 1) + ((j + 1) & 1) * 16);
+          if (j < 2 * N - 1) tmem_load16(r[(j + 1) & 1], at + column((j + 1) >> 1) + ((j + 1) & 1) * 16);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const float2 v = make_float2(__uint_as_float(r[j & 1][2 * k]), __uint_as_float(r[j & 1][2 * k + 1]));
@@ -378,12 +401,12 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
       const int rows = ok ? q.rows : 0;
 
       if constexpr (EP == STORE) {
-        const int col0 = t.n * 2 * kHalf + half * 128;
-        if (q.splits > 1) {
+        const int col0 = t.n * W + half * (W / 2);
+        if (W == 256 && q.splits > 1) {  // narrow tiles are not split
           float* const to = q.parts + ((int64_t)t.split * q.matrices + t.of) * q.rows * q.cols +
                             (int64_t)row0 * q.cols + col0;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < N; ++j) {
 #pragma unroll
             for (int c = 0; c < 8; ++c)
               way.put128(c, make_uint4(acc[j][4 * c], acc[j][4 * c + 1], acc[j][4 * c + 2], acc[j][4 * c + 3]));
@@ -392,24 +415,35 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
         } else {
           uint16_t* const to = static_cast<uint16_t*>(q.result[t.of]) + (int64_t)row0 * q.cols + col0;
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < H; ++j)
             way.send16<BF16>(acc[2 * j], acc[2 * j + 1], to + j * 64, q.cols, rows - row0, q.cols - col0 - j * 64);
         }
       } else {
-        const int col0 = t.n * kHalf + half * 64;
+        const int col0 = t.n * G::kHidden + half * (W / 4);
         const int down = rows - row0, across = q.cols - col0;  // what is left of the matrix
         const int64_t at = (int64_t)row0 * q.cols + col0;
-        if (col0 + 64 > q.cols) {  // columns past the end: 0 * inf has made NaN of them in a row with infinities
+        // 32 H rounded columns from acc[first] on
+        auto send = [&](auto first, void* base, int64_t from, int64_t pitch) {
+          constexpr int k = decltype(first)::value;
+          uint16_t* const to = static_cast<uint16_t*>(base) + from;
+          if constexpr (H == 2)
+            way.send16<BF16>(acc[k], acc[k + 1], to, pitch, down, across);
+          else
+            way.send16<BF16>(acc[k], to, pitch, down, across);
+        };
+        constexpr auto of_g = std::integral_constant<int, 0>{};
+        constexpr auto of_u = std::integral_constant<int, H>{};
+        if (col0 + W / 4 > q.cols) {  // columns past the end: 0 * inf has made NaN of them in a row with infinities
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < N; ++j)
 #pragma unroll
-            for (int k = 0; k < 32; ++k) acc[j][k] = col0 + (j & 1) * 32 + k < q.cols ? acc[j][k] : 0u;
+            for (int k = 0; k < 32; ++k) acc[j][k] = col0 + j % H * 32 + k < q.cols ? acc[j][k] : 0u;
         }
         if constexpr (EP == AGAIN) {
           const uint4* from = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(f.o.dp) +
                                                               ((int64_t)row * q.cols + col0));
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
+          for (int c = 0; c < 4 * H; ++c) {
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
             if (row < rows && col0 + c * 8 < q.cols) v = ld_plain(from + c);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -417,43 +451,41 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
             for (int i = 0; i < 4; ++i) {
               const int j = c >> 2, k = (c & 3) * 4 + i;
               float2 dg, du;
-              slopes(pair16<BF16>(w[i]), pair_of(acc[j], k), pair_of(acc[2 + j], k), &dg, &du);
+              slopes(pair16<BF16>(w[i]), pair_of(acc[j], k), pair_of(acc[H + j], k), &dg, &du);
               set_pair(acc[j], k, dg);
-              set_pair(acc[2 + j], k, du);
+              set_pair(acc[H + j], k, du);
             }
           }
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            way.send16<BF16>(acc[2 * j], acc[2 * j + 1], static_cast<uint16_t*>(j ? f.o.du : f.o.dg) + at, q.cols, down, across);
+          send(of_g, f.o.dg, at, q.cols);
+          send(of_u, f.o.du, at, q.cols);
         } else {
           const int tile = t.n;  // 128 columns are a tile of scales
           if (f.o.gate) {
             const int64_t kept = (int64_t)row0 * f.o.ld + col0;
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              way.send16<BF16>(acc[2 * j], acc[2 * j + 1], static_cast<uint16_t*>(j ? f.o.up : f.o.gate) + kept, f.o.ld, down,
-                               across);
+            send(of_g, f.o.gate, kept, f.o.ld);
+            send(of_u, f.o.up, kept, f.o.ld);
           }
-          if (f.o.ckpt) {
+          if constexpr (W == 256)  // a tile of scales has 128 columns
+            if (f.o.ckpt) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t m = both_halves(max(amax32(acc[2 * j]), amax32(acc[2 * j + 1])), red + j * 2 * kHalf, half,
-                                             in_cta, quad);
-              float mul;
-              const float scale = tile_scale(m, 448.0f, &mul);
-              if (half == 0 && row < rows) f.o.ckpt_scales[((int64_t)j * q.rows + row) * f.o.tiles + tile] = scale;
-              codes32(acc[2 * j], way, 0, m, mul, false, false);
-              codes32(acc[2 * j + 1], way, 2, m, mul, false, false);
-              way.send<64>(f.o.ckpt + (int64_t)j * q.rows * q.cols + at, q.cols, down, across);
+              for (int j = 0; j < 2; ++j) {
+                const uint32_t m = both_halves(max(amax32(acc[2 * j]), amax32(acc[2 * j + 1])), red + j * 2 * kHalf, half,
+                                               in_cta, quad);
+                float mul;
+                const float scale = tile_scale(m, 448.0f, &mul);
+                if (half == 0 && row < rows) f.o.ckpt_scales[((int64_t)j * q.rows + row) * f.o.tiles + tile] = scale;
+                codes32(acc[2 * j], way, 0, m, mul, false, false);
+                codes32(acc[2 * j + 1], way, 2, m, mul, false, false);
+                way.send<64>(f.o.ckpt + (int64_t)j * q.rows * q.cols + at, q.cols, down, across);
+              }
+              named_barrier(1 + quad, 64);  // the slots have been read
             }
-            named_barrier(1 + quad, 64);  // the slots have been read
-          }
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < H; ++j)
 #pragma unroll
-            for (int k = 0; k < 16; ++k) set_pair(acc[j], k, gated(pair_of(acc[j], k), pair_of(acc[2 + j], k)));
+            for (int k = 0; k < 16; ++k) set_pair(acc[j], k, gated(pair_of(acc[j], k), pair_of(acc[H + j], k)));
           if constexpr (EP == FWD16) {
-            way.send16<BF16>(acc[0], acc[1], static_cast<uint16_t*>(f.o.p) + at, q.cols, down, across);
+            send(of_g, f.o.p, at, q.cols);
           } else {
             uint32_t m[2] = {amax32(acc[0]), amax32(acc[1])};
             float mul[2];
@@ -485,7 +517,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
   __syncthreads();
   cluster_sync();  // no CTA leaves while the other's instructions may read or signal it
   tmem_fence_after();
-  if (warp == kResultWarps + 1) tmem_free<2>(tmem, kTmemColumns);
+  if (warp == kResultWarps + 1) tmem_free<2>(tmem, G::kTmemColumns);
 }
 
 // Adds the parts of up to two products split along their contraction, in order,
@@ -520,6 +552,14 @@ __global__ __launch_bounds__(256) void k_ffn_join(const __grid_constant__ Join f
 
 // What a tile costs, in stages: a short one waits for its results' way out.
 int64_t cost_of(int blocks) { return blocks > 6 ? blocks : 6; }
+// The same of a tile of 128 columns, in stages of the wider one: half of its
+// matrix instructions, but three quarters of its operands, which bound it where
+// all pairs copy (2048 x 4096 x 14336 forward 338 us, in tiles of 256 250).
+int64_t narrow_cost(int blocks, bool all_pairs) {
+  const int64_t c = (int64_t)blocks * (all_pairs ? 11 : 9) / 16;
+  return c > 4 ? c : 4;
+}
+constexpr int kJoinStages = 22;  // what parts cost: their way through memory and the launch that joins them
 
 // Evens out what the pairs have to do (Walk): those without the last turn's
 // item of the first product take as many stages of the second product ahead.
@@ -533,10 +573,10 @@ void share(Ffn& f, int pairs) {
   f.ahead = longer < b.items / others ? longer : b.items / others;
 }
 
-template <bool BF16, int EP>
+template <bool BF16, int EP, int W>
 mp_status launch(Ffn& f, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  const auto kernel = k_ffn<BF16, EP>;
+  const auto kernel = k_ffn<BF16, EP, W>;
   if (!smem_opt_in(kernel, kSmem, done)) return MP_ECUDA;
   const int64_t items = (int64_t)f.p[0].items + f.p[1].items, most = sm_count() < 2 ? 1 : sm_count() / 2;
   const int pairs = (int)(items < most ? items : most);
@@ -587,11 +627,14 @@ void lay_out(Product& f, int matrices, int rows_of_tiles, int tiles_n, int split
 // at work on both products each would have `even` stages to do; a tile longer
 // than that by a quarter or more is split into parts of at most about that length,
 // of four stages at least, if that saves more than the parts' way through memory
-// costs (16 stages take 4 us).  Whichever gradients are asked for, the parts are
+// costs (16 stages take 4 us).  Where whole tiles of 128 columns end earlier by
+// these costs, they are taken (2048 x 256 x 688 11.0 us, in tiles of 256, split, 15.7;
+// 1500 x 768 x 2048 21.9 and 23.5; 500 x 1024 x 2816 27.5 and 18.2).  Whichever gradients are asked for, the parts are
 // these, so that results do not depend on that.
 struct Plan {
   int64_t dx_tiles, dw_tiles;
   int dx_blocks, dw_blocks, dx_splits, dw_splits;
+  bool narrow;                // tiles of 128 columns
   size_t dx_parts, dw_parts;  // bytes
 };
 int splits_of(int64_t tiles, int blocks, int64_t even) {
@@ -602,21 +645,39 @@ int splits_of(int64_t tiles, int blocks, int64_t even) {
 }
 Plan plan_of(int64_t rows, int64_t width, int64_t hidden) {
   Plan p;
-  const int64_t tiles_n = ceil_div(width, 2 * kHalf);
-  p.dx_tiles = rows <= kFewDxRows ? 0 : ceil_div(rows, 2 * kHalf) * tiles_n;
-  p.dw_tiles = 2 * ceil_div(hidden, 2 * kHalf) * tiles_n;
   p.dx_blocks = 2 * ceil_div(hidden, kBlockK), p.dw_blocks = ceil_div(rows, kBlockK);
   const int64_t pairs = sm_count() / 2 < 1 ? 1 : sm_count() / 2;
-  const int64_t even = (p.dx_tiles * cost_of(p.dx_blocks) + p.dw_tiles * cost_of(p.dw_blocks) + pairs - 1) / pairs;
-  p.dx_splits = splits_of(p.dx_tiles, p.dx_blocks, even), p.dw_splits = splits_of(p.dw_tiles, p.dw_blocks, even);
+  const auto tiles = [&](int columns) {
+    p.dx_tiles = rows <= kFewDxRows ? 0 : (int64_t)ceil_div(rows, 2 * kHalf) * ceil_div(width, columns);
+    p.dw_tiles = 2ll * ceil_div(hidden, 2 * kHalf) * ceil_div(width, columns);
+  };
+  const auto even = [&](int64_t dx, int64_t dw) { return (p.dx_tiles * dx + p.dw_tiles * dw + pairs - 1) / pairs; };
+  const auto longest = [&](int64_t dx, int64_t dw) { return p.dx_tiles && dx > dw ? dx : dw; };
+  // in tiles of 128 columns, whole
+  tiles(128);
+  const bool many = p.dx_tiles + p.dw_tiles > pairs;
+  const int64_t dx1 = narrow_cost(p.dx_blocks, many), dw1 = narrow_cost(p.dw_blocks, many), all1 = even(dx1, dw1);
+  const int64_t narrow = all1 > longest(dx1, dw1) ? all1 : longest(dx1, dw1);
+  // in tiles of 256, split
+  tiles(256);
+  const int64_t all = even(cost_of(p.dx_blocks), cost_of(p.dw_blocks));
+  p.dx_splits = splits_of(p.dx_tiles, p.dx_blocks, all), p.dw_splits = splits_of(p.dw_tiles, p.dw_blocks, all);
+  const int64_t part = longest(p.dx_blocks / p.dx_splits, p.dw_blocks / p.dw_splits);
+  const int64_t wide = (all > part ? all : part) + (p.dx_splits > 1 || p.dw_splits > 1 ? kJoinStages : 0);
+  p.narrow = narrow < wide;
+  if (p.narrow) {
+    tiles(128);
+    p.dx_splits = p.dw_splits = 1;
+  }
   p.dx_parts = p.dx_splits > 1 ? (size_t)p.dx_splits * rows * width * 4 : 0;
   p.dw_parts = p.dw_splits > 1 ? (size_t)p.dw_splits * 2 * hidden * width * 4 : 0;
   return p;
 }
 
 // The products of f, and the joining of those that are split.
-mp_status multiply(bool bf16, Ffn& f, cudaStream_t st) {
-  const mp_status s = bf16 ? launch<true, STORE>(f, st) : launch<false, STORE>(f, st);
+mp_status multiply(bool bf16, bool narrow, Ffn& f, cudaStream_t st) {
+  const mp_status s = bf16 ? narrow ? launch<true, STORE, 128>(f, st) : launch<true, STORE, 256>(f, st)
+                           : narrow ? launch<false, STORE, 128>(f, st) : launch<false, STORE, 256>(f, st);
   if (s != MP_OK) return s;
   Join j = {};
   unsigned ctas[2] = {0, 0};
@@ -645,6 +706,16 @@ bool pitch_ok(int64_t ld, int64_t cols, int64_t rows) {
   return rows <= 1 || (ld >= cols && ld < (1ll << 61) / rows && ld % 8 == 0);
 }
 
+// Whether tiles of 128 columns end earlier, by the longest pair's work (301 x
+// 1040 x 1456 9 us, in tiles of 256 11.7; 200 x 1024 x 2048 6.8 and 8.9; 700 x 4096 x
+// 4096 46 and 40.5).
+bool narrow_forward(int64_t tiles_m, int64_t hidden, int blocks) {
+  const int64_t pairs = sm_count() < 2 ? 1 : sm_count() / 2;
+  const auto waves = [&](int columns) { return (tiles_m * ceil_div(hidden, columns) + pairs - 1) / pairs; };
+  const int64_t narrow = waves(Wide<128>::kHidden);
+  return narrow * narrow_cost(blocks, narrow > 1) < waves(Wide<256>::kHidden) * cost_of(blocks);
+}
+
 // Forms g and u (FWD16, FWD8, AGAIN).
 template <int EP>
 mp_status project(bool bf16, const void* x, const void* w_gate, const void* w_up, int64_t rows, int64_t width,
@@ -652,14 +723,19 @@ mp_status project(bool bf16, const void* x, const void* w_gate, const void* w_up
   if (rows <= kFewRows) return ffn_few_project(EP, bf16, x, w_gate, w_up, rows, width, hidden, o, st);
   Ffn f = {};
   Product& q = f.p[0];
-  if (!map16(&q.a[0], x, rows, width, width, kHalf) || !map16(&q.b[0], w_gate, hidden, width, width, kHalf) ||
-      !map16(&q.b[1], w_up, hidden, width, width, kHalf))
+  q.blocks = q.blocks0 = ceil_div(width, kBlockK);
+  const bool narrow = EP != FWD8 && !o.ckpt && narrow_forward(ceil_div(rows, 2 * kHalf), hidden, q.blocks);
+  const int box = narrow ? Wide<128>::kHidden : Wide<256>::kHidden;
+  if (!map16(&q.a[0], x, rows, width, width, kHalf) || !map16(&q.b[0], w_gate, hidden, width, width, box) ||
+      !map16(&q.b[1], w_up, hidden, width, width, box))
     return MP_ECUDA;
   f.o = o;
-  q.blocks = q.blocks0 = ceil_div(width, kBlockK);
   q.rows = (int32_t)rows, q.cols = (int32_t)hidden;
-  lay_out(q, 1, ceil_div(rows, 2 * kHalf), ceil_div(hidden, kHalf), 1, kForwardShift);
-  return bf16 ? launch<true, EP>(f, st) : launch<false, EP>(f, st);
+  lay_out(q, 1, ceil_div(rows, 2 * kHalf), ceil_div(hidden, box), 1, kForwardShift);
+  if constexpr (EP != FWD8) {
+    if (narrow) return bf16 ? launch<true, EP, 128>(f, st) : launch<false, EP, 128>(f, st);
+  }
+  return bf16 ? launch<true, EP, 256>(f, st) : launch<false, EP, 256>(f, st);
 }
 
 }  // namespace
@@ -773,7 +849,7 @@ extern "C" MP_API mp_status linear_swiglu_backward(const void* dp, mp_dtype x_dt
     q.blocks0 = plan.dx_blocks / 2, q.blocks = plan.dx_blocks;
     q.rows = (int32_t)rows, q.cols = (int32_t)width;
     q.result[0] = dx, q.parts = reinterpret_cast<float*>(parts);
-    lay_out(q, 1, ceil_div(rows, 2 * kHalf), ceil_div(width, 2 * kHalf), plan.dx_splits, kGradientShift);
+    lay_out(q, 1, ceil_div(rows, 2 * kHalf), ceil_div(width, plan.narrow ? 128 : 256), plan.dx_splits, kGradientShift);
   }
   if (dw_gate) {
     Product& q = f.p[1];
@@ -783,7 +859,7 @@ extern "C" MP_API mp_status linear_swiglu_backward(const void* dp, mp_dtype x_dt
     q.blocks0 = q.blocks = plan.dw_blocks, q.a_mn = true;
     q.rows = (int32_t)hidden, q.cols = (int32_t)width;
     q.result[0] = dw_gate, q.result[1] = dw_up, q.parts = reinterpret_cast<float*>(parts + up256(plan.dx_parts));
-    lay_out(q, 2, ceil_div(hidden, 2 * kHalf), ceil_div(width, 2 * kHalf), plan.dw_splits, kGradientShift);
+    lay_out(q, 2, ceil_div(hidden, 2 * kHalf), ceil_div(width, plan.narrow ? 128 : 256), plan.dw_splits, kGradientShift);
   }
-  return multiply(bf16, f, st);
+  return multiply(bf16, plan.narrow, f, st);
 }
