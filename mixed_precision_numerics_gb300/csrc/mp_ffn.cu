@@ -66,7 +66,7 @@ static_assert((2 * kMostStages + 4) * 8 + 8 <= kBarrierBytes, "barriers and the 
 // One product in tiles.
 struct Product {
   CUtensorMap a[2], b[2];
-  int32_t items, tiles_m, shift;  // work items = tiles * splits; 2^shift rows of tiles to a band
+  int32_t items, tiles_m;  // work items = tiles * splits
   FastDiv tiles, band, last, per_matrix;  // tiles of a split, of a band; rows of tiles in the last band, in a matrix
   int32_t blocks0, blocks, splits, matrices;  // stages of the contraction in the first operand pair, and in all
   int32_t rows, cols;      // of a result matrix
@@ -114,10 +114,20 @@ __device__ unsigned int g_ffn_wait_failures;  // bounded waits that gave up (rea
 struct Tile {
   int32_t m, n, k0, k1, split, of;  // row and column of tiles, stages from k0 to k1, which matrix
 };
-// Items walk the tiles in bands of 2^shift rows of tiles, column by column, so
+// Items walk the tiles in bands of kBand rows of tiles, column by column, so
 // that those in flight together share operands in L2; all tiles of a split
-// first.  (Every role does this for every tile, one thread after another: with
-// plain divisions the tiles of short contractions waited for it.)
+// first.  (Every role does this for every tile, one thread after another: plain
+// divisions, or a band whose height is not a constant, take 300 cycles of a tile
+// that has 3,000 where the contraction is short.)
+//
+// A band has 16 rows of tiles in the forward product and 8 in the gradients'.  A
+// wave of 76 tiles that is 8 x 9.5 has the fewest different operand rows; twice
+// as high a band reads the weights half as often, which pays where the band's
+// rows of x stay in L2 (8192 x 4096 x 14336: 16 rows 1057 us, 8 1083, 32 1131;
+// gradients 8 rows 2410 us, 16 2445, 32 2522).
+template <int EP>
+constexpr int kBand = EP == STORE ? 8 : 16;
+template <int BAND>
 __device__ __forceinline__ Tile tile_of(const Product& f, uint32_t item) {
   Tile t;
   t.split = 0, t.k0 = 0, t.k1 = f.blocks;
@@ -129,9 +139,9 @@ __device__ __forceinline__ Tile tile_of(const Product& f, uint32_t item) {
   }
   const uint32_t band = div_by(item, f.band);
   item -= band * f.band.d;
-  const bool whole = (int)((band + 1) << f.shift) <= f.tiles_m;
-  t.n = whole ? item >> f.shift : div_by(item, f.last);
-  t.m = (band << f.shift) + item - t.n * (whole ? 1 << f.shift : f.last.d);
+  const bool whole = (int)(band + 1) * BAND <= f.tiles_m;
+  t.n = whole ? item / BAND : div_by(item, f.last);
+  t.m = band * BAND + item - t.n * (whole ? BAND : f.last.d);
   t.of = div_by(t.m, f.per_matrix);  // 0 unless two matrices are stored
   t.m -= t.of * f.per_matrix.d;
   return t;
@@ -276,7 +286,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
       uint32_t it = 0;
       for (Walk w(f); ok && w.next(f);) {
         const Product& q = f.p[w.which];
-        const Tile t = tile_of(q, w.item);
+        const Tile t = tile_of<kBand<EP>>(q, w.item);
         const bool mn = EP == STORE && (is_b || q.a_mn);
         int at;                             // the first of the tile's 128 rows of this operand in this CTA
         const CUtensorMap *map0, *map1;     // of the first operand pair and of the second
@@ -313,7 +323,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
       uint32_t it = 0, chunk = 0;
       for (Walk w(f); ok && w.next(f);) {
         const Product& q = f.p[w.which];
-        const Tile t = tile_of(q, w.item);
+        const Tile t = tile_of<kBand<EP>>(q, w.item);
         constexpr bool B_MN = EP == STORE;
         const bool a_mn = B_MN && q.a_mn;
         const uint32_t idesc = a_mn ? instr_desc<BF16, true, B_MN>(2 * kHalf, W)
@@ -349,7 +359,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
     uint32_t chunk = 0;
     for (Walk w(f); w.next(f);) {
       const Product& q = f.p[w.which];
-      const Tile t = tile_of(q, w.item);
+      const Tile t = tile_of<kBand<EP>>(q, w.item);
       const int row0 = t.m * 2 * kHalf + rank * kHalf + quad * 32, row = row0 + lane;
       // FWD, AGAIN: acc[j] are 32 columns of g and acc[H + j] the same of u.  STORE: half of the tile's columns.
       uint32_t acc[N][32];
@@ -550,37 +560,47 @@ __global__ __launch_bounds__(256) void k_ffn_join(const __grid_constant__ Join f
   *reinterpret_cast<uint4*>(to) = make_uint4(pack16<BF16>(v[0]), pack16<BF16>(v[1]), pack16<BF16>(v[2]), pack16<BF16>(v[3]));
 }
 
-// What a tile costs, in stages: a short one waits for its results' way out.
-int64_t cost_of(int blocks) { return blocks > 6 ? blocks : 6; }
-// The same of a tile of 128 columns, in stages of the wider one: half of its
-// matrix instructions, but three quarters of its operands, which bound it where
-// all pairs copy (2048 x 4096 x 14336 forward 338 us, in tiles of 256 250).
-int64_t narrow_cost(int blocks, bool all_pairs) {
-  const int64_t c = (int64_t)blocks * (all_pairs ? 11 : 9) / 16;
-  return c > 4 ? c : 4;
-}
-constexpr int kJoinStages = 22;  // what parts cost: their way through memory and the launch that joins them
+// Pairs of CTAs that the device runs at once.
+int64_t most_pairs() { return sm_count() < 2 ? 1 : sm_count() / 2; }
 
-// Evens out what the pairs have to do (Walk): those without the last turn's
-// item of the first product take as many stages of the second product ahead.
-void share(Ffn& f, int pairs) {
-  const Product &a = f.p[0], &b = f.p[1];
-  f.long_pairs = a.items % pairs, f.ahead = 0;
-  const int others = pairs - f.long_pairs;
-  if (f.long_pairs == 0 || b.items == 0) return;
-  const int64_t one = cost_of(b.blocks / b.splits);
-  const int longer = (int)((cost_of(a.blocks / a.splits) + one / 2) / one);
-  f.ahead = longer < b.items / others ? longer : b.items / others;
+// Evens out what the pairs have to do (Walk) with `a` items of the first product
+// and `b` of the second: those without the last turn's item of the first take as
+// many stages of the second ahead.  (A tile of a short contraction takes six
+// stages' time, for its results' way out.)
+struct Turns {
+  int long_pairs, ahead;
+};
+Turns turns_of(int64_t a, int64_t a_stages, int64_t b, int64_t b_stages, int64_t pairs) {
+  Turns t{(int)(a % pairs), 0};
+  if (t.long_pairs == 0 || b == 0) return t;
+  const int64_t one = b_stages > 6 ? b_stages : 6, longer = ((a_stages > 6 ? a_stages : 6) + one / 2) / one;
+  const int64_t others = pairs - t.long_pairs;
+  t.ahead = (int)(longer < b / others ? longer : b / others);
+  return t;
 }
+// When the last pair is done, in stages of 256 columns, results' way out included.
+int64_t end_of(int64_t a, int64_t a_stages, int64_t a_out, int64_t b, int64_t b_stages, int64_t b_out) {
+  const int64_t pairs = a + b < most_pairs() ? a + b : most_pairs();
+  const Turns t = turns_of(a, a_stages, b, b_stages, pairs);
+  const int64_t rest = (b - t.ahead * (pairs - t.long_pairs) + pairs - 1) / pairs, each = a / pairs;
+  const int64_t ca = a_stages + a_out, cb = b_stages + b_out;
+  const int64_t longs = t.long_pairs ? (each + 1) * ca + rest * cb : 0, others = each * ca + (t.ahead + rest) * cb;
+  return longs > others ? longs : others;
+}
+// Stages of 256 columns that stages of 128 take: half the matrix instructions, but
+// three quarters of the operands, and their copies bound them.
+int64_t narrow_stages(int64_t blocks) { return (blocks * 7 + 7) / 8; }
 
 template <bool BF16, int EP, int W>
 mp_status launch(Ffn& f, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   const auto kernel = k_ffn<BF16, EP, W>;
   if (!smem_opt_in(kernel, kSmem, done)) return MP_ECUDA;
-  const int64_t items = (int64_t)f.p[0].items + f.p[1].items, most = sm_count() < 2 ? 1 : sm_count() / 2;
-  const int pairs = (int)(items < most ? items : most);
-  share(f, pairs);
+  const Product &a = f.p[0], &b = f.p[1];
+  const int64_t items = (int64_t)a.items + b.items;
+  const int pairs = (int)(items < most_pairs() ? items : most_pairs());
+  const Turns t = turns_of(a.items, a.items ? a.blocks / a.splits : 0, b.items, b.items ? b.blocks / b.splits : 0, pairs);
+  f.long_pairs = t.long_pairs, f.ahead = t.ahead;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
@@ -604,21 +624,12 @@ mp_status launch(Ffn& f, cudaStream_t st) {
 bool type16(mp_dtype t) { return t == MP_F16 || t == MP_BF16; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 // Tiles, and the walk over them.
-//
-// How high a band is: 16 rows of tiles in the forward product and 8 in the
-// gradients'.  A wave of 76 tiles that is 8 x 9.5 has the fewest different
-// operand rows; twice as high a band reads the weights half as often, which pays
-// where the band's rows of x stay in L2 (8192 x 4096 x 14336: 16 rows 1057 us, 8
-// 1083, 32 1131; gradients 8 rows 2410 us, 16 2445, 32 2522).
-constexpr int kForwardShift = 4, kGradientShift = 3;
-void lay_out(Product& f, int matrices, int rows_of_tiles, int tiles_n, int splits, int shift) {
+void lay_out(Product& f, int matrices, int rows_of_tiles, int tiles_n, int splits, int band) {
   f.matrices = matrices, f.splits = splits;
   f.tiles_m = matrices * rows_of_tiles;
   f.items = f.tiles_m * tiles_n * splits;
-  f.shift = shift;
-  const int high = 1 << shift;
-  f.tiles = fast_div(f.tiles_m * tiles_n), f.band = fast_div(high * tiles_n);
-  f.last = fast_div(f.tiles_m % high ? f.tiles_m % high : high), f.per_matrix = fast_div(rows_of_tiles);
+  f.tiles = fast_div(f.tiles_m * tiles_n), f.band = fast_div(band * tiles_n);
+  f.last = fast_div(f.tiles_m % band ? f.tiles_m % band : band), f.per_matrix = fast_div(rows_of_tiles);
 }
 
 // The gradients' products: tiles and stages of the contraction of dx (none up to
@@ -626,11 +637,14 @@ void lay_out(Product& f, int matrices, int rows_of_tiles, int tiles_n, int split
 // and into how many parts each is split along its contraction.  With all pairs
 // at work on both products each would have `even` stages to do; a tile longer
 // than that by a quarter or more is split into parts of at most about that length,
-// of four stages at least, if that saves more than the parts' way through memory
-// costs (16 stages take 4 us).  Where whole tiles of 128 columns end earlier by
-// these costs, they are taken (2048 x 256 x 688 11.0 us, in tiles of 256, split, 15.7;
-// 1500 x 768 x 2048 21.9 and 23.5; 500 x 1024 x 2816 27.5 and 18.2).  Whichever gradients are asked for, the parts are
-// these, so that results do not depend on that.
+// of four stages at least, if that saves 16 stages, what the parts' way through
+// memory costs.  Or both products have whole tiles of 128 columns, where that
+// ends a sixth earlier by what the steps have measured: a tile's results take 6
+// stages' time on their way out, 3 with 128 columns, 11 in parts, and the launch
+// that joins them 24 (2048 x 256 x 688 11.5 us, in tiles of 256, split, 16.1; 1024 x
+// 1024 x 256 7.5 and 8.6; 301 x 1040 x 1456 18.3 and 15.8; 260 x 768 x 2992 28.8 and
+// 18.8).  Whichever gradients are asked for, the tiles and parts are these, so
+// that results do not depend on that.
 struct Plan {
   int64_t dx_tiles, dw_tiles;
   int dx_blocks, dw_blocks, dx_splits, dw_splits;
@@ -646,25 +660,21 @@ int splits_of(int64_t tiles, int blocks, int64_t even) {
 Plan plan_of(int64_t rows, int64_t width, int64_t hidden) {
   Plan p;
   p.dx_blocks = 2 * ceil_div(hidden, kBlockK), p.dw_blocks = ceil_div(rows, kBlockK);
-  const int64_t pairs = sm_count() / 2 < 1 ? 1 : sm_count() / 2;
   const auto tiles = [&](int columns) {
     p.dx_tiles = rows <= kFewDxRows ? 0 : (int64_t)ceil_div(rows, 2 * kHalf) * ceil_div(width, columns);
     p.dw_tiles = 2ll * ceil_div(hidden, 2 * kHalf) * ceil_div(width, columns);
   };
-  const auto even = [&](int64_t dx, int64_t dw) { return (p.dx_tiles * dx + p.dw_tiles * dw + pairs - 1) / pairs; };
-  const auto longest = [&](int64_t dx, int64_t dw) { return p.dx_tiles && dx > dw ? dx : dw; };
-  // in tiles of 128 columns, whole
   tiles(128);
-  const bool many = p.dx_tiles + p.dw_tiles > pairs;
-  const int64_t dx1 = narrow_cost(p.dx_blocks, many), dw1 = narrow_cost(p.dw_blocks, many), all1 = even(dx1, dw1);
-  const int64_t narrow = all1 > longest(dx1, dw1) ? all1 : longest(dx1, dw1);
-  // in tiles of 256, split
+  const int64_t narrow = end_of(p.dx_tiles, narrow_stages(p.dx_blocks), 3, p.dw_tiles, narrow_stages(p.dw_blocks), 3);
   tiles(256);
-  const int64_t all = even(cost_of(p.dx_blocks), cost_of(p.dw_blocks));
-  p.dx_splits = splits_of(p.dx_tiles, p.dx_blocks, all), p.dw_splits = splits_of(p.dw_tiles, p.dw_blocks, all);
-  const int64_t part = longest(p.dx_blocks / p.dx_splits, p.dw_blocks / p.dw_splits);
-  const int64_t wide = (all > part ? all : part) + (p.dx_splits > 1 || p.dw_splits > 1 ? kJoinStages : 0);
-  p.narrow = narrow < wide;
+  const auto least = [](int blocks) { return blocks > 6 ? blocks : 6; };
+  const int64_t even =
+      (p.dx_tiles * least(p.dx_blocks) + p.dw_tiles * least(p.dw_blocks) + most_pairs() - 1) / most_pairs();
+  p.dx_splits = splits_of(p.dx_tiles, p.dx_blocks, even), p.dw_splits = splits_of(p.dw_tiles, p.dw_blocks, even);
+  const int64_t wide = end_of(p.dx_tiles * p.dx_splits, p.dx_blocks / p.dx_splits, p.dx_splits > 1 ? 11 : 6,
+                              p.dw_tiles * p.dw_splits, p.dw_blocks / p.dw_splits, p.dw_splits > 1 ? 11 : 6) +
+                       (p.dx_splits > 1 || p.dw_splits > 1 ? 24 : 0);
+  p.narrow = narrow * 6 < wide * 5;
   if (p.narrow) {
     tiles(128);
     p.dx_splits = p.dw_splits = 1;
@@ -706,14 +716,16 @@ bool pitch_ok(int64_t ld, int64_t cols, int64_t rows) {
   return rows <= 1 || (ld >= cols && ld < (1ll << 61) / rows && ld % 8 == 0);
 }
 
-// Whether tiles of 128 columns end earlier, by the longest pair's work (301 x
-// 1040 x 1456 9 us, in tiles of 256 11.7; 200 x 1024 x 2048 6.8 and 8.9; 700 x 4096 x
-// 4096 46 and 40.5).
+// Whether tiles of 128 columns end earlier: a wave takes its stages, or the ten (or
+// five) that a tile's activation and results take, which the last wave adds (301 x
+// 1040 x 1456 7.5 us, in tiles of 256 9.5; 1000 x 1024 x 1024 7.7 and 9.3; 260 x 768 x
+// 2992 9.3 and 8.1; 700 x 4096 x 4096 46 and 40.5).
 bool narrow_forward(int64_t tiles_m, int64_t hidden, int blocks) {
-  const int64_t pairs = sm_count() < 2 ? 1 : sm_count() / 2;
-  const auto waves = [&](int columns) { return (tiles_m * ceil_div(hidden, columns) + pairs - 1) / pairs; };
-  const int64_t narrow = waves(Wide<128>::kHidden);
-  return narrow * narrow_cost(blocks, narrow > 1) < waves(Wide<256>::kHidden) * cost_of(blocks);
+  const auto end = [&](int columns, int64_t stages, int64_t out) {
+    const int64_t waves = (tiles_m * ceil_div(hidden, columns) + most_pairs() - 1) / most_pairs();
+    return waves * (stages > out ? stages : out) + out;
+  };
+  return end(Wide<128>::kHidden, narrow_stages(blocks), 5) < end(Wide<256>::kHidden, blocks, 10);
 }
 
 // Forms g and u (FWD16, FWD8, AGAIN).
@@ -731,7 +743,7 @@ mp_status project(bool bf16, const void* x, const void* w_gate, const void* w_up
     return MP_ECUDA;
   f.o = o;
   q.rows = (int32_t)rows, q.cols = (int32_t)hidden;
-  lay_out(q, 1, ceil_div(rows, 2 * kHalf), ceil_div(hidden, box), 1, kForwardShift);
+  lay_out(q, 1, ceil_div(rows, 2 * kHalf), ceil_div(hidden, box), 1, kBand<EP>);
   if constexpr (EP != FWD8) {
     if (narrow) return bf16 ? launch<true, EP, 128>(f, st) : launch<false, EP, 128>(f, st);
   }
@@ -849,7 +861,7 @@ extern "C" MP_API mp_status linear_swiglu_backward(const void* dp, mp_dtype x_dt
     q.blocks0 = plan.dx_blocks / 2, q.blocks = plan.dx_blocks;
     q.rows = (int32_t)rows, q.cols = (int32_t)width;
     q.result[0] = dx, q.parts = reinterpret_cast<float*>(parts);
-    lay_out(q, 1, ceil_div(rows, 2 * kHalf), ceil_div(width, plan.narrow ? 128 : 256), plan.dx_splits, kGradientShift);
+    lay_out(q, 1, ceil_div(rows, 2 * kHalf), ceil_div(width, plan.narrow ? 128 : 256), plan.dx_splits, kBand<STORE>);
   }
   if (dw_gate) {
     Product& q = f.p[1];
@@ -859,7 +871,7 @@ extern "C" MP_API mp_status linear_swiglu_backward(const void* dp, mp_dtype x_dt
     q.blocks0 = q.blocks = plan.dw_blocks, q.a_mn = true;
     q.rows = (int32_t)hidden, q.cols = (int32_t)width;
     q.result[0] = dw_gate, q.result[1] = dw_up, q.parts = reinterpret_cast<float*>(parts + up256(plan.dx_parts));
-    lay_out(q, 2, ceil_div(hidden, 2 * kHalf), ceil_div(width, plan.narrow ? 128 : 256), plan.dw_splits, kGradientShift);
+    lay_out(q, 2, ceil_div(hidden, 2 * kHalf), ceil_div(width, plan.narrow ? 128 : 256), plan.dw_splits, kBand<STORE>);
   }
   return multiply(bf16, plan.narrow, f, st);
 }
