@@ -496,7 +496,7 @@ MP_API mp_status swiglu_backward(const void* dp, mp_dtype x_dtype, int64_t rows,
  * 2^20, rows < 2^31 - 256 (else MP_ESHAPE); tensors 16-byte aligned, FP32
  * scales 4-byte.  rows or hidden 0: nothing is written; width 0 otherwise:
  * MP_ESHAPE.  A row's results do not depend on the other rows' values (they do on
- * whether there are more than 128).  One kernel launch, reading its operands through tile copies: MP_ECUDA if the driver's
+ * how many rows there are).  One kernel launch, reading its operands through tile copies: MP_ECUDA if the driver's
  * tensor-map encoder is unavailable. */
 MP_API mp_status linear_swiglu(const void* x, mp_dtype x_dtype, int64_t rows, int64_t width, int64_t hidden,
                                const void* w_gate, const void* w_up, void* p, mp_dtype p_dtype, int32_t scale_block,

@@ -732,7 +732,7 @@ bool narrow_forward(int64_t tiles_m, int64_t hidden, int blocks) {
 template <int EP>
 mp_status project(bool bf16, const void* x, const void* w_gate, const void* w_up, int64_t rows, int64_t width,
                   int64_t hidden, const FfnOut& o, cudaStream_t st) {
-  if (rows <= kFewRows) return ffn_few_project(EP, bf16, x, w_gate, w_up, rows, width, hidden, o, st);
+  if (few_forward(rows, width, hidden)) return ffn_few_project(EP, bf16, x, w_gate, w_up, rows, width, hidden, o, st);
   Ffn f = {};
   Product& q = f.p[0];
   q.blocks = q.blocks0 = ceil_div(width, kBlockK);

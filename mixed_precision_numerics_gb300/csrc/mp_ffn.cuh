@@ -17,12 +17,18 @@ enum {
 };
 
 constexpr int kBlockK = 64;    // steps of the contraction in a stage: 128 bytes
-// Up to this many rows the products have the kernel of few rows.  (Its time grows
-// with them: 128 rows of 4096 x 14336 47 us, the other kernel's 129 rows 49; of
-// 2048 x 5504 16.1 and 15.4.  dx has it up to fewer: above, it shares the launch of
-// the weights' gradients; 100 rows of 2048 x 5504 backward 39.6 us with a kernel
-// of its own, 129 rows without 33.8, 37 rows of 4096 x 14336 98 and 105.)
+// Up to kFewDxRows rows the products have the kernel of few rows, the forward
+// product up to kFewRows where the weights are large, so that their way from DRAM
+// counts most.  (Its time grows with the rows: 100 rows of 4096 x 14336 44.2 us, the
+// other kernel's 129 rows 48.6; of 2048 x 5504 15.5 and 15.8, of 1024 x 2816 9.0 and
+// 7.5.  dx of more rows shares the launch of the weights' gradients: 100 rows of
+// 2048 x 5504 backward 39.6 us with a kernel of its own, 32.4 without, 37 rows of
+// 4096 x 14336 94 and 105.)
 constexpr int kFewRows = 128, kFewDxRows = 64;
+constexpr int64_t kLargeWeights = 1 << 23;  // elements of each
+inline bool few_forward(int64_t rows, int64_t width, int64_t hidden) {
+  return rows <= kFewDxRows || (rows <= kFewRows && width * hidden >= kLargeWeights);
+}
 
 // Stages added up inside the tensor core before the sums move on to registers:
 // 512 terms where FP32 scales show the truncation (1024 would save 4 % of the

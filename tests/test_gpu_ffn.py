@@ -8,7 +8,8 @@ pytestmark = pytest.mark.gpu
 BF16, F16 = torch.bfloat16, torch.float16
 SIZES = [(1, 16, 16), (1, 4096, 512), (3, 64, 128), (17, 80, 144), (37, 1040, 272), (64, 512, 1456), (129, 48, 400),
          (256, 256, 688), (257, 5120, 96), (301, 1040, 1456), (513, 592, 16), (4113, 32, 48),
-         (2, 8192, 160), (16, 1552, 4112), (33, 272, 128), (100, 4096, 528), (128, 2064, 256)]
+         (2, 8192, 160), (16, 1552, 4112), (33, 272, 128), (100, 4096, 528), (128, 2064, 256),
+         (100, 4096, 2064), (128, 8192, 1040)]
 
 
 @pytest.fixture
@@ -58,7 +59,7 @@ def test_forward(M, rows, width, hidden, dtype):
 
 @pytest.mark.parametrize("out,fp8", [(128, "e4m3"), (128, "e5m2"), (32, "e4m3"), (32, "e5m2")])
 @pytest.mark.parametrize("save", [0, 8, 16])
-@pytest.mark.parametrize("rows,width,hidden", [(1, 48, 32), (37, 1040, 288), (301, 528, 1440), (130, 2048, 160)])
+@pytest.mark.parametrize("rows,width,hidden", [(1, 48, 32), (37, 1040, 288), (301, 528, 1440), (130, 2048, 160), (97, 4096, 2080)])
 def test_forward_in_8_bits(M, rows, width, hidden, out, fp8, save):
     x, wg, wu, _ = U.inputs(rows, width, hidden, BF16, seed=3)
     (g, eg), (u, eu), (p, ep) = U.gated(x, wg, wu)
