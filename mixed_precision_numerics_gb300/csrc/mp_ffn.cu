@@ -25,11 +25,11 @@
 //
 // Bound by the tensor pipe, which is active 89 % of the cycles of [2048 x 4096 x
 // 14336], and in a warm loop by the power limit: [8192 x 4096 x 14336] BF16
-// forward 972 us cold and 1060 warm (the library product of the same shape
-// without the activation 1030 and 1090), with an FP8 product and the 8-bit
-// checkpoint 1010 and 1150, whose runs are shorter; dx and the weights' gradients
-// 2260 and 2330 (2145 and 2240).  Small products are a chain of latencies: 12,600
-// cycles for one tile, half of them before and after its work.
+// forward 939 us cold and 1075 warm (the library product of the same shape
+// without the activation 1052 and 1085), with an FP8 product and the 8-bit
+// checkpoint 998 and 1138, whose runs are shorter; dx and the weights' gradients
+// 2250 and 2320 to 2450 (2161 and 2254).  Small products are a chain of latencies:
+// 12,600 cycles for one tile, half of them before and after its work.
 #include <type_traits>
 
 #include "mp_chain.cuh"

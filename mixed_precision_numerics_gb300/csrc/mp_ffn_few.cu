@@ -1,4 +1,4 @@
-// mp_ffn_few.cu — the gated feed-forward products for up to 128 rows: a decoding
+// mp_ffn_few.cu — the gated feed-forward products for few rows (few_forward): a decoding
 // step, or the backward pass of a short sequence.
 //
 // The weights are read once and everything else is small, so the weights are
@@ -11,7 +11,7 @@
 //
 // Bound by DRAM: the stages of the CTAs on an SM, some 200 KB, are its bytes in
 // flight.  One row of 4096 x 14336 BF16: 37.5 us, 0.92 of the copy rate; 64 rows
-// 43.0; 128 rows 47; dx of one row 37.9.  What is left is the chain before the
+// 42; 128 rows 47; dx of one row 38.  What is left is the chain before the
 // first tile and after the last: sums to shared memory, the cluster's barrier,
 // the other CTAs' sums.
 #include "mp_chain.cuh"
