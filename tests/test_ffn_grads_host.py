@@ -118,3 +118,21 @@ def test_host_tensors_are_refused():
 
 def test_struct_layout():
     assert ctypes.sizeof(M.MpGrad) == 32 and M.MpGrad.numel.offset == 16 and M.MpGrad.out_dtype.offset == 28
+
+
+def test_a_plain_c_program_calls_them(tmp_path):
+    import os
+    import shutil
+    import subprocess
+
+    from tests.conftest import ROOT
+
+    pkg, exe, cc = os.path.join(ROOT, "mixed_precision_numerics_gb300"), str(tmp_path / "check"), shutil.which("gcc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    p = subprocess.run([cc, "-std=c99", "-Wall", "-Wextra", "-Werror", "-I", os.path.join(ROOT, "include"),
+                        os.path.join(ROOT, "tests", "products_abi_check.c"), "-L", pkg, "-lmpnum", f"-Wl,-rpath,{pkg}",
+                        "-o", exe], capture_output=True, text=True)
+    assert p.returncode == 0, p.stderr
+    p = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert p.returncode == 0 and "products abi ok" in p.stdout, p.stderr

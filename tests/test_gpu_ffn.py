@@ -156,8 +156,9 @@ def test_gradients_against_differences(M):
         assert abs(got - slope) <= limit, name
 
 
-def test_non_finite_rows_stay_to_themselves(M):
-    rows, width, hidden = 40, 64, 144
+@pytest.mark.parametrize("rows", [40, 100, 300])
+def test_non_finite_rows_stay_to_themselves(M, rows):
+    width, hidden = 64, 144
     x, wg, wu, dp = U.inputs(rows, width, hidden, BF16)
     clean = run_forward(M, x, wg, wu, 128, 8)
     x[7, 3], x[20, 5] = float("nan"), float("inf")
@@ -206,6 +207,41 @@ def test_only_the_outputs_are_written(M):
     M.linear_swiglu_backward(dp, x, wg, wu, *[g[1] for g in grads.values()], ws)
     for raw in [v[0] for v in outs.values()] + [v[0] for v in grads.values()] + [ws_raw, wide_raw, p_raw]:
         assert (raw[:4096] == 0xA5).all() and (raw[-4096:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("rows", [40, 300])
+def test_non_finite_gradients(M, rows):
+    """A row of dp with a NaN: its row of dx, and what its hidden elements give the weights; nothing else."""
+    width, hidden = 272, 400
+    x, wg, wu, dp = U.inputs(rows, width, hidden, BF16, seed=11)
+    dp[9, 33] = float("nan")
+    dx, dw = torch.empty_like(x), torch.empty(2, hidden, width, dtype=BF16, device="cuda")
+    M.linear_swiglu_backward(dp, x, wg, wu, dx, dw[0], dw[1], M.new_linear_swiglu_workspace(rows, width, hidden))
+    assert dx[9].isnan().all() and torch.isfinite(torch.cat([dx[:9], dx[10:]])).all()
+    assert dw[:, 33].isnan().all() and torch.isfinite(torch.cat([dw[:, :33], dw[:, 34:]], 1)).all()
+
+
+def test_the_calls_allocate_nothing(M):
+    sizes = [(5, 512, 288), (300, 512, 288), (200, 1040, 2064)]
+    made = [(U.inputs(*s, BF16), [torch.empty(s[0], s[2], dtype=BF16, device="cuda"), torch.empty(s[0], s[1], dtype=BF16, device="cuda"),
+                                  torch.empty(2, s[2], s[1], dtype=BF16, device="cuda"), M.new_linear_swiglu_workspace(*s)]) for s in sizes]
+    norm = torch.empty(1, device="cuda")
+    lists = [M.make_grad_array([o[2]]) for _, o in made]
+    spaces = [M.new_grad_norm_workspace(a) for a in lists]
+
+    def run():
+        for (v, o), a, w in zip(made, lists, spaces):
+            M.linear_swiglu(*v[:3], o[0])
+            M.linear_swiglu_backward(v[3], *v[:3], o[1], o[2][0], o[2][1], o[3])
+            M.mp_grad_norm(a, norm, w)
+            M.mp_grad_clip(a, norm, 1.0)
+        torch.cuda.synchronize()
+
+    run()  # the kernels are loaded
+    free, held = torch.cuda.mem_get_info()[0], torch.cuda.memory_stats()["allocation.all.allocated"]
+    for _ in range(3):
+        run()
+    assert free - torch.cuda.mem_get_info()[0] < 2 << 20 and torch.cuda.memory_stats()["allocation.all.allocated"] == held
 
 
 def test_captured_and_on_two_streams(M):
