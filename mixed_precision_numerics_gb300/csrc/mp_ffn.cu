@@ -234,6 +234,16 @@ __device__ __forceinline__ void codes32(const uint32_t (&r)[32], const Way& way,
   }
 }
 
+// A place in the ring of stages: its number, and the parity of the phase that a
+// full stage completes.
+template <int STAGES>
+struct Turn {
+  uint32_t s = 0, parity = 0;
+  __device__ __forceinline__ void step() {
+    if (++s == STAGES) s = 0, parity ^= 1;
+  }
+};
+
 // A row's 128 columns are in two threads, `half` 0 and 1: the larger of both.
 __device__ __forceinline__ uint32_t both_halves(uint32_t m, uint32_t* slot, int half, int row, int quad) {
   slot[half * kHalf + row] = m;
@@ -283,7 +293,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
       // weights' gradients of 8192 x 4096 x 14336 took 1280 us, then 1125.)
       const bool is_b = warp != kResultWarps;
       const uint32_t bars = map_rank(smem_u32(full), 0), tiles = smem_u32(smem) + (is_b ? kOperandBytes : 0);
-      uint32_t it = 0;
+      Turn<kStages> at_stage;
+      uint32_t filled = 0;  // stages that have been filled, kStages at most
       for (Walk w(f); ok && w.next(f);) {
         const Product& q = f.p[w.which];
         const Tile t = tile_of<kBand<EP>>(q, w.item);
@@ -300,9 +311,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
           at = t.n * G::kHidden;
           map0 = map1 = q.b + rank;
         }
-        for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
-          const int s = it % kStages;
-          if (!(ok = mbar_wait_bounded(empty + s, ((it / kStages) & 1) ^ 1))) break;
+        for (int kb = t.k0; kb < t.k1; ++kb, at_stage.step()) {
+          const uint32_t s = at_stage.s;
+          if (!(ok = mbar_wait_bounded(empty + s, at_stage.parity ^ 1))) break;
+          if (filled < kStages) ++filled;
           if (rank == 0 && !is_b) mbar_arrive_expect_tx(full + s, 2 * kStageBytes);
           const uint32_t bar = bars + s * 8, to = tiles + s * kStageBytes;
           const bool second = kb >= q.blocks0;
@@ -317,10 +329,12 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
         }
       }
       // The last arrivals at `empty` come from the other CTA: wait for them.
-      for (uint32_t j = it > kStages ? it - kStages : 0; j < it && ok; ++j)
-        ok = mbar_wait_bounded(empty + j % kStages, (j / kStages) & 1);
+      if (filled < kStages) at_stage = Turn<kStages>();
+      for (uint32_t j = 0; j < filled && ok; ++j, at_stage.step())
+        ok = mbar_wait_bounded(empty + at_stage.s, at_stage.parity ^ (filled == kStages));
     } else if (warp == kResultWarps + 1 && lane == 0 && rank == 0) {  // matrix instructions
-      uint32_t it = 0, chunk = 0;
+      Turn<kStages> at_stage;
+      uint32_t chunk = 0;
       for (Walk w(f); ok && w.next(f);) {
         const Product& q = f.p[w.which];
         const Tile t = tile_of<kBand<EP>>(q, w.item);
@@ -334,9 +348,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
           if (!(ok = mbar_wait_bounded(tempty + b, ((chunk >> 1) & 1) ^ 1))) break;
           tmem_fence_after();
           const int k1 = min(t.k1, k0 + kRun<EP>);
-          for (int kb = k0; kb < k1; ++kb, ++it) {
-            const int s = it % kStages;
-            if (!(ok = mbar_wait_bounded(full + s, (it / kStages) & 1))) break;
+          for (int kb = k0; kb < k1; ++kb, at_stage.step()) {
+            const uint32_t s = at_stage.s;
+            if (!(ok = mbar_wait_bounded(full + s, at_stage.parity))) break;
             tmem_fence_after();
             const uint32_t pa = smem_u32(smem + s * kStageBytes);
             const uint64_t da = a_mn ? operand_desc<true>(pa) : operand_desc<false>(pa);
