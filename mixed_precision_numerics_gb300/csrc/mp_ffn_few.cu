@@ -169,14 +169,14 @@ __global__ __launch_bounds__(kThreads, Shape<N, EP>::kCtas) void k_ffn_few(const
   }
   if (warp == 0 && lane < 2) prefetch_tensor_map(f.w + lane);
   if (warp == 1 && lane < (EP == STORE ? 2 : 1)) prefetch_tensor_map(f.x + lane);
-  if (warp == kResultWarps + 1) tmem_alloc<1>(smem_u32(tmem_at), S::kColumns);
-  tmem_fence_before();
   __syncthreads();
-  tmem_fence_after();
-  const uint32_t tmem = *tmem_at;
   chain_wait();
-  chain_release();
 
+  // An SM has room for other kernels beside this one, and tensor memory has to be
+  // waited for where they hold it.  So this CTA waits for nobody while it holds
+  // some itself: not for the kernel before (it is allocated after that), nor for
+  // the cluster (freed before its barriers); and the next kernel is let in when
+  // this one has got its own.  The first tiles are on their way meanwhile.
   bool ok = true;
   if (warp == kResultWarps) {
     if (lane == 0) {
@@ -198,6 +198,11 @@ __global__ __launch_bounds__(kThreads, Shape<N, EP>::kCtas) void k_ffn_few(const
       }
     }
   } else if (warp == kResultWarps + 1) {
+    tmem_alloc<1>(smem_u32(tmem_at), S::kColumns);
+    chain_release();
+    __syncwarp();
+    asm volatile("bar.arrive 1, %0;" ::"n"((kResultWarps + 1) * 32) : "memory");
+    const uint32_t tmem = *tmem_at;
     if (lane == 0) {
       constexpr bool MN = EP == STORE;
       constexpr uint32_t idesc = instr_desc<BF16, MN, false>(kTileRows, N);
@@ -222,6 +227,8 @@ __global__ __launch_bounds__(kThreads, Shape<N, EP>::kCtas) void k_ffn_few(const
         for (int s = 0; s < S::kStages; ++s) mbar_drain(full + s);
     }
   } else {
+    named_barrier(1, (kResultWarps + 1) * 32);  // tensor memory is there
+    const uint32_t tmem = *tmem_at;
     ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(done, 0));
     tmem_fence_after();
     // This part's sums: [row of x][matrix][128], where the ring was.
@@ -251,6 +258,9 @@ __global__ __launch_bounds__(kThreads, Shape<N, EP>::kCtas) void k_ffn_few(const
     }
     tmem_fence_before();
   }
+  __syncthreads();
+  tmem_fence_after();
+  if (warp == kResultWarps + 1) tmem_free<1>(*tmem_at, S::kColumns);
   __syncwarp();
   cluster_sync();  // every part's sums stand
   if (warp < kResultWarps) {
@@ -275,7 +285,6 @@ __global__ __launch_bounds__(kThreads, Shape<N, EP>::kCtas) void k_ffn_few(const
   }
   if (!ok) atomicAdd(&g_few_wait_failures, 1u);
   cluster_sync();  // no CTA leaves while another reads its sums
-  if (warp == kResultWarps + 1) tmem_free<1>(tmem, S::kColumns);
 }
 
 template <bool BF16, int N, int EP>
