@@ -60,7 +60,11 @@ struct Wide {
 constexpr int kMostStages = Wide<128>::kStages;
 constexpr int kBarrierBytes = 256;
 constexpr int kSmem = kRingBytes + kResultWarps * kStagingBytes + 2 * 2 * kHalf * 4 + kBarrierBytes;
-static_assert(kSmem <= 232448, "227 KB a CTA");
+// A pair allocates tensor memory on two SMs, so it can hold one's while it waits
+// for the other's, and it holds both while it waits for the kernel before.  No
+// other kernel that uses tensor memory can be on those SMs meanwhile: this one
+// leaves it less shared memory than its barriers need.
+static_assert(kSmem <= 232448 && kSmem > 231 * 1000, "227 KB a CTA");
 static_assert((2 * kMostStages + 4) * 8 + 8 <= kBarrierBytes, "barriers and the TMEM address");
 
 // One product in tiles.
