@@ -532,7 +532,8 @@ MP_API mp_status linear_swiglu_backward(const void* dp, mp_dtype x_dtype, int64_
 
 /* One gradient: numel >= 0 elements of grad_dtype and, for mp_grad_clip, where
  * the clipped ones go (out may be grad if out_dtype is grad_dtype).  Both types
- * MP_F32, MP_F16 or MP_BF16; pointers 16-byte aligned. */
+ * MP_F32, MP_F16 or MP_BF16; pointers 16-byte aligned, of any value where numel
+ * is 0. */
 typedef struct {
   const void* grad;
   void* out;

@@ -311,16 +311,17 @@ Extent extent_of(const mp_grad* g, int32_t n) {
 int64_t launches_of(const Extent& x) { return x.count <= kFew ? 1 : (x.count + kCap - 1) / kCap; }
 int most_ctas() { return sm_count() * kNormCtas; }
 
+// An empty gradient has types and nothing else: its pointers are not looked at.
 mp_status check(const mp_grad* g, int32_t n, bool outs) {
   if (n < 0 || (n > 0 && !g)) return MP_EINVAL;
   for (int32_t i = 0; i < n; ++i) {
-    if (g[i].numel < 0 || !float_type(g[i].grad_dtype)) return MP_EINVAL;
-    if (g[i].numel > 0 && !g[i].grad) return MP_EINVAL;
-    if (outs && (!float_type(g[i].out_dtype) || (g[i].numel > 0 && !g[i].out))) return MP_EINVAL;
+    if (g[i].numel < 0 || !float_type(g[i].grad_dtype) || (outs && !float_type(g[i].out_dtype))) return MP_EINVAL;
+    if (g[i].numel == 0) continue;
+    if (!g[i].grad || (outs && !g[i].out)) return MP_EINVAL;
     if (outs && g[i].out == g[i].grad && g[i].out_dtype != g[i].grad_dtype) return MP_EINVAL;
   }
   for (int32_t i = 0; i < n; ++i)
-    if (!aligned16(g[i].grad) || (outs && !aligned16(g[i].out))) return MP_EALIGN;
+    if (g[i].numel > 0 && (!aligned16(g[i].grad) || (outs && !aligned16(g[i].out)))) return MP_EALIGN;
   return MP_OK;
 }
 
