@@ -5,9 +5,10 @@
 // the operand with 128 rows (of M = 128 matrix instructions) and x is the other
 // one, padded to 16, 32, 64 or 128 columns.  A cluster of up to eight CTAs
 // shares a tile of 128 hidden elements (both matrices' rows of them), each
-// with a part of the contraction; their sums meet in shared memory and are
-// added in the order of the parts, a few rows of x for each CTA.  dx is the
-// same with tiles of 128 columns of the weights, taken as they lie (MN-major).
+// with a part of the contraction, whose runs are added in registers as they end;
+// the parts' sums meet in shared memory and are added in the order of the parts, a
+// few rows of x for each CTA.  dx is the same with tiles of 128 columns of the
+// weights, taken as they lie (MN-major).
 //
 // Bound by DRAM: the stages of the CTAs on an SM, some 200 KB, are its bytes in
 // flight.  One row of 4096 x 14336 BF16: 37.5 us, 0.92 of the copy rate; 64 rows
@@ -24,7 +25,7 @@ constexpr int kTileRows = 128;                       // of a matrix instruction
 constexpr int kWeightBytes = kTileRows * kBlockK * 2;  // one matrix's part of a stage
 constexpr int kResultWarps = 8;
 constexpr int kThreads = (kResultWarps + 2) * 32;    // one more warp copies, another issues
-constexpr int kBarrierBytes = 128;
+constexpr int kBarrierBytes = 256;
 
 // Columns N of x's operand, matrices in a tile: two (FWD, AGAIN) or one (STORE).
 template <int N, int EP>
@@ -40,11 +41,14 @@ struct Shape {
   static constexpr int kStages = ((kCtas == 2 ? 113 : 226) * 1024 - kBarrierBytes) / kStageBytes;
   static constexpr int kRing = kStages * kStageBytes;
   static constexpr int kSmem = (kRing > kSumBytes ? kRing : kSumBytes) + kBarrierBytes;
-  // Runs of the contraction have columns of TMEM of their own.
+  // Runs of the contraction take turns in places of their own in TMEM: one is
+  // added to registers while the next is formed.
   static constexpr int kRunColumns = kMatrices * N;
   static constexpr int kColumns = 512 / kCtas;
-  static constexpr int kRuns = kColumns / kRunColumns < 8 ? kColumns / kRunColumns : 8;
-  static_assert(kStages >= 2 && kStages <= 7 && kRuns >= 1 && kSumBytes <= 128 * 1024, "stages, TMEM columns");
+  static constexpr int kPlaces = kColumns / kRunColumns < 8 ? kColumns / kRunColumns : 8;
+  static constexpr int kGroups = kRunColumns < 32 ? 1 : kRunColumns / 32;  // of 16 columns, in a result thread
+  static_assert(kStages >= 2 && kPlaces >= 2 && kSumBytes <= 128 * 1024, "stages, TMEM columns");
+  static_assert((2 * kStages + 2 * kPlaces) * 8 + 4 <= kBarrierBytes, "barriers and the TMEM address");
 };
 
 struct Few {
@@ -155,16 +159,15 @@ __global__ __launch_bounds__(kThreads, Shape<N, EP>::kCtas) void k_ffn_few(const
   using S = Shape<N, EP>;
   extern __shared__ __align__(1024) unsigned char smem[];
   uint64_t* const full = reinterpret_cast<uint64_t*>(smem + S::kSmem - kBarrierBytes);
-  uint64_t *const empty = full + S::kStages, *const done = empty + S::kStages;
-  uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(done + 1);
-  static_assert((2 * S::kStages + 1) * 8 + 4 <= kBarrierBytes, "barriers and the TMEM address");
+  uint64_t *const empty = full + S::kStages, *const done = empty + S::kStages, *const free = done + S::kPlaces;
+  uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(free + S::kPlaces);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = blockIdx.x % f.parts, tile = blockIdx.x / f.parts;
   const int k0 = (int)((int64_t)f.blocks * part / f.parts), k1 = (int)((int64_t)f.blocks * (part + 1) / f.parts);
 
   if (warp == kResultWarps && lane == 0) {
     for (int s = 0; s < S::kStages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
-    mbar_init(done, 1);
+    for (int b = 0; b < S::kPlaces; ++b) mbar_init(done + b, 1), mbar_init(free + b, kResultWarps);
     fence_mbar_init();
   }
   if (warp == 0 && lane < 2) prefetch_tensor_map(f.w + lane);
@@ -206,55 +209,84 @@ __global__ __launch_bounds__(kThreads, Shape<N, EP>::kCtas) void k_ffn_few(const
     if (lane == 0) {
       constexpr bool MN = EP == STORE;
       constexpr uint32_t idesc = instr_desc<BF16, MN, false>(kTileRows, N);
-      for (int kb = k0, it = 0; kb < k1; ++kb, ++it) {
+      // r: the run, left: its stages to come
+      for (int kb = k0, it = 0, r = -1, left = 0; kb < k1; ++kb, ++it, --left) {
+        if (left == 0) {
+          left = f.run, ++r;
+          if (!(ok = mbar_wait_bounded(free + r % S::kPlaces, ((r / S::kPlaces) & 1) ^ 1))) break;
+        }
         const int s = it % S::kStages;
         if (!(ok = mbar_wait_bounded(full + s, (it / S::kStages) & 1))) break;
         tmem_fence_after();
         const uint32_t at = smem_u32(smem + s * S::kStageBytes);
         const uint64_t x = operand_desc<false>(at + S::kMatrices * kWeightBytes);
-        const uint32_t d = tmem + it / f.run * S::kRunColumns;
+        const uint32_t d = tmem + r % S::kPlaces * S::kRunColumns;
 #pragma unroll
         for (int m = 0; m < S::kMatrices; ++m) {
           const uint64_t w = operand_desc<MN>(at + m * kWeightBytes);
 #pragma unroll
           for (int j = 0; j < kBlockK / 16; ++j)
-            mma_f16<1>(d + m * N, w + j * kDescStep<MN>, x + j * kDescStep<false>, idesc, it % f.run != 0 || j != 0);
+            mma_f16<1>(d + m * N, w + j * kDescStep<MN>, x + j * kDescStep<false>, idesc, left != f.run || j != 0);
         }
         mma_commit<1>(empty + s);
+        if (left == 1 || kb == k1 - 1) mma_commit<1>(done + r % S::kPlaces);
       }
-      if (ok) mma_commit<1>(done);
-      else
+      if (!ok)
         for (int s = 0; s < S::kStages; ++s) mbar_drain(full + s);
     }
   } else {
     named_barrier(1, (kResultWarps + 1) * 32);  // tensor memory is there
     const uint32_t tmem = *tmem_at;
-    ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(done, 0));
-    tmem_fence_after();
-    // This part's sums: [row of x][matrix][128], where the ring was.
-    float* const sums = reinterpret_cast<float*>(smem);
     const int quad = warp & 3;  // the lanes that a warp can read
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     const int runs = (k1 - k0 + f.run - 1) / f.run;
+    // The warp's columns of a run, 16 at a time; those without a row of x stay out.
+    const auto column = [&](int i) { return (2 * i + (warp >> 2)) * 16; };
+    const auto used = [&](int c) { return c < S::kRunColumns && c % N < f.rows; };
+    // Waits for a run's sums; where they are.
+    const auto run_done = [&](int r) {
+      const int place = r % S::kPlaces;
+      ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(done + place, (r / S::kPlaces) & 1));
+      tmem_fence_after();
+      return lanes + place * S::kRunColumns;
+    };
+    const auto run_read = [&](int r) {  // their place is free
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(free + r % S::kPlaces);
+    };
+    uint32_t acc[S::kGroups][16];
+    uint32_t from = run_done(0);
 #pragma unroll
-    for (int c0 = 0; c0 < S::kMatrices * N; c0 += 32) {
-      const int c = c0 + (warp >> 2) * 16;
-      if (c >= S::kMatrices * N || c % N >= f.rows) continue;  // columns without a row
-      uint32_t acc[16];
-      tmem_load16(acc, lanes + c);
-      tmem_wait();
-      loaded(acc);
-      for (int r = 1; r < runs; ++r) {
+    for (int i = 0; i < S::kGroups; ++i)
+      if (used(column(i))) tmem_load16(acc[i], from + column(i));
+    tmem_wait();
+#pragma unroll
+    for (int i = 0; i < S::kGroups; ++i) loaded(acc[i]);
+    run_read(0);
+    for (int r = 1; r < runs; ++r) {
+      from = run_done(r);
+#pragma unroll
+      for (int i = 0; i < S::kGroups; ++i) {
+        if (!used(column(i))) continue;
         uint32_t v[16];
-        tmem_load16(v, lanes + r * S::kRunColumns + c);
+        tmem_load16(v, from + column(i));
         tmem_wait();
         loaded(v);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = __float_as_uint(__uint_as_float(acc[i]) + __uint_as_float(v[i]));
+        for (int k = 0; k < 16; ++k) acc[i][k] = __float_as_uint(__uint_as_float(acc[i][k]) + __uint_as_float(v[k]));
       }
+      run_read(r);
+    }
+    // This part's sums: [row of x][matrix][128], where the ring was.
+    float* const sums = reinterpret_cast<float*>(smem);
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        sums[((c % N + i) * S::kMatrices + c / N) * kTileRows + quad * 32 + lane] = __uint_as_float(acc[i]);
+    for (int i = 0; i < S::kGroups; ++i) {
+      const int c = column(i);
+      if (!used(c)) continue;
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        sums[((c % N + k) * S::kMatrices + c / N) * kTileRows + quad * 32 + lane] = __uint_as_float(acc[i][k]);
     }
     tmem_fence_before();
   }
@@ -300,8 +332,7 @@ mp_status launch(Few& f, int tiles, cudaStream_t st) {
   f.parts = 1;
   while (f.parts < 8 && tiles * f.parts * 2 <= sm_count() * S::kCtas && f.blocks >= 4 * f.parts) f.parts *= 2;
   const int most = ceil_div(f.blocks, f.parts);  // stages of a part
-  const int runs = ceil_div(most, kRun<EP>) < S::kRuns ? ceil_div(most, kRun<EP>) : S::kRuns;
-  f.run = ceil_div(most, runs);
+  f.run = ceil_div(most, ceil_div(most, kRun<EP>));  // runs of one length
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = f.parts, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
