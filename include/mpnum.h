@@ -483,7 +483,7 @@ MP_API mp_status swiglu_backward(const void* dp, mp_dtype x_dtype, int64_t rows,
  * x [rows, width], w_gate and w_up [hidden, width], of one type, MP_F16 or
  * MP_BF16.  Sums are binary32: within a run of terms they are the tensor core's,
  * which truncates, and runs are added rounded to nearest.  A run has at most 512
- * terms where p is FP8, 2048 otherwise.
+ * terms where p is FP8 or a checkpoint is written, 2048 otherwise.
  * p [rows, hidden]: of x's type (p_dtype = x_dtype, p_scales NULL), or FP8
  * (p_dtype MP_E4M3 or MP_E5M2) with scale_block 128 (FP32) or 32 (UE8M0) and
  * p_scales, by the rules of section 5 applied to the binary32 product.

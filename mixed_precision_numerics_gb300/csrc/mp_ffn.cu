@@ -19,8 +19,8 @@
 // weights' gradients are one launch, so that no pair waits between them.
 //
 // Sums: the tensor core adds to its binary32 accumulator by truncation, which
-// over a contraction of 4096 leaves results 4e-6 too small.  So every kRun
-// stages the sums so far leave TMEM and are added to registers with correct
+// over a contraction of 4096 leaves results 4e-6 too small.  So after every run
+// of stages the sums so far leave TMEM and are added to registers with correct
 // rounding, while the next run goes into the other half of TMEM.
 //
 // Bound by the tensor pipe, which is active 89 % of the cycles of [2048 x 4096 x
@@ -268,6 +268,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
   uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(tempty + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
+  const int run = W == 128 ? kLongRun : run_of<EP>(f.o);  // no checkpoint in narrow tiles
 
   if (warp == kResultWarps && lane == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
@@ -347,11 +348,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
         const uint32_t idesc = a_mn ? instr_desc<BF16, true, B_MN>(2 * kHalf, W)
                                     : instr_desc<BF16, false, B_MN>(2 * kHalf, W);
         const uint32_t step = a_mn ? kDescStep<true> : kDescStep<false>;
-        for (int k0 = t.k0; k0 < t.k1 && ok; k0 += kRun<EP>, ++chunk) {
+        for (int k0 = t.k0; k0 < t.k1 && ok; k0 += run, ++chunk) {
           const uint32_t b = chunk & 1, d = tmem + b * W;
           if (!(ok = mbar_wait_bounded(tempty + b, ((chunk >> 1) & 1) ^ 1))) break;
           tmem_fence_after();
-          const int k1 = min(t.k1, k0 + kRun<EP>);
+          const int k1 = min(t.k1, k0 + run);
           for (int kb = k0; kb < k1; ++kb, at_stage.step()) {
             const uint32_t s = at_stage.s;
             if (!(ok = mbar_wait_bounded(full + s, at_stage.parity))) break;
@@ -407,7 +408,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
         for (int j = 0; j < N; ++j) loaded(acc[j]);
         run_read();
       }
-      for (int k0 = t.k0 + kRun<EP>; k0 < t.k1; k0 += kRun<EP>) {
+      for (int k0 = t.k0 + run; k0 < t.k1; k0 += run) {
         const uint32_t at = run_done();
         // the next 16 columns on their way while 16 are added
         uint32_t r[2][16];

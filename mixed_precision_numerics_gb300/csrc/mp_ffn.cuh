@@ -31,12 +31,11 @@ inline bool few_forward(int64_t rows, int64_t width, int64_t hidden) {
 }
 
 // Stages added up inside the tensor core, at most, before the sums move on to
-// registers: 512 terms where FP32 scales show the truncation (1024 would save 4 %
-// of the time), 2048 where results are rounded to 16 bits.  Every instruction cuts
-// off up to a step of a binary32 sum, so a run of T terms ends up to T / 16 * 2^-23
-// too small, relative.
-template <int EP>
-constexpr int kRun = EP == FWD8 ? 8 : 32;
+// registers: 512 terms where FP32 scales show the truncation, those of an FP8
+// product or of the 8-bit checkpoint (1024 would save 4 % of the time), 2048 where
+// results are rounded to 16 bits.  Every instruction cuts off up to a step of a
+// binary32 sum, so a run of T terms ends up to T / 16 * 2^-23 too small, relative.
+constexpr int kShortRun = 8, kLongRun = 32;
 
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack16(float2 v) {  // a NaN gives 0x7FFF
@@ -89,6 +88,11 @@ struct FfnOut {
   const void* dp;          // AGAIN
   void *dg, *du;           // AGAIN: [rows][hidden] each
 };
+
+template <int EP>
+__host__ __device__ __forceinline__ int run_of(const FfnOut& o) {
+  return EP == FWD8 || (EP == FWD16 && o.ckpt) ? kShortRun : kLongRun;
+}
 
 // x [rows, width] and the weights [hidden, width]: FWD16, FWD8 or AGAIN for up to kFewRows rows.
 mp_status ffn_few_project(int ep, bool bf16, const void* x, const void* w_gate, const void* w_up, int64_t rows,

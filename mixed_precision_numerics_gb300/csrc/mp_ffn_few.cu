@@ -332,7 +332,7 @@ mp_status launch(Few& f, int tiles, cudaStream_t st) {
   f.parts = 1;
   while (f.parts < 8 && tiles * f.parts * 2 <= sm_count() * S::kCtas && f.blocks >= 4 * f.parts) f.parts *= 2;
   const int most = ceil_div(f.blocks, f.parts);  // stages of a part
-  f.run = ceil_div(most, ceil_div(most, kRun<EP>));  // runs of one length
+  f.run = ceil_div(most, ceil_div(most, run_of<EP>(f.o)));  // runs of one length
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = f.parts, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
