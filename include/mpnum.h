@@ -76,9 +76,11 @@ MP_API int32_t mp_version(void);
 /* Number of kernels this library has launched in this process (diagnostic). */
 MP_API uint64_t mp_launch_count(void);
 /* Number of bounded waits on a tile copy that gave up inside this library's
- * FP8 casts, norm backward kernel and feed-forward products since it was loaded (0 in normal operation).  A kernel whose
- * copy engine stopped answering waits about two seconds per wait, counts the
- * failure here and returns; the outputs of that call are then incomplete.
+ * FP8 casts, norm backward kernel and feed-forward products since it was loaded
+ * (0 in normal operation).  A kernel whose copy engine stopped answering waits
+ * about two seconds per wait, counts the failure here and returns.  The outputs of
+ * that call are then not to be used: parts of them are missing or NaN, or wrong
+ * where a later launch of the same call has read what was missing.
  * Reads device memory synchronously: call it after synchronising the streams
  * that ran the calls.  *out written; MP_EINVAL if out is NULL. */
 MP_API mp_status mp_wait_failures(uint32_t* out);

@@ -237,7 +237,7 @@ def mp_launch_count() -> int:
 
 
 def mp_wait_failures() -> int:
-    """Bounded tile-copy waits that gave up in the library's FP8 casts and norm backward kernel (0 normally)."""
+    """Bounded waits that gave up in the library's FP8 casts, norm backward kernel and feed-forward products (0 normally)."""
     out = ctypes.c_uint32(0)
     _check("mp_wait_failures", lib.mp_wait_failures(ctypes.byref(out)))
     return int(out.value)

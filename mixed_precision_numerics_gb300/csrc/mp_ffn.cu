@@ -248,9 +248,10 @@ struct Turn {
   }
 };
 
-// A row's 128 columns are in two threads, `half` 0 and 1: the larger of both.
-__device__ __forceinline__ uint32_t both_halves(uint32_t m, uint32_t* slot, int half, int row, int quad) {
-  slot[half * kHalf + row] = m;
+// A row's 128 columns are in two threads, `half` 0 and 1: the larger of both;
+// NaN for the other thread where this one's sums are not complete (!ok).
+__device__ __forceinline__ uint32_t both_halves(uint32_t m, bool ok, uint32_t* slot, int half, int row, int quad) {
+  slot[half * kHalf + row] = complete_or_nan(ok, m);
   named_barrier(1 + quad, 64);
   return max(m, slot[(half ^ 1) * kHalf + row]);
 }
@@ -498,8 +499,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
             if (f.o.ckpt) {
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                const uint32_t m = both_halves(max(amax32(acc[2 * j]), amax32(acc[2 * j + 1])), red + j * 2 * kHalf, half,
-                                               in_cta, quad);
+                const uint32_t m = both_halves(max(amax32(acc[2 * j]), amax32(acc[2 * j + 1])), ok, red + j * 2 * kHalf,
+                                               half, in_cta, quad);
                 float mul;
                 const float scale = tile_scale(m, 448.0f, &mul);
                 if (half == 0 && row < rows) f.o.ckpt_scales[((int64_t)j * q.rows + row) * f.o.tiles + tile] = scale;
@@ -527,7 +528,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ffn(const __grid_constant__ Ffn
                   static_cast<uint8_t*>(f.o.p_scales)[(int64_t)row * f.o.per_row + (col0 >> 5) + j] = (uint8_t)byte;
               }
             } else {
-              m[0] = m[1] = both_halves(max(m[0], m[1]), red, half, in_cta, quad);
+              m[0] = m[1] = both_halves(max(m[0], m[1]), ok, red, half, in_cta, quad);
               const float scale = tile_scale(m[0], f.o.e5m2 ? 57344.0f : 448.0f, &mul[0]);
               mul[1] = mul[0];
               if (half == 0 && row < rows) static_cast<float*>(f.o.p_scales)[(int64_t)row * f.o.per_row + tile] = scale;

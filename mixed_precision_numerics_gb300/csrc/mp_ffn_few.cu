@@ -68,14 +68,6 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const void* map, int32_t 
       "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
 
 // Four values of a row in each lane.
 struct Four {
@@ -161,6 +153,7 @@ __global__ __launch_bounds__(kThreads, Shape<N, EP>::kCtas) void k_ffn_few(const
   uint64_t* const full = reinterpret_cast<uint64_t*>(smem + S::kSmem - kBarrierBytes);
   uint64_t *const empty = full + S::kStages, *const done = empty + S::kStages, *const free = done + S::kPlaces;
   uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(free + S::kPlaces);
+  float* const sums = reinterpret_cast<float*>(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = blockIdx.x % f.parts, tile = blockIdx.x / f.parts;
   const int k0 = (int)((int64_t)f.blocks * part / f.parts), k1 = (int)((int64_t)f.blocks * (part + 1) / f.parts);
@@ -279,7 +272,6 @@ __global__ __launch_bounds__(kThreads, Shape<N, EP>::kCtas) void k_ffn_few(const
       run_read(r);
     }
     // This part's sums: [row of x][matrix][128], where the ring was.
-    float* const sums = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int i = 0; i < S::kGroups; ++i) {
       const int c = column(i);
@@ -292,14 +284,16 @@ __global__ __launch_bounds__(kThreads, Shape<N, EP>::kCtas) void k_ffn_few(const
   }
   __syncthreads();
   tmem_fence_after();
+  if (warp < kResultWarps && !ok)  // sums that are not complete, now that no copy is on its way to the ring
+    for (int i = threadIdx.x; i < S::kSumBytes / 4; i += kResultWarps * 32) sums[i] = __uint_as_float(complete_or_nan(ok, 0));
   if (warp == kResultWarps + 1) tmem_free<1>(*tmem_at, S::kColumns);
   __syncwarp();
   cluster_sync();  // every part's sums stand
   if (warp < kResultWarps) {
     const int col = tile * kTileRows + lane * 4;
     const bool in = col < f.cols;
-    uint32_t from = smem_u32(smem) + lane * 16;
-    for (int row = part + warp * f.parts; row < (ok ? f.rows : 0); row += kResultWarps * f.parts) {
+    const uint32_t from = smem_u32(sums) + lane * 16;
+    for (int row = part + warp * f.parts; row < f.rows; row += kResultWarps * f.parts) {
       Four v[S::kMatrices];
 #pragma unroll
       for (int m = 0; m < S::kMatrices; ++m) v[m].a = v[m].b = both(0.0f);

@@ -25,6 +25,18 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+__device__ __forceinline__ float4 ld_cluster(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
+// What others add or compare, as bits of a binary32 number: NaN where a wait for it
+// gave up (!ok), so that nothing finite comes of it.  (A flag for each CTA that the
+// others read costs 0.1 us of a launch.)
+__device__ __forceinline__ uint32_t complete_or_nan(bool ok, uint32_t bits) { return ok ? bits : 0x7FFFFFFFu; }
 // Orders nothing but tensor-memory accesses fenced before it.  A release would
 // wait for the warp's global stores: handing a run's tensor memory back took 2250
 // cycles that way and takes 310 (weights' gradients of one row of 4096 x 14336: 60
