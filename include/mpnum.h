@@ -551,8 +551,9 @@ typedef struct {
  * before its first use; every completed call leaves what it needs zero.  One
  * kernel launch for up to 512 tensors with elements, one more for each 512 further.
  *
- * mp_grad_clip — out = grad * c, c = min(1, max_norm / (*d_norm + 1e-6)) in
- * binary32 (formed in binary64), rounded once to out_dtype.  If *d_norm is not
+ * mp_grad_clip — out = grad * c, c = min(1, max_norm / (*d_norm + 1e-6)) formed
+ * in binary64 and rounded to binary32; the binary32 product is then rounded to
+ * out_dtype.  If *d_norm is not
  * finite c is NaN, so that every list clipped by it is seen as bad by the check
  * of a step.  c = 1 leaves gradients clipped in place untouched.  max_norm
  * finite and > 0 (else MP_EINVAL).  The gradients keep their loss scale.

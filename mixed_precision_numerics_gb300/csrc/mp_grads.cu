@@ -1,7 +1,8 @@
 // mp_grads.cu — the global norm of a list of gradients, and their clipping.
 //
 //   norm = sqrt(sum over all tensors of g^2) / S,  c = min(1, max / (norm + 1e-6)),
-//   out = g * c, in place or into tensors of another type.
+//   out = g * c, in place or into tensors of another type: a binary32 product,
+//   then rounded to that type.
 //
 // The optimizer's check pass (mp_adamw.cu) has the norm of one call's 16-bit
 // gradients, for that call alone.  These two calls are for what it does not

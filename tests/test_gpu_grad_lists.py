@@ -1,4 +1,4 @@
-"""Clipping: empty gradients in a list."""
+"""Clipping: empty gradients in a list, the clipped bits."""
 import pytest
 import torch
 
@@ -29,3 +29,17 @@ def test_empty_gradients_into_another_type(M, sizes, out):
     M.mp_grad_clip(grads, norm, 0.5, out=outs)
     c = torch.tensor(min(1.0, 0.5 / (float(norm) + 1e-6)), dtype=F32, device="cuda")
     assert all(torch.equal(o, (g * c).to(out)) for g, o in zip(grads, outs))
+
+
+@pytest.mark.parametrize("out", [F32, F16, BF16])
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+def test_clipped_bits(M, dtype, out):
+    """The binary32 product of the gradient and the factor, then that rounded to the type written."""
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    grads = [(torch.randn(n, generator=gen, device="cuda") * 2.0**-6).to(dtype) for n in (1 << 20, 16391, 3)]
+    outs = [torch.empty(g.numel(), dtype=out, device="cuda") for g in grads]
+    norm = norm_of(M, grads)
+    M.mp_grad_clip(grads, norm, 0.7, out=outs)
+    most = float(torch.tensor(0.7))  # a C float
+    c = torch.tensor(min(1.0, most / (float(norm) + 1e-6)), dtype=F32, device="cuda")
+    assert all(torch.equal(o, (g.float() * c).to(out)) for g, o in zip(grads, outs))
