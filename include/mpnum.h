@@ -546,7 +546,7 @@ typedef struct {
  * as mp_adamw_check forms it for its own list.  Squares neither overflow nor
  * underflow; sums are binary32 over 64 elements (32 in FP32) and binary64 above, in an order
  * fixed by the list and the device.  An infinite or NaN gradient gives an infinite or
- * NaN norm; an empty list 0.  out and out_dtype are not read.  d_workspace:
+ * NaN norm, finite ones whose norm is beyond binary32 an infinite one; an empty list 0.  out and out_dtype are not read.  d_workspace:
  * mp_grad_norm_workspace_size(grads, n) bytes, 16-byte aligned, zero-filled
  * before its first use; every completed call leaves what it needs zero.  One
  * kernel launch for up to 512 tensors with elements, one more for each 512 further.

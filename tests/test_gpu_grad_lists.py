@@ -1,4 +1,6 @@
-"""Clipping: empty gradients in a list, the clipped bits."""
+"""Clipping: empty gradients in a list, the clipped bits, norms beyond binary32."""
+import math
+
 import pytest
 import torch
 
@@ -43,3 +45,12 @@ def test_clipped_bits(M, dtype, out):
     most = float(torch.tensor(0.7))  # a C float
     c = torch.tensor(min(1.0, most / (float(norm) + 1e-6)), dtype=F32, device="cuda")
     assert all(torch.equal(o, (g.float() * c).to(out)) for g, o in zip(grads, outs))
+
+
+def test_a_norm_beyond_binary32(M):
+    """Finite FP32 gradients whose norm is not: infinity, and NaN for every clipped gradient."""
+    grads = [torch.full((5000,), 1e38, device="cuda"), torch.ones(3, dtype=BF16, device="cuda")]
+    norm = norm_of(M, grads)
+    assert float(norm) == math.inf
+    M.mp_grad_clip(grads, norm, 1.0)
+    assert all(g.isnan().all() for g in grads)
