@@ -511,8 +511,9 @@ MP_API mp_status linear_swiglu(const void* x, mp_dtype x_dtype, int64_t rows, in
  *     dg = dp * u * (s + g * s * (1 - s)),   du = dp * (g * s)
  *     dx = dg w_gate + du w_up               [rows, width]
  *     dw_gate = dg^T x,  dw_up = du^T x      [hidden, width], overwritten
- * all of x_dtype.  dg and du are rounded to it once, as operands; sums as in
- * the forward call, in an order fixed by the shape and the device.  dx may be
+ * all of x_dtype.  dg and du are rounded to it once, as operands (in MP_F16 one
+ * beyond 65504 becomes infinite, and so do the gradients that it goes into, even
+ * where their own values would be in range); sums as in the forward call, in an order fixed by the shape and the device.  dx may be
  * NULL, and dw_gate and dw_up together; what the others are does not depend on
  * that.  No output may overlap an input.
  * d_workspace: linear_swiglu_workspace_size(rows, width, hidden) bytes (for the
