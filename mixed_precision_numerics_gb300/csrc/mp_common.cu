@@ -57,20 +57,19 @@ bool encode_tile_map_2d(CUtensorMap* map, const void* base, int esize, int64_t r
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool encode_swizzled_map_2d(CUtensorMap* map, const void* base, int esize, int64_t rows, int64_t cols,
-                            int64_t pitch_bytes, int box_rows, int box_cols) {
+bool encode_swizzled_map_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t pitch_bytes,
+                            int box_rows) {
   if (rows < 1 || cols < 1 || rows >= (1ll << 31) || cols >= (1ll << 31)) return false;  // int32 box coordinates
   if ((reinterpret_cast<uintptr_t>(base) & 15u) || (pitch_bytes & 15)) return false;
   const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return false;
-  const CUtensorMapDataType dt = esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   const cuuint64_t pitch[1] = {(cuuint64_t)pitch_bytes};
-  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
   const cuuint32_t unit[2] = {1, 1};
-  return enc(map, dt, 2, const_cast<void*>(base), dims, pitch, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             box_cols * esize == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, pitch, box, unit,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace mp

@@ -72,7 +72,7 @@ inline int32_t ceil_div(int64_t a, int64_t b) { return (int32_t)((a + b - 1) / b
 
 // A matrix of 16-bit elements with rows `pitch` elements apart, in boxes of box_rows x 64.
 inline bool map16(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t pitch, int box_rows) {
-  return encode_swizzled_map_2d(m, p, 2, rows, cols, pitch * 2, box_rows, 64);
+  return encode_swizzled_map_2d(m, p, rows, cols, pitch * 2, box_rows);
 }
 
 // What the forward call writes, and what AGAIN reads and writes.

@@ -34,10 +34,10 @@ inline int grid_for(int64_t work_ctas, int per_sm) {
 bool encode_tile_map_2d(CUtensorMap* map, const void* base, int esize, int64_t rows, int64_t cols, int box_rows,
                         int box_cols);
 
-// The same with rows `pitch_bytes` apart, of 16-bit or 8-bit elements, in boxes
-// whose rows of 128 or 64 bytes are swizzled in shared memory by that length.
-bool encode_swizzled_map_2d(CUtensorMap* map, const void* base, int esize, int64_t rows, int64_t cols,
-                            int64_t pitch_bytes, int box_rows, int box_cols);
+// The same for 16-bit elements in rows `pitch_bytes` apart, in boxes of 64 columns,
+// whose rows of 128 bytes are swizzled in shared memory.
+bool encode_swizzled_map_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t pitch_bytes,
+                            int box_rows);
 
 // Bounded waits that gave up in this library's kernels since it was loaded.
 uint32_t fp8_wait_failures();   // mp_fp8.cu
