@@ -25,10 +25,11 @@
 //
 // Bound by the tensor pipe, which is active 89 % of the cycles of [2048 x 4096 x
 // 14336], and in a warm loop by the power limit: [8192 x 4096 x 14336] BF16
-// forward 939 us cold and 1075 warm (the library product of the same shape
+// forward 945 to 970 us cold and 1075 warm (the library product of the same shape
 // without the activation 1052 and 1085), with an FP8 product and the 8-bit
-// checkpoint 998 and 1138, whose runs are shorter; dx and the weights' gradients
-// 2250 and 2320 to 2450 (2161 and 2254).  Small products are a chain of latencies:
+// checkpoint 990 to 1025 and 1148, with the checkpoint beside a 16-bit product 1000
+// to 1020 cold, since their runs are shorter; dx and the weights' gradients 2250 and
+// 2320 to 2450 (2161 and 2254).  Small products are a chain of latencies:
 // 12,600 cycles for one tile, half of them before and after its work.
 #include <type_traits>
 

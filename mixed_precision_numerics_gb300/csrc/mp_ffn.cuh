@@ -21,9 +21,17 @@ constexpr int kBlockK = 64;    // steps of the contraction in a stage: 128 bytes
 // product up to kFewRows where the weights are large, so that their way from DRAM
 // counts most.  (Its time grows with the rows: 100 rows of 4096 x 14336 44.2 us, the
 // other kernel's 129 rows 48.6; of 2048 x 5504 15.5 and 15.8, of 1024 x 2816 9.0 and
-// 7.5.  dx of more rows shares the launch of the weights' gradients: 100 rows of
-// 2048 x 5504 backward 39.6 us with a kernel of its own, 32.4 without, 37 rows of
-// 4096 x 14336 94 and 105.)
+// 7.5.)
+// dx of more rows shares the launch of the weights' gradients.  Its bits must not
+// depend on whether those are asked for, so one rule serves both calls.  Up to 64
+// rows a kernel of its own is much faster alone and not far off beside them (us by
+// rows, of its own and in the shared launch, swiglu_backward included):
+//                 dx alone             all gradients
+//   4096 x 14336  1: 40, 70  64: 46, 70    1: 92, 97   64: 97, 100
+//   2048 x 5504   1: 13, 24  64: 17, 25    1: 27, 28   64: 35, 31
+//   1024 x 2816   1: 8, 13   64: 9, 13     1: 14, 13.5 64: 20, 19
+//   256 x 688     1: 5, 9    64: 6.5, 9    1: 8.4, 8.9 64: 10.1, 9.3
+// 100 rows of 2048 x 5504 with all gradients: 39.6 and 32.4.
 constexpr int kFewRows = 128, kFewDxRows = 64;
 constexpr int64_t kLargeWeights = 1 << 23;  // elements of each
 inline bool few_forward(int64_t rows, int64_t width, int64_t hidden) {

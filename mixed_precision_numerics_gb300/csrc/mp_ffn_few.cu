@@ -11,8 +11,8 @@
 // weights, taken as they lie (MN-major).
 //
 // Bound by DRAM: the stages of the CTAs on an SM, some 200 KB, are its bytes in
-// flight.  One row of 4096 x 14336 BF16: 37.5 us, 0.92 of the copy rate; 64 rows
-// 42; 128 rows 47; dx of one row 38.  What is left is the chain before the
+// flight.  One row of 4096 x 14336 BF16: 38 us, 0.92 of the copy rate; 64 rows 42;
+// 128 rows 46; dx of one row 38.  What is left is the chain before the
 // first tile and after the last: sums to shared memory, the cluster's barrier,
 // the other CTAs' sums.
 #include "mp_chain.cuh"
@@ -320,9 +320,12 @@ mp_status launch(Few& f, int tiles, cudaStream_t st) {
   const auto kernel = k_ffn_few<BF16, N, EP>;
   if (!smem_opt_in(kernel, S::kSmem, done)) return MP_ECUDA;
   // As many parts, by twos, as there is place for at once, each with two stages
-  // at least: clusters of 3, 5, 6 and 7 leave places empty (2048 x 5504 for one
-  // row: four parts 11.0 us, seven 16.1), and a second wave costs as much
-  // (4096 x 14336: two parts 38 us, four 40).
+  // at least: clusters of 3, 5, 6 and 7 leave places empty where two CTAs share an SM
+  // (2048 x 5504 for one row: four parts 11.0 us, seven 16.1).  Where a CTA has its
+  // SM alone they go either way: three parts for two take 100 rows of 2048 x 5504
+  // from 15.7 to 14.8 us and 64 rows from 13.6 to 13.5, six for four 64 rows of 1024 x
+  // 2816 from 7.4 to 8.4.  A second wave costs as much (4096 x 14336: two parts 38 us,
+  // four 40).
   f.parts = 1;
   while (f.parts < 8 && tiles * f.parts * 2 <= sm_count() * S::kCtas && f.blocks >= 4 * f.parts) f.parts *= 2;
   const int most = ceil_div(f.blocks, f.parts);  // stages of a part

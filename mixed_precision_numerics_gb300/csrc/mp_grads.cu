@@ -17,7 +17,7 @@
 // Bound by DRAM: the norm reads every gradient once; the clipping reads and
 // writes it.  The clipping walks the list backwards, so that it begins with
 // what the norm has left in L2.  839M BF16 gradients: norm 236 us (7.1 TB/s),
-// clipping 525 (6.4), both 767, which is 0.97 of three passes at the copy rate;
+// clipping 525 (6.4), both 761, which is 0.98 of three passes at the copy rate;
 // 81M FP32 into FP16 118 us, 1.0.  Three CTAs an SM, 96 KB of loads in flight:
 // four have 64 registers a thread and spill (norm 300 us).  Few small tensors are
 // the latency of two launches (20 tensors of 2.6M elements 9.8 us on the GPU).
