@@ -202,8 +202,8 @@ __global__ __launch_bounds__(kThreads, Shape<N, EP>::kCtas) void k_ffn_few(const
     if (lane == 0) {
       constexpr bool MN = EP == STORE;
       constexpr uint32_t idesc = instr_desc<BF16, MN, false>(kTileRows, N);
-      // r: the run, left: its stages to come
-      for (int kb = k0, it = 0, r = -1, left = 0; kb < k1; ++kb, ++it, --left) {
+      int r = -1;  // the run
+      for (int kb = k0, it = 0, left = 0; kb < k1; ++kb, ++it, --left) {  // left: its stages to come
         if (left == 0) {
           left = f.run, ++r;
           if (!(ok = mbar_wait_bounded(free + r % S::kPlaces, ((r / S::kPlaces) & 1) ^ 1))) break;
@@ -224,6 +224,9 @@ __global__ __launch_bounds__(kThreads, Shape<N, EP>::kCtas) void k_ffn_few(const
         mma_commit<1>(empty + s);
         if (left == 1 || kb == k1 - 1) mma_commit<1>(done + r % S::kPlaces);
       }
+      // No instruction is left at work on shared or tensor memory, also where the
+      // warps that read the results have given up.
+      if (ok) ok = mbar_wait_bounded(done + r % S::kPlaces, (r / S::kPlaces) & 1);
       if (!ok)
         for (int s = 0; s < S::kStages; ++s) mbar_drain(full + s);
     }
